@@ -55,10 +55,22 @@ typedef enum convrot_status {
     CONVROT_ERR_BITS = 6,      /* bits is not 8 or 4                                             */
     CONVROT_ERR_WORKSPACE = 7, /* workspace NULL, misaligned or smaller than the call requires  */
     CONVROT_ERR_HIP = 8,       /* a HIP runtime call or kernel launch failed                     */
-    CONVROT_ERR_DEVICE = 9     /* the current device is not gfx950                               */
+    CONVROT_ERR_DEVICE = 9,    /* the current device is not gfx950                               */
+    CONVROT_ERR_ACT = 10,      /* unknown activation code                                        */
+    CONVROT_ERR_OVERLAP = 11   /* an output overlaps another array it must not (see the call)   */
 } convrot_status;
 
 enum { CONVROT_DTYPE_F32 = 0, CONVROT_DTYPE_BF16 = 1 };
+
+/* Activations of the fused linears: z;  max(z, 0);  z / (1 + e^-z);  z Phi(z) with the normal
+ * distribution Phi;  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+enum {
+    CONVROT_ACT_NONE = 0,
+    CONVROT_ACT_RELU = 1,
+    CONVROT_ACT_SILU = 2,
+    CONVROT_ACT_GELU = 3,
+    CONVROT_ACT_GELU_TANH = 4
+};
 
 #define CONVROT_MAX_K 131072
 /* The tiled GEMMs (the W8A8 linear at M > 16 and every W4A4 call) need N < CONVROT_GEMM_MAX_N:
@@ -126,6 +138,64 @@ size_t convrot_workspace_bytes(int64_t M, int64_t N, int64_t K, int bits);
 int convrot_linear(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,
                    int64_t K, int group, const int8_t *wq, const float *w_scale, const float *bias, void *y,
                    void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * INT8 ConvRot linear with an activation and a residual in its epilogue:
+ *   z = (xq . wq^T) * sx[m] * sw[n] + bias[n]  in fp32;   y = bf16( act(z) + residual[m,n] )
+ *   act one of CONVROT_ACT_*; residual bf16 [M, N] or NULL, added in fp32 (one rounding).
+ *   pre bf16 [M, N] or NULL: when given, receives bf16(z) for convrot_linear_act_backward.
+ * All other arguments, the dispatch by M, the workspace (convrot_workspace_bytes(M, N, K, 8)) and the
+ * split-K tail are convrot_linear's; with act NONE and no residual the outputs are its outputs
+ * bit for bit.  residual may be y itself (added in place); any other overlap of y, pre and
+ * residual returns CONVROT_ERR_OVERLAP.  residual, pre: 16-byte aligned.
+ */
+int convrot_linear_act(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,
+                       int64_t K, int group, const int8_t *wq, const float *w_scale, const float *bias, int act,
+                       const void *residual, void *pre, void *y, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/*
+ * Gate and up projections of a gated feed-forward block, the activation and the product in one
+ * kernel:
+ *   g = (xq . wq_gate^T) * sx * gate_scale + gate_bias,  u likewise from wq_up;   h = bf16( act(g) * u )
+ *   wq_gate, wq_up int8 [N, K] and their scales fp32 [N] from convrot_prepare_weight(bits = 8, the
+ *   group of x); gate_bias, up_bias fp32 [N] or NULL; h bf16 [M, N].
+ *   pre bf16 [2, M, N] or NULL: when given, receives bf16(g), then bf16(u), for
+ *   convrot_linear_gated_backward; h is formed from the unrounded g and u.
+ * x (or xq, x_scale) and the dispatch by M as in convrot_linear; the workspace is
+ * convrot_workspace_bytes_gated(M, N, K) bytes under the same rules.  An overlap of h and pre
+ * returns CONVROT_ERR_OVERLAP.
+ */
+int convrot_linear_gated(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,
+                         int64_t K, int group, const int8_t *wq_gate, const float *gate_scale, const float *gate_bias,
+                         const int8_t *wq_up, const float *up_scale, const float *up_bias, int act, void *pre, void *h,
+                         void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of convrot_linear_gated (the quantized x, then room for the GEMM's split-K
+ * tail); 0 on invalid arguments. */
+size_t convrot_workspace_bytes_gated(int64_t M, int64_t N, int64_t K);
+
+/*
+ * Gated feed-forward block: h as in convrot_linear_gated (F hidden channels), then
+ *   y = bf16( linear(h) + down_bias + residual )
+ * where linear is the INT8 ConvRot linear of h with wq_down int8 [K, F]: h (bf16) is rotated in groups
+ * of group_h and quantized per token like any activation.
+ *   x bf16/fp32 [M, K]; wq_gate, wq_up int8 [F, K] (prepared with group), wq_down int8 [K, F] (prepared
+ *   with group_h); biases fp32 or NULL; residual bf16 [M, K] or NULL, may be y itself;
+ *   pre bf16 [2, M, F] or NULL as in convrot_linear_gated; y bf16 [M, K].
+ *   K % 64 == 0, F % 64 == 0, both in [64, CONVROT_MAX_K] and multiples of their groups.
+ *   workspace: convrot_workspace_bytes_ffn(M, F, K) bytes, 256-byte aligned, required (the codes of x
+ *   and h, h itself, the split-K tails).
+ * The result is that of convrot_linear_gated followed by convrot_linear_act, bit for bit.
+ */
+int convrot_ffn_gated(const void *x, int x_dtype, int64_t M, int64_t F, int64_t K, int group, int group_h,
+                      const int8_t *wq_gate, const float *gate_scale, const float *gate_bias, const int8_t *wq_up,
+                      const float *up_scale, const float *up_bias, const int8_t *wq_down, const float *down_scale,
+                      const float *down_bias, int act, const void *residual, void *pre, void *y, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of convrot_ffn_gated; 0 on invalid arguments. */
+size_t convrot_workspace_bytes_ffn(int64_t M, int64_t F, int64_t K);
 
 /* Size of the fixed scratch array convrot_linear_noalloc uses on each GPU (32 MiB). */
 #define CONVROT_NOALLOC_SCRATCH_BYTES 33554432

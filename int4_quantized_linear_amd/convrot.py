@@ -18,7 +18,8 @@ LIB_PATH = os.path.join(_HERE, "libconvrot.so")
 CONVROT_DTYPE_F32, CONVROT_DTYPE_BF16 = 0, 1
 STATUS = {0: "CONVROT_OK", 1: "CONVROT_ERR_NULL", 2: "CONVROT_ERR_SHAPE", 3: "CONVROT_ERR_GROUP",
           4: "CONVROT_ERR_ALIGN", 5: "CONVROT_ERR_DTYPE", 6: "CONVROT_ERR_BITS", 7: "CONVROT_ERR_WORKSPACE",
-          8: "CONVROT_ERR_HIP", 9: "CONVROT_ERR_DEVICE"}
+          8: "CONVROT_ERR_HIP", 9: "CONVROT_ERR_DEVICE", 10: "CONVROT_ERR_ACT", 11: "CONVROT_ERR_OVERLAP"}
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 # name -> (argtypes, restype); mirrors include/convrot.h
 P, I64, I, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -27,6 +28,11 @@ SIGNATURES = {
     "convrot_quantize_act": ([P, I, I64, I64, I, I, P, P, P], I),
     "convrot_workspace_bytes": ([I64, I64, I64, I], SZ),
     "convrot_linear": ([P, I, P, P, I64, I64, I64, I, P, P, P, P, P, SZ, P], I),
+    "convrot_linear_act": ([P, I, P, P, I64, I64, I64, I, P, P, P, I, P, P, P, P, SZ, P], I),
+    "convrot_linear_gated": ([P, I, P, P, I64, I64, I64, I, P, P, P, P, P, P, I, P, P, P, SZ, P], I),
+    "convrot_workspace_bytes_gated": ([I64, I64, I64], SZ),
+    "convrot_ffn_gated": ([P, I, I64, I64, I64, I, I, P, P, P, P, P, P, P, P, P, I, P, P, P, P, SZ, P], I),
+    "convrot_workspace_bytes_ffn": ([I64, I64, I64], SZ),
     "convrot_linear_noalloc": ([P, I, P, P, I64, I64, I64, I, P, P, P, P, P], I),
     "convrot_linear_w4a4": ([P, I, P, P, I64, I64, I64, I, P, P, P, P, P, SZ, P], I),
     "convrot_pack_weight_w4a4": ([P, I64, I64, P, P], I),
@@ -167,6 +173,134 @@ def linear(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, bias
     _call("convrot_linear", _ptr(x), _dtype_code(x) if x is not None else 0, _ptr(xq), _ptr(x_scale), M, N, K, group,
           _ptr(wq), _ptr(w_scale), _ptr(bias), _ptr(y), _ptr(ws), ws.numel() if ws is not None else 0, _stream(dev))
     return y
+
+
+def _act_code(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError("act is one of %s, got %r" % (", ".join(ACTS), act))
+    return ACTS[act]
+
+
+def _check(dev: torch.device, **tensors):
+    """name=(tensor or None, shape, dtype or tuple of dtypes): contiguous, on dev, of that shape and type."""
+    for name, (t, shape, dtype) in tensors.items():
+        if t is None:
+            continue
+        if t.device != dev or not t.is_cuda:
+            raise ValueError("%s is on %s; the call runs on the weights' GPU, %s" % (name, t.device, dev))
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+        if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+            raise TypeError("%s is %s, expected %s" % (name, t.dtype, dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+def _call_on(dev: torch.device, name: str, *args):
+    """_call with the tensors' device current (the library launches on the current device), on its
+    current torch stream, which is appended as the last argument."""
+    if torch.cuda.current_device() == dev.index:
+        return _call(name, *args, _stream(dev))
+    with torch.cuda.device(dev):
+        return _call(name, *args, _stream(dev))
+
+
+_X_DTYPES = (torch.bfloat16, torch.float32)
+
+
+def _tokens(x, xq, x_scale, K: int, dev: torch.device) -> int:
+    """Checks x, or the pre-quantized pair, and returns the token count."""
+    if x is None and (xq is None or x_scale is None):
+        raise ValueError("give x, or both xq and x_scale")
+    M = x.shape[0] if x is not None else xq.shape[0]
+    if x is not None:
+        _check(dev, x=(x, (M, K), _X_DTYPES))
+    else:
+        _check(dev, xq=(xq, (M, K), torch.int8), x_scale=(x_scale, (M,), torch.float32))
+    return M
+
+
+def linear_act(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, bias: torch.Tensor | None = None,
+               act: str = "none", residual: torch.Tensor | None = None, group: int = 256,
+               xq: torch.Tensor | None = None, x_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               save_pre: bool = False):
+    """INT8 ConvRot linear with its activation and residual in the epilogue:
+    z = (q(xR) . q(wR)^T) * sx * sw + bias,  y = bf16(act(z) + residual).  x (or xq, x_scale) and the
+    weight as in linear(); act one of ACTS; residual bf16 [M, N], may be ``out`` (added in place).
+    save_pre=True returns (y, pre) with pre = bf16(z) [M, N] for linear_act_backward."""
+    code = _act_code(act)
+    N, K = wq.shape
+    dev = wq.device
+    M = _tokens(x, xq, x_scale, K, dev)
+    _check(dev, wq=(wq, (N, K), torch.int8), w_scale=(w_scale, (N,), torch.float32), bias=(bias, (N,), torch.float32),
+           residual=(residual, (M, N), torch.bfloat16), out=(out, (M, N), torch.bfloat16))
+    y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    pre = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if save_pre else None
+    ws = _workspace(M, N, K, 8, dev)
+    _call_on(dev, "convrot_linear_act", _ptr(x), _dtype_code(x) if x is not None else 0, _ptr(xq), _ptr(x_scale), M, N,
+             K, group, _ptr(wq), _ptr(w_scale), _ptr(bias), code, _ptr(residual), _ptr(pre), _ptr(y), _ptr(ws),
+             ws.numel())
+    return (y, pre) if save_pre else y
+
+
+def workspace_bytes_gated(M: int, N: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_gated(M, N, K))
+
+
+def linear_gated(x: torch.Tensor | None, wq_gate: torch.Tensor, gate_scale: torch.Tensor, wq_up: torch.Tensor,
+                 up_scale: torch.Tensor, bias_gate: torch.Tensor | None = None, bias_up: torch.Tensor | None = None,
+                 act: str = "silu", group: int = 256, xq: torch.Tensor | None = None,
+                 x_scale: torch.Tensor | None = None, out: torch.Tensor | None = None, save_pre: bool = False):
+    """Gate and up projections of one input, the activation and the product in one kernel:
+    h = bf16(act(g) * u) with g and u the INT8 ConvRot linears of x.  save_pre=True returns (h, pre)
+    with pre = bf16 [2, M, N], g then u, for linear_gated_backward."""
+    code = _act_code(act)
+    N, K = wq_gate.shape
+    dev = wq_gate.device
+    M = _tokens(x, xq, x_scale, K, dev)
+    f32 = torch.float32
+    _check(dev, wq_gate=(wq_gate, (N, K), torch.int8), gate_scale=(gate_scale, (N,), f32),
+           wq_up=(wq_up, (N, K), torch.int8), up_scale=(up_scale, (N,), f32), bias_gate=(bias_gate, (N,), f32),
+           bias_up=(bias_up, (N,), f32), out=(out, (M, N), torch.bfloat16))
+    h = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    pre = torch.empty((2, M, N), dtype=torch.bfloat16, device=dev) if save_pre else None
+    ws = torch.empty(max(workspace_bytes_gated(M, N, K), 256), dtype=torch.uint8, device=dev)
+    _call_on(dev, "convrot_linear_gated", _ptr(x), _dtype_code(x) if x is not None else 0, _ptr(xq), _ptr(x_scale), M,
+             N, K, group, _ptr(wq_gate), _ptr(gate_scale), _ptr(bias_gate), _ptr(wq_up), _ptr(up_scale), _ptr(bias_up),
+             code, _ptr(pre), _ptr(h), _ptr(ws), ws.numel())
+    return (h, pre) if save_pre else h
+
+
+def workspace_bytes_ffn(M: int, F: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_ffn(M, F, K))
+
+
+def ffn_gated(x: torch.Tensor, wq_gate: torch.Tensor, gate_scale: torch.Tensor, wq_up: torch.Tensor,
+              up_scale: torch.Tensor, wq_down: torch.Tensor, down_scale: torch.Tensor,
+              bias_gate: torch.Tensor | None = None, bias_up: torch.Tensor | None = None,
+              bias_down: torch.Tensor | None = None, act: str = "silu", residual: torch.Tensor | None = None,
+              group: int = 256, group_h: int = 256, out: torch.Tensor | None = None, save_pre: bool = False):
+    """Gated feed-forward block on INT8 ConvRot weights: h = bf16(act(g) * u) as in linear_gated
+    (gate, up [F, K], prepared with ``group``), then y = bf16(linear(h) + bias_down + residual) (down
+    [K, F], prepared with ``group_h``).  residual bf16 [M, K], may be ``out``.  save_pre=True returns
+    (y, pre) with pre = bf16 [2, M, F], g then u, for ffn_gated_backward."""
+    code = _act_code(act)
+    F, K = wq_gate.shape
+    dev = wq_gate.device
+    M = _tokens(x, None, None, K, dev)
+    f32 = torch.float32
+    _check(dev, wq_gate=(wq_gate, (F, K), torch.int8), gate_scale=(gate_scale, (F,), f32),
+           wq_up=(wq_up, (F, K), torch.int8), up_scale=(up_scale, (F,), f32),
+           wq_down=(wq_down, (K, F), torch.int8), down_scale=(down_scale, (K,), f32), bias_gate=(bias_gate, (F,), f32),
+           bias_up=(bias_up, (F,), f32), bias_down=(bias_down, (K,), f32), residual=(residual, (M, K), torch.bfloat16),
+           out=(out, (M, K), torch.bfloat16))
+    y = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    pre = torch.empty((2, M, F), dtype=torch.bfloat16, device=dev) if save_pre else None
+    ws = torch.empty(max(workspace_bytes_ffn(M, F, K), 256), dtype=torch.uint8, device=dev)
+    _call_on(dev, "convrot_ffn_gated", _ptr(x), _dtype_code(x), M, F, K, group, group_h, _ptr(wq_gate),
+             _ptr(gate_scale), _ptr(bias_gate), _ptr(wq_up), _ptr(up_scale), _ptr(bias_up), _ptr(wq_down),
+             _ptr(down_scale), _ptr(bias_down), code, _ptr(residual), _ptr(pre), _ptr(y), _ptr(ws), ws.numel())
+    return (y, pre) if save_pre else y
 
 
 def linear_noalloc(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, bias: torch.Tensor | None = None,

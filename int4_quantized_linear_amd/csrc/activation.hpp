@@ -1,0 +1,76 @@
+// activation.hpp -- the activations of the fused linears and their derivatives, in fp32 (gfx950).
+// Codes are the CONVROT_ACT_* values of include/convrot.h.  The code is uniform over a launch, so
+// each switch is a scalar branch.
+//
+// silu(z) = z s(z) and the tanh form of gelu, z (1 + tanh v) / 2 = z s(2v), share the logistic
+// s(t) = 1 / (1 + e^-t), taken as one v_exp_f32 and one v_rcp_f32 (1 ulp each; e^-t rounds its
+// argument once, so the relative error is about |t| 2^-24 + 3 ulp, far below the bf16 the result is
+// rounded to).  At t -> -inf, e^-t is infinite and s is 0; at t -> +inf s is 1: no clamps needed.
+// gelu is z erfc(-z / sqrt 2) / 2, which keeps its relative precision in the negative tail.
+#pragma once
+#include <hip/hip_runtime.h>
+
+namespace convrot {
+
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4;
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kTanhA = 1.59576912160573071f;               // 2 sqrt(2 / pi)
+constexpr float kTanhB = 0.044715f * 1.59576912160573071f;
+
+__device__ __forceinline__ float logistic(float t)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * t));
+}
+
+__device__ __forceinline__ float act_value(float z, int act)
+{
+    switch (act) {
+    case kActRelu: return z < 0.0f ? 0.0f : z;                // keeps a NaN
+    case kActSilu: return z * logistic(z);
+    case kActGelu: return 0.5f * z * erfcf(-kSqrtHalf * z);
+    case kActGeluTanh: return z * logistic(z * __builtin_fmaf(kTanhB * z, z, kTanhA));
+    default: return z;
+    }
+}
+
+// act(z) and act'(z) together.
+//   silu': p + z p (1 - p);  gelu': Phi(z) + z phi(z);  gelu_tanh': p + z p (1 - p) (2v)'
+// with 1 - p = s(-t), so nothing cancels.  (2v)' grows as z^2 while p (1 - p) is 0 in fp32 beyond
+// |z| = 10, so the tanh form clamps z there before it could overflow to inf * 0.
+__device__ __forceinline__ void act_value_slope(float z, int act, float &value, float &slope)
+{
+    switch (act) {
+    case kActRelu:
+        value = z < 0.0f ? 0.0f : z;
+        slope = z > 0.0f ? 1.0f : 0.0f;
+        break;
+    case kActSilu: {
+        const float p = logistic(z);
+        value = z * p;
+        slope = __builtin_fmaf(value, logistic(-z), p);
+        break;
+    }
+    case kActGelu: {
+        const float cdf = 0.5f * erfcf(-kSqrtHalf * z);
+        value = z * cdf;
+        slope = __builtin_fmaf(z * kInvSqrt2Pi, __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z), cdf);
+        break;
+    }
+    case kActGeluTanh: {
+        value = z * logistic(z * __builtin_fmaf(kTanhB * z, z, kTanhA));
+        const float c = __builtin_fminf(__builtin_fmaxf(z, -16.0f), 16.0f);
+        const float t = c * __builtin_fmaf(kTanhB * c, c, kTanhA);
+        const float p = logistic(t);
+        slope = __builtin_fmaf(c * p * logistic(-t), __builtin_fmaf(3.0f * kTanhB * c, c, kTanhA), p);
+        break;
+    }
+    default:
+        value = z;
+        slope = 1.0f;
+    }
+}
+
+} // namespace convrot

@@ -91,7 +91,7 @@ struct WsLayout {
     size_t xq = 0, xs = 0, tiles = 0, part = 0, total = 0;
 };
 
-WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int bits)
+WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int bits, bool gated = false)
 {
     WsLayout L;
     size_t off = 0;
@@ -102,7 +102,7 @@ WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int bits)
         off += round256((size_t)M * 4);
         // optional: the split-K tail's int32 partial sums (GEMM path only)
         L.part = off;
-        if (M > 16) off += round256(convrot::gemm_i8_split_bytes(M, N, (int)K));
+        if (M > 16) off += round256(convrot::gemm_i8_split_bytes(M, N, (int)K, gated));
     } else {
         L.xq = off;
         off += round256((size_t)(M * K / 2));
@@ -126,6 +126,20 @@ WsLayout ws_layout_w4a8(int64_t M, int64_t K)
     off += round256((size_t)M * 4);
     L.total = off;
     return L;
+}
+
+// [a, a + an) and [b, b + bn) share a byte (either may be NULL: they share none).
+bool overlap(const void *a, size_t an, const void *b, size_t bn)
+{
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + bn && y < x + an;
+}
+
+int check_act(int act, const char *who)
+{
+    return act >= CONVROT_ACT_NONE && act <= CONVROT_ACT_GELU_TANH
+               ? CONVROT_OK
+               : fail(CONVROT_ERR_ACT, "%s: act=%d is not one of CONVROT_ACT_*", who, act);
 }
 
 int quantize_common(const void *x, int dtype, int64_t R, int64_t K, int group, int bits, void *q, void *scale,
@@ -166,6 +180,8 @@ const char *convrot_status_string(int s)
     case CONVROT_ERR_WORKSPACE: return "CONVROT_ERR_WORKSPACE";
     case CONVROT_ERR_HIP: return "CONVROT_ERR_HIP";
     case CONVROT_ERR_DEVICE: return "CONVROT_ERR_DEVICE";
+    case CONVROT_ERR_ACT: return "CONVROT_ERR_ACT";
+    case CONVROT_ERR_OVERLAP: return "CONVROT_ERR_OVERLAP";
     default: return "CONVROT_ERR_UNKNOWN";
     }
 }
@@ -205,32 +221,43 @@ size_t convrot_workspace_bytes(int64_t M, int64_t N, int64_t K, int bits)
 
 namespace {
 
-// Shared by convrot_linear (caller's workspace) and convrot_linear_noalloc (the library's fixed
-// scratch array).  scratch_fn, when given, is called only after every precondition holds and
-// returns the scratch buffer (or sets the status), so a rejected call touches no device.
+// Shared by convrot_linear, convrot_linear_act, convrot_linear_gated (caller's workspace) and
+// convrot_linear_noalloc (the library's fixed scratch array).  scratch_fn, when given, is called
+// only after every precondition holds and returns the scratch buffer (or sets the status), so a
+// rejected call touches no device.
 int linear_i8(const char *who, const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M,
               int64_t N, int64_t K, int group, const int8_t *wq, const float *w_scale, const float *bias, void *y,
-              void *workspace, size_t workspace_bytes, void *(*scratch_fn)(int *), hipStream_t stream)
+              void *workspace, size_t workspace_bytes, void *(*scratch_fn)(int *), hipStream_t stream,
+              convrot::Epi epi = convrot::Epi::Bf16, const convrot::FusedEpi &f = convrot::FusedEpi())
 {
+    const bool gated = epi == convrot::Epi::Gated;
     int rc = check_shape(M, N, K, group, who);
     if (rc) return rc;
     if (M > 16 && (rc = check_gemm_n(N, who))) return rc;
+    if ((rc = check_act(f.act, who))) return rc;
     if (M == 0 || N == 0) return CONVROT_OK;
     if (!wq || !w_scale || !y) return fail(CONVROT_ERR_NULL, "%s: wq, w_scale and y must be non-NULL", who);
+    if (gated && (!f.wq2 || !f.sw2)) return fail(CONVROT_ERR_NULL, "%s: wq_up and up_scale must be non-NULL", who);
     if (!x && (!xq || !x_scale)) return fail(CONVROT_ERR_NULL, "%s: give x, or both xq and x_scale", who);
     if (x && x_dtype != CONVROT_DTYPE_F32 && x_dtype != CONVROT_DTYPE_BF16)
         return fail(CONVROT_ERR_DTYPE, "%s: x_dtype=%d", who, x_dtype);
     if ((x && !aligned(x, 16)) || (!x && (!aligned(xq, 16) || !aligned(x_scale, 4))) || !aligned(wq, 16) ||
         !aligned(w_scale, 4) || !aligned(y, 16) || (bias && !aligned(bias, 4)))
         return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
-    const WsLayout L = ws_layout(M, N, K, 8);
+    if (!aligned(f.residual, 16) || !aligned(f.pre, 16) || !aligned(f.wq2, 16) || !aligned(f.sw2, 4) ||
+        !aligned(f.bias2, 4))
+        return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+    const size_t out_bytes = (size_t)M * (size_t)N * 2, pre_bytes = out_bytes * (gated ? 2 : 1);
+    if ((f.residual != y && overlap(f.residual, out_bytes, y, out_bytes)) || overlap(f.pre, pre_bytes, y, out_bytes) ||
+        overlap(f.pre, pre_bytes, f.residual, out_bytes))
+        return fail(CONVROT_ERR_OVERLAP, "%s: an output overlaps pre or residual (only residual == y is allowed)", who);
+    const WsLayout L = ws_layout(M, N, K, 8, gated);
     if (scratch_fn && x && workspace_bytes < L.part)
         return fail(CONVROT_ERR_WORKSPACE, "%s: M*K = %lld needs %zu bytes of scratch; the fixed scratch holds %zu "
                     "(use convrot_linear with a workspace)", who, (long long)(M * K), L.part, workspace_bytes);
     if (!scratch_fn && x && (!workspace || workspace_bytes < L.part || !aligned(workspace, 256)))
         return fail(CONVROT_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of at least %zu bytes (got %zu)",
                     who, L.part, workspace ? workspace_bytes : (size_t)0);
-    if (M == 0 || N == 0) return CONVROT_OK;
     if ((rc = check_device())) return rc;
     if (scratch_fn) {
         workspace = scratch_fn(&rc);
@@ -255,11 +282,26 @@ int linear_i8(const char *who, const void *x, int x_dtype, const int8_t *xq, con
         xq = qx;
         x_scale = sx;
     }
-    hipError_t e = M <= 16 ? convrot::launch_gemv_i8(xq, wq, x_scale, w_scale, bias, y, convrot::Epi::Bf16, M, N,
-                                                      (int)K, stream)
-                           : convrot::launch_gemm_i8(xq, wq, x_scale, w_scale, bias, y, convrot::Epi::Bf16, M, N,
-                                                      (int)K, part, part_bytes, stream);
+    hipError_t e = M <= 16 ? convrot::launch_gemv_i8(xq, wq, x_scale, w_scale, bias, y, epi, M, N, (int)K, stream, f)
+                           : convrot::launch_gemm_i8(xq, wq, x_scale, w_scale, bias, y, epi, M, N, (int)K, part,
+                                                      part_bytes, stream, f);
     return hip_status(e, M <= 16 ? "gemv_i8" : "gemm_i8");
+}
+
+// Workspace of convrot_ffn_gated: the gated linear's, with h [M, F] bf16 and the down linear's
+// after it (the two linears run in stream order, but the second quantizes h while the first's
+// region is idle, so only h needs its own room: both layouts start at 0).
+struct FfnLayout {
+    size_t h = 0, total = 0;
+};
+
+FfnLayout ffn_layout(int64_t M, int64_t F, int64_t K)
+{
+    FfnLayout L;
+    const size_t up = ws_layout(M, F, K, 8, true).total, down = ws_layout(M, K, F, 8).total;
+    L.h = up > down ? up : down;
+    L.total = L.h + round256((size_t)M * (size_t)F * 2);
+    return L;
 }
 
 // Scratch of convrot_linear_noalloc: one fixed array per GPU, held until the process ends.  On
@@ -315,6 +357,87 @@ int convrot_linear_noalloc(const void *x, int x_dtype, const int8_t *xq, const f
 {
     return linear_i8("convrot_linear_noalloc", x, x_dtype, xq, x_scale, M, N, K, group, wq, w_scale, bias, y, nullptr,
                      CONVROT_NOALLOC_SCRATCH_BYTES, scratch_for_current_device, stream);
+}
+
+int convrot_linear_act(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,
+                       int64_t K, int group, const int8_t *wq, const float *w_scale, const float *bias, int act,
+                       const void *residual, void *pre, void *y, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream)
+{
+    convrot::FusedEpi f;
+    f.act = act;
+    f.residual = static_cast<const uint16_t *>(residual);
+    f.pre = static_cast<uint16_t *>(pre);
+    return linear_i8("convrot_linear_act", x, x_dtype, xq, x_scale, M, N, K, group, wq, w_scale, bias, y, workspace,
+                     workspace_bytes, nullptr, stream, convrot::Epi::Act, f);
+}
+
+size_t convrot_workspace_bytes_gated(int64_t M, int64_t N, int64_t K)
+{
+    // shapes check_shape accepts; an empty batch needs none
+    if (!convrot_workspace_bytes(M, N, K, 8)) return 0;
+    return ws_layout(M, N, K, 8, true).total;
+}
+
+int convrot_linear_gated(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,
+                         int64_t K, int group, const int8_t *wq_gate, const float *gate_scale, const float *gate_bias,
+                         const int8_t *wq_up, const float *up_scale, const float *up_bias, int act, void *pre, void *h,
+                         void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    convrot::FusedEpi f;
+    f.act = act;
+    f.pre = static_cast<uint16_t *>(pre);
+    f.wq2 = wq_up;
+    f.sw2 = up_scale;
+    f.bias2 = up_bias;
+    return linear_i8("convrot_linear_gated", x, x_dtype, xq, x_scale, M, N, K, group, wq_gate, gate_scale, gate_bias, h,
+                     workspace, workspace_bytes, nullptr, stream, convrot::Epi::Gated, f);
+}
+
+size_t convrot_workspace_bytes_ffn(int64_t M, int64_t F, int64_t K)
+{
+    if (!convrot_workspace_bytes(M, F, K, 8) || !convrot_workspace_bytes(M, K, F, 8)) return 0;
+    return ffn_layout(M, F, K).total;
+}
+
+int convrot_ffn_gated(const void *x, int x_dtype, int64_t M, int64_t F, int64_t K, int group, int group_h,
+                      const int8_t *wq_gate, const float *gate_scale, const float *gate_bias, const int8_t *wq_up,
+                      const float *up_scale, const float *up_bias, const int8_t *wq_down, const float *down_scale,
+                      const float *down_bias, int act, const void *residual, void *pre, void *y, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream)
+{
+    const char *who = "convrot_ffn_gated";
+    // everything the two linears would reject, before the first of them enqueues anything
+    int rc = check_shape(M, F, K, group, who);
+    if (rc) return rc;
+    if ((rc = check_shape(M, K, F, group_h, who))) return rc;
+    if ((rc = check_act(act, who))) return rc;
+    if (M == 0) return CONVROT_OK;
+    if (!x || !wq_gate || !gate_scale || !wq_up || !up_scale || !wq_down || !down_scale || !y)
+        return fail(CONVROT_ERR_NULL, "%s: x, the weights, their scales and y must be non-NULL", who);
+    if (x_dtype != CONVROT_DTYPE_F32 && x_dtype != CONVROT_DTYPE_BF16)
+        return fail(CONVROT_ERR_DTYPE, "%s: x_dtype=%d", who, x_dtype);
+    if (!aligned(x, 16) || !aligned(wq_gate, 16) || !aligned(wq_up, 16) || !aligned(wq_down, 16) || !aligned(y, 16) ||
+        !aligned(pre, 16) || !aligned(residual, 16) || !aligned(gate_scale, 4) || !aligned(up_scale, 4) ||
+        !aligned(down_scale, 4) || !aligned(gate_bias, 4) || !aligned(up_bias, 4) || !aligned(down_bias, 4))
+        return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+    const size_t y_bytes = (size_t)M * (size_t)K * 2, pre_bytes = (size_t)M * (size_t)F * 4;
+    const size_t x_bytes = (size_t)M * (size_t)K * (x_dtype == CONVROT_DTYPE_F32 ? 4 : 2);
+    // pre and h are written before the residual is read
+    if ((residual != y && overlap(residual, y_bytes, y, y_bytes)) || overlap(pre, pre_bytes, y, y_bytes) ||
+        overlap(pre, pre_bytes, residual, y_bytes) || overlap(pre, pre_bytes, x, x_bytes))
+        return fail(CONVROT_ERR_OVERLAP, "%s: an output overlaps pre, x or residual (only residual == y is allowed)", who);
+    const FfnLayout L = ffn_layout(M, F, K);
+    if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
+        return fail(CONVROT_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of at least %zu bytes (got %zu)", who,
+                    L.total, workspace ? workspace_bytes : (size_t)0);
+    if ((rc = check_device())) return rc;
+    void *h = static_cast<uint8_t *>(workspace) + L.h;
+    rc = convrot_linear_gated(x, x_dtype, nullptr, nullptr, M, F, K, group, wq_gate, gate_scale, gate_bias, wq_up,
+                              up_scale, up_bias, act, pre, h, workspace, L.h, stream);
+    if (rc) return rc;
+    return convrot_linear_act(h, CONVROT_DTYPE_BF16, nullptr, nullptr, M, K, F, group_h, wq_down, down_scale, down_bias,
+                              CONVROT_ACT_NONE, residual, nullptr, y, workspace, L.h, stream);
 }
 
 int convrot_gemm_i8_i32(const int8_t *xq, const int8_t *wq, int64_t M, int64_t N, int64_t K, int32_t *acc,

@@ -42,6 +42,7 @@
 //    the same epilogue arithmetic, so the outputs are bit-identical to the whole-tile path.
 #include <type_traits>
 
+#include "activation.hpp"
 #include "device_common.hpp"
 #include "launchers.hpp"
 
@@ -80,7 +81,15 @@ struct GemmParams {
     // and dequantizes them.  S == 1: no split (T_dp == T).
     int32_t *part;
     int T_dp, S;
+    FusedEpi f;                // Act and Gated epilogues
 };
+
+// Gated: a tile's 256 weight rows are 128 features of both weights, in alternating 16-row blocks
+// (gate, up, gate, ...), so a lane's accumulators acc[2 i] and acc[2 i + 1] hold the gate and the up
+// value of the same tokens and features and the product needs no exchange.  Tile column c is
+// feature 16 (c / 32) + c % 16 of the gate (c / 16 even) or the up weight.
+template <Epi E>
+constexpr int tile_features() { return E == Epi::Gated ? BN / 2 : BN; }
 
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -135,6 +144,7 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = w & 1, wm = w >> 1;   // wn: 128-row half of N, wm: 64-row quarter of M
     const int K = p.K;
+    constexpr int NF = tile_features<E>();     // output columns per tile
     const int KT = (K + BK - 1) / BK;          // the last K-tile may be half (K % 128 == 64)
     const int T = p.tiles_m * p.tiles_n;
     const int U = p.T_dp + (T - p.T_dp) * p.S;
@@ -184,16 +194,23 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
     auto set_load_tile = [&](int tm, int tn) {
         ld_tm = tm;
         ld_tn = tn;
-        const int64_t m0 = (int64_t)ld_tm * BM, n0 = (int64_t)ld_tn * BN;
-        wbase_addr = reinterpret_cast<uint64_t>(p.wq + n0 * K);
+        const int64_t m0 = (int64_t)ld_tm * BM, n0 = (int64_t)ld_tn * NF;
+        const int8_t *wsrc = p.wq;
+        if constexpr (E == Epi::Gated) wsrc = (w & 2) ? p.f.wq2 : p.wq;   // lrow / 16 is odd where w & 2
+        wbase_addr = reinterpret_cast<uint64_t>(wsrc + n0 * K);
         xbase_addr = reinterpret_cast<uint64_t>(p.xq + m0 * K);
         // rows left in the operands past the tile's first row (32-bit: N, M < 2^31)
-        const int nrem = __builtin_amdgcn_readfirstlane(p.N - ld_tn * BN);
+        const int nrem = __builtin_amdgcn_readfirstlane(p.N - ld_tn * NF);
         const int mrem = __builtin_amdgcn_readfirstlane(p.M - ld_tm * BM);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t o = (uint32_t)(lrow[i] * K + 16 * lchunk[i]);
-            offw[i] = lrow[i] < nrem ? o : OOB;
+            if constexpr (E == Epi::Gated) {
+                const int wr = 16 * (lrow[i] >> 5) + (lrow[i] & 15);
+                offw[i] = wr < nrem ? (uint32_t)(wr * K + 16 * lchunk[i]) : OOB;
+            } else {
+                offw[i] = lrow[i] < nrem ? o : OOB;
+            }
             offx[i] = lrow[i] < mrem ? o : OOB;
         }
     };
@@ -201,7 +218,25 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
     // tile's first K-tile: 12 dword load-to-LDS instructions, 2 on each of waves 0-5.
     // Out-of-range entries and a missing bias read as zeros.
     auto issue_scales = [&](int t) {
-        if constexpr (E == Epi::Bf16) {
+        if constexpr (E == Epi::Gated) {
+            // the same 1 KiB arrays, gate in the first half and up in the second: the odd waves of
+            // arrays 0 and 1 take the up half
+            const int64_t m0 = (int64_t)ld_tm * BM, n0 = (int64_t)ld_tn * NF;
+            const int nb = (int)(4 * (p.N - n0 < NF ? p.N - n0 : NF)), mb = (int)(4 * (p.M - m0 < BM ? p.M - m0 : BM));
+            uint8_t *sb = smem + SCALE_OFF + (t & (NSCALE - 1)) * SCALE_BYTES;
+            if (w < 6) {
+                const int arr = w >> 1, up = w & 1;
+                const float *scl = up ? p.f.sw2 : p.sw, *bia = up ? p.f.bias2 : p.bias;
+                const float *src = arr == 0 ? scl + n0 : arr == 1 ? (bia ? bia + n0 : scl) : p.sx + m0;
+                const int bytes = arr == 0 ? nb : arr == 1 ? (bia ? nb : 0) : mb;
+                const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(reinterpret_cast<uint64_t>(src), bytes);
+                const int skip = arr == 2 ? 512 * up : 0;        // sx is one array of 256
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(sb + arr * 1024 + up * 512 + j * 256), 4,
+                                                             (uint32_t)(skip + j * 256 + 4 * lane), 0, 0, 0);
+            }
+        } else if constexpr (E != Epi::Int32) {
             const int64_t m0 = (int64_t)ld_tm * BM, n0 = (int64_t)ld_tn * BN;
             const int nb = (int)(4 * (p.N - n0 < BN ? p.N - n0 : BN)), mb = (int)(4 * (p.M - m0 < BM ? p.M - m0 : BM));
             uint8_t *sb = smem + SCALE_OFF + (t & (NSCALE - 1)) * SCALE_BYTES;
@@ -330,7 +365,7 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
         if (ld_kt == ld_ke) next_job();
     };
     auto epilogue = [&](const Job &J, int j, int g) {
-        const int m0 = J.tm * BM, n0 = J.tn * BN;
+        const int m0 = J.tm * BM, n0 = J.tn * NF;
         const int Mi = p.M, Ni = p.N;
         // lane-dependent bases laundered so the addresses below are formed here, not hoisted out
         // of the tile loop (where they would stay live through the main loop): the lane's token
@@ -385,11 +420,103 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                     const int nl = pcol + 16 * bi;
                     const v4u d = {(unsigned)acc[bi][bj][0], (unsigned)acc[bi][bj][1], (unsigned)acc[bi][bj][2],
                                    (unsigned)acc[bi][bj][3]};
-                    const uint32_t off = (rok && n0 + nl < Ni) ? (uint32_t)(prow * BN + nl) * 4u : OOB;
+                    const int nf = E == Epi::Gated ? 16 * (nl >> 5) + (nl & 15) : nl;
+                    const uint32_t off = (rok && n0 + nf < Ni) ? (uint32_t)(prow * BN + nl) * 4u : OOB;
                     __builtin_amdgcn_raw_buffer_store_b128(d, rp, off, 0, 0);
                 }
                 fence();
             }
+        } else if constexpr (VEC && (E == Epi::Act || E == Epi::Gated)) {
+            // Two phases per 16-token block, so that the activation's code exists once and not per
+            // accumulator register.  (Applied where the accumulators are, fully unrolled, it spilled
+            // 64 (Gated) and 145 (Act) registers.)  First the block's int32 sums go to the wave's own 8 KiB
+            // (the region of the bf16 branch below): row r is half of piece r / 2, its 32 chunks of 16
+            // bytes at chunk ^ r, so the 16 rows a write covers fall on distinct bank groups.  Then
+            // a rolled loop takes whole row pieces, 8 output columns per lane, through the scales,
+            // the activation, the residual or the product, and stores 16 bytes of each output.
+            // Residual rows are requested two iterations ahead (a null one has no records: its
+            // loads read 0).  y may be the residual itself: every element is read by the lane that
+            // later writes it.
+            const float *ls = reinterpret_cast<const float *>(smem + SCALE_OFF + (j & (NSCALE - 1)) * SCALE_BYTES);
+            uint8_t *reg = smem + (g & (NST - 1)) * STAGE + w * 1024;
+            constexpr int LPR = E == Epi::Gated ? 8 : 16;              // lanes per row
+            constexpr int RPI = 64 / LPR;                              // rows per iteration
+            auto row_base = [](int r) { return ((r >> 1) & 3) * 8192 + (r >> 3) * OPB + (r & 1) * 512; };
+            int wbase = row_base(erow), lrow = lane / LPR, lcol = lane % LPR;
+            asm volatile("" : "+v"(wbase), "+v"(lrow), "+v"(lcol));
+            const int c0 = wn * (NF / 2) + 8 * lcol;                   // first output column in the tile
+            const int n = n0 + c0, mw = m0 + wm * 64;
+            // chunk of the lane's first 4 columns; Gated: of the gate's, up is 4 chunks on
+            const int ch = E == Epi::Gated ? 8 * (lcol >> 1) + 2 * (lcol & 1) : 2 * lcol;
+            auto rows_of = [&](const uint16_t *base) {
+                return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(base) + (int64_t)mw * p.N, (short)0,
+                                                         base ? NUM_RECORDS : 0, 0x00020000);
+            };
+            const __amdgpu_buffer_rsrc_t ry = rows_of(static_cast<uint16_t *>(p.y));
+            const __amdgpu_buffer_rsrc_t rres = rows_of(E == Epi::Act ? p.f.residual : nullptr);
+            const __amdgpu_buffer_rsrc_t rpre = rows_of(p.f.pre);
+            const __amdgpu_buffer_rsrc_t rpre2 =
+                rows_of(E == Epi::Gated && p.f.pre ? p.f.pre + (int64_t)Mi * p.N : nullptr);
+            const int act = p.f.act;
+            auto offset = [&](int r) {                                 // r: row in the wave's 64
+                return (r < 64 && mw + r < Mi && n < Ni) ? (uint32_t)(r * Ni + n) * 2u : OOB;
+            };
+            auto store8 = [&](const float (&v)[8], __amdgpu_buffer_rsrc_t to, uint32_t off) {
+                const v4u d = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7])};
+                __builtin_amdgcn_raw_buffer_store_b128(d, to, off, 0, 0);
+            };
+            v4u res0 = {}, res1 = {};
+            if constexpr (E == Epi::Act) {
+                res0 = __builtin_amdgcn_raw_buffer_load_b128(rres, offset(lrow), 0, 0);
+                res1 = __builtin_amdgcn_raw_buffer_load_b128(rres, offset(lrow + RPI), 0, 0);
+            }
+#pragma unroll
+            for (int bj = 0; bj < 4; ++bj) {
+#pragma unroll
+                for (int bi = 0; bi < 8; ++bi)
+                    *reinterpret_cast<v4i *>(reg + wbase + 16 * ((4 * bi + efq) ^ erow)) = acc[bi][bj];
+#pragma unroll 1
+                for (int q = 0; q < 16 / RPI; ++q) {
+                    const int rb = RPI * q + lrow, r = 16 * bj + rb;
+                    const uint8_t *row = reg + row_base(rb);
+                    const float sxm = ls[2 * BN + wm * 64 + r];
+                    int cl = c0;                       // laundered: scales and biases are re-read, not
+                    asm volatile("" : "+v"(cl));       // kept in 16 or 32 registers across the loop
+                    auto z8 = [&](int chunk, int col, float (&v)[8]) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const v4i a4 = *reinterpret_cast<const v4i *>(row + 16 * ((chunk + h) ^ rb));
+                            const v4f s4 = *reinterpret_cast<const v4f *>(ls + col + 4 * h);
+                            const v4f b4 = *reinterpret_cast<const v4f *>(ls + BN + col + 4 * h);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                v[4 * h + i] = __builtin_fmaf((float)a4[i], sxm * s4[i], b4[i]);
+                        }
+                    };
+                    const uint32_t off = offset(r);
+                    float v[8];
+                    z8(ch, cl, v);
+                    if (p.f.pre) store8(v, rpre, off);
+                    if constexpr (E == Epi::Gated) {
+                        float u[8];
+                        z8(ch + 4, cl + NF, u);
+                        if (p.f.pre) store8(u, rpre2, off);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], act) * u[i];
+                    } else {
+                        const v4u rr = res0;
+                        res0 = res1;
+                        res1 = __builtin_amdgcn_raw_buffer_load_b128(rres, offset(r + 2 * RPI), 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = act_value(v[i], act) + (i & 1 ? bf16hi_to_f32(rr[i >> 1]) : bf16lo_to_f32(rr[i >> 1]));
+                    }
+                    store8(v, ry, off);
+                }
+                fence();
+            }
+            issue_after_epilogue_reads(g);
         } else if constexpr (VEC) {
             const float *ls = reinterpret_cast<const float *>(smem + SCALE_OFF + (j & (NSCALE - 1)) * SCALE_BYTES);
             // the wave's region: piece q (0..7) at 1024 w + 8192 (q & 3) (+ OPB for q >= 4); row r
@@ -461,10 +588,52 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                 const float sxm = ls[2 * BN + wm * 64 + 16 * bj + erow];
 #pragma unroll
                 for (int bi = 0; bi < 8; ++bi) {
+                    if constexpr (E == Epi::Gated) {
+                        if (bi & 1) continue;                 // the pair (bi, bi + 1) is one feature block
+                        const int nl = wn * 64 + 4 * efq + 8 * bi, n = n0 + nl;
+                        const v4f s4 = *reinterpret_cast<const v4f *>(ls + nl), t4 = *reinterpret_cast<const v4f *>(ls + nl + 128);
+                        const v4f b4 = *reinterpret_cast<const v4f *>(ls + BN + nl),
+                                  c4 = *reinterpret_cast<const v4f *>(ls + BN + nl + 128);
+                        const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
+                            p.f.pre + (int64_t)mr * p.N, (short)0, p.f.pre ? NUM_RECORDS : 0, 0x00020000);
+                        const __amdgpu_buffer_rsrc_t ru = __builtin_amdgcn_make_buffer_rsrc(
+                            p.f.pre + ((int64_t)Mi + mr) * p.N, (short)0, p.f.pre ? NUM_RECORDS : 0, 0x00020000);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float gv = __builtin_fmaf((float)acc[bi][bj][e], sxm * s4[e], b4[e]);
+                            const float uv = __builtin_fmaf((float)acc[bi + 1][bj][e], sxm * t4[e], c4[e]);
+                            const uint32_t off = (rok && n + e < Ni) ? (uint32_t)(erow * Ni + n + e) * 2u : OOB;
+                            const uint32_t gu = pack_bf16x2(gv, uv);
+                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(gu & 0xffffu), rg, off, 0, 0);
+                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(gu >> 16), ru, off, 0, 0);
+                            const float hv = act_value(gv, p.f.act) * uv;
+                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(pack_bf16x2(hv, 0.0f) & 0xffffu), ry,
+                                                                  off, 0, 0);
+                        }
+                        continue;
+                    }
                     const int nl = ecol + 16 * bi;
                     const v4f s4 = *reinterpret_cast<const v4f *>(ls + nl);
                     const v4f b4 = *reinterpret_cast<const v4f *>(ls + BN + nl);
                     const int n = n0 + nl;
+                    if constexpr (E == Epi::Act) {
+                        // a null residual or pre has no records: its loads read 0, its stores drop
+                        const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc(
+                            const_cast<uint16_t *>(p.f.residual) + (int64_t)mr * p.N, (short)0,
+                            p.f.residual ? NUM_RECORDS : 0, 0x00020000);
+                        const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
+                            p.f.pre + (int64_t)mr * p.N, (short)0, p.f.pre ? NUM_RECORDS : 0, 0x00020000);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float z = __builtin_fmaf((float)acc[bi][bj][e], sxm * s4[e], b4[e]);
+                            const uint32_t off = (rok && n + e < Ni) ? (uint32_t)(erow * Ni + n + e) * 2u : OOB;
+                            const float r = bf16lo_to_f32((uint32_t)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rr, off, 0, 0));
+                            const uint32_t zy = pack_bf16x2(z, act_value(z, p.f.act) + r);
+                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(zy & 0xffffu), rp, off, 0, 0);
+                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(zy >> 16), ry, off, 0, 0);
+                        }
+                        continue;
+                    }
                     // rows not 16-byte aligned (N % 8 != 0): element stores, clipped at N
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -487,7 +656,8 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
     // Stores each wavefront issues after the loads of the next job's second K-tile, in an
     // epilogue (vmcnt counts them too; the int32 and split-unit epilogues issue all 32 of theirs
     // after those loads; the bf16 one 8 of its 16).
-    constexpr int EPI_STORES = E == Epi::Int32 ? 32 : 8;
+    // The Act and Gated epilogues issue theirs before those loads.
+    constexpr int EPI_STORES = E == Epi::Int32 ? 32 : E == Epi::Bf16 ? 8 : 0;
     // Instruction interleaving inside one sub-step's scheduling region (sched_group_barrier masks:
     // 0x008 MFMA, 0x100 LDS read, 0x020 global read): the matrix pipe keeps its queue while the
     // fragment reads and the global loads go out between its instructions.
@@ -581,8 +751,9 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
 // Split-K tail, second pass: for each split tile, sum its S int32 partial slots (exact, in any
 // order) and apply the same epilogue arithmetic as gemm_i8_kernel, fma(float(acc), sx*sw, bias)
 // then bf16 RNE, so a split tile's outputs are bit-identical to a whole tile's.  A thread owns 8
-// consecutive columns of one row (N % 8 == 0, so all 8 exist; 32 threads cover a row's 256 columns) and a 256-thread
-// workgroup 8 rows; rb workgroups cover the rows of a tile that exist (all 256 unless M < 256).
+// consecutive columns of one row (N % 8 == 0, so all 8 exist; 32 threads cover a row's 256 columns, 16 a gated
+// tile's 128 features) and a 256-thread workgroup 8 (16) rows; rb workgroups cover the rows of a tile that exist
+// (all 256 unless M < 256).
 // All S slices' loads are issued before the first add.
 constexpr int MAX_SPLIT = 8;
 struct ReduceParams {
@@ -594,18 +765,12 @@ struct ReduceParams {
     int64_t M, N;
     int tiles_m, tiles_n;
     int T_dp, S, rb;
+    FusedEpi f;
 };
 
-__global__ void __launch_bounds__(256) split_reduce_kernel(ReduceParams p)
+// Sum of the S slots' 8 columns from column nl of row ml of tail tile i (r tail tiles).
+__device__ __forceinline__ void sum_slots(const ReduceParams &p, int i, int r, int ml, int nl, int32_t (&sum)[8])
 {
-    const int i = (int)blockIdx.x / p.rb;                               // tail tile
-    const int ml = ((int)blockIdx.x % p.rb) * 8 + ((int)threadIdx.x >> 5);
-    const int nl = ((int)threadIdx.x & 31) * 8;
-    int tm, tn;
-    tile_coords(p.T_dp + i, p.tiles_m, p.tiles_n, tm, tn);
-    const int64_t m = (int64_t)tm * BM + ml, n = (int64_t)tn * BN + nl;
-    if (m >= p.M || n >= p.N) return;
-    const int r = p.tiles_m * p.tiles_n - p.T_dp;
     v4i a[MAX_SPLIT], b[MAX_SPLIT];
 #pragma unroll
     for (int s = 0; s < MAX_SPLIT; ++s) {
@@ -615,7 +780,8 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(ReduceParams p)
             b[s] = *reinterpret_cast<const v4i *>(src + 4);
         }
     }
-    int32_t sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0;
 #pragma unroll
     for (int s = 0; s < MAX_SPLIT; ++s) {
         if (s < p.S) {
@@ -626,15 +792,59 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(ReduceParams p)
             }
         }
     }
+}
+
+__device__ __forceinline__ void store_row8(uint16_t *dst, const float (&v)[8])
+{
+    uint32_t pk[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pk[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+    *reinterpret_cast<v4u *>(dst) = v4u{pk[0], pk[1], pk[2], pk[3]};
+}
+
+template <Epi E>
+__global__ void __launch_bounds__(256) split_reduce_kernel(ReduceParams p)
+{
+    constexpr int NF = tile_features<E>();
+    constexpr int TPR = NF / 8, RPW = 256 / TPR;                        // threads per row, rows per workgroup
+    const int i = (int)blockIdx.x / p.rb;                               // tail tile
+    const int ml = ((int)blockIdx.x % p.rb) * RPW + (int)threadIdx.x / TPR;
+    const int nl = ((int)threadIdx.x % TPR) * 8;
+    int tm, tn;
+    tile_coords(p.T_dp + i, p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t m = (int64_t)tm * BM + ml, n = (int64_t)tn * NF + nl;
+    if (m >= p.M || n >= p.N) return;
+    const int r = p.tiles_m * p.tiles_n - p.T_dp;
     const float sxm = p.sx[m];
+    // Gated: features nl..nl+7 (8 of a 16-feature block) of the gate, 16 columns on those of up
+    const int cl = E == Epi::Gated ? 32 * (nl >> 4) + (nl & 15) : nl;
+    int32_t sum[8];
+    sum_slots(p, i, r, ml, cl, sum);
     float yv[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         yv[e] = __builtin_fmaf((float)sum[e], sxm * p.sw[n + e], p.bias ? p.bias[n + e] : 0.0f);
-    uint32_t pk[4];
+    if constexpr (E == Epi::Act) {
+        if (p.f.pre) store_row8(p.f.pre + m * p.N + n, yv);
+        v4u res = v4u{0, 0, 0, 0};
+        if (p.f.residual) res = *reinterpret_cast<const v4u *>(p.f.residual + m * p.N + n);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) pk[e] = pack_bf16x2(yv[2 * e], yv[2 * e + 1]);
-    *reinterpret_cast<v4u *>(p.y + m * p.N + n) = v4u{pk[0], pk[1], pk[2], pk[3]};
+        for (int e = 0; e < 8; ++e)
+            yv[e] = act_value(yv[e], p.f.act) + (e & 1 ? bf16hi_to_f32(res[e >> 1]) : bf16lo_to_f32(res[e >> 1]));
+    } else if constexpr (E == Epi::Gated) {
+        float uv[8];
+        sum_slots(p, i, r, ml, cl + 16, sum);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            uv[e] = __builtin_fmaf((float)sum[e], sxm * p.f.sw2[n + e], p.f.bias2 ? p.f.bias2[n + e] : 0.0f);
+        if (p.f.pre) {
+            store_row8(p.f.pre + m * p.N + n, yv);
+            store_row8(p.f.pre + (p.M + m) * p.N + n, uv);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) yv[e] = act_value(yv[e], p.f.act) * uv[e];
+    }
+    store_row8(p.y + m * p.N + n, yv);
 }
 
 int cu_count_cached()
@@ -667,9 +877,9 @@ struct SplitPlan {
 // element of the tail and slice, counted at 2.5 TB/s: each unit's int32 stores leave in a burst at
 // its end, and a q|k|v-shaped tail of 64 tiles in 3 slices measured no faster than whole) and the
 // second launch.  A split is planned only if it saves at least 5% of the estimated GEMM time.
-SplitPlan plan_split(int64_t M, int64_t N, int K)
+SplitPlan plan_split(int64_t M, int64_t N, int K, int nf)
 {
-    const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
+    const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + nf - 1) / nf;
     const int64_t T = tiles_m * tiles_n;
     const int cap = grid_capacity();
     SplitPlan pl = {(int)T, 1, 0};
@@ -699,19 +909,31 @@ SplitPlan plan_split(int64_t M, int64_t N, int K)
 
 } // namespace
 
-size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K)
+size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K, bool gated)
 {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
-    return plan_split(M, N, K).bytes;
+    return plan_split(M, N, K, gated ? tile_features<Epi::Gated>() : BN).bytes;
 }
+
+namespace {
+
+template <Epi E>
+void launch_whole(bool vec, unsigned grid, hipStream_t stream, const GemmParams &p)
+{
+    if (vec) hipLaunchKernelGGL((gemm_i8_kernel<E, true>), dim3(grid), dim3(NTHREADS), 0, stream, p);
+    else hipLaunchKernelGGL((gemm_i8_kernel<E, false>), dim3(grid), dim3(NTHREADS), 0, stream, p);
+}
+
+} // namespace
 
 hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, const float *sw, const float *bias,
                           void *y, Epi epi, int64_t M, int64_t N, int K, void *part, size_t part_bytes,
-                          hipStream_t stream)
+                          hipStream_t stream, const FusedEpi &fused)
 {
     if (M <= 0 || N <= 0) return hipSuccess;
     // the epilogue's byte offset within a 32-row output block, 32 * N * 4 bytes at most, is 32-bit
     if (N >= ((int64_t)1 << 24)) return hipErrorInvalidValue;
+    const int nf = epi == Epi::Gated ? tile_features<Epi::Gated>() : BN;
     GemmParams p;
     p.xq = xq;
     p.wq = wq;
@@ -722,15 +944,16 @@ hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
     p.M = (int)M;
     p.N = (int)N;
     p.K = K;
+    p.f = fused;
     // the tile walk counts tiles in int
-    if (((M + BM - 1) / BM) * ((N + BN - 1) / BN) >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (((M + BM - 1) / BM) * ((N + nf - 1) / nf) >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
     p.tiles_m = (int)((M + BM - 1) / BM);
-    p.tiles_n = (int)((N + BN - 1) / BN);
+    p.tiles_n = (int)((N + nf - 1) / nf);
     const int T = p.tiles_m * p.tiles_n;
-    // split-K tail (bf16 output only, and only with room for the partial sums)
+    // split-K tail (not for the int32 sums, and only with room for the partial sums)
     SplitPlan pl = {T, 1, 0};
-    if (epi == Epi::Bf16 && part) {
-        pl = plan_split(M, N, K);
+    if (epi != Epi::Int32 && part) {
+        pl = plan_split(M, N, K, nf);
         if (pl.S > 1 && part_bytes < pl.bytes) pl = {T, 1, 0};
     }
     p.part = static_cast<int32_t *>(part);
@@ -741,14 +964,13 @@ hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
     int grid = grid_capacity();
     if (U < grid) grid = (U + 7) & ~7;
     // 16-byte stores of 4 (int32) or 8 (bf16) columns need N % 8 == 0; otherwise element stores
-    if (epi == Epi::Int32 && N % 8 == 0)
-        hipLaunchKernelGGL((gemm_i8_kernel<Epi::Int32, true>), dim3((unsigned)grid), dim3(NTHREADS), 0, stream, p);
-    else if (epi == Epi::Int32)
-        hipLaunchKernelGGL((gemm_i8_kernel<Epi::Int32, false>), dim3((unsigned)grid), dim3(NTHREADS), 0, stream, p);
-    else if (N % 8 == 0)
-        hipLaunchKernelGGL((gemm_i8_kernel<Epi::Bf16, true>), dim3((unsigned)grid), dim3(NTHREADS), 0, stream, p);
-    else
-        hipLaunchKernelGGL((gemm_i8_kernel<Epi::Bf16, false>), dim3((unsigned)grid), dim3(NTHREADS), 0, stream, p);
+    const bool vec = N % 8 == 0;
+    switch (epi) {
+    case Epi::Int32: launch_whole<Epi::Int32>(vec, (unsigned)grid, stream, p); break;
+    case Epi::Act: launch_whole<Epi::Act>(vec, (unsigned)grid, stream, p); break;
+    case Epi::Gated: launch_whole<Epi::Gated>(vec, (unsigned)grid, stream, p); break;
+    default: launch_whole<Epi::Bf16>(vec, (unsigned)grid, stream, p);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.S == 1) return e;
     ReduceParams r;
@@ -763,9 +985,15 @@ hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
     r.tiles_n = p.tiles_n;
     r.T_dp = pl.T_dp;
     r.S = pl.S;
-    r.rb = (int)((M < BM ? M : BM) + 7) / 8;
+    r.f = fused;
+    const int rows_per_wg = 256 / (nf / 8);
+    r.rb = (int)((M < BM ? M : BM) + rows_per_wg - 1) / rows_per_wg;
     const unsigned rgrid = (unsigned)(T - pl.T_dp) * (unsigned)r.rb;
-    hipLaunchKernelGGL(split_reduce_kernel, dim3(rgrid), dim3(256), 0, stream, r);
+    switch (epi) {
+    case Epi::Act: hipLaunchKernelGGL((split_reduce_kernel<Epi::Act>), dim3(rgrid), dim3(256), 0, stream, r); break;
+    case Epi::Gated: hipLaunchKernelGGL((split_reduce_kernel<Epi::Gated>), dim3(rgrid), dim3(256), 0, stream, r); break;
+    default: hipLaunchKernelGGL((split_reduce_kernel<Epi::Bf16>), dim3(rgrid), dim3(256), 0, stream, r);
+    }
     return hipGetLastError();
 }
 

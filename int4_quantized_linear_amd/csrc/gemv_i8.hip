@@ -19,6 +19,7 @@
 // the int32 sums).  There is no cross-workgroup split of K: joining partial sums across CUs
 // needs several trips to the device-coherent level, about a microsecond each, which is more
 // than a small decode call costs in total; small N gets more wavefronts per workgroup instead.
+#include "activation.hpp"
 #include "device_common.hpp"
 #include "launchers.hpp"
 
@@ -45,7 +46,13 @@ struct GemvParams {
     void *y;
     int64_t N;
     int M, K;
+    FusedEpi f;                          // Act and Gated epilogues
 };
+
+// Gated: the RB blocks alternate gate, up, gate, ...: block b is rows 16 (b / 2) .. of the
+// workgroup's 8 RB features of one weight, so a lane holds the gate and up sums of its features.
+template <Epi E>
+__host__ __device__ constexpr int features_per_block() { return E == Epi::Gated ? 8 : 16; }
 
 // s_waitcnt immediate waiting for vmcnt <= n only (gfx9 encoding)
 constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
@@ -59,8 +66,9 @@ constexpr int stage_bytes() { return (16 * RB + 16) * KC; }   // weight rows + 1
 // tokens past M); here they get the chunk's K position, and bit 31 for pieces past K or for a
 // chunk past the run (out of range: zeros, no memory access).  Plain arithmetic rather than
 // selects, which the compiler would turn into branches around the loads.
-template <int RB>
-__device__ __forceinline__ void copy_chunk(uint8_t *st, __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rx,
+template <Epi E, int RB>
+__device__ __forceinline__ void copy_chunk(uint8_t *st, __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rw2,
+                                           __amdgpu_buffer_rsrc_t rx,
                                            const uint32_t *wrow, const uint32_t *xrow, int k0, uint32_t dead, int K,
                                            int cr, int px)
 {
@@ -68,7 +76,8 @@ __device__ __forceinline__ void copy_chunk(uint8_t *st, __amdgpu_buffer_rsrc_t r
     for (int j = 0; j < 4 * RB; ++j) {
         const int rr = 4 * j + cr;
         const uint32_t past = (uint32_t)(k0 + 16 * (px ^ (rr & 15)) >= K) << 31;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void *)(st + 1024 * j), 16,
+        const bool second = E == Epi::Gated && (j & 4);   // copies 4 b .. 4 b + 3 are block b
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? rw2 : rw, (lds_void *)(st + 1024 * j), 16,
                                                  (wrow[j] + (uint32_t)k0) | dead | past, 0, 0, 2);
     }
 #pragma unroll
@@ -90,7 +99,7 @@ __global__ void __launch_bounds__(64 * MAX_NW) gemv_i8_kernel(GemvParams p)
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nw = blockDim.x >> 6;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * RB);
+    const int64_t n0 = (int64_t)blockIdx.x * (features_per_block<E>() * RB);
     const int K = p.K;
     const int C = (K + KC - 1) / KC;
     const int c_beg = C * w / nw;                        // nw <= C: every run has a chunk
@@ -102,21 +111,35 @@ __global__ void __launch_bounds__(64 * MAX_NW) gemv_i8_kernel(GemvParams p)
 
     // epilogue operands first, so that their latency hides under the main loop
     float coef[RB][4], bia[RB][4];
-    if (E == Epi::Bf16 && w == 0) {
+    if (E != Epi::Int32 && w == 0) {
         const float sxm = p.sx[m < M ? m : 0];
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const int64_t nn = n0 + 16 * b + 4 * q + v;
+                const bool second = E == Epi::Gated && (b & 1);
+                const int64_t nn = n0 + 16 * (E == Epi::Gated ? b / 2 : b) + 4 * q + v;
                 const int64_t nc = nn < p.N ? nn : 0;
-                coef[b][v] = sxm * p.sw[nc];
-                bia[b][v] = p.bias ? p.bias[nc] : 0.0f;
+                const float *sw = second ? p.f.sw2 : p.sw, *bias = second ? p.f.bias2 : p.bias;
+                coef[b][v] = sxm * sw[nc];
+                bia[b][v] = bias ? bias[nc] : 0.0f;
+            }
+    }
+    uint16_t res[RB][4];
+    if (E == Epi::Act && w == 0) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int64_t nn = n0 + 16 * b + 4 * q + v;
+                res[b][v] = p.f.residual && m < M && nn < p.N ? p.f.residual[(int64_t)m * p.N + nn] : (uint16_t)0;
             }
     }
 
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<int8_t *>(p.wq + n0 * K), (short)0, NUM_RECORDS, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rw2 = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<int8_t *>((E == Epi::Gated ? p.f.wq2 : p.wq) + n0 * K), (short)0, NUM_RECORDS, 0x00020000);
     const __amdgpu_buffer_rsrc_t rx =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(p.xq), (short)0, NUM_RECORDS, 0x00020000);
     uint8_t *ring = smem + w * (D * STAGE);
@@ -125,7 +148,8 @@ __global__ void __launch_bounds__(64 * MAX_NW) gemv_i8_kernel(GemvParams p)
 #pragma unroll
     for (int j = 0; j < WL; ++j) {
         const int rr = 4 * j + cr;
-        wrow[j] = ((uint32_t)(rr * K + 16 * (px ^ (rr & 15)))) | ((uint32_t)(n0 + rr >= p.N) << 31);
+        const int wr = E == Epi::Gated ? 16 * (rr >> 5) + (rr & 15) : rr;   // row in its weight
+        wrow[j] = ((uint32_t)(wr * K + 16 * (px ^ (rr & 15)))) | ((uint32_t)(n0 + wr >= p.N) << 31);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -134,7 +158,7 @@ __global__ void __launch_bounds__(64 * MAX_NW) gemv_i8_kernel(GemvParams p)
     }
     // chunk c of this wavefront = K bytes [256 (c_beg + c), +256)
     auto load = [&](int slot, int c) {
-        copy_chunk<RB>(ring + slot * STAGE, rw, rx, wrow, xrow, (c_beg + c) * KC, (uint32_t)(c >= n) << 31, K, cr, px);
+        copy_chunk<E, RB>(ring + slot * STAGE, rw, rw2, rx, wrow, xrow, (c_beg + c) * KC, (uint32_t)(c >= n) << 31, K, cr, px);
     };
 
     v4i acc[RB];
@@ -195,13 +219,37 @@ __global__ void __launch_bounds__(64 * MAX_NW) gemv_i8_kernel(GemvParams p)
     }
     if (m >= M) return;
     // 16x16 layout: lane holds token m = lane%16 and rows 4*(lane/16) + v of each 16-row block
+    if constexpr (E == Epi::Gated) {
+#pragma unroll
+        for (int b = 0; b < RB; b += 2)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int64_t nn = n0 + 8 * b + 4 * q + v;
+                if (nn >= p.N) continue;
+                const float gv = __builtin_fmaf((float)acc[b][v], coef[b][v], bia[b][v]);
+                const float uv = __builtin_fmaf((float)acc[b + 1][v], coef[b + 1][v], bia[b + 1][v]);
+                const int64_t o = (int64_t)m * p.N + nn;
+                if (p.f.pre) {
+                    const uint32_t gu = pack_bf16x2(gv, uv);
+                    p.f.pre[o] = (uint16_t)(gu & 0xffffu);
+                    p.f.pre[M * p.N + o] = (uint16_t)(gu >> 16);
+                }
+                static_cast<uint16_t *>(p.y)[o] = (uint16_t)(pack_bf16x2(act_value(gv, p.f.act) * uv, 0.0f) & 0xffffu);
+            }
+        return;
+    }
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int64_t nn = n0 + 16 * b + 4 * q + v;
             if (nn >= p.N) continue;
-            if constexpr (E == Epi::Int32) {
+            if constexpr (E == Epi::Act) {
+                const float z = __builtin_fmaf((float)acc[b][v], coef[b][v], bia[b][v]);
+                const uint32_t zy = pack_bf16x2(z, act_value(z, p.f.act) + bf16lo_to_f32(res[b][v]));
+                if (p.f.pre) p.f.pre[(int64_t)m * p.N + nn] = (uint16_t)(zy & 0xffffu);
+                static_cast<uint16_t *>(p.y)[(int64_t)m * p.N + nn] = (uint16_t)(zy >> 16);
+            } else if constexpr (E == Epi::Int32) {
                 static_cast<int32_t *>(p.y)[(int64_t)m * p.N + nn] = acc[b][v];
             } else {
                 const float yv = __builtin_fmaf((float)acc[b][v], coef[b][v], bia[b][v]);
@@ -220,11 +268,14 @@ struct Plan {
 // with at least MIN_CHUNKS chunks, within the LDS budget (D stages per wavefront).  Both
 // measured on the decode shapes (N x K = 8192/1024/25600 x 5120, 5120 x 25600): fewer,
 // longer-running wavefronts beat many short ones.
-Plan plan(int64_t N, int K)
+// Gated: the same rule on the 2 N weight rows of both weights, with at least one gate|up pair of blocks.
+Plan plan(int64_t N, int K, bool gated)
 {
     Plan pl;
-    pl.rb = N >= 16384 ? 4 : N >= 4096 ? 2 : 1;
-    pl.tiles = (N + 16 * pl.rb - 1) / (16 * pl.rb);
+    const int64_t rows = gated ? 2 * N : N;
+    pl.rb = rows >= 16384 ? 4 : rows >= 4096 || gated ? 2 : 1;
+    const int rows_per_tile = 16 * pl.rb / (gated ? 2 : 1);
+    pl.tiles = (N + rows_per_tile - 1) / rows_per_tile;
     const int C = (K + KC - 1) / KC;
     int64_t nw = (TARGET_WAVES + pl.tiles - 1) / pl.tiles;
     if (nw > C / MIN_CHUNKS) nw = C / MIN_CHUNKS;
@@ -235,10 +286,21 @@ Plan plan(int64_t N, int K)
     return pl;
 }
 
+template <Epi E>
+void launch_plan(const Plan &pl, hipStream_t stream, const GemvParams &p)
+{
+    const dim3 grid((unsigned)pl.tiles), block(64 * pl.nw);
+    const size_t lds =
+        (size_t)pl.nw * D * (pl.rb == 4 ? stage_bytes<4>() : pl.rb == 2 ? stage_bytes<2>() : stage_bytes<1>());
+    if (pl.rb == 4) hipLaunchKernelGGL((gemv_i8_kernel<E, 4>), grid, block, lds, stream, p);
+    else if (pl.rb == 2) hipLaunchKernelGGL((gemv_i8_kernel<E, 2>), grid, block, lds, stream, p);
+    else if constexpr (E != Epi::Gated) hipLaunchKernelGGL((gemv_i8_kernel<E, 1>), grid, block, lds, stream, p);
+}
+
 } // namespace
 
 hipError_t launch_gemv_i8(const int8_t *xq, const int8_t *wq, const float *sx, const float *sw, const float *bias,
-                          void *y, Epi epi, int64_t M, int64_t N, int K, hipStream_t stream)
+                          void *y, Epi epi, int64_t M, int64_t N, int K, hipStream_t stream, const FusedEpi &fused)
 {
     if (M <= 0 || N <= 0) return hipSuccess;
     GemvParams p;
@@ -251,24 +313,13 @@ hipError_t launch_gemv_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
     p.N = N;
     p.M = (int)M;
     p.K = K;
-    const Plan pl = plan(N, K);
-    const dim3 grid((unsigned)pl.tiles), block(64 * pl.nw);
-    const size_t lds =
-        (size_t)pl.nw * D * (pl.rb == 4 ? stage_bytes<4>() : pl.rb == 2 ? stage_bytes<2>() : stage_bytes<1>());
-    if (epi == Epi::Int32) {
-        if (pl.rb == 4)
-            hipLaunchKernelGGL((gemv_i8_kernel<Epi::Int32, 4>), grid, block, lds, stream, p);
-        else if (pl.rb == 2)
-            hipLaunchKernelGGL((gemv_i8_kernel<Epi::Int32, 2>), grid, block, lds, stream, p);
-        else
-            hipLaunchKernelGGL((gemv_i8_kernel<Epi::Int32, 1>), grid, block, lds, stream, p);
-    } else {
-        if (pl.rb == 4)
-            hipLaunchKernelGGL((gemv_i8_kernel<Epi::Bf16, 4>), grid, block, lds, stream, p);
-        else if (pl.rb == 2)
-            hipLaunchKernelGGL((gemv_i8_kernel<Epi::Bf16, 2>), grid, block, lds, stream, p);
-        else
-            hipLaunchKernelGGL((gemv_i8_kernel<Epi::Bf16, 1>), grid, block, lds, stream, p);
+    p.f = fused;
+    const Plan pl = plan(N, K, epi == Epi::Gated);
+    switch (epi) {
+    case Epi::Int32: launch_plan<Epi::Int32>(pl, stream, p); break;
+    case Epi::Act: launch_plan<Epi::Act>(pl, stream, p); break;
+    case Epi::Gated: launch_plan<Epi::Gated>(pl, stream, p); break;
+    default: launch_plan<Epi::Bf16>(pl, stream, p);
     }
     return hipGetLastError();
 }

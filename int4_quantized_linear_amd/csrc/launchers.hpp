@@ -17,7 +17,20 @@ hipError_t launch_rotate_quant_fp6(const void *x, bool x_f32, int64_t rows, int 
                                    void *scale, hipStream_t stream);
 
 // Epilogue selector of the integer GEMM / GEMV kernels.
-enum class Epi { Bf16 = 0, Int32 = 1 };
+//   Act:   z = acc * sx[m] * sw[n] + bias[n];  y = bf16(act(z) + residual);  pre = bf16(z)
+//   Gated: two weights share the tokens: g, u as z;  y = bf16(act(g) * u);  pre = bf16([g; u])
+enum class Epi { Bf16 = 0, Int32 = 1, Act = 2, Gated = 3 };
+
+// What the Act and Gated epilogues take besides the plain one's arguments (activation.hpp holds
+// the codes of act).  residual, pre, bias2: may be null.  residual may be y itself.
+struct FusedEpi {
+    int act = 0;
+    const uint16_t *residual = nullptr;   // bf16 [M, N] (Act)
+    uint16_t *pre = nullptr;              // bf16 [M, N] (Act), [2, M, N] gate then up (Gated)
+    const int8_t *wq2 = nullptr;          // the up weight [N, K], its scales and bias (Gated)
+    const float *sw2 = nullptr;
+    const float *bias2 = nullptr;
+};
 
 // y[M,N] = bf16(acc * sx[m] * sw[n] + bias[n])  or  acc32[M,N] = acc,   acc = xq . wq^T  (M > 16).
 // part: optional scratch for the split-K tail (bf16 output only): when the tiles leave the last
@@ -26,14 +39,15 @@ enum class Epi { Bf16 = 0, Int32 = 1 };
 // kernel sums them and applies the epilogue (bit-identical outputs).  part == nullptr: no split.
 hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, const float *sw, const float *bias,
                           void *y, Epi epi, int64_t M, int64_t N, int K, void *part, size_t part_bytes,
-                          hipStream_t stream);
+                          hipStream_t stream, const FusedEpi &fused = FusedEpi());
 // Bytes of `part` the split-K tail uses for this shape on the current device (0: no split).
-size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K);
+size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K, bool gated = false);
 
 // Same contraction for M <= 16 (weight streaming; K split among the wavefronts of a workgroup,
 // no scratch memory).
 hipError_t launch_gemv_i8(const int8_t *xq, const int8_t *wq, const float *sx, const float *sw, const float *bias,
-                          void *y, Epi epi, int64_t M, int64_t N, int K, hipStream_t stream);
+                          void *y, Epi epi, int64_t M, int64_t N, int K, hipStream_t stream,
+                          const FusedEpi &fused = FusedEpi());
 
 // W4A4: y = bf16(sum_g acc_g * sx[m,g] * sw[n,g] + bias[n]) with packed int4 operands and
 // fp16 group scales (group = 256 or 128, K % group == 0, K >= 256), or the unscaled int32 total
