@@ -197,6 +197,63 @@ int convrot_ffn_gated(const void *x, int x_dtype, int64_t M, int64_t F, int64_t 
 /* Workspace bytes of convrot_ffn_gated; 0 on invalid arguments. */
 size_t convrot_workspace_bytes_ffn(int64_t M, int64_t F, int64_t K);
 
+/* The backward calls need N < CONVROT_BACKWARD_MAX_N (32-bit offsets within 256 rows of their bf16
+ * operand, 2 N columns for gate and up). */
+#define CONVROT_BACKWARD_MAX_N 1048576
+
+/*
+ * Input gradient of convrot_linear_act (act NONE, no residual: of convrot_linear) through its frozen
+ * INT8 weight, and the bias gradient.  The token quantizer counts as the identity (straight
+ * through):
+ *   dz = dy * act'(pre)  in fp32 (act NONE: dz = dy, pre is not read and may be NULL)
+ *   dx = bf16( ( sum_n bf16(dz[m,n] * w_scale[n]) * wq[n,:] ) R + dx_add[m,:] )
+ *   dbias[n] = sum_m dz[m,n]  (fp32)
+ *   dy bf16 [M, N]; pre bf16 [M, N] from the forward call; wq, w_scale, group as there (any group the
+ *   forward takes); dx bf16 [M, K]; dx_add bf16 [M, K] or NULL, added in fp32 before the rounding: the
+ *   gradient of a residual path, or of other linears with the same input; may be dx itself;
+ *   dbias fp32 [N] or NULL.  The gradient of the residual is dy.
+ * The products run on the bf16 matrix core: the codes are exact in bf16, and rounding dz * w_scale to
+ * bf16 is the only rounding before the fp32 sums.  Sums are taken in a fixed order: the same call
+ * gives the same bits.
+ *   M == 0: dbias is zeros.  N == 0 or K out of range: CONVROT_ERR_SHAPE (there is no gradient to
+ *   form).  N < CONVROT_BACKWARD_MAX_N.  dx overlapping dx_add (other than dx == dx_add) or dbias:
+ *   CONVROT_ERR_OVERLAP.
+ * workspace: convrot_workspace_bytes_backward(M, N, K) bytes, 256-byte aligned, required; scratch.
+ */
+int convrot_linear_act_backward(const void *dy, const void *pre, int64_t M, int64_t N, int64_t K, int group,
+                                const int8_t *wq, const float *w_scale, int act, const void *dx_add, void *dx,
+                                float *dbias, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The same for convrot_linear_gated: dh bf16 [M, N], pre bf16 [2, M, N] (gate, up) from the forward call,
+ *   dg = dh * u * act'(g),  du = dh * act(g),   dx = bf16( (dg Wg + du Wu) R + dx_add )
+ * with each product's operand rounded as above; dgate_bias, dup_bias fp32 [N] or NULL: the column sums
+ * of dg and du.  workspace: convrot_workspace_bytes_gated_backward(M, N, K) bytes.
+ */
+int convrot_linear_gated_backward(const void *dh, const void *pre, int64_t M, int64_t N, int64_t K, int group,
+                                  const int8_t *wq_gate, const float *gate_scale, const int8_t *wq_up,
+                                  const float *up_scale, int act, const void *dx_add, void *dx, float *dgate_bias,
+                                  float *dup_bias, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The same for convrot_ffn_gated: dy bf16 [M, K], pre bf16 [2, M, F] from the forward call.  The gradient dh of
+ * h is taken through wq_down and rounded to bf16 (h's type), then goes through the product and gate
+ * and up: the result is that of convrot_linear_act_backward followed by
+ * convrot_linear_gated_backward, bit for bit.  Bias gradients fp32 ([F], [F], [K]) or NULL.  When the
+ * forward's residual was x itself, pass dx_add = dy.
+ * workspace: convrot_workspace_bytes_ffn_backward(M, F, K) bytes.
+ */
+int convrot_ffn_gated_backward(const void *dy, const void *pre, int64_t M, int64_t F, int64_t K, int group, int group_h,
+                               const int8_t *wq_gate, const float *gate_scale, const int8_t *wq_up,
+                               const float *up_scale, const int8_t *wq_down, const float *down_scale, int act,
+                               const void *dx_add, void *dx, float *dgate_bias, float *dup_bias, float *ddown_bias,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of the backward calls; 0 on invalid arguments (and for M == 0). */
+size_t convrot_workspace_bytes_backward(int64_t M, int64_t N, int64_t K);
+size_t convrot_workspace_bytes_gated_backward(int64_t M, int64_t N, int64_t K);
+size_t convrot_workspace_bytes_ffn_backward(int64_t M, int64_t F, int64_t K);
+
 /* Size of the fixed scratch array convrot_linear_noalloc uses on each GPU (32 MiB). */
 #define CONVROT_NOALLOC_SCRATCH_BYTES 33554432
 

@@ -33,6 +33,12 @@ SIGNATURES = {
     "convrot_workspace_bytes_gated": ([I64, I64, I64], SZ),
     "convrot_ffn_gated": ([P, I, I64, I64, I64, I, I, P, P, P, P, P, P, P, P, P, I, P, P, P, P, SZ, P], I),
     "convrot_workspace_bytes_ffn": ([I64, I64, I64], SZ),
+    "convrot_linear_act_backward": ([P, P, I64, I64, I64, I, P, P, I, P, P, P, P, SZ, P], I),
+    "convrot_linear_gated_backward": ([P, P, I64, I64, I64, I, P, P, P, P, I, P, P, P, P, P, SZ, P], I),
+    "convrot_ffn_gated_backward": ([P, P, I64, I64, I64, I, I, P, P, P, P, P, P, I, P, P, P, P, P, P, SZ, P], I),
+    "convrot_workspace_bytes_backward": ([I64, I64, I64], SZ),
+    "convrot_workspace_bytes_gated_backward": ([I64, I64, I64], SZ),
+    "convrot_workspace_bytes_ffn_backward": ([I64, I64, I64], SZ),
     "convrot_linear_noalloc": ([P, I, P, P, I64, I64, I64, I, P, P, P, P, P], I),
     "convrot_linear_w4a4": ([P, I, P, P, I64, I64, I64, I, P, P, P, P, P, SZ, P], I),
     "convrot_pack_weight_w4a4": ([P, I64, I64, P, P], I),
@@ -301,6 +307,88 @@ def ffn_gated(x: torch.Tensor, wq_gate: torch.Tensor, gate_scale: torch.Tensor, 
              _ptr(gate_scale), _ptr(bias_gate), _ptr(wq_up), _ptr(up_scale), _ptr(bias_up), _ptr(wq_down),
              _ptr(down_scale), _ptr(bias_down), code, _ptr(residual), _ptr(pre), _ptr(y), _ptr(ws), ws.numel())
     return (y, pre) if save_pre else y
+
+
+def workspace_bytes_backward(M: int, N: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_backward(M, N, K))
+
+
+def workspace_bytes_gated_backward(M: int, N: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_gated_backward(M, N, K))
+
+
+def workspace_bytes_ffn_backward(M: int, F: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_ffn_backward(M, F, K))
+
+
+def _backward_buffers(M: int, K: int, ws_bytes: int, out: torch.Tensor | None, dev: torch.device):
+    dx = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    return dx, torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=dev)
+
+
+def linear_act_backward(dy: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, pre: torch.Tensor | None = None,
+                        act: str = "none", group: int = 256, bias_grad: bool = False,
+                        dx_add: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """Input gradient of linear_act (or linear) through its frozen weight, the token quantizer taken as
+    the identity: dz = dy * act'(pre), dx = bf16((sum_n bf16(dz * sw) wq) R + dx_add).  dy bf16 [M, N];
+    pre as the forward saved it (not needed for act "none"); dx_add bf16 [M, K], may be ``out``.
+    Returns (dx, dbias), dbias fp32 [N] with bias_grad=True, else None."""
+    code = _act_code(act)
+    N, K = wq.shape
+    M = dy.shape[0]
+    dev, bf16 = wq.device, torch.bfloat16
+    _check(dev, dy=(dy, (M, N), bf16), wq=(wq, (N, K), torch.int8), w_scale=(w_scale, (N,), torch.float32),
+           pre=(pre, (M, N), bf16), dx_add=(dx_add, (M, K), bf16), out=(out, (M, K), bf16))
+    dx, ws = _backward_buffers(M, K, workspace_bytes_backward(M, N, K), out, dev)
+    db = torch.empty((N,), dtype=torch.float32, device=dev) if bias_grad else None
+    _call_on(dev, "convrot_linear_act_backward", _ptr(dy), _ptr(pre), M, N, K, group, _ptr(wq), _ptr(w_scale), code,
+             _ptr(dx_add), _ptr(dx), _ptr(db), _ptr(ws), ws.numel())
+    return dx, db
+
+
+def linear_gated_backward(dh: torch.Tensor, pre: torch.Tensor, wq_gate: torch.Tensor, gate_scale: torch.Tensor,
+                          wq_up: torch.Tensor, up_scale: torch.Tensor, act: str = "silu", group: int = 256,
+                          bias_grad: bool = False, dx_add: torch.Tensor | None = None,
+                          out: torch.Tensor | None = None):
+    """Input gradient of linear_gated through both frozen weights: dg = dh * u * act'(g), du = dh * act(g),
+    dx = bf16((dg Wg + du Wu) R + dx_add).  pre bf16 [2, M, N] as the forward saved it.  Returns dx, or
+    (dx, dbias_gate, dbias_up) with bias_grad=True."""
+    code = _act_code(act)
+    N, K = wq_gate.shape
+    M = dh.shape[0]
+    dev, bf16, f32 = wq_gate.device, torch.bfloat16, torch.float32
+    _check(dev, dh=(dh, (M, N), bf16), pre=(pre, (2, M, N), bf16), wq_gate=(wq_gate, (N, K), torch.int8),
+           gate_scale=(gate_scale, (N,), f32), wq_up=(wq_up, (N, K), torch.int8), up_scale=(up_scale, (N,), f32),
+           dx_add=(dx_add, (M, K), bf16), out=(out, (M, K), bf16))
+    dx, ws = _backward_buffers(M, K, workspace_bytes_gated_backward(M, N, K), out, dev)
+    db = [torch.empty((N,), dtype=f32, device=dev) if bias_grad else None for _ in range(2)]
+    _call_on(dev, "convrot_linear_gated_backward", _ptr(dh), _ptr(pre), M, N, K, group, _ptr(wq_gate),
+             _ptr(gate_scale), _ptr(wq_up), _ptr(up_scale), code, _ptr(dx_add), _ptr(dx), _ptr(db[0]), _ptr(db[1]),
+             _ptr(ws), ws.numel())
+    return (dx, *db) if bias_grad else dx
+
+
+def ffn_gated_backward(dy: torch.Tensor, pre: torch.Tensor, wq_gate: torch.Tensor, gate_scale: torch.Tensor,
+                       wq_up: torch.Tensor, up_scale: torch.Tensor, wq_down: torch.Tensor, down_scale: torch.Tensor,
+                       act: str = "silu", group: int = 256, group_h: int = 256, bias_grad: bool = False,
+                       dx_add: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """Input gradient of ffn_gated: dy bf16 [M, K] through down (rounded to bf16, h's type), the product,
+    gate and up.  pre bf16 [2, M, F] as the forward saved it; dx_add = dy where the residual was x.
+    Returns dx, or (dx, dbias_gate, dbias_up, dbias_down) with bias_grad=True."""
+    code = _act_code(act)
+    F, K = wq_gate.shape
+    M = dy.shape[0]
+    dev, bf16, f32, i8 = wq_gate.device, torch.bfloat16, torch.float32, torch.int8
+    _check(dev, dy=(dy, (M, K), bf16), pre=(pre, (2, M, F), bf16), wq_gate=(wq_gate, (F, K), i8),
+           gate_scale=(gate_scale, (F,), f32), wq_up=(wq_up, (F, K), i8), up_scale=(up_scale, (F,), f32),
+           wq_down=(wq_down, (K, F), i8), down_scale=(down_scale, (K,), f32), dx_add=(dx_add, (M, K), bf16),
+           out=(out, (M, K), bf16))
+    dx, ws = _backward_buffers(M, K, workspace_bytes_ffn_backward(M, F, K), out, dev)
+    db = [torch.empty((n,), dtype=f32, device=dev) if bias_grad else None for n in (F, F, K)]
+    _call_on(dev, "convrot_ffn_gated_backward", _ptr(dy), _ptr(pre), M, F, K, group, group_h, _ptr(wq_gate),
+             _ptr(gate_scale), _ptr(wq_up), _ptr(up_scale), _ptr(wq_down), _ptr(down_scale), code, _ptr(dx_add),
+             _ptr(dx), _ptr(db[0]), _ptr(db[1]), _ptr(db[2]), _ptr(ws), ws.numel())
+    return (dx, *db) if bias_grad else dx
 
 
 def linear_noalloc(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, bias: torch.Tensor | None = None,

@@ -304,6 +304,72 @@ FfnLayout ffn_layout(int64_t M, int64_t F, int64_t K)
     return L;
 }
 
+// Shapes the backward calls take besides check_shape's rules: the tiles have to be countable in int.
+bool grad_shape_ok(int64_t M, int64_t N, int64_t K)
+{
+    return M >= 0 && M < ((int64_t)1 << 31) && N >= 1 && N < CONVROT_BACKWARD_MAX_N && K >= 64 && K <= CONVROT_MAX_K &&
+           K % 64 == 0 && ((M + 255) / 256) * ((K + 255) / 256) < ((int64_t)1 << 24);
+}
+
+int check_grad(const char *who, const convrot::GradArgs &g, int64_t K, int group, bool gated, const void *workspace,
+               size_t workspace_bytes)
+{
+    int rc = check_shape(g.M, g.N, K, group, who);
+    if (rc) return rc;
+    if (!grad_shape_ok(g.M, g.N, K))
+        return fail(CONVROT_ERR_SHAPE, "%s: M=%lld N=%lld K=%lld: the backward calls need 1 <= N < %d and at most 2^24 "
+                    "tiles of 256 x 256", who, (long long)g.M, (long long)g.N, (long long)K, CONVROT_BACKWARD_MAX_N);
+    if ((rc = check_act(g.act, who))) return rc;
+    if (g.M == 0) {
+        if (!aligned(g.db1, 4) || !aligned(g.db2, 4)) return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+        return CONVROT_OK;
+    }
+    const bool needs_pre = gated || g.act != CONVROT_ACT_NONE;
+    if (!g.dy || !g.wq1 || !g.sw1 || !g.dx || (gated && (!g.wq2 || !g.sw2)) || (needs_pre && !g.pre))
+        return fail(CONVROT_ERR_NULL, "%s: the gradient, the weights, their scales, dx and, with an activation, pre must "
+                    "be non-NULL", who);
+    if (!aligned(g.dy, 16) || !aligned(g.pre, 16) || !aligned(g.wq1, 16) || !aligned(g.wq2, 16) || !aligned(g.sw1, 4) ||
+        !aligned(g.sw2, 4) || !aligned(g.add, 16) || !aligned(g.dx, 16) || !aligned(g.db1, 4) || !aligned(g.db2, 4))
+        return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+    const size_t dx_bytes = (size_t)g.M * (size_t)K * 2, db_bytes = (size_t)g.N * 4;
+    if ((g.add != g.dx && overlap(g.add, dx_bytes, g.dx, dx_bytes)) || overlap(g.db1, db_bytes, g.dx, dx_bytes) ||
+        overlap(g.db2, db_bytes, g.dx, dx_bytes) || overlap(g.db1, db_bytes, g.db2, db_bytes))
+        return fail(CONVROT_ERR_OVERLAP, "%s: outputs overlap each other or dx_add (only dx_add == dx is allowed)", who);
+    const size_t need = convrot::grad_workspace_bytes(g.M, g.N, (int)K, gated);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(CONVROT_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of at least %zu bytes (got %zu)", who,
+                    need, workspace ? workspace_bytes : (size_t)0);
+    return CONVROT_OK;
+}
+
+int grad_i8(const char *who, convrot::GradArgs g, int64_t K, int group, bool gated, void *workspace,
+            size_t workspace_bytes, hipStream_t stream)
+{
+    int rc = check_grad(who, g, K, group, gated, workspace, workspace_bytes);
+    if (rc) return rc;
+    if (g.M == 0 && !g.db1 && !g.db2) return CONVROT_OK;
+    if ((rc = check_device())) return rc;
+    g.K = (int)K;
+    g.log2g = log2i(group);
+    g.ws = workspace;
+    return hip_status(convrot::launch_grad_i8(g, gated, stream), "grad_i8");
+}
+
+// Workspace of convrot_ffn_gated_backward: the larger of the two steps', then dh [M, F] bf16.
+struct FfnGradLayout {
+    size_t dh = 0, total = 0;
+};
+
+FfnGradLayout ffn_grad_layout(int64_t M, int64_t F, int64_t K)
+{
+    FfnGradLayout L;
+    const size_t down = convrot::grad_workspace_bytes(M, K, (int)F, false);
+    const size_t up = convrot::grad_workspace_bytes(M, F, (int)K, true);
+    L.dh = round256(up > down ? up : down);
+    L.total = L.dh + round256((size_t)M * (size_t)F * 2);
+    return L;
+}
+
 // Scratch of convrot_linear_noalloc: one fixed array per GPU, held until the process ends.  On
 // the host the array's name is only a stand-in for its device address: the address each device
 // holds is looked up once per device (with that device current) and kept in scratch_ptr.
@@ -438,6 +504,104 @@ int convrot_ffn_gated(const void *x, int x_dtype, int64_t M, int64_t F, int64_t 
     if (rc) return rc;
     return convrot_linear_act(h, CONVROT_DTYPE_BF16, nullptr, nullptr, M, K, F, group_h, wq_down, down_scale, down_bias,
                               CONVROT_ACT_NONE, residual, nullptr, y, workspace, L.h, stream);
+}
+
+size_t convrot_workspace_bytes_backward(int64_t M, int64_t N, int64_t K)
+{
+    return grad_shape_ok(M, N, K) ? convrot::grad_workspace_bytes(M, N, (int)K, false) : 0;
+}
+
+size_t convrot_workspace_bytes_gated_backward(int64_t M, int64_t N, int64_t K)
+{
+    return grad_shape_ok(M, N, K) ? convrot::grad_workspace_bytes(M, N, (int)K, true) : 0;
+}
+
+size_t convrot_workspace_bytes_ffn_backward(int64_t M, int64_t F, int64_t K)
+{
+    return grad_shape_ok(M, F, K) && grad_shape_ok(M, K, F) ? ffn_grad_layout(M, F, K).total : 0;
+}
+
+int convrot_linear_act_backward(const void *dy, const void *pre, int64_t M, int64_t N, int64_t K, int group,
+                                const int8_t *wq, const float *w_scale, int act, const void *dx_add, void *dx,
+                                float *dbias, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    convrot::GradArgs g;
+    g.dy = static_cast<const uint16_t *>(dy);
+    g.pre = act == CONVROT_ACT_NONE ? nullptr : static_cast<const uint16_t *>(pre);
+    g.M = M;
+    g.N = N;
+    g.act = act;
+    g.wq1 = wq;
+    g.sw1 = w_scale;
+    g.add = static_cast<const uint16_t *>(dx_add);
+    g.dx = static_cast<uint16_t *>(dx);
+    g.db1 = dbias;
+    return grad_i8("convrot_linear_act_backward", g, K, group, false, workspace, workspace_bytes, stream);
+}
+
+int convrot_linear_gated_backward(const void *dh, const void *pre, int64_t M, int64_t N, int64_t K, int group,
+                                  const int8_t *wq_gate, const float *gate_scale, const int8_t *wq_up,
+                                  const float *up_scale, int act, const void *dx_add, void *dx, float *dgate_bias,
+                                  float *dup_bias, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    convrot::GradArgs g;
+    g.dy = static_cast<const uint16_t *>(dh);
+    g.pre = static_cast<const uint16_t *>(pre);
+    g.M = M;
+    g.N = N;
+    g.act = act;
+    g.wq1 = wq_gate;
+    g.sw1 = gate_scale;
+    g.wq2 = wq_up;
+    g.sw2 = up_scale;
+    g.add = static_cast<const uint16_t *>(dx_add);
+    g.dx = static_cast<uint16_t *>(dx);
+    g.db1 = dgate_bias;
+    g.db2 = dup_bias;
+    return grad_i8("convrot_linear_gated_backward", g, K, group, true, workspace, workspace_bytes, stream);
+}
+
+int convrot_ffn_gated_backward(const void *dy, const void *pre, int64_t M, int64_t F, int64_t K, int group, int group_h,
+                               const int8_t *wq_gate, const float *gate_scale, const int8_t *wq_up,
+                               const float *up_scale, const int8_t *wq_down, const float *down_scale, int act,
+                               const void *dx_add, void *dx, float *dgate_bias, float *dup_bias, float *ddown_bias,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const char *who = "convrot_ffn_gated_backward";
+    int rc = check_shape(M, F, K, group, who);
+    if (rc) return rc;
+    if ((rc = check_shape(M, K, F, group_h, who))) return rc;
+    // the second call's checks first, on everything but dh, which is the library's own
+    convrot::GradArgs down, up;
+    const FfnGradLayout L = grad_shape_ok(M, F, K) && grad_shape_ok(M, K, F) ? ffn_grad_layout(M, F, K) : FfnGradLayout();
+    if (M > 0 && (!workspace || workspace_bytes < L.total || !aligned(workspace, 256)))
+        return fail(CONVROT_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of at least %zu bytes (got %zu)", who,
+                    L.total, workspace ? workspace_bytes : (size_t)0);
+    uint16_t *dh = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(workspace) + L.dh);
+    down.dy = static_cast<const uint16_t *>(dy);
+    down.M = up.M = M;
+    down.N = K;
+    down.act = CONVROT_ACT_NONE;
+    down.wq1 = wq_down;
+    down.sw1 = down_scale;
+    down.dx = dh;
+    down.db1 = ddown_bias;
+    up.dy = dh;
+    up.pre = static_cast<const uint16_t *>(pre);
+    up.N = F;
+    up.act = act;
+    up.wq1 = wq_gate;
+    up.sw1 = gate_scale;
+    up.wq2 = wq_up;
+    up.sw2 = up_scale;
+    up.add = static_cast<const uint16_t *>(dx_add);
+    up.dx = static_cast<uint16_t *>(dx);
+    up.db1 = dgate_bias;
+    up.db2 = dup_bias;
+    if ((rc = check_grad(who, up, K, group, true, workspace, L.dh))) return rc;
+    if ((rc = check_grad(who, down, F, group_h, false, workspace, L.dh))) return rc;
+    if ((rc = grad_i8(who, down, F, group_h, false, workspace, L.dh, stream))) return rc;
+    return grad_i8(who, up, K, group, true, workspace, L.dh, stream);
 }
 
 int convrot_gemm_i8_i32(const int8_t *xq, const int8_t *wq, int64_t M, int64_t N, int64_t K, int32_t *acc,

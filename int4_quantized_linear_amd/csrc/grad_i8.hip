@@ -1,0 +1,664 @@
+// grad_i8.hip -- input gradients of the INT8 ConvRot linears, through the frozen weights (gfx950).
+//
+// Forward: z = (Q(x R) . wq^T) sx sw + b.  With the token quantizer Q taken as the identity (straight
+// through) and the weights frozen, a gradient dz of z gives
+//   dx[m,k] = sum_k' ( sum_n dz[m,n] sw[n] wq[n,k'] ) R[k',k],     db[n] = sum_m dz[m,n]
+// (R symmetric).  Two weights that share the tokens (gate and up) add their products, so they are one
+// contraction over their stacked rows.  Three steps:
+//   1. grad_prep_kernel: dz from the incoming gradient, the saved pre-activations and the activation's
+//      slope; a[m,n] = bf16(dz sw) for the matrix core, fp32 column sums of dz for db.
+//   2. grad_gemm_kernel: a . wq with v_mfma_f32_16x16x32_bf16.  The codes are integers up to 127 in
+//      magnitude, exact in bf16, so a's rounding (2^-8 of each term at most, what bf16 training
+//      rounds its gradients to anyway) is the only one before the fp32 sums.
+//   3. the rotation, dx_add and the one rounding to bf16: in the GEMM's epilogue (a tile spans 256
+//      channels, whole groups), or in grad_join_kernel where tiles are split along n.
+#include "activation.hpp"
+#include "device_common.hpp"
+#include "launchers.hpp"
+
+namespace convrot {
+namespace {
+
+typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int BM = 256, BC = 256;             // tokens and channels of a tile
+constexpr int BN = 64;                        // contraction rows per step
+constexpr int OPB = 256 * BN * 2;             // bytes of one operand per stage (32 KiB)
+constexpr int STAGE = 2 * OPB;                // weights (by channel), then tokens
+constexpr int SMEM = 2 * STAGE;
+constexpr int NTHREADS = 512;
+constexpr int GROUP_M = 4;
+constexpr uint32_t OOB = 0x80000000u;
+constexpr int NUM_RECORDS = 0x7ffffff0;
+constexpr int MAX_SPLIT = 64;
+
+struct GradParams {
+    const uint16_t *a;         // [M, lda] bf16; columns [0, 64 nt1) the first weight's, then the second's
+    const int8_t *w1, *w2;     // [N, K]
+    const uint16_t *add;       // dx_add [M, K] or null
+    uint16_t *dx;              // [M, K]
+    float *part;               // split tiles' partial sums: slots of 256 x 256
+    int64_t lda;
+    int M, N, K, lg;
+    int nt1, nt;               // contraction steps of the first weight, in all
+    int tiles_m, tiles_c;
+    int T_dp, S;               // whole tiles, then the rest in S slices each
+    float norm;                // 2^(-lg / 2)
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(uint64_t a, int bytes)
+{
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(((uint64_t)hi << 32) | (uint64_t)lo), (short)0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
+constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
+
+// Unit of workgroup id: ids go round-robin over the 8 XCDs, and each XCD takes a contiguous range of
+// the whole tiles, then one of the slices (T_dp is a multiple of 8 whenever there are slices).
+__device__ __forceinline__ int unit_of(int pid, int T_dp, int U)
+{
+    const int xcd = pid & 7, local = pid >> 3;
+    const int dper = T_dp >> 3, drem = T_dp & 7;
+    const int dn = dper + (xcd < drem);
+    if (local < dn) return xcd * dper + min(xcd, drem) + local;
+    const int ut = U - T_dp, tper = ut >> 3, trem = ut & 7;
+    return T_dp + xcd * tper + min(xcd, trem) + (local - dn);
+}
+
+__device__ __forceinline__ void tile_coords(int q, int tiles_m, int tiles_c, int &tm, int &tc)
+{
+    const int span = GROUP_M * tiles_c;
+    const int first_m = (q / span) * GROUP_M;
+    const int gsz = min(tiles_m - first_m, GROUP_M);
+    const int r = q % span;
+    tm = first_m + r % gsz;
+    tc = r / gsz;
+}
+
+__device__ __forceinline__ void bfly(float &a, float &b)
+{
+    const float s = a + b;
+    b = a - b;
+    a = s;
+}
+
+// Swap the odd 16-lane rows of a with the even ones of b (v_permlane16_swap).
+__device__ __forceinline__ void swap16f(float &a, float &b)
+{
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ int swz_x(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int swz_w(int row) { return ((row >> 1) & 7) ^ ((row >> 4) & 1); }
+
+// Signed byte b of d.
+template <int B>
+__device__ __forceinline__ float byte_f32(uint32_t d)
+{
+    return (float)(int8_t)(d >> (8 * B));
+}
+
+// A 256 x 256 tile (tokens x channels) per workgroup, 8 wavefronts in 2 (channels) x 4 (tokens) of
+// 128 x 64 each: 8 x 4 blocks of 16x16x32, 128 accumulators per lane.  LDS holds two stages of 64
+// contraction rows, both operands with the contraction contiguous (128 bytes per row, 16-byte
+// chunks XOR-swizzled by row so that 16 consecutive rows' reads hit all banks).  The tokens go
+// global -> LDS directly.  The weights are stored the other way round ([n][channel]), so they pass
+// through registers: a lane loads 4 channels of 8 rows (8 dwords, 256 contiguous bytes per row and
+// wavefront), and the conversion to bf16 picks the bytes of one channel together, which is the
+// transposition: 4 chunks of 8 contraction values each.
+// During step g the next step's weights are converted and written, and the loads of the one after
+// are issued; the tokens of step g + 2 are issued once step g's stage is free (after the barrier).
+__global__ void __launch_bounds__(NTHREADS, 1) grad_gemm_kernel(GradParams p)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = w & 1, wm = w >> 1;
+    const int T = p.tiles_m * p.tiles_c, U = p.T_dp + (T - p.T_dp) * p.S;
+    const int K = p.K;
+    // the grid is rounded up to a multiple of 8
+    if ((int)blockIdx.x >= U) return;
+    const int u = unit_of((int)blockIdx.x, p.T_dp, U);
+    int tile = u, kb = 0, ke = p.nt, slot = -1;
+    if (u >= p.T_dp) {
+        const int r = T - p.T_dp, v = u - p.T_dp, sl = v / r;
+        tile = p.T_dp + v % r;
+        kb = (int)((int64_t)sl * p.nt / p.S);
+        ke = (int)((int64_t)(sl + 1) * p.nt / p.S);
+        slot = v;
+    }
+    int tm, tc;
+    tile_coords(tile, p.tiles_m, p.tiles_c, tm, tc);
+    const int m0 = tm * BM, c0 = tc * BC;
+
+    // tokens: instruction i of wave w fills rows 8 (8 i + w) .. + 7; lane -> row + lane / 8,
+    // position lane % 8
+    uint32_t offx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * (8 * i + w) + (lane >> 3);
+        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz_x(r))) : OOB;
+    }
+    const uint64_t xbase = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
+    auto issue_x = [&](int t) {
+        const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(xbase, NUM_RECORDS);
+        uint8_t *base = smem + ((t - kb) & 1) * STAGE + OPB + w * 1024;
+        const uint32_t past = t < ke ? 0u : OOB;
+        const int k0 = __builtin_amdgcn_readfirstlane((t < ke ? t : 0) * (BN * 2));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void *)(base + 8192 * i), 16, offx[i] | past, k0, 0, 0);
+    };
+    // weights: wave w takes rows 8 w .. 8 w + 7 of a step, lane l channels c0 + 4 l .. + 3
+    const uint32_t offw = c0 + 4 * lane < K ? (uint32_t)(8 * w * K + 4 * lane) : OOB;
+    uint32_t raw[8];
+    auto load_w = [&](int t) {
+        const int second = t >= p.nt1;
+        const int n0 = (t - (second ? p.nt1 : 0)) * BN;
+        const uint64_t base = reinterpret_cast<uint64_t>((second ? p.w2 : p.w1) + (int64_t)(t < ke ? n0 : 0) * K + c0);
+        const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(base, NUM_RECORDS);
+        const int rem = t < ke ? p.N - n0 - 8 * w : 0;            // rows left from this wave's first
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            raw[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rw, offw | (i < rem ? 0u : OOB), i * K, 0);
+    };
+    auto convert_w = [&](int t) {
+        uint8_t *base = smem + ((t - kb) & 1) * STAGE;
+        auto column = [&](auto byte, int j) {
+            const int r = 4 * lane + j;
+            v4u d;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = pack_bf16x2(byte(raw[2 * i]), byte(raw[2 * i + 1]));
+            *reinterpret_cast<v4u *>(base + r * 128 + 16 * (w ^ swz_w(r))) = d;
+        };
+        column([](uint32_t d) { return byte_f32<0>(d); }, 0);
+        column([](uint32_t d) { return byte_f32<1>(d); }, 1);
+        column([](uint32_t d) { return byte_f32<2>(d); }, 2);
+        column([](uint32_t d) { return byte_f32<3>(d); }, 3);
+    };
+
+    const int frow = lane & 15, fq = lane >> 4;
+    const int arow = (wn * 128 + frow) * 128, brow = OPB + (wm * 64 + frow) * 128;
+    v8bf16 fa[2][4], fb[2][4];
+    auto read_a = [&](int g, int kk, int h) {
+        const uint8_t *s0 = smem + (g & 1) * STAGE + arow;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            fa[h][b] = *reinterpret_cast<const v8bf16 *>(s0 + (4 * h + b) * 2048 +
+                                                         16 * ((4 * kk + fq) ^ swz_x(frow) ^ (b & 1)));
+    };
+    auto read_b = [&](int g, int kk) {
+        const uint8_t *s0 = smem + (g & 1) * STAGE + brow + 16 * ((4 * kk + fq) ^ swz_x(frow));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) fb[kk][b] = *reinterpret_cast<const v8bf16 *>(s0 + b * 2048);
+    };
+    v4f acc[8][4];
+#pragma unroll
+    for (int a = 0; a < 8; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[a][b] = v4f{};
+    auto mfma_range = [&](int kk, int h, int j0, int j1) {
+#pragma unroll
+        for (int j = j0; j < j1; ++j) {
+            const int bi = 4 * h + (j >> 2), bj = j & 3;
+            acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[h][j >> 2], fb[kk][bj], acc[bi][bj], 0, 0, 0);
+        }
+    };
+    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+
+    load_w(kb);
+    issue_x(kb);
+    convert_w(kb);
+    load_w(kb + 1);
+    issue_x(kb + 1);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(12));          // the tokens of step kb have landed
+    __syncthreads();
+    read_a(0, 0, 0);
+    read_b(0, 0);
+    for (int t = kb, g = 0; t < ke; ++t, ++g) {
+        read_a(g, 0, 1);
+        mfma_range(0, 0, 0, 16);
+        convert_w(t + 1);
+        fence();
+        load_w(t + 2);
+        read_a(g, 1, 0);
+        read_b(g, 1);
+        mfma_range(0, 1, 0, 16);
+        fence();
+        read_a(g, 1, 1);
+        mfma_range(1, 0, 0, 16);
+        fence();
+        mfma_range(1, 1, 0, 4);
+        fence();
+        // the tokens of step t + 1 have landed: only the 8 weight loads of step t + 2 are younger
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(8));
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        issue_x(t + 2);
+        read_a(g + 1, 0, 0);
+        read_b(g + 1, 0);
+        mfma_range(1, 1, 4, 16);
+        fence();
+    }
+    // every load into LDS has landed and every wave is done reading before the epilogue reuses it
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __syncthreads();
+
+    // lane: token lane % 16 of block bj; channels wn 128 + 16 bi + 4 (lane / 16) + v
+    if (slot >= 0) {
+        float *dst = p.part + (int64_t)slot * (BM * BC);
+#pragma unroll
+        for (int bj = 0; bj < 4; ++bj) {
+            const int ml = wm * 64 + 16 * bj + frow;
+            if (m0 + ml < p.M) {
+#pragma unroll
+                for (int bi = 0; bi < 8; ++bi)
+                    *reinterpret_cast<v4f *>(dst + ml * BC + wn * 128 + 16 * bi + 4 * fq) = acc[bi][bj];
+            }
+        }
+        return;
+    }
+    // Walsh-Hadamard over the channel bits below lg: 0, 1 in v, 4 .. 6 in bi, 2 and 3 across the
+    // lanes' 16-lane rows (a swap puts both partners of two registers into one lane), 7 across
+    // the two waves of a token range, through LDS
+    const int lg = p.lg;
+#pragma unroll
+    for (int bj = 0; bj < 4; ++bj) {
+#pragma unroll
+        for (int bi = 0; bi < 8; ++bi) {
+            v4f &v = acc[bi][bj];
+            if (lg > 0) {
+                float a = v[0], b = v[1], c = v[2], d = v[3];
+                bfly(a, b);
+                bfly(c, d);
+                if (lg > 1) {
+                    bfly(a, c);
+                    bfly(b, d);
+                }
+                v = v4f{a, b, c, d};
+            }
+        }
+#pragma unroll
+        for (int bi = 0; bi < 8; ++bi) {
+#pragma unroll
+            for (int v = 0; v < 4; v += 2) {
+                float a = acc[bi][bj][v], b = acc[bi][bj][v + 1];
+                if (lg > 2) {
+                    swap16f(a, b);
+                    bfly(a, b);
+                    swap16f(a, b);
+                }
+                if (lg > 3) {
+                    swap32f(a, b);
+                    bfly(a, b);
+                    swap32f(a, b);
+                }
+                acc[bi][bj][v] = a;
+                acc[bi][bj][v + 1] = b;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+            if (lg > 4 + s) {
+#pragma unroll
+                for (int bi = 0; bi < 8; ++bi)
+                    if (!(bi & (1 << s))) {
+                        const v4f a = acc[bi][bj], b = acc[bi | (1 << s)][bj];
+                        acc[bi][bj] = a + b;
+                        acc[bi | (1 << s)][bj] = a - b;
+                    }
+            }
+        }
+    }
+    // 16 tokens x 256 channels per token range and round, rows of 1 KiB with 16-byte chunk c at
+    // c ^ row; rounds alternate between two buffers, so one barrier a round is enough
+#pragma unroll
+    for (int bj = 0; bj < 4; ++bj) {
+        uint8_t *buf = smem + (bj & 1) * 65536 + wm * 16384;
+#pragma unroll
+        for (int bi = 0; bi < 8; ++bi)
+            *reinterpret_cast<v4f *>(buf + frow * 1024 + 16 * ((32 * wn + 4 * bi + fq) ^ frow)) = acc[bi][bj];
+        __syncthreads();
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+            const int r = 8 * wn + 4 * it + (lane >> 4), cc = lane & 15;    // 8 channels at 8 cc of each half
+            const int m = m0 + wm * 64 + 16 * bj + r;
+            if (m >= p.M) continue;
+            float v[2][8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const v4f d = *reinterpret_cast<const v4f *>(buf + r * 1024 + 16 * ((32 * h + 2 * cc + q) ^ r));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[h][4 * q + e] = d[e];
+                }
+            if (lg > 7) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) bfly(v[0][e], v[1][e]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = c0 + 128 * h + 8 * cc;
+                if (c >= K) continue;
+                const int64_t o = (int64_t)m * K + c;
+                v4u add = v4u{0, 0, 0, 0};
+                if (p.add) add = *reinterpret_cast<const v4u *>(p.add + o);
+                v4u out;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    out[e] = pack_bf16x2(__builtin_fmaf(v[h][2 * e], p.norm, bf16lo_to_f32(add[e])),
+                                         __builtin_fmaf(v[h][2 * e + 1], p.norm, bf16hi_to_f32(add[e])));
+                *reinterpret_cast<v4u *>(p.dx + o) = out;
+            }
+        }
+    }
+}
+
+// Split tiles: the S partial sums of a token's 256 channels, added in slice order (the same order at
+// every call), then the rotation, dx_add and the rounding.  32 lanes per token, 8 channels each:
+// channel bits 0 .. 2 in registers, 3 .. 7 across lanes.
+__global__ void __launch_bounds__(256) grad_join_kernel(GradParams p, int rb)
+{
+    const int i = (int)blockIdx.x / rb;                                 // split tile
+    const int ml = ((int)blockIdx.x % rb) * 8 + ((int)threadIdx.x >> 5);
+    const int l = (int)threadIdx.x & 31;
+    int tm, tc;
+    tile_coords(p.T_dp + i, p.tiles_m, p.tiles_c, tm, tc);
+    const int m = tm * BM + ml;
+    const int c = tc * BC + 8 * l;
+    const bool row_ok = ml < BM && m < p.M;
+    const int r = p.tiles_m * p.tiles_c - p.T_dp;
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (row_ok) {
+        const float *src = p.part + (int64_t)i * (BM * BC) + ml * BC + 8 * l;
+#pragma unroll 4
+        for (int s = 0; s < p.S; ++s, src += (int64_t)r * (BM * BC)) {
+            const v4f a = *reinterpret_cast<const v4f *>(src), b = *reinterpret_cast<const v4f *>(src + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] += a[e];
+                v[e + 4] += b[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < 3; ++b)
+        if (p.lg > b) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (!(e & (1 << b))) bfly(v[e], v[e | (1 << b)]);
+        }
+#pragma unroll
+    for (int b = 0; b < 5; ++b)
+        if (p.lg > 3 + b) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float o = __shfl_xor(v[e], 1 << b);
+                v[e] = (l >> b) & 1 ? o - v[e] : v[e] + o;
+            }
+        }
+    if (!row_ok || c >= p.K) return;
+    const int64_t o = (int64_t)m * p.K + c;
+    v4u add = v4u{0, 0, 0, 0};
+    if (p.add) add = *reinterpret_cast<const v4u *>(p.add + o);
+    v4u out;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        out[e] = pack_bf16x2(__builtin_fmaf(v[2 * e], p.norm, bf16lo_to_f32(add[e])),
+                             __builtin_fmaf(v[2 * e + 1], p.norm, bf16hi_to_f32(add[e])));
+    *reinterpret_cast<v4u *>(p.dx + o) = out;
+}
+
+struct PrepParams {
+    const uint16_t *dy;        // [M, N]
+    const uint16_t *pre;       // [M, N], or [2, M, N] (gate, up), or null (no activation)
+    const float *sw1, *sw2;    // [N]
+    uint16_t *a;               // [M, lda], columns Np on the second weight's
+    float *sums;               // [chunks][N (2 N)] partial column sums, or null
+    int64_t M, N, Np, lda;
+    int act, col_blocks, rows; // rows per chunk
+};
+
+// A workgroup takes 256 columns and a chunk of rows: 32 lanes of 8 columns, 8 rows at a time.  VEC:
+// N % 8 == 0, 16-byte loads; otherwise rows are not aligned and elements are read one by one.
+// Columns from N to Np are zeros.
+template <bool GATED, bool VEC>
+__global__ void __launch_bounds__(256) grad_prep_kernel(PrepParams p)
+{
+    __shared__ float red[GATED ? 2 : 1][8][256];
+    const int cb = (int)blockIdx.x % p.col_blocks, chunk = (int)blockIdx.x / p.col_blocks;
+    const int tr = (int)threadIdx.x >> 5, tl = (int)threadIdx.x & 31;
+    const int64_t n = (int64_t)cb * 256 + 8 * tl;
+    const int64_t r0 = (int64_t)chunk * p.rows, r1 = r0 + p.rows < p.M ? r0 + p.rows : p.M;
+    float s1[8], s2[8], sum1[8], sum2[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        s1[e] = n + e < p.N ? p.sw1[n + e] : 0.0f;
+        s2[e] = GATED && n + e < p.N ? p.sw2[n + e] : 0.0f;
+        sum1[e] = sum2[e] = 0.0f;
+    }
+    auto load8 = [&](const uint16_t *base, int64_t m, float (&v)[8]) {
+        const uint16_t *src = base + m * p.N + n;
+        if constexpr (VEC) {
+            v4u d = v4u{0, 0, 0, 0};
+            if (n < p.N) d = *reinterpret_cast<const v4u *>(src);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = bf16lo_to_f32(d[e]);
+                v[2 * e + 1] = bf16hi_to_f32(d[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = n + e < p.N ? bf16lo_to_f32(src[e]) : 0.0f;
+        }
+    };
+    auto store8 = [&](int64_t m, int64_t col, const float (&v)[8], const float (&s)[8]) {
+        *reinterpret_cast<v4u *>(p.a + m * p.lda + col) =
+            v4u{pack_bf16x2(v[0] * s[0], v[1] * s[1]), pack_bf16x2(v[2] * s[2], v[3] * s[3]),
+                pack_bf16x2(v[4] * s[4], v[5] * s[5]), pack_bf16x2(v[6] * s[6], v[7] * s[7])};
+    };
+    for (int64_t m = r0 + tr; m < r1; m += 8) {
+        float d[8];
+        load8(p.dy, m, d);
+        if constexpr (GATED) {
+            float g[8], u[8];
+            load8(p.pre, m, g);
+            load8(p.pre + p.M * p.N, m, u);
+            float du[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float val, slope;
+                act_value_slope(g[e], p.act, val, slope);
+                du[e] = d[e] * val;
+                d[e] = d[e] * u[e] * slope;
+                sum2[e] += du[e];
+            }
+            if (n < p.Np) store8(m, p.Np + n, du, s2);
+        } else if (p.pre) {
+            float z[8];
+            load8(p.pre, m, z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float val, slope;
+                act_value_slope(z[e], p.act, val, slope);
+                d[e] *= slope;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum1[e] += d[e];
+        if (n < p.Np) store8(m, n, d, s1);
+    }
+    if (!p.sums) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        red[0][tr][8 * tl + e] = sum1[e];
+        if constexpr (GATED) red[1][tr][8 * tl + e] = sum2[e];
+    }
+    __syncthreads();
+    const int64_t col = (int64_t)cb * 256 + threadIdx.x;
+    if (col >= p.N) return;
+#pragma unroll
+    for (int q = 0; q < (GATED ? 2 : 1); ++q) {
+        float s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s += red[q][r][threadIdx.x];
+        p.sums[((int64_t)chunk * (GATED ? 2 : 1) + q) * p.N + col] = s;
+    }
+}
+
+// db[n] = sum of the chunks' partial sums, in chunk order (0 chunks: 0).
+__global__ void __launch_bounds__(256) grad_bias_kernel(const float *sums, int chunks, int which, int parts, int64_t N,
+                                                        float *db)
+{
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (n >= N) return;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int c = 0; c < chunks; ++c) s += sums[((int64_t)c * parts + which) * N + n];
+    db[n] = s;
+}
+
+int cu_count()
+{
+    static int cus = [] {
+        int dev = 0, n = 0;
+        if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+            n = 256;
+        return n >= 8 ? n : 256;
+    }();
+    return cus;
+}
+
+struct Plan {
+    int64_t Np, lda;
+    int nt1, nt, tiles_m, tiles_c, T_dp, S;
+    int chunks, rows;
+    size_t a_bytes, sum_bytes, part_bytes;
+};
+
+size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+Plan make_plan(int64_t M, int64_t N, int K, bool gated)
+{
+    Plan pl;
+    pl.Np = (N + BN - 1) / BN * BN;
+    pl.lda = gated ? 2 * pl.Np : pl.Np;
+    pl.nt1 = (int)(pl.Np / BN);
+    pl.nt = (int)(pl.lda / BN);
+    pl.tiles_m = (int)((M + BM - 1) / BM);
+    pl.tiles_c = (K + BC - 1) / BC;
+    const int T = pl.tiles_m * pl.tiles_c, cap = cu_count() & ~7;
+    // Whole rounds of tiles run whole; the rest of the last round is split along the contraction so
+    // that it fills the CUs.  A step takes about 1 us; a slice costs its partial sums' round trip
+    // (8 bytes per element, counted at 2.5 TB/s) and the second launch.
+    pl.T_dp = T;
+    pl.S = 1;
+    const int r = T % cap;
+    if (r) {
+        const double step = 1.0e-6, rows = (double)(M < BM ? M : BM);
+        double best = pl.nt * step;
+        for (int S = 2; S <= MAX_SPLIT && pl.nt / S >= 2; ++S) {
+            const double rounds = (double)((r * S + cap - 1) / cap);
+            const double t = rounds * ((pl.nt + S - 1) / S) * step + (double)r * S * rows * BC * 8.0 / 2.5e12 + 4e-6;
+            if (t < best) {
+                best = t;
+                pl.T_dp = T - r;
+                pl.S = S;
+            }
+        }
+    }
+    // at most 1024 chunks of rows, 64 rows at least
+    int64_t rows = (M + 1023) / 1024;
+    rows = rows < 64 ? 64 : (rows + 7) / 8 * 8;
+    pl.rows = (int)rows;
+    pl.chunks = (int)((M + rows - 1) / rows);
+    pl.a_bytes = round256((size_t)M * (size_t)pl.lda * 2);
+    pl.sum_bytes = round256((size_t)pl.chunks * (size_t)N * (gated ? 8 : 4));
+    pl.part_bytes = pl.S > 1 ? (size_t)(T - pl.T_dp) * pl.S * BM * BC * 4 : 0;
+    return pl;
+}
+
+} // namespace
+
+size_t grad_workspace_bytes(int64_t M, int64_t N, int K, bool gated)
+{
+    if (M <= 0 || N <= 0) return 0;
+    const Plan pl = make_plan(M, N, K, gated);
+    return pl.a_bytes + pl.sum_bytes + pl.part_bytes;
+}
+
+hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
+{
+    if (g.N <= 0) return hipSuccess;
+    const Plan pl = make_plan(g.M, g.N, g.K, gated);
+    uint8_t *ws = static_cast<uint8_t *>(g.ws);
+    float *sums = reinterpret_cast<float *>(ws + pl.a_bytes);
+    const bool bias = g.db1 || g.db2;
+    if (g.M > 0) {
+        PrepParams q;
+        q.dy = g.dy;
+        q.pre = g.pre;
+        q.sw1 = g.sw1;
+        q.sw2 = g.sw2;
+        q.a = reinterpret_cast<uint16_t *>(ws);
+        q.sums = bias ? sums : nullptr;
+        q.M = g.M;
+        q.N = g.N;
+        q.Np = pl.Np;
+        q.lda = pl.lda;
+        q.act = g.act;
+        q.col_blocks = (int)((pl.Np + 255) / 256);
+        q.rows = pl.rows;
+        const dim3 grid((unsigned)q.col_blocks * (unsigned)pl.chunks);
+        const bool vec = g.N % 8 == 0;
+        if (gated && vec) hipLaunchKernelGGL((grad_prep_kernel<true, true>), grid, dim3(256), 0, stream, q);
+        else if (gated) hipLaunchKernelGGL((grad_prep_kernel<true, false>), grid, dim3(256), 0, stream, q);
+        else if (vec) hipLaunchKernelGGL((grad_prep_kernel<false, true>), grid, dim3(256), 0, stream, q);
+        else hipLaunchKernelGGL((grad_prep_kernel<false, false>), grid, dim3(256), 0, stream, q);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    for (int which = 0; which < 2; ++which) {
+        float *db = which ? g.db2 : g.db1;
+        if (!db) continue;
+        hipLaunchKernelGGL(grad_bias_kernel, dim3((unsigned)((g.N + 255) / 256)), dim3(256), 0, stream, sums,
+                           g.M > 0 ? pl.chunks : 0, which, gated ? 2 : 1, g.N, db);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (g.M <= 0) return hipSuccess;
+    GradParams p;
+    p.a = reinterpret_cast<const uint16_t *>(ws);
+    p.w1 = g.wq1;
+    p.w2 = gated ? g.wq2 : g.wq1;
+    p.add = g.add;
+    p.dx = g.dx;
+    p.part = reinterpret_cast<float *>(ws + pl.a_bytes + pl.sum_bytes);
+    p.lda = pl.lda;
+    p.M = (int)g.M;
+    p.N = (int)g.N;
+    p.K = g.K;
+    p.lg = g.log2g;
+    p.nt1 = pl.nt1;
+    p.nt = pl.nt;
+    p.tiles_m = pl.tiles_m;
+    p.tiles_c = pl.tiles_c;
+    p.T_dp = pl.T_dp;
+    p.S = pl.S;
+    p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g)));
+    const int T = pl.tiles_m * pl.tiles_c, U = pl.T_dp + (T - pl.T_dp) * pl.S;
+    hipLaunchKernelGGL(grad_gemm_kernel, dim3((unsigned)((U + 7) & ~7)), dim3(NTHREADS), 0, stream, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || pl.S == 1) return e;
+    const int rb = (int)((g.M < BM ? g.M : BM) + 7) / 8;
+    hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)(T - pl.T_dp) * (unsigned)rb), dim3(256), 0, stream, p, rb);
+    return hipGetLastError();
+}
+
+} // namespace convrot

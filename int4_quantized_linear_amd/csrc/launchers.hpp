@@ -49,6 +49,24 @@ hipError_t launch_gemv_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
                           void *y, Epi epi, int64_t M, int64_t N, int K, hipStream_t stream,
                           const FusedEpi &fused = FusedEpi());
 
+// Input gradient of an INT8 linear, or of two that share their tokens (gated: gate and up):
+//   dz = dy act'(pre)  (pre null: dy);   gate/up: dg = dy u act'(g), du = dy act(g), pre = [g; u]
+//   dx = bf16((sum_n dz sw wq) R + add),  db = column sums of dz (fp32; null: not computed)
+// ws: grad_workspace_bytes(M, N, K, gated) bytes, 256-byte aligned.  M == 0 still writes db.
+struct GradArgs {
+    const uint16_t *dy = nullptr, *pre = nullptr;
+    int64_t M = 0, N = 0;
+    int K = 0, log2g = 0, act = 0;
+    const int8_t *wq1 = nullptr, *wq2 = nullptr;
+    const float *sw1 = nullptr, *sw2 = nullptr;
+    const uint16_t *add = nullptr;
+    uint16_t *dx = nullptr;
+    float *db1 = nullptr, *db2 = nullptr;
+    void *ws = nullptr;
+};
+size_t grad_workspace_bytes(int64_t M, int64_t N, int K, bool gated);
+hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream);
+
 // W4A4: y = bf16(sum_g acc_g * sx[m,g] * sw[n,g] + bias[n]) with packed int4 operands and
 // fp16 group scales (group = 256 or 128, K % group == 0, K >= 256), or the unscaled int32 total
 // sum_k cx*cw (scales ignored).

@@ -89,3 +89,9 @@ def hadamard(g):
 def rotate(v, g):
     h = hadamard(g)
     return (v.reshape(-1, g) @ h).reshape(v.shape)
+
+
+def rotate_abs(v, g):
+    """Bound of |rotate(w)| for |w| <= v: each channel sums its whole group's magnitudes / sqrt(g)."""
+    s = v.reshape(-1, g).sum(1, keepdims=True) / np.sqrt(g)
+    return np.broadcast_to(s, (s.shape[0], g)).reshape(v.shape)

@@ -60,6 +60,40 @@ CASES += [("convrot_ffn_gated", ffn_args(**kw), s) for kw, s in [
     (dict(pre=A), "OVERLAP"), (dict(res=G, pre=G), "OVERLAP")]]
 
 
+def bwd_args(dy=A, pre=G, M=32, N=256, K=512, group=256, wq=B, sw=C, act=2, add=None, dx=D, db=None, ws=E,
+             wsb=1 << 26):
+    return (dy, pre, M, N, K, group, wq, sw, act, add, dx, db, ws, wsb, None)
+
+
+def gated_bwd_args(dy=A, pre=G, M=32, N=256, K=512, group=256, wg=B, sg=C, wu=B, su=C, act=2, add=None, dx=D, db1=None,
+                   db2=None, ws=E, wsb=1 << 26):
+    return (dy, pre, M, N, K, group, wg, sg, wu, su, act, add, dx, db1, db2, ws, wsb, None)
+
+
+def ffn_bwd_args(dy=A, pre=G, M=32, N=256, K=512, group=256, group_h=256, wg=B, sg=C, wu=B, su=C, wd=B, sd=C, act=2,
+                 add=None, dx=D, db1=None, db2=None, db3=None, ws=E, wsb=1 << 26):
+    return (dy, pre, M, N, K, group, group_h, wg, sg, wu, su, wd, sd, act, add, dx, db1, db2, db3, ws, wsb, None)
+
+
+BACKWARD = [("convrot_linear_act_backward", bwd_args), ("convrot_linear_gated_backward", gated_bwd_args),
+            ("convrot_ffn_gated_backward", ffn_bwd_args)]
+CASES += [(n, f(**kw), s) for n, f in BACKWARD for kw, s in [
+    (dict(M=-1), "SHAPE"), (dict(M=1 << 31), "SHAPE"), (dict(N=0), "SHAPE"), (dict(K=100), "SHAPE"),
+    (dict(N=1 << 20), "SHAPE"), (dict(K=131072, M=(1 << 31) - 1, wsb=1 << 62), "SHAPE"), (dict(group=3), "GROUP"),
+    (dict(K=320, group=128), "SHAPE"), (dict(act=5), "ACT"), (dict(act=-1), "ACT"), (dict(dy=None), "NULL"),
+    (dict(pre=None), "NULL"), (dict(dx=None), "NULL"), (dict(dy=MIS), "ALIGN"), (dict(pre=MIS), "ALIGN"),
+    (dict(dx=MIS), "ALIGN"), (dict(add=MIS), "ALIGN"), (dict(add=D + 256), "OVERLAP"), (dict(ws=None), "WORKSPACE"),
+    (dict(ws=E + 16), "WORKSPACE"), (dict(wsb=100), "WORKSPACE")]]
+CASES += [("convrot_linear_act_backward", bwd_args(**kw), s) for kw, s in [
+    (dict(wq=None), "NULL"), (dict(sw=None), "NULL"), (dict(db=MIS - 1), "ALIGN"), (dict(db=D + 16), "OVERLAP")]]
+CASES += [("convrot_linear_gated_backward", gated_bwd_args(**kw), s) for kw, s in [
+    (dict(wu=None), "NULL"), (dict(su=None), "NULL"), (dict(db1=H, db2=H + 512), "OVERLAP"), (dict(db2=D), "OVERLAP"),
+    (dict(act=0, pre=None), "NULL")]]
+CASES += [("convrot_ffn_gated_backward", ffn_bwd_args(**kw), s) for kw, s in [
+    (dict(wd=None), "NULL"), (dict(sd=None), "NULL"), (dict(wu=None), "NULL"), (dict(group_h=7), "GROUP"),
+    (dict(N=320, group_h=128), "SHAPE"), (dict(N=100), "SHAPE"), (dict(db3=MIS - 1), "ALIGN")]]
+
+
 @pytest.mark.parametrize("i", range(len(CASES)))
 def test_refusals(lib, i):
     name, args, status = CASES[i]
@@ -72,6 +106,11 @@ def test_refusals(lib, i):
     ("convrot_linear_act", act_args()), ("convrot_linear_act", act_args(res=D)),
     ("convrot_linear_act", act_args(M=4, N=1 << 24)),
     ("convrot_linear_act", act_args(x=None, xq=A, xs=C, ws=None, wsb=0, res=G, pre=H)),
+    ("convrot_linear_act_backward", bwd_args(act=0, pre=None)), ("convrot_linear_act_backward", bwd_args(add=D, db=H)),
+    ("convrot_linear_gated_backward", gated_bwd_args(db1=H, db2=H + 1024)),
+    ("convrot_ffn_gated_backward", ffn_bwd_args(add=A, db1=H, db2=H + 1024, db3=H + 2048)),
+    ("convrot_ffn_gated_backward", ffn_bwd_args(dx=A, add=A)),
+    ("convrot_linear_act_backward", bwd_args(M=0, db=H)),
     ("convrot_linear_gated", gated_args(pre=G, bg=C, bu=C)), ("convrot_ffn_gated", ffn_args(res=D, pre=G))])
 def test_valid_calls_reach_the_device(lib, name, args):
     assert getattr(lib, name)(*args) == ERR["CONVROT_ERR_HIP"], lib.convrot_last_error().decode()
@@ -83,6 +122,26 @@ def test_empty_inputs(lib):
     assert lib.convrot_linear_act(None, 1, None, None, 5, 0, 512, 256, *[None] * 3, 0, *[None] * 4, 0, None) == 0
     assert lib.convrot_linear_gated(None, 1, None, None, 0, 256, 512, 256, *[None] * 6, 2, None, None, None, 0, None) == 0
     assert lib.convrot_ffn_gated(None, 1, 0, 256, 512, 256, 256, *[None] * 9, 2, *[None] * 4, 0, None) == 0
+    assert lib.convrot_linear_act_backward(None, None, 0, 256, 512, 256, None, None, 2, *[None] * 4, 0, None) == 0
+    assert lib.convrot_linear_gated_backward(None, None, 0, 256, 512, 256, *[None] * 4, 2, *[None] * 5, 0, None) == 0
+    assert lib.convrot_ffn_gated_backward(None, None, 0, 256, 512, 256, 256, *[None] * 6, 2, *[None] * 6, 0, None) == 0
+
+
+def test_backward_workspace_queries(lib):
+    for q in (lib.convrot_workspace_bytes_backward, lib.convrot_workspace_bytes_gated_backward,
+              lib.convrot_workspace_bytes_ffn_backward):
+        assert q(-1, 256, 512) == 0 and q(4, 0, 512) == 0 and q(4, 256, 100) == 0 and q(4, 1 << 20, 512) == 0
+        assert q(0, 256, 512) == 0 and q((1 << 31) - 1, 256, 131072) == 0
+    for M, N, K in [(1, 64, 64), (12, 8192, 5120), (2048, 25600, 5120), (4096, 16128, 5376)]:
+        assert lib.convrot_workspace_bytes_backward(M, N, K) >= 2 * M * N
+        assert lib.convrot_workspace_bytes_gated_backward(M, N, K) >= 4 * M * N
+        w = lib.convrot_workspace_bytes_ffn_backward(M, N, K)
+        assert w % 256 == 0 and w >= 6 * M * N
+        args = list(ffn_bwd_args(M=M, N=N, K=K, group=64, group_h=64, dy=1 << 40, pre=2 << 40, ws=3 << 40, dx=4 << 40,
+                                 wsb=w))
+        assert lib.convrot_ffn_gated_backward(*args) == ERR["CONVROT_ERR_HIP"]
+        args[-2] = w - 1
+        assert lib.convrot_ffn_gated_backward(*args) == ERR["CONVROT_ERR_WORKSPACE"]
 
 
 def test_workspace_queries(lib):
