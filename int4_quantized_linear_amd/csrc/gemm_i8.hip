@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                 }
                 fence();
             }
-        } else if constexpr (VEC && (E == Epi::Act || E == Epi::Gated)) {
+        } else if constexpr (E == Epi::Act || E == Epi::Gated) {
             // Two phases per 16-token block, so that the activation's code exists once and not per
             // accumulator register.  (Applied where the accumulators are, fully unrolled, it spilled
             // 64 (Gated) and 145 (Act) registers.)  First the block's int32 sums go to the wave's own 8 KiB
@@ -461,15 +461,35 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
             auto offset = [&](int r) {                                 // r: row in the wave's 64
                 return (r < 64 && mw + r < Mi && n < Ni) ? (uint32_t)(r * Ni + n) * 2u : OOB;
             };
+            // rows not 16-byte aligned (N % 8 != 0): element by element, clipped at N
             auto store8 = [&](const float (&v)[8], __amdgpu_buffer_rsrc_t to, uint32_t off) {
                 const v4u d = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                pack_bf16x2(v[6], v[7])};
-                __builtin_amdgcn_raw_buffer_store_b128(d, to, off, 0, 0);
+                if constexpr (VEC) {
+                    __builtin_amdgcn_raw_buffer_store_b128(d, to, off, 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(e & 1 ? d[e >> 1] >> 16 : d[e >> 1] & 0xffffu),
+                                                              to, n + e < Ni ? off + 2u * (uint32_t)e : OOB, 0, 0);
+                }
+            };
+            auto load8 = [&](uint32_t off) {
+                if constexpr (VEC) {
+                    return __builtin_amdgcn_raw_buffer_load_b128(rres, off, 0, 0);
+                } else {
+                    v4u d = {};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        d[e >> 1] |= (uint32_t)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(
+                                         rres, n + e < Ni ? off + 2u * (uint32_t)e : OOB, 0, 0) << (16 * (e & 1));
+                    return d;
+                }
             };
             v4u res0 = {}, res1 = {};
             if constexpr (E == Epi::Act) {
-                res0 = __builtin_amdgcn_raw_buffer_load_b128(rres, offset(lrow), 0, 0);
-                res1 = __builtin_amdgcn_raw_buffer_load_b128(rres, offset(lrow + RPI), 0, 0);
+                res0 = load8(offset(lrow));
+                res1 = load8(offset(lrow + RPI));
             }
 #pragma unroll
             for (int bj = 0; bj < 4; ++bj) {
@@ -502,15 +522,17 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                         float u[8];
                         z8(ch + 4, cl + NF, u);
                         if (p.f.pre) store8(u, rpre2, off);
+                        act_values(v, act);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], act) * u[i];
+                        for (int i = 0; i < 8; ++i) v[i] *= u[i];
                     } else {
                         const v4u rr = res0;
                         res0 = res1;
-                        res1 = __builtin_amdgcn_raw_buffer_load_b128(rres, offset(r + 2 * RPI), 0, 0);
+                        res1 = load8(offset(r + 2 * RPI));
+                        act_values(v, act);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            v[i] = act_value(v[i], act) + (i & 1 ? bf16hi_to_f32(rr[i >> 1]) : bf16lo_to_f32(rr[i >> 1]));
+                            v[i] += (i & 1 ? bf16hi_to_f32(rr[i >> 1]) : bf16lo_to_f32(rr[i >> 1]));
                     }
                     store8(v, ry, off);
                 }
@@ -588,52 +610,10 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                 const float sxm = ls[2 * BN + wm * 64 + 16 * bj + erow];
 #pragma unroll
                 for (int bi = 0; bi < 8; ++bi) {
-                    if constexpr (E == Epi::Gated) {
-                        if (bi & 1) continue;                 // the pair (bi, bi + 1) is one feature block
-                        const int nl = wn * 64 + 4 * efq + 8 * bi, n = n0 + nl;
-                        const v4f s4 = *reinterpret_cast<const v4f *>(ls + nl), t4 = *reinterpret_cast<const v4f *>(ls + nl + 128);
-                        const v4f b4 = *reinterpret_cast<const v4f *>(ls + BN + nl),
-                                  c4 = *reinterpret_cast<const v4f *>(ls + BN + nl + 128);
-                        const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
-                            p.f.pre + (int64_t)mr * p.N, (short)0, p.f.pre ? NUM_RECORDS : 0, 0x00020000);
-                        const __amdgpu_buffer_rsrc_t ru = __builtin_amdgcn_make_buffer_rsrc(
-                            p.f.pre + ((int64_t)Mi + mr) * p.N, (short)0, p.f.pre ? NUM_RECORDS : 0, 0x00020000);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float gv = __builtin_fmaf((float)acc[bi][bj][e], sxm * s4[e], b4[e]);
-                            const float uv = __builtin_fmaf((float)acc[bi + 1][bj][e], sxm * t4[e], c4[e]);
-                            const uint32_t off = (rok && n + e < Ni) ? (uint32_t)(erow * Ni + n + e) * 2u : OOB;
-                            const uint32_t gu = pack_bf16x2(gv, uv);
-                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(gu & 0xffffu), rg, off, 0, 0);
-                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(gu >> 16), ru, off, 0, 0);
-                            const float hv = act_value(gv, p.f.act) * uv;
-                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(pack_bf16x2(hv, 0.0f) & 0xffffu), ry,
-                                                                  off, 0, 0);
-                        }
-                        continue;
-                    }
                     const int nl = ecol + 16 * bi;
                     const v4f s4 = *reinterpret_cast<const v4f *>(ls + nl);
                     const v4f b4 = *reinterpret_cast<const v4f *>(ls + BN + nl);
                     const int n = n0 + nl;
-                    if constexpr (E == Epi::Act) {
-                        // a null residual or pre has no records: its loads read 0, its stores drop
-                        const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc(
-                            const_cast<uint16_t *>(p.f.residual) + (int64_t)mr * p.N, (short)0,
-                            p.f.residual ? NUM_RECORDS : 0, 0x00020000);
-                        const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
-                            p.f.pre + (int64_t)mr * p.N, (short)0, p.f.pre ? NUM_RECORDS : 0, 0x00020000);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float z = __builtin_fmaf((float)acc[bi][bj][e], sxm * s4[e], b4[e]);
-                            const uint32_t off = (rok && n + e < Ni) ? (uint32_t)(erow * Ni + n + e) * 2u : OOB;
-                            const float r = bf16lo_to_f32((uint32_t)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rr, off, 0, 0));
-                            const uint32_t zy = pack_bf16x2(z, act_value(z, p.f.act) + r);
-                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(zy & 0xffffu), rp, off, 0, 0);
-                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(zy >> 16), ry, off, 0, 0);
-                        }
-                        continue;
-                    }
                     // rows not 16-byte aligned (N % 8 != 0): element stores, clipped at N
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -828,9 +808,10 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(ReduceParams p)
         if (p.f.pre) store_row8(p.f.pre + m * p.N + n, yv);
         v4u res = v4u{0, 0, 0, 0};
         if (p.f.residual) res = *reinterpret_cast<const v4u *>(p.f.residual + m * p.N + n);
+        act_values(yv, p.f.act);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            yv[e] = act_value(yv[e], p.f.act) + (e & 1 ? bf16hi_to_f32(res[e >> 1]) : bf16lo_to_f32(res[e >> 1]));
+            yv[e] += e & 1 ? bf16hi_to_f32(res[e >> 1]) : bf16lo_to_f32(res[e >> 1]);
     } else if constexpr (E == Epi::Gated) {
         float uv[8];
         sum_slots(p, i, r, ml, cl + 16, sum);
@@ -841,8 +822,9 @@ __global__ void __launch_bounds__(256) split_reduce_kernel(ReduceParams p)
             store_row8(p.f.pre + m * p.N + n, yv);
             store_row8(p.f.pre + (p.M + m) * p.N + n, uv);
         }
+        act_values(yv, p.f.act);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) yv[e] = act_value(yv[e], p.f.act) * uv[e];
+        for (int e = 0; e < 8; ++e) yv[e] *= uv[e];
     }
     store_row8(p.y + m * p.N + n, yv);
 }
