@@ -144,15 +144,20 @@ int convrot_linear(const void *x, int x_dtype, const int8_t *xq, const float *x_
  *   z = (xq . wq^T) * sx[m] * sw[n] + bias[n]  in fp32;   y = bf16( act(z) + residual[m,n] )
  *   act one of CONVROT_ACT_*; residual bf16 [M, N] or NULL, added in fp32 (one rounding).
  *   pre bf16 [M, N] or NULL: when given, receives bf16(z) for convrot_linear_act_backward.
- * All other arguments, the dispatch by M, the workspace (convrot_workspace_bytes(M, N, K, 8)) and the
- * split-K tail are convrot_linear's; with act NONE and no residual the outputs are its outputs
- * bit for bit.  residual may be y itself (added in place); any other overlap of y, pre and
+ * All other arguments are convrot_linear's, and so are the workspace's rules with
+ * convrot_workspace_bytes_act(M, N, K) bytes; with act NONE and no residual the outputs are its
+ * outputs bit for bit.  For M > 16 the tiles and slices of K are chosen by size; they never change the
+ * outputs.  residual may be y itself (added in place); any other overlap of y, pre and
  * residual returns CONVROT_ERR_OVERLAP.  residual, pre: 16-byte aligned.
  */
 int convrot_linear_act(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,
                        int64_t K, int group, const int8_t *wq, const float *w_scale, const float *bias, int act,
                        const void *residual, void *pre, void *y, void *workspace, size_t workspace_bytes,
                        hipStream_t stream);
+
+/* Workspace bytes of convrot_linear_act (the quantized x, then room for the partial sums of slices of
+ * K, without which it runs unsliced); 0 on invalid arguments. */
+size_t convrot_workspace_bytes_act(int64_t M, int64_t N, int64_t K);
 
 /*
  * Gate and up projections of a gated feed-forward block, the activation and the product in one
@@ -171,8 +176,7 @@ int convrot_linear_gated(const void *x, int x_dtype, const int8_t *xq, const flo
                          const int8_t *wq_up, const float *up_scale, const float *up_bias, int act, void *pre, void *h,
                          void *workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* Workspace bytes of convrot_linear_gated (the quantized x, then room for the GEMM's split-K
- * tail); 0 on invalid arguments. */
+/* The same for convrot_linear_gated. */
 size_t convrot_workspace_bytes_gated(int64_t M, int64_t N, int64_t K);
 
 /*
@@ -185,7 +189,7 @@ size_t convrot_workspace_bytes_gated(int64_t M, int64_t N, int64_t K);
  *   pre bf16 [2, M, F] or NULL as in convrot_linear_gated; y bf16 [M, K].
  *   K % 64 == 0, F % 64 == 0, both in [64, CONVROT_MAX_K] and multiples of their groups.
  *   workspace: convrot_workspace_bytes_ffn(M, F, K) bytes, 256-byte aligned, required (the codes of x
- *   and h, h itself, the split-K tails).
+ *   and h, h itself, the partial sums).
  * The result is that of convrot_linear_gated followed by convrot_linear_act, bit for bit.
  */
 int convrot_ffn_gated(const void *x, int x_dtype, int64_t M, int64_t F, int64_t K, int group, int group_h,

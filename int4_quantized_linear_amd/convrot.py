@@ -30,6 +30,7 @@ SIGNATURES = {
     "convrot_linear": ([P, I, P, P, I64, I64, I64, I, P, P, P, P, P, SZ, P], I),
     "convrot_linear_act": ([P, I, P, P, I64, I64, I64, I, P, P, P, I, P, P, P, P, SZ, P], I),
     "convrot_linear_gated": ([P, I, P, P, I64, I64, I64, I, P, P, P, P, P, P, I, P, P, P, SZ, P], I),
+    "convrot_workspace_bytes_act": ([I64, I64, I64], SZ),
     "convrot_workspace_bytes_gated": ([I64, I64, I64], SZ),
     "convrot_ffn_gated": ([P, I, I64, I64, I64, I, I, P, P, P, P, P, P, P, P, P, I, P, P, P, P, SZ, P], I),
     "convrot_workspace_bytes_ffn": ([I64, I64, I64], SZ),
@@ -181,6 +182,10 @@ def linear(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, bias
     return y
 
 
+def workspace_bytes_act(M: int, N: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_act(M, N, K))
+
+
 def _act_code(act: str) -> int:
     if act not in ACTS:
         raise ValueError("act is one of %s, got %r" % (", ".join(ACTS), act))
@@ -242,7 +247,7 @@ def linear_act(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, 
            residual=(residual, (M, N), torch.bfloat16), out=(out, (M, N), torch.bfloat16))
     y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     pre = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if save_pre else None
-    ws = _workspace(M, N, K, 8, dev)
+    ws = torch.empty(max(workspace_bytes_act(M, N, K), 256), dtype=torch.uint8, device=dev)
     _call_on(dev, "convrot_linear_act", _ptr(x), _dtype_code(x) if x is not None else 0, _ptr(xq), _ptr(x_scale), M, N,
              K, group, _ptr(wq), _ptr(w_scale), _ptr(bias), code, _ptr(residual), _ptr(pre), _ptr(y), _ptr(ws),
              ws.numel())

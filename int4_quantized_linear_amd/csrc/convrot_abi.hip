@@ -91,7 +91,8 @@ struct WsLayout {
     size_t xq = 0, xs = 0, tiles = 0, part = 0, total = 0;
 };
 
-WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int bits, bool gated = false)
+// epi: the Act and Gated linears plan their K slices themselves.
+WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int bits, convrot::Epi epi = convrot::Epi::Bf16)
 {
     WsLayout L;
     size_t off = 0;
@@ -102,7 +103,10 @@ WsLayout ws_layout(int64_t M, int64_t N, int64_t K, int bits, bool gated = false
         off += round256((size_t)M * 4);
         // optional: the split-K tail's int32 partial sums (GEMM path only)
         L.part = off;
-        if (M > 16) off += round256(convrot::gemm_i8_split_bytes(M, N, (int)K, gated));
+        if (M > 16)
+            off += round256(epi == convrot::Epi::Bf16
+                                ? convrot::gemm_i8_split_bytes(M, N, (int)K)
+                                : convrot::plan_gemm_i8_tile(M, N, (int)K, epi == convrot::Epi::Gated, true).part_bytes);
     } else {
         L.xq = off;
         off += round256((size_t)(M * K / 2));
@@ -251,7 +255,7 @@ int linear_i8(const char *who, const void *x, int x_dtype, const int8_t *xq, con
     if ((f.residual != y && overlap(f.residual, out_bytes, y, out_bytes)) || overlap(f.pre, pre_bytes, y, out_bytes) ||
         overlap(f.pre, pre_bytes, f.residual, out_bytes))
         return fail(CONVROT_ERR_OVERLAP, "%s: an output overlaps pre or residual (only residual == y is allowed)", who);
-    const WsLayout L = ws_layout(M, N, K, 8, gated);
+    const WsLayout L = ws_layout(M, N, K, 8, epi);
     if (scratch_fn && x && workspace_bytes < L.part)
         return fail(CONVROT_ERR_WORKSPACE, "%s: M*K = %lld needs %zu bytes of scratch; the fixed scratch holds %zu "
                     "(use convrot_linear with a workspace)", who, (long long)(M * K), L.part, workspace_bytes);
@@ -282,10 +286,19 @@ int linear_i8(const char *who, const void *x, int x_dtype, const int8_t *xq, con
         xq = qx;
         x_scale = sx;
     }
-    hipError_t e = M <= 16 ? convrot::launch_gemv_i8(xq, wq, x_scale, w_scale, bias, y, epi, M, N, (int)K, stream, f)
-                           : convrot::launch_gemm_i8(xq, wq, x_scale, w_scale, bias, y, epi, M, N, (int)K, part,
-                                                      part_bytes, stream, f);
-    return hip_status(e, M <= 16 ? "gemv_i8" : "gemm_i8");
+    if (M <= 16)
+        return hip_status(convrot::launch_gemv_i8(xq, wq, x_scale, w_scale, bias, y, epi, M, N, (int)K, stream, f),
+                          "gemv_i8");
+    if (epi != convrot::Epi::Bf16) {
+        const convrot::TilePlan pl = convrot::plan_gemm_i8_tile(M, N, (int)K, gated, part || L.total == L.part);
+        if (pl.bm)
+            return hip_status(convrot::launch_gemm_i8_tile(pl, xq, wq, x_scale, w_scale, bias, y, epi, M, N, (int)K, part,
+                                                           stream, f),
+                              "gemm_i8_tile");
+    }
+    return hip_status(convrot::launch_gemm_i8(xq, wq, x_scale, w_scale, bias, y, epi, M, N, (int)K, part, part_bytes,
+                                              stream, f),
+                      "gemm_i8");
 }
 
 // Workspace of convrot_ffn_gated: the gated linear's, with h [M, F] bf16 and the down linear's
@@ -298,7 +311,8 @@ struct FfnLayout {
 FfnLayout ffn_layout(int64_t M, int64_t F, int64_t K)
 {
     FfnLayout L;
-    const size_t up = ws_layout(M, F, K, 8, true).total, down = ws_layout(M, K, F, 8).total;
+    const size_t up = ws_layout(M, F, K, 8, convrot::Epi::Gated).total;
+    const size_t down = ws_layout(M, K, F, 8, convrot::Epi::Act).total;
     L.h = up > down ? up : down;
     L.total = L.h + round256((size_t)M * (size_t)F * 2);
     return L;
@@ -438,11 +452,14 @@ int convrot_linear_act(const void *x, int x_dtype, const int8_t *xq, const float
                      workspace_bytes, nullptr, stream, convrot::Epi::Act, f);
 }
 
+size_t convrot_workspace_bytes_act(int64_t M, int64_t N, int64_t K)
+{
+    return convrot_workspace_bytes(M, N, K, 8) ? ws_layout(M, N, K, 8, convrot::Epi::Act).total : 0;
+}
+
 size_t convrot_workspace_bytes_gated(int64_t M, int64_t N, int64_t K)
 {
-    // shapes check_shape accepts; an empty batch needs none
-    if (!convrot_workspace_bytes(M, N, K, 8)) return 0;
-    return ws_layout(M, N, K, 8, true).total;
+    return convrot_workspace_bytes(M, N, K, 8) ? ws_layout(M, N, K, 8, convrot::Epi::Gated).total : 0;
 }
 
 int convrot_linear_gated(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,

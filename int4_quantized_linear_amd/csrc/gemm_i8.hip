@@ -45,6 +45,7 @@
 #include "activation.hpp"
 #include "device_common.hpp"
 #include "launchers.hpp"
+#include "tile_common.hpp"
 
 namespace convrot {
 namespace {
@@ -60,10 +61,7 @@ constexpr int NSCALE = 4;
 constexpr int DUMMY_OFF = SCALE_OFF + NSCALE * SCALE_BYTES;
 constexpr int SMEM = DUMMY_OFF + 8 * 1024;
 constexpr int NTHREADS = 512;
-constexpr int GROUP_M = 4;
 constexpr int WG_PER_CU = 1;
-constexpr uint32_t OOB = 0x80000000u;         // buffer offset past num_records -> loads return 0
-constexpr int NUM_RECORDS = 0x7ffffff0;
 
 struct GemmParams {
     const int8_t *xq;
@@ -90,51 +88,6 @@ struct GemmParams {
 // feature 16 (c / 32) + c % 16 of the gate (c / 16 even) or the up weight.
 template <Epi E>
 constexpr int tile_features() { return E == Epi::Gated ? BN / 2 : BN; }
-
-typedef __attribute__((address_space(3))) void lds_void;
-
-__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
-
-// Buffer descriptor from a wave-uniform address and size, built from readfirstlane'd halves so it
-// stays in scalar registers.  (readfirstlane returns int: each half goes through uint32_t, so the
-// low half is zero-extended, not sign-extended, into the 64-bit address.)
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(uint64_t a, int bytes)
-{
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(((uint64_t)hi << 32) | (uint64_t)lo), (short)0,
-                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
-}
-
-// s_waitcnt immediate (gfx9 encoding) waiting for vmcnt <= n only.
-constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
-
-// Unit of virtual id pid (= blockIdx.x + k * gridDim.x, gridDim.x a multiple of 8).  Dispatch ids
-// are spread round-robin over the 8 XCDs, so pid keeps its XCD.  Units 0..T_dp-1 are the whole
-// tiles, then come the split units; each XCD walks a contiguous range of the whole tiles, then a
-// contiguous range of the split units (T_dp is a multiple of 8 whenever there are split units, so
-// this is a bijection of [0, U)).
-__device__ __forceinline__ int unit_of(int pid, int T_dp, int U)
-{
-    const int xcd = pid & 7, local = pid >> 3;
-    const int dper = T_dp >> 3, drem = T_dp & 7;
-    const int dn = dper + (xcd < drem);
-    if (local < dn) return xcd * dper + min(xcd, drem) + local;
-    const int ut = U - T_dp, tper = ut >> 3, trem = ut & 7;
-    return T_dp + xcd * tper + min(xcd, trem) + (local - dn);
-}
-
-// Tile q of the M-grouped order: groups of GROUP_M tile rows, walked column by column, so the
-// tiles an XCD runs at the same time share their weight tiles in its L2.
-__device__ __forceinline__ void tile_coords(int q, int tiles_m, int tiles_n, int &tm, int &tn)
-{
-    const int span = GROUP_M * tiles_n;
-    const int first_m = (q / span) * GROUP_M;
-    const int gsz = min(tiles_m - first_m, GROUP_M);
-    const int r = q % span;
-    tm = first_m + r % gsz;
-    tn = r / gsz;
-}
 
 template <Epi E, bool VEC>
 __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams p)
@@ -890,6 +843,27 @@ SplitPlan plan_split(int64_t M, int64_t N, int K, int nf)
 }
 
 } // namespace
+
+// plan_split's model, with what it leaves out when it compares one grid with itself: about 8 us of
+// prologue and epilogue, and the weights' stream (3.4 TB/s where one tile row reads them all: a
+// 256 x 256 tile has few loads in flight for the few tokens it serves).
+double gemm_i8_seconds(int64_t M, int64_t N, int K, bool gated, bool split)
+{
+    const int nf = gated ? tile_features<Epi::Gated>() : BN;
+    const int64_t T = ((M + BM - 1) / BM) * ((N + nf - 1) / nf);
+    const int cap = grid_capacity(), KT = (K + BK - 1) / BK;
+    SplitPlan pl = {(int)T, 1, 0};
+    if (split) pl = plan_split(M, N, K, nf);
+    const int64_t r = T % cap, full = T / cap;
+    const double t_full = 1.84e-6, t_fast = 1.38e-6;
+    const double power = (double)r * KT * t_full / cap;
+    const double clock = (double)((r * pl.S + cap - 1) / cap) * ((double)KT / pl.S) * t_fast;
+    const double tail = power > clock ? power : clock;
+    const double joined = pl.S > 1 ? (double)r * pl.S * (double)(M < BM ? M : BM) * BN * 8.0 / 2.5e12 + 4e-6 : 0.0;
+    const double math = (double)full * KT * t_full + tail + joined;
+    const double stream = (double)N * K * (gated ? 2.0 : 1.0) / 3.4e12;
+    return (math > stream ? math : stream) + 8e-6;
+}
 
 size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K, bool gated)
 {

@@ -15,12 +15,12 @@
 #include "activation.hpp"
 #include "device_common.hpp"
 #include "launchers.hpp"
+#include "tile_common.hpp"
 
 namespace convrot {
 namespace {
 
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int BM = 256, BC = 256;             // tokens and channels of a tile
 constexpr int BN = 64;                        // contraction rows per step
@@ -28,9 +28,6 @@ constexpr int OPB = 256 * BN * 2;             // bytes of one operand per stage 
 constexpr int STAGE = 2 * OPB;                // weights (by channel), then tokens
 constexpr int SMEM = 2 * STAGE;
 constexpr int NTHREADS = 512;
-constexpr int GROUP_M = 4;
-constexpr uint32_t OOB = 0x80000000u;
-constexpr int NUM_RECORDS = 0x7ffffff0;
 constexpr int MAX_SPLIT = 64;
 
 struct GradParams {
@@ -47,38 +44,6 @@ struct GradParams {
     float norm;                // 2^(-lg / 2)
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(uint64_t a, int bytes)
-{
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(((uint64_t)hi << 32) | (uint64_t)lo), (short)0,
-                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
-}
-
-constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
-
-// Unit of workgroup id: ids go round-robin over the 8 XCDs, and each XCD takes a contiguous range of
-// the whole tiles, then one of the slices (T_dp is a multiple of 8 whenever there are slices).
-__device__ __forceinline__ int unit_of(int pid, int T_dp, int U)
-{
-    const int xcd = pid & 7, local = pid >> 3;
-    const int dper = T_dp >> 3, drem = T_dp & 7;
-    const int dn = dper + (xcd < drem);
-    if (local < dn) return xcd * dper + min(xcd, drem) + local;
-    const int ut = U - T_dp, tper = ut >> 3, trem = ut & 7;
-    return T_dp + xcd * tper + min(xcd, trem) + (local - dn);
-}
-
-__device__ __forceinline__ void tile_coords(int q, int tiles_m, int tiles_c, int &tm, int &tc)
-{
-    const int span = GROUP_M * tiles_c;
-    const int first_m = (q / span) * GROUP_M;
-    const int gsz = min(tiles_m - first_m, GROUP_M);
-    const int r = q % span;
-    tm = first_m + r % gsz;
-    tc = r / gsz;
-}
-
 __device__ __forceinline__ void bfly(float &a, float &b)
 {
     const float s = a + b;
@@ -94,8 +59,9 @@ __device__ __forceinline__ void swap16f(float &a, float &b)
     b = __uint_as_float(r[1]);
 }
 
-__device__ __forceinline__ int swz_x(int row) { return (row >> 1) & 7; }
-__device__ __forceinline__ int swz_w(int row) { return ((row >> 1) & 7) ^ ((row >> 4) & 1); }
+// The weights' rows are written 4 apart (a lane's 4 channels), so their position takes row bit 4 too:
+// 8 lanes then write 8 distinct chunks of one 128-byte window.
+__device__ __forceinline__ int swz_w(int row) { return swz(row) ^ ((row >> 4) & 1); }
 
 // Signed byte b of d.
 template <int B>
@@ -143,7 +109,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) grad_gemm_kernel(GradParams p)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 8 * (8 * i + w) + (lane >> 3);
-        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz_x(r))) : OOB;
+        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz(r))) : OOB;
     }
     const uint64_t xbase = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
     auto issue_x = [&](int t) {
@@ -191,10 +157,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) grad_gemm_kernel(GradParams p)
 #pragma unroll
         for (int b = 0; b < 4; ++b)
             fa[h][b] = *reinterpret_cast<const v8bf16 *>(s0 + (4 * h + b) * 2048 +
-                                                         16 * ((4 * kk + fq) ^ swz_x(frow) ^ (b & 1)));
+                                                         16 * ((4 * kk + fq) ^ swz(frow) ^ (b & 1)));
     };
     auto read_b = [&](int g, int kk) {
-        const uint8_t *s0 = smem + (g & 1) * STAGE + brow + 16 * ((4 * kk + fq) ^ swz_x(frow));
+        const uint8_t *s0 = smem + (g & 1) * STAGE + brow + 16 * ((4 * kk + fq) ^ swz(frow));
 #pragma unroll
         for (int b = 0; b < 4; ++b) fb[kk][b] = *reinterpret_cast<const v8bf16 *>(s0 + b * 2048);
     };

@@ -42,6 +42,19 @@ hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
                           hipStream_t stream, const FusedEpi &fused = FusedEpi());
 // Bytes of `part` the split-K tail uses for this shape on the current device (0: no split).
 size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K, bool gated = false);
+// Estimated seconds of launch_gemm_i8's fused epilogues, with or without `part`, for the choice below.
+double gemm_i8_seconds(int64_t M, int64_t N, int K, bool gated, bool split);
+
+// The Act and Gated linears in tiles of bm (64 or 128) tokens x 128 weight rows, each in S slices of K
+// (part: the plan's part_bytes when S > 1).  Same outputs as launch_gemm_i8, bit for bit.
+struct TilePlan {
+    int bm = 0, S = 1;         // bm == 0: launch_gemm_i8's 256 x 256 tiles are the better choice
+    size_t part_bytes = 0;     // for either
+};
+TilePlan plan_gemm_i8_tile(int64_t M, int64_t N, int K, bool gated, bool split);
+hipError_t launch_gemm_i8_tile(const TilePlan &pl, const int8_t *xq, const int8_t *wq, const float *sx, const float *sw,
+                               const float *bias, void *y, Epi epi, int64_t M, int64_t N, int K, void *part,
+                               hipStream_t stream, const FusedEpi &fused);
 
 // Same contraction for M <= 16 (weight streaming; K split among the wavefronts of a workgroup,
 // no scratch memory).

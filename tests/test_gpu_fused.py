@@ -119,27 +119,35 @@ def test_linear_gated(cr, M, N, K, g, act):
         assert torch.equal(alone, h), "pre-quantized tokens, or not saving, change the result"
 
 
-# the whole-tile and the split-K tail walk have to give the same bits (a workspace without room for
-# the partial sums runs whole)
-@pytest.mark.parametrize("M,N,K", [(64, 4096, 5120), (300, 504, 4096), (17, 264, 1024), (2048, 512, 5120)])
-def test_split_tail_is_bit_identical(cr, M, N, K):
-    P.say("split tail M=%d N=%d K=%d" % (M, N, K))
-    x, gate, up = _tokens(M, K, 5), _weight(cr, N, K, 256, 1), _weight(cr, N, K, 256, 2)
-    xq, xs = cr.quantize_act(x, 256, 8)
+# Every choice of tiles and slices of K gives the same bits: with a workspace the call slices where that
+# is faster, without one it runs whole.  The sizes cover 64- and 128-token tiles, sliced and whole, 256 x 256
+# tiles with and without a sliced tail, and ragged N on each.  A token's outputs do not depend on the
+# others, so a few tokens alone (other tiles) have to give the same bits too.
+@pytest.mark.parametrize("M,N,K", [(64, 4096, 5120), (300, 504, 4096), (17, 264, 1024), (2048, 512, 5120), (100, 41, 8192),
+                                   (130, 3000, 4096), (640, 2049, 2112), (1500, 2056, 1024), (1400, 8200, 576),
+                                   (3328, 3736, 512), (3328, 3737, 512), (1792, 3488, 512), (2304, 7208, 2048),
+                                   (1536, 5472, 1536)])
+def test_tiles_and_slices_are_bit_identical(cr, M, N, K):
+    P.say("tiles and slices M=%d N=%d K=%d" % (M, N, K))
+    g = cr.dynamic_group(K)
+    x, gate, up = _tokens(M, K, 5), _weight(cr, N, K, g, 1), _weight(cr, N, K, g, 2)
+    xq, xs = cr.quantize_act(x, g, 8)
     r = _randn(M, N, seed=6)
-    whole_ws = (M * K + 255) // 256 * 256 + (4 * M + 255) // 256 * 256
-    assert cr.workspace_bytes(M, N, K) > whole_ws and cr.workspace_bytes_gated(M, N, K) > whole_ws
     st = torch.cuda.current_stream().cuda_stream
-    y = cr.linear_act(x, gate[0], gate[1], act="gelu", residual=r)
-    h, pre = cr.linear_gated(x, *gate, *up, act="silu", save_pre=True)
+    y = cr.linear_act(x, gate[0], gate[1], act="gelu", residual=r, group=g)
+    h, pre = cr.linear_gated(x, *gate, *up, act="silu", group=g, save_pre=True)
     y2, h2, pre2 = torch.empty_like(y), torch.empty_like(h), torch.empty_like(pre)
     ptr = cr._ptr
-    cr._call("convrot_linear_act", None, 0, ptr(xq), ptr(xs), M, N, K, 256, ptr(gate[0]), ptr(gate[1]), None, 3, ptr(r),
+    cr._call("convrot_linear_act", None, 0, ptr(xq), ptr(xs), M, N, K, g, ptr(gate[0]), ptr(gate[1]), None, 3, ptr(r),
              None, ptr(y2), None, 0, st)
-    cr._call("convrot_linear_gated", None, 0, ptr(xq), ptr(xs), M, N, K, 256, ptr(gate[0]), ptr(gate[1]), None,
+    cr._call("convrot_linear_gated", None, 0, ptr(xq), ptr(xs), M, N, K, g, ptr(gate[0]), ptr(gate[1]), None,
              ptr(up[0]), ptr(up[1]), None, 2, ptr(pre2), ptr(h2), None, 0, st)
     torch.cuda.synchronize()
     assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(pre, pre2)
+    for a, b in ((0, min(M, 77)), (max(0, M - 5), M)):
+        q = dict(group=g, xq=xq[a:b].clone(), x_scale=xs[a:b].clone())
+        assert torch.equal(cr.linear_act(None, *gate, act="gelu", residual=r[a:b].clone(), **q), y[a:b])
+        assert torch.equal(cr.linear_gated(None, *gate, *up, act="silu", **q), h[a:b])
 
 
 @pytest.mark.parametrize("M,K,F,dtype", [(1, 64, 64, torch.bfloat16), (1, 5120, 2560, torch.bfloat16),
