@@ -116,4 +116,22 @@ __device__ __forceinline__ void act_value_slope(float z, int act, float &value, 
     }
 }
 
+// The same of N values: v becomes act(v), slope act'(v).
+template <int N>
+__device__ __forceinline__ void act_values_slopes(float (&v)[N], float (&slope)[N], int act)
+{
+#define CONVROT_ACT_CASE(label, code)                                                             \
+    label:                                                                                        \
+        _Pragma("unroll") for (int i = 0; i < N; ++i) act_value_slope(v[i], code, v[i], slope[i]); \
+        break;
+    switch (act) {
+        CONVROT_ACT_CASE(case kActRelu, kActRelu)
+        CONVROT_ACT_CASE(case kActSilu, kActSilu)
+        CONVROT_ACT_CASE(case kActGelu, kActGelu)
+        CONVROT_ACT_CASE(case kActGeluTanh, kActGeluTanh)
+        CONVROT_ACT_CASE(default, kActNone)
+    }
+#undef CONVROT_ACT_CASE
+}
+
 } // namespace convrot

@@ -369,18 +369,25 @@ int grad_i8(const char *who, convrot::GradArgs g, int64_t K, int group, bool gat
     return hip_status(convrot::launch_grad_i8(g, gated, stream), "grad_i8");
 }
 
-// Workspace of convrot_ffn_gated_backward: the larger of the two steps', then dh [M, F] bf16.
+// Workspace of convrot_ffn_gated_backward.  Without gate and up bias gradients the first step's epilogue
+// writes the second step's operand [M, 2 F] bf16; with them (fp32 column sums over the tokens) dh [M, F]
+// bf16 goes through the second step's own first pass.  Both: the larger of the two steps' own
+// workspaces, then that buffer.
 struct FfnGradLayout {
-    size_t dh = 0, total = 0;
+    size_t steps = 0, steps_dh = 0, total = 0;
 };
 
 FfnGradLayout ffn_grad_layout(int64_t M, int64_t F, int64_t K)
 {
     FfnGradLayout L;
     const size_t down = convrot::grad_workspace_bytes(M, K, (int)F, false);
-    const size_t up = convrot::grad_workspace_bytes(M, F, (int)K, true);
-    L.dh = round256(up > down ? up : down);
-    L.total = L.dh + round256((size_t)M * (size_t)F * 2);
+    const size_t up = convrot::grad_workspace_bytes(M, F, (int)K, true, true);
+    const size_t up_dh = convrot::grad_workspace_bytes(M, F, (int)K, true);
+    L.steps = round256(up > down ? up : down);
+    L.steps_dh = round256(up_dh > down ? up_dh : down);
+    const size_t with_a = L.steps + round256((size_t)M * (size_t)F * 4);
+    const size_t with_dh = L.steps_dh + round256((size_t)M * (size_t)F * 2);
+    L.total = with_a > with_dh ? with_a : with_dh;
     return L;
 }
 
@@ -594,7 +601,9 @@ int convrot_ffn_gated_backward(const void *dy, const void *pre, int64_t M, int64
     if (M > 0 && (!workspace || workspace_bytes < L.total || !aligned(workspace, 256)))
         return fail(CONVROT_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of at least %zu bytes (got %zu)", who,
                     L.total, workspace ? workspace_bytes : (size_t)0);
-    uint16_t *dh = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(workspace) + L.dh);
+    const bool sums = dgate_bias || dup_bias;
+    const size_t steps = sums ? L.steps_dh : L.steps;
+    uint16_t *dh = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(workspace) + steps);
     down.dy = static_cast<const uint16_t *>(dy);
     down.M = up.M = M;
     down.N = K;
@@ -615,10 +624,18 @@ int convrot_ffn_gated_backward(const void *dy, const void *pre, int64_t M, int64
     up.dx = static_cast<uint16_t *>(dx);
     up.db1 = dgate_bias;
     up.db2 = dup_bias;
-    if ((rc = check_grad(who, up, K, group, true, workspace, L.dh))) return rc;
-    if ((rc = check_grad(who, down, F, group_h, false, workspace, L.dh))) return rc;
-    if ((rc = grad_i8(who, down, F, group_h, false, workspace, L.dh, stream))) return rc;
-    return grad_i8(who, up, K, group, true, workspace, L.dh, stream);
+    if ((rc = check_grad(who, up, K, group, true, workspace, L.steps_dh))) return rc;
+    if ((rc = check_grad(who, down, F, group_h, false, workspace, L.steps_dh))) return rc;
+    if (!sums) {
+        down.next.pre = up.pre;
+        down.next.sw_gate = gate_scale;
+        down.next.sw_up = up_scale;
+        down.next.act = act;
+        down.next.a = dh;
+        up.a = dh;
+    }
+    if ((rc = grad_i8(who, down, F, group_h, false, workspace, L.steps_dh, stream))) return rc;
+    return grad_i8(who, up, K, group, true, workspace, L.steps_dh, stream);
 }
 
 int convrot_gemm_i8_i32(const int8_t *xq, const int8_t *wq, int64_t M, int64_t N, int64_t K, int32_t *acc,

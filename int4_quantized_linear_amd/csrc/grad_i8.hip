@@ -39,10 +39,59 @@ struct GradParams {
     int64_t lda;
     int M, N, K, lg;
     int nt1, nt;               // contraction steps of the first weight, in all
+    int bm;                    // tokens per tile, 256 or 64
     int tiles_m, tiles_c;
     int T_dp, S;               // whole tiles, then the rest in S slices each
     float norm;                // 2^(-lg / 2)
+    GradNext next;             // next.a non-null: the gated product's gradient goes there, not to dx
 };
+
+// N channels c .. of token m, rotated but not yet normalised, to where the launch puts them:
+//   dx = bf16(v norm + add), or, for the hidden gradient of a gated block, dh = bf16(v norm) and on to
+//   both operands of the next contraction, bf16(dh u act'(g) sw_gate) and bf16(dh act(g) sw_up), which
+//   saves writing dh and reading it back in a pass of its own.
+// (N channels are 2 N bytes: one load or store each; K % 64 == 0, so all exist.)
+template <int N>
+__device__ __forceinline__ void finish(const GradParams &p, int m, int c, float (&v)[N])
+{
+    typedef uint32_t vec __attribute__((ext_vector_type(N / 2)));
+    auto load = [](const uint16_t *src, float (&to)[N]) {
+        const vec d = *reinterpret_cast<const vec *>(src);
+#pragma unroll
+        for (int e = 0; e < N; ++e) to[e] = e & 1 ? bf16hi_to_f32(d[e >> 1]) : bf16lo_to_f32(d[e >> 1]);
+    };
+    auto store = [](uint16_t *dst, const float (&from)[N]) {
+        vec d;
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) d[e] = pack_bf16x2(from[2 * e], from[2 * e + 1]);
+        *reinterpret_cast<vec *>(dst) = d;
+    };
+    const int64_t o = (int64_t)m * p.K + c;
+    if (!p.next.a) {
+        float add[N] = {};
+        if (p.add) load(p.add + o, add);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = __builtin_fmaf(v[e], p.norm, add[e]);
+        store(p.dx + o, v);
+        return;
+    }
+    float g[N], u[N], slope[N];
+    load(p.next.pre + o, g);
+    load(p.next.pre + (int64_t)p.M * p.K + o, u);
+    act_values_slopes(g, slope, p.next.act);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const uint32_t d = pack_bf16x2(v[e] * p.norm, v[e + 1] * p.norm);
+        const float d0 = bf16lo_to_f32(d), d1 = bf16hi_to_f32(d);
+        u[e] = d0 * u[e] * slope[e] * p.next.sw_gate[c + e];
+        u[e + 1] = d1 * u[e + 1] * slope[e + 1] * p.next.sw_gate[c + e + 1];
+        g[e] = d0 * g[e] * p.next.sw_up[c + e];
+        g[e + 1] = d1 * g[e + 1] * p.next.sw_up[c + e + 1];
+    }
+    uint16_t *a = p.next.a + (int64_t)m * 2 * p.K + c;       // K % 64 == 0: no padding between the two
+    store(a, u);
+    store(a + p.K, g);
+}
 
 __device__ __forceinline__ void bfly(float &a, float &b)
 {
@@ -68,6 +117,23 @@ template <int B>
 __device__ __forceinline__ float byte_f32(uint32_t d)
 {
     return (float)(int8_t)(d >> (8 * B));
+}
+
+// A step's weights of this wave in LDS order: raw holds 4 channels (4 lane .. + 3) of rows 8 chunk ..
+// 8 chunk + 7; each channel's 8 values become one 16-byte chunk of its row.
+__device__ __forceinline__ void transpose_to_lds(const uint32_t *raw, uint8_t *stage, int lane, int chunk)
+{
+    auto column = [&](auto byte, int j) {
+        const int r = 4 * lane + j;
+        v4u d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = pack_bf16x2(byte(raw[2 * i]), byte(raw[2 * i + 1]));
+        *reinterpret_cast<v4u *>(stage + r * 128 + 16 * (chunk ^ swz_w(r))) = d;
+    };
+    column([](uint32_t d) { return byte_f32<0>(d); }, 0);
+    column([](uint32_t d) { return byte_f32<1>(d); }, 1);
+    column([](uint32_t d) { return byte_f32<2>(d); }, 2);
+    column([](uint32_t d) { return byte_f32<3>(d); }, 3);
 }
 
 // A 256 x 256 tile (tokens x channels) per workgroup, 8 wavefronts in 2 (channels) x 4 (tokens) of
@@ -119,7 +185,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) grad_gemm_kernel(GradParams p)
         const int k0 = __builtin_amdgcn_readfirstlane((t < ke ? t : 0) * (BN * 2));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void *)(base + 8192 * i), 16, offx[i] | past, k0, 0, 0);
+            load16_to_lds(rx, base + 8192 * i, offx[i] | past, k0);
     };
     // weights: wave w takes rows 8 w .. 8 w + 7 of a step, lane l channels c0 + 4 l .. + 3
     const uint32_t offw = c0 + 4 * lane < K ? (uint32_t)(8 * w * K + 4 * lane) : OOB;
@@ -134,20 +200,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) grad_gemm_kernel(GradParams p)
         for (int i = 0; i < 8; ++i)
             raw[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rw, offw | (i < rem ? 0u : OOB), i * K, 0);
     };
-    auto convert_w = [&](int t) {
-        uint8_t *base = smem + ((t - kb) & 1) * STAGE;
-        auto column = [&](auto byte, int j) {
-            const int r = 4 * lane + j;
-            v4u d;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = pack_bf16x2(byte(raw[2 * i]), byte(raw[2 * i + 1]));
-            *reinterpret_cast<v4u *>(base + r * 128 + 16 * (w ^ swz_w(r))) = d;
-        };
-        column([](uint32_t d) { return byte_f32<0>(d); }, 0);
-        column([](uint32_t d) { return byte_f32<1>(d); }, 1);
-        column([](uint32_t d) { return byte_f32<2>(d); }, 2);
-        column([](uint32_t d) { return byte_f32<3>(d); }, 3);
-    };
+    auto convert_w = [&](int t) { transpose_to_lds(raw, smem + ((t - kb) & 1) * STAGE, lane, w); };
 
     const int frow = lane & 15, fq = lane >> 4;
     const int arow = (wn * 128 + frow) * 128, brow = OPB + (wm * 64 + frow) * 128;
@@ -281,47 +334,237 @@ __global__ void __launch_bounds__(NTHREADS, 1) grad_gemm_kernel(GradParams p)
             }
         }
     }
-    // 16 tokens x 256 channels per token range and round, rows of 1 KiB with 16-byte chunk c at
-    // c ^ row; rounds alternate between two buffers, so one barrier a round is enough
+    // 128 tokens (32 of each token range) a round, rows of 1 KiB with 16-byte chunk c at c ^ row % 16;
+    // then 32 threads per token, 8 channels each.  (The loop is rolled: finish() appears twice, with 64
+    // accumulators live; unrolled over the accumulators' 16-token blocks it spilled 185 registers.)
 #pragma unroll
-    for (int bj = 0; bj < 4; ++bj) {
-        uint8_t *buf = smem + (bj & 1) * 65536 + wm * 16384;
+    for (int pass = 0; pass < 2; ++pass) {
+        if (pass) __syncthreads();
 #pragma unroll
-        for (int bi = 0; bi < 8; ++bi)
-            *reinterpret_cast<v4f *>(buf + frow * 1024 + 16 * ((32 * wn + 4 * bi + fq) ^ frow)) = acc[bi][bj];
+        for (int b2 = 0; b2 < 2; ++b2)
+#pragma unroll
+            for (int bi = 0; bi < 8; ++bi)
+                *reinterpret_cast<v4f *>(smem + (wm * 32 + 16 * b2 + frow) * 1024 +
+                                         16 * ((32 * wn + 4 * bi + fq) ^ frow)) = acc[bi][2 * pass + b2];
         __syncthreads();
+        const int cc = (int)threadIdx.x & 31, c = c0 + 8 * cc;
+#pragma unroll 1
+        for (int it = 0; it < 8; ++it) {
+            const int row = 16 * it + ((int)threadIdx.x >> 5);
+            const int m = m0 + (row >> 5) * 64 + 32 * pass + (row & 31);
+            if (m >= p.M || c >= K) continue;
+            float v[8];
 #pragma unroll
-        for (int it = 0; it < 2; ++it) {
-            const int r = 8 * wn + 4 * it + (lane >> 4), cc = lane & 15;    // 8 channels at 8 cc of each half
-            const int m = m0 + wm * 64 + 16 * bj + r;
-            if (m >= p.M) continue;
-            float v[2][8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const v4f d = *reinterpret_cast<const v4f *>(buf + r * 1024 + 16 * ((32 * h + 2 * cc + q) ^ r));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[h][4 * q + e] = d[e];
-                }
-            if (lg > 7) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) bfly(v[0][e], v[1][e]);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = c0 + 128 * h + 8 * cc;
-                if (c >= K) continue;
-                const int64_t o = (int64_t)m * K + c;
-                v4u add = v4u{0, 0, 0, 0};
-                if (p.add) add = *reinterpret_cast<const v4u *>(p.add + o);
-                v4u out;
+            for (int q = 0; q < 2; ++q) {
+                const v4f own = *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * ((2 * cc + q) ^ (row & 15)));
+                const v4f other = *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * (((2 * cc + q) ^ 32) ^ (row & 15)));
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    out[e] = pack_bf16x2(__builtin_fmaf(v[h][2 * e], p.norm, bf16lo_to_f32(add[e])),
-                                         __builtin_fmaf(v[h][2 * e + 1], p.norm, bf16hi_to_f32(add[e])));
-                *reinterpret_cast<v4u *>(p.dx + o) = out;
+                    v[4 * q + e] = lg <= 7 ? own[e] : cc & 16 ? other[e] - own[e] : own[e] + other[e];
             }
+            finish<8>(p, m, c, v);
+        }
+    }
+}
+
+// The same for 64 tokens x 256 channels, for batches whose 256-token tiles would not fill the GPU or
+// would mostly compute padding: 256 threads, 80 KiB of LDS, two workgroups per CU.  Each of the 4
+// wavefronts takes 64 channels of all 64 tokens.  A step is short here against the latency of its
+// loads, so both operands go through registers, loaded three steps ahead of their use into two sets
+// (steps alternate between them; the loop runs an even number of steps, one past the end adds zeros).
+__global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
+{
+    constexpr int TM = 64, WB = 256 * 128, TSTAGE = WB + TM * 128;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * TSTAGE];
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int T = p.tiles_m * p.tiles_c, U = p.T_dp + (T - p.T_dp) * p.S;
+    const int K = p.K;
+    if ((int)blockIdx.x >= U) return;                    // the grid is rounded up to a multiple of 8
+    const int u = unit_of((int)blockIdx.x, p.T_dp, U);
+    int tile = u, kb = 0, ke = p.nt, slot = -1;
+    if (u >= p.T_dp) {
+        const int r = T - p.T_dp, v = u - p.T_dp, sl = v / r;
+        tile = p.T_dp + v % r;
+        kb = (int)((int64_t)sl * p.nt / p.S);
+        ke = (int)((int64_t)(sl + 1) * p.nt / p.S);
+        slot = v;
+    }
+    int tm, tc;
+    tile_coords(tile, p.tiles_m, p.tiles_c, tm, tc);
+    const int m0 = tm * TM, c0 = tc * BC;
+
+    // tokens: row 8 (4 i + w) + lane / 8, 16-byte chunk lane % 8
+    uint32_t offx[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = 8 * (4 * i + w) + (lane >> 3);
+        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * (lane & 7)) : OOB;
+    }
+    const uint64_t xbase = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
+    const uint32_t offw = c0 + 4 * lane < K ? (uint32_t)(16 * w * K + 4 * lane) : OOB;
+    struct Set {
+        uint32_t w[16];
+        v4u x[2];
+    };
+    Set set0, set1;
+    auto load = [&](int t, Set &to) {
+        const int second = t >= p.nt1;
+        const int n0 = (t - (second ? p.nt1 : 0)) * BN;
+        const uint64_t base = reinterpret_cast<uint64_t>((second ? p.w2 : p.w1) + (int64_t)(t < ke ? n0 : 0) * K + c0);
+        const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(base, NUM_RECORDS), rx = uniform_rsrc(xbase, NUM_RECORDS);
+        const int rem = t < ke ? p.N - n0 - 16 * w : 0;
+        const uint32_t past = t < ke ? 0u : OOB;
+        const int k0 = __builtin_amdgcn_readfirstlane((t < ke ? t : 0) * (BN * 2));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) to.x[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, offx[i] | past, k0, 0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            to.w[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rw, offw | (i < rem ? 0u : OOB), i * K, 0);
+    };
+    auto store = [&](int t, const Set &from) {
+        uint8_t *stage = smem + ((t - kb) & 1) * TSTAGE;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 8 * (4 * i + w) + (lane >> 3);
+            *reinterpret_cast<v4u *>(stage + WB + r * 128 + 16 * ((lane & 7) ^ swz(r))) = from.x[i];
+        }
+        transpose_to_lds(from.w, stage, lane, 2 * w);
+        transpose_to_lds(from.w + 8, stage, lane, 2 * w + 1);
+    };
+    const int frow = lane & 15, fq = lane >> 4;
+    v4f acc[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[a][b] = v4f{};
+    auto step = [&](int t, Set &next) {
+        const uint8_t *st = smem + ((t - kb) & 1) * TSTAGE;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const int pos = (4 * kk + fq) ^ swz(frow);
+            v8bf16 fa[4], fb[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                fa[b] = *reinterpret_cast<const v8bf16 *>(st + (64 * w + 16 * b + frow) * 128 + 16 * (pos ^ (b & 1)));
+                fb[b] = *reinterpret_cast<const v8bf16 *>(st + WB + (16 * b + frow) * 128 + 16 * pos);
+            }
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[b], acc[a][b], 0, 0, 0);
+        }
+        store(t + 1, next);
+        load(t + 3, next);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    load(kb, set0);
+    load(kb + 1, set1);
+    store(kb, set0);
+    load(kb + 2, set0);
+    __syncthreads();
+    for (int t = kb; t < ke; t += 2) {
+        step(t, set1);
+        step(t + 1, set0);
+    }
+    __syncthreads();
+
+    // lane: token lane % 16 of block b; channels 64 w + 16 a + 4 (lane / 16) + v
+    if (slot >= 0) {
+        float *dst = p.part + (int64_t)slot * (TM * BC);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int ml = 16 * b + frow;
+            if (m0 + ml < p.M) {
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+                    *reinterpret_cast<v4f *>(dst + ml * BC + 64 * w + 16 * a + 4 * fq) = acc[a][b];
+            }
+        }
+        return;
+    }
+    // the rotation as in the kernel above: channel bits 0, 1 in v, 2, 3 across lanes, 4, 5 in a; 6 and 7
+    // across the four waves
+    const int lg = p.lg;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            float x0 = acc[a][b][0], x1 = acc[a][b][1], x2 = acc[a][b][2], x3 = acc[a][b][3];
+            if (lg > 0) {
+                bfly(x0, x1);
+                bfly(x2, x3);
+            }
+            if (lg > 1) {
+                bfly(x0, x2);
+                bfly(x1, x3);
+            }
+            if (lg > 2) {
+                swap16f(x0, x1);
+                bfly(x0, x1);
+                swap16f(x0, x1);
+                swap16f(x2, x3);
+                bfly(x2, x3);
+                swap16f(x2, x3);
+            }
+            if (lg > 3) {
+                swap32f(x0, x1);
+                bfly(x0, x1);
+                swap32f(x0, x1);
+                swap32f(x2, x3);
+                bfly(x2, x3);
+                swap32f(x2, x3);
+            }
+            acc[a][b] = v4f{x0, x1, x2, x3};
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (lg > 4 + s) {
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+                    if (!(a & (1 << s))) {
+                        const v4f x = acc[a][b], y = acc[a | (1 << s)][b];
+                        acc[a][b] = x + y;
+                        acc[a | (1 << s)][b] = x - y;
+                    }
+            }
+        }
+    }
+    // 16 tokens a round, in two buffers in turn: a thread takes one token's channels 4 cc .. + 3 of all
+    // four quarters
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        uint8_t *buf = smem + (b & 1) * 16384;
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+            *reinterpret_cast<v4f *>(buf + frow * 1024 + 16 * ((16 * w + 4 * a + fq) ^ frow)) = acc[a][b];
+        __syncthreads();
+        const int r = (int)threadIdx.x >> 4, cc = (int)threadIdx.x & 15;
+        const int m = m0 + 16 * b + r;
+        if (m >= p.M) continue;
+        v4f v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const v4f *>(buf + r * 1024 + 16 * ((16 * q + cc) ^ r));
+        if (lg > 6) {
+            const v4f x = v[0], y = v[2];
+            v[0] = x + v[1];
+            v[1] = x - v[1];
+            v[2] = y + v[3];
+            v[3] = y - v[3];
+        }
+        if (lg > 7) {
+            const v4f x = v[0], y = v[1];
+            v[0] = x + v[2];
+            v[2] = x - v[2];
+            v[1] = y + v[3];
+            v[3] = y - v[3];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int c = c0 + 64 * q + 4 * cc;
+            float out[4] = {v[q][0], v[q][1], v[q][2], v[q][3]};
+            if (c < K) finish<4>(p, m, c, out);
         }
     }
 }
@@ -336,15 +579,15 @@ __global__ void __launch_bounds__(256) grad_join_kernel(GradParams p, int rb)
     const int l = (int)threadIdx.x & 31;
     int tm, tc;
     tile_coords(p.T_dp + i, p.tiles_m, p.tiles_c, tm, tc);
-    const int m = tm * BM + ml;
+    const int m = tm * p.bm + ml, slot = p.bm * BC;
     const int c = tc * BC + 8 * l;
-    const bool row_ok = ml < BM && m < p.M;
+    const bool row_ok = ml < p.bm && m < p.M;
     const int r = p.tiles_m * p.tiles_c - p.T_dp;
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (row_ok) {
-        const float *src = p.part + (int64_t)i * (BM * BC) + ml * BC + 8 * l;
+        const float *src = p.part + (int64_t)i * slot + ml * BC + 8 * l;
 #pragma unroll 4
-        for (int s = 0; s < p.S; ++s, src += (int64_t)r * (BM * BC)) {
+        for (int s = 0; s < p.S; ++s, src += (int64_t)r * slot) {
             const v4f a = *reinterpret_cast<const v4f *>(src), b = *reinterpret_cast<const v4f *>(src + 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -369,16 +612,7 @@ __global__ void __launch_bounds__(256) grad_join_kernel(GradParams p, int rb)
                 v[e] = (l >> b) & 1 ? o - v[e] : v[e] + o;
             }
         }
-    if (!row_ok || c >= p.K) return;
-    const int64_t o = (int64_t)m * p.K + c;
-    v4u add = v4u{0, 0, 0, 0};
-    if (p.add) add = *reinterpret_cast<const v4u *>(p.add + o);
-    v4u out;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        out[e] = pack_bf16x2(__builtin_fmaf(v[2 * e], p.norm, bf16lo_to_f32(add[e])),
-                             __builtin_fmaf(v[2 * e + 1], p.norm, bf16hi_to_f32(add[e])));
-    *reinterpret_cast<v4u *>(p.dx + o) = out;
+    if (row_ok && c < p.K) finish<8>(p, m, c, v);
 }
 
 struct PrepParams {
@@ -436,25 +670,21 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(PrepParams p)
             float g[8], u[8];
             load8(p.pre, m, g);
             load8(p.pre + p.M * p.N, m, u);
-            float du[8];
+            float du[8], slope[8];
+            act_values_slopes(g, slope, p.act);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float val, slope;
-                act_value_slope(g[e], p.act, val, slope);
-                du[e] = d[e] * val;
-                d[e] = d[e] * u[e] * slope;
+                du[e] = d[e] * g[e];
+                d[e] = d[e] * u[e] * slope[e];
                 sum2[e] += du[e];
             }
             if (n < p.Np) store8(m, p.Np + n, du, s2);
         } else if (p.pre) {
-            float z[8];
+            float z[8], slope[8];
             load8(p.pre, m, z);
+            act_values_slopes(z, slope, p.act);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float val, slope;
-                act_value_slope(z[e], p.act, val, slope);
-                d[e] *= slope;
-            }
+            for (int e = 0; e < 8; ++e) d[e] *= slope[e];
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum1[e] += d[e];
@@ -503,12 +733,44 @@ int cu_count()
 
 struct Plan {
     int64_t Np, lda;
-    int nt1, nt, tiles_m, tiles_c, T_dp, S;
-    int chunks, rows;
+    int nt1, nt, bm, tiles_m, tiles_c, T_dp, S;
+    int chunks;                // of partial column sums
     size_t a_bytes, sum_bytes, part_bytes;
 };
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+// Tokens per tile and slices of the contraction, by estimated time.  Whole rounds of tiles run whole; the
+// rest of the last round may be split so that it fills the GPU.  Slices cost their partial sums' round
+// trip (8 bytes per element, counted at 2.5 TB/s) and the second launch.
+void tile_plan(Plan &pl, int64_t M)
+{
+    double best = 1e30;
+    for (int bm = 64; bm <= BM; bm *= 4) {
+        const int64_t tiles = (M + bm - 1) / bm * pl.tiles_c;
+        if (tiles >= (int64_t)1 << 24) continue;
+        const int T = (int)tiles, cap = (cu_count() & ~7) * (bm == 64 ? 2 : 1);
+        const double step = bm == 64 ? 1.0e-6 : 1.1e-6, rows = (double)(M < bm ? M : bm);
+        const int r = T % cap;
+        for (int S = 1; S <= (r ? MAX_SPLIT : 1); ++S) {
+            if (S > 1 && pl.nt / S < 2) break;
+            const double rounds = (double)((r * S + cap - 1) / cap);
+            const double t = ((double)(T / cap) * pl.nt + rounds * ((pl.nt + S - 1) / S)) * step +
+                             (S > 1 ? (double)r * S * rows * BC * 8.0 / 2.5e12 + 4e-6 : 0.0);
+            if (t < best) {
+                best = t;
+                pl.bm = bm;
+                pl.tiles_m = (int)((M + bm - 1) / bm);
+                pl.T_dp = S > 1 ? T - r : T;
+                pl.S = S;
+            }
+        }
+    }
+}
+
+// Rows of a grad_prep workgroup: 8, one per thread, where no bias gradient needs its column sums.  With
+// one, a multiple of 8 that gives at most about 64 chunks of partial sums to add up.
+int prep_rows(int64_t M, bool bias) { return bias && M > 512 ? (int)((M + 511) / 512 * 8) : 8; }
 
 Plan make_plan(int64_t M, int64_t N, int K, bool gated)
 {
@@ -517,46 +779,23 @@ Plan make_plan(int64_t M, int64_t N, int K, bool gated)
     pl.lda = gated ? 2 * pl.Np : pl.Np;
     pl.nt1 = (int)(pl.Np / BN);
     pl.nt = (int)(pl.lda / BN);
-    pl.tiles_m = (int)((M + BM - 1) / BM);
     pl.tiles_c = (K + BC - 1) / BC;
-    const int T = pl.tiles_m * pl.tiles_c, cap = cu_count() & ~7;
-    // Whole rounds of tiles run whole; the rest of the last round is split along the contraction so
-    // that it fills the CUs.  A step takes about 1 us; a slice costs its partial sums' round trip
-    // (8 bytes per element, counted at 2.5 TB/s) and the second launch.
-    pl.T_dp = T;
-    pl.S = 1;
-    const int r = T % cap;
-    if (r) {
-        const double step = 1.0e-6, rows = (double)(M < BM ? M : BM);
-        double best = pl.nt * step;
-        for (int S = 2; S <= MAX_SPLIT && pl.nt / S >= 2; ++S) {
-            const double rounds = (double)((r * S + cap - 1) / cap);
-            const double t = rounds * ((pl.nt + S - 1) / S) * step + (double)r * S * rows * BC * 8.0 / 2.5e12 + 4e-6;
-            if (t < best) {
-                best = t;
-                pl.T_dp = T - r;
-                pl.S = S;
-            }
-        }
-    }
-    // at most 1024 chunks of rows, 64 rows at least
-    int64_t rows = (M + 1023) / 1024;
-    rows = rows < 64 ? 64 : (rows + 7) / 8 * 8;
-    pl.rows = (int)rows;
+    tile_plan(pl, M);
+    const int rows = prep_rows(M, true);
     pl.chunks = (int)((M + rows - 1) / rows);
     pl.a_bytes = round256((size_t)M * (size_t)pl.lda * 2);
     pl.sum_bytes = round256((size_t)pl.chunks * (size_t)N * (gated ? 8 : 4));
-    pl.part_bytes = pl.S > 1 ? (size_t)(T - pl.T_dp) * pl.S * BM * BC * 4 : 0;
+    pl.part_bytes = pl.S > 1 ? (size_t)(pl.tiles_m * pl.tiles_c - pl.T_dp) * pl.S * pl.bm * BC * 4 : 0;
     return pl;
 }
 
 } // namespace
 
-size_t grad_workspace_bytes(int64_t M, int64_t N, int K, bool gated)
+size_t grad_workspace_bytes(int64_t M, int64_t N, int K, bool gated, bool a_given)
 {
     if (M <= 0 || N <= 0) return 0;
     const Plan pl = make_plan(M, N, K, gated);
-    return pl.a_bytes + pl.sum_bytes + pl.part_bytes;
+    return (a_given ? 0 : pl.a_bytes + pl.sum_bytes) + pl.part_bytes;
 }
 
 hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
@@ -564,48 +803,53 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
     if (g.N <= 0) return hipSuccess;
     const Plan pl = make_plan(g.M, g.N, g.K, gated);
     uint8_t *ws = static_cast<uint8_t *>(g.ws);
-    float *sums = reinterpret_cast<float *>(ws + pl.a_bytes);
-    const bool bias = g.db1 || g.db2;
-    if (g.M > 0) {
-        PrepParams q;
-        q.dy = g.dy;
-        q.pre = g.pre;
-        q.sw1 = g.sw1;
-        q.sw2 = g.sw2;
-        q.a = reinterpret_cast<uint16_t *>(ws);
-        q.sums = bias ? sums : nullptr;
-        q.M = g.M;
-        q.N = g.N;
-        q.Np = pl.Np;
-        q.lda = pl.lda;
-        q.act = g.act;
-        q.col_blocks = (int)((pl.Np + 255) / 256);
-        q.rows = pl.rows;
-        const dim3 grid((unsigned)q.col_blocks * (unsigned)pl.chunks);
-        const bool vec = g.N % 8 == 0;
-        if (gated && vec) hipLaunchKernelGGL((grad_prep_kernel<true, true>), grid, dim3(256), 0, stream, q);
-        else if (gated) hipLaunchKernelGGL((grad_prep_kernel<true, false>), grid, dim3(256), 0, stream, q);
-        else if (vec) hipLaunchKernelGGL((grad_prep_kernel<false, true>), grid, dim3(256), 0, stream, q);
-        else hipLaunchKernelGGL((grad_prep_kernel<false, false>), grid, dim3(256), 0, stream, q);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    for (int which = 0; which < 2; ++which) {
-        float *db = which ? g.db2 : g.db1;
-        if (!db) continue;
-        hipLaunchKernelGGL(grad_bias_kernel, dim3((unsigned)((g.N + 255) / 256)), dim3(256), 0, stream, sums,
-                           g.M > 0 ? pl.chunks : 0, which, gated ? 2 : 1, g.N, db);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    const size_t part_at = g.a ? 0 : pl.a_bytes + pl.sum_bytes;
+    if (!g.a) {
+        float *sums = reinterpret_cast<float *>(ws + pl.a_bytes);
+        const bool bias = g.db1 || g.db2;
+        if (g.M > 0) {
+            PrepParams q;
+            q.dy = g.dy;
+            q.pre = g.pre;
+            q.sw1 = g.sw1;
+            q.sw2 = g.sw2;
+            q.a = reinterpret_cast<uint16_t *>(ws);
+            q.sums = bias ? sums : nullptr;
+            q.M = g.M;
+            q.N = g.N;
+            q.Np = pl.Np;
+            q.lda = pl.lda;
+            q.act = g.act;
+            q.col_blocks = (int)((pl.Np + 255) / 256);
+            q.rows = prep_rows(g.M, bias);
+            const int64_t blocks = (g.M + q.rows - 1) / q.rows * q.col_blocks;
+            if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+            const dim3 grid((unsigned)blocks);
+            const bool vec = g.N % 8 == 0;
+            if (gated && vec) hipLaunchKernelGGL((grad_prep_kernel<true, true>), grid, dim3(256), 0, stream, q);
+            else if (gated) hipLaunchKernelGGL((grad_prep_kernel<true, false>), grid, dim3(256), 0, stream, q);
+            else if (vec) hipLaunchKernelGGL((grad_prep_kernel<false, true>), grid, dim3(256), 0, stream, q);
+            else hipLaunchKernelGGL((grad_prep_kernel<false, false>), grid, dim3(256), 0, stream, q);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        for (int which = 0; which < 2; ++which) {
+            float *db = which ? g.db2 : g.db1;
+            if (!db) continue;
+            hipLaunchKernelGGL(grad_bias_kernel, dim3((unsigned)((g.N + 255) / 256)), dim3(256), 0, stream, sums,
+                               g.M > 0 ? pl.chunks : 0, which, gated ? 2 : 1, g.N, db);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
     }
     if (g.M <= 0) return hipSuccess;
     GradParams p;
-    p.a = reinterpret_cast<const uint16_t *>(ws);
+    p.a = g.a ? g.a : reinterpret_cast<const uint16_t *>(ws);
     p.w1 = g.wq1;
     p.w2 = gated ? g.wq2 : g.wq1;
     p.add = g.add;
     p.dx = g.dx;
-    p.part = reinterpret_cast<float *>(ws + pl.a_bytes + pl.sum_bytes);
+    p.part = reinterpret_cast<float *>(ws + part_at);
     p.lda = pl.lda;
     p.M = (int)g.M;
     p.N = (int)g.N;
@@ -613,16 +857,20 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
     p.lg = g.log2g;
     p.nt1 = pl.nt1;
     p.nt = pl.nt;
+    p.bm = pl.bm;
     p.tiles_m = pl.tiles_m;
     p.tiles_c = pl.tiles_c;
     p.T_dp = pl.T_dp;
     p.S = pl.S;
+    p.next = g.next;
     p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g)));
     const int T = pl.tiles_m * pl.tiles_c, U = pl.T_dp + (T - pl.T_dp) * pl.S;
-    hipLaunchKernelGGL(grad_gemm_kernel, dim3((unsigned)((U + 7) & ~7)), dim3(NTHREADS), 0, stream, p);
+    const dim3 grid((unsigned)((U + 7) & ~7));
+    if (pl.bm == 64) hipLaunchKernelGGL(grad_tile_kernel, grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(grad_gemm_kernel, grid, dim3(NTHREADS), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.S == 1) return e;
-    const int rb = (int)((g.M < BM ? g.M : BM) + 7) / 8;
+    const int rb = (int)((g.M < pl.bm ? g.M : pl.bm) + 7) / 8;
     hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)(T - pl.T_dp) * (unsigned)rb), dim3(256), 0, stream, p, rb);
     return hipGetLastError();
 }

@@ -66,6 +66,14 @@ hipError_t launch_gemv_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
 //   dz = dy act'(pre)  (pre null: dy);   gate/up: dg = dy u act'(g), du = dy act(g), pre = [g; u]
 //   dx = bf16((sum_n dz sw wq) R + add),  db = column sums of dz (fp32; null: not computed)
 // ws: grad_workspace_bytes(M, N, K, gated) bytes, 256-byte aligned.  M == 0 still writes db.
+// next.a: instead of dx, the gradient through a gated product whose h this launch's input was:
+// [M, 2 K] bf16, dg sw_gate then du sw_up, from pre = [g; u] ([2, M, K]) and dh = bf16(the gradient).
+struct GradNext {
+    const uint16_t *pre = nullptr;
+    const float *sw_gate = nullptr, *sw_up = nullptr;
+    uint16_t *a = nullptr;
+    int act = 0;
+};
 struct GradArgs {
     const uint16_t *dy = nullptr, *pre = nullptr;
     int64_t M = 0, N = 0;
@@ -75,9 +83,12 @@ struct GradArgs {
     const uint16_t *add = nullptr;
     uint16_t *dx = nullptr;
     float *db1 = nullptr, *db2 = nullptr;
+    const uint16_t *a = nullptr;          // the operand as a previous launch's `next` wrote it: dy, pre
+                                          // and the scales are not read, no db
+    GradNext next;
     void *ws = nullptr;
 };
-size_t grad_workspace_bytes(int64_t M, int64_t N, int K, bool gated);
+size_t grad_workspace_bytes(int64_t M, int64_t N, int K, bool gated, bool a_given = false);
 hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream);
 
 // W4A4: y = bf16(sum_g acc_g * sx[m,g] * sw[n,g] + bias[n]) with packed int4 operands and
