@@ -7,9 +7,9 @@
 // contraction over their stacked rows.  Three steps:
 //   1. grad_prep_kernel: dz from the incoming gradient, the saved pre-activations and the activation's
 //      slope; a[m,n] = bf16(dz sw) for the matrix core, fp32 column sums of dz for db.
-//   2. grad_gemm_kernel: a . wq with v_mfma_f32_16x16x32_bf16.  The codes are integers up to 127 in
-//      magnitude, exact in bf16, so a's rounding (2^-8 of each term at most, what bf16 training
-//      rounds its gradients to anyway) is the only one before the fp32 sums.
+//   2. grad_gemm_kernel: a . wq with v_mfma_f32_16x16x32_bf16.  The codes are exact in bf16, so a's
+//      rounding (2^-8 of each term at most, what bf16 training rounds its gradients to anyway) is the
+//      only one before the fp32 sums.
 //   3. the rotation, dx_add and the one rounding to bf16: in the GEMM's epilogue (a tile spans 256
 //      channels, whole groups), or in grad_join_kernel where tiles are split along n.
 #include "activation.hpp"
@@ -20,6 +20,20 @@
 namespace convrot {
 namespace {
 
+// Codes as bf16 without a conversion (grad_tile_kernel).  The 16 bits 0x00uu are the bf16 number uu * 2^-133 for
+// every byte uu (below 128 a denormal, from 128 on the first binade, which continues the same grid; the
+// matrix core takes bf16 denormals as they are).  With u = q + 128 (the code's byte with its top bit
+// flipped), two codes become one register with a single byte permute, and
+//   sum_n a q = 2^133 sum_n a (u 2^-133) - 128 sum_n a.
+// The second sum is taken from the operand itself (two values per v_dot2_f32_bf16) and subtracted in fp32.
+// a carries a factor 2^80 in both kernels, so that these products stay in fp32's normal range: |dz sw| has
+// to be below 2^47 (1.4e14), and sums keep full precision above 2^-73 (1e-22).
+constexpr float kOperandScale = 0x1p80f;
+constexpr float kOffset = 0x1p-126f;          // 128 * 2^-133
+constexpr float kTileUnscale = 0x1p53f;       // 2^133 / 2^80
+
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) v2i lds_v2i;
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
 
 constexpr int BM = 256, BC = 256;             // tokens and channels of a tile
@@ -31,7 +45,7 @@ constexpr int NTHREADS = 512;
 constexpr int MAX_SPLIT = 64;
 
 struct GradParams {
-    const uint16_t *a;         // [M, lda] bf16; columns [0, 64 nt1) the first weight's, then the second's
+    const uint16_t *a;         // [M, lda] bf16 times 2^80; columns [0, 64 nt1) the first weight's, then the second's
     const int8_t *w1, *w2;     // [N, K]
     const uint16_t *add;       // dx_add [M, K] or null
     uint16_t *dx;              // [M, K]
@@ -42,51 +56,49 @@ struct GradParams {
     int bm;                    // tokens per tile, 256 or 64
     int tiles_m, tiles_c;
     int T_dp, S;               // whole tiles, then the rest in S slices each
-    float norm;                // 2^(-lg / 2)
+    float norm;                // 2^(-lg / 2), and the operands' scales taken back
     GradNext next;             // next.a non-null: the gated product's gradient goes there, not to dx
 };
 
-// N channels c .. of token m, rotated but not yet normalised, to where the launch puts them:
+// 8 channels c .. of token m, rotated but not yet normalised, to where the launch puts them:
 //   dx = bf16(v norm + add), or, for the hidden gradient of a gated block, dh = bf16(v norm) and on to
 //   both operands of the next contraction, bf16(dh u act'(g) sw_gate) and bf16(dh act(g) sw_up), which
 //   saves writing dh and reading it back in a pass of its own.
-// (N channels are 2 N bytes: one load or store each; K % 64 == 0, so all exist.)
-template <int N>
-__device__ __forceinline__ void finish(const GradParams &p, int m, int c, float (&v)[N])
+// (16 bytes each; K % 64 == 0, so all 8 exist.)
+__device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float (&v)[8])
 {
-    typedef uint32_t vec __attribute__((ext_vector_type(N / 2)));
-    auto load = [](const uint16_t *src, float (&to)[N]) {
-        const vec d = *reinterpret_cast<const vec *>(src);
+    auto load = [](const uint16_t *src, float (&to)[8]) {
+        const v4u d = *reinterpret_cast<const v4u *>(src);
 #pragma unroll
-        for (int e = 0; e < N; ++e) to[e] = e & 1 ? bf16hi_to_f32(d[e >> 1]) : bf16lo_to_f32(d[e >> 1]);
+        for (int e = 0; e < 8; ++e) to[e] = e & 1 ? bf16hi_to_f32(d[e >> 1]) : bf16lo_to_f32(d[e >> 1]);
     };
-    auto store = [](uint16_t *dst, const float (&from)[N]) {
-        vec d;
+    auto store = [](uint16_t *dst, const float (&from)[8]) {
+        v4u d;
 #pragma unroll
-        for (int e = 0; e < N / 2; ++e) d[e] = pack_bf16x2(from[2 * e], from[2 * e + 1]);
-        *reinterpret_cast<vec *>(dst) = d;
+        for (int e = 0; e < 4; ++e) d[e] = pack_bf16x2(from[2 * e], from[2 * e + 1]);
+        *reinterpret_cast<v4u *>(dst) = d;
     };
     const int64_t o = (int64_t)m * p.K + c;
     if (!p.next.a) {
-        float add[N] = {};
+        float add[8] = {};
         if (p.add) load(p.add + o, add);
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = __builtin_fmaf(v[e], p.norm, add[e]);
+        for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], p.norm, add[e]);
         store(p.dx + o, v);
         return;
     }
-    float g[N], u[N], slope[N];
+    float g[8], u[8], slope[8];
     load(p.next.pre + o, g);
     load(p.next.pre + (int64_t)p.M * p.K + o, u);
     act_values_slopes(g, slope, p.next.act);
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
+    for (int e = 0; e < 8; e += 2) {
         const uint32_t d = pack_bf16x2(v[e] * p.norm, v[e + 1] * p.norm);
         const float d0 = bf16lo_to_f32(d), d1 = bf16hi_to_f32(d);
-        u[e] = d0 * u[e] * slope[e] * p.next.sw_gate[c + e];
-        u[e + 1] = d1 * u[e + 1] * slope[e + 1] * p.next.sw_gate[c + e + 1];
-        g[e] = d0 * g[e] * p.next.sw_up[c + e];
-        g[e + 1] = d1 * g[e + 1] * p.next.sw_up[c + e + 1];
+        u[e] = d0 * u[e] * slope[e] * (p.next.sw_gate[c + e] * kOperandScale);
+        u[e + 1] = d1 * u[e + 1] * slope[e + 1] * (p.next.sw_gate[c + e + 1] * kOperandScale);
+        g[e] = d0 * g[e] * (p.next.sw_up[c + e] * kOperandScale);
+        g[e + 1] = d1 * g[e + 1] * (p.next.sw_up[c + e + 1] * kOperandScale);
     }
     uint16_t *a = p.next.a + (int64_t)m * 2 * p.K + c;       // K % 64 == 0: no padding between the two
     store(a, u);
@@ -335,7 +347,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) grad_gemm_kernel(GradParams p)
         }
     }
     // 128 tokens (32 of each token range) a round, rows of 1 KiB with 16-byte chunk c at c ^ row % 16;
-    // then 32 threads per token, 8 channels each.  (The loop is rolled: finish() appears twice, with 64
+    // then 32 threads per token, 8 channels each.  (The loop is rolled: finish8() appears twice, with 64
     // accumulators live; unrolled over the accumulators' 16-token blocks it spilled 185 registers.)
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
@@ -362,20 +374,72 @@ __global__ void __launch_bounds__(NTHREADS, 1) grad_gemm_kernel(GradParams p)
                 for (int e = 0; e < 4; ++e)
                     v[4 * q + e] = lg <= 7 ? own[e] : cc & 16 ? other[e] - own[e] : own[e] + other[e];
             }
-            finish<8>(p, m, c, v);
+            finish8(p, m, c, v);
         }
     }
 }
 
-// The same for 64 tokens x 256 channels, for batches whose 256-token tiles would not fill the GPU or
-// would mostly compute padding: 256 threads, 80 KiB of LDS, two workgroups per CU.  Each of the 4
-// wavefronts takes 64 channels of all 64 tokens.  A step is short here against the latency of its
-// loads, so both operands go through registers, loaded three steps ahead of their use into two sets
-// (steps alternate between them; the loop runs an even number of steps, one past the end adds zeros).
+// 16 bytes per lane, global -> LDS (lane l to byte lds + 16 l).  Written out because the compiler, which knows the
+// builtin to write LDS, waits for every such load in flight before each transposing read: one load latency
+// a step.  The kernel's own s_waitcnt and barrier order the two.  It has no output register, and a load the
+// compiler issues itself is only waited for longer than it counts.  (Nothing else in the kernel uses m0.)
+__device__ __forceinline__ void dma16(v4u rsrc, uint32_t lds, uint32_t off, uint32_t soff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(rsrc), "s"(soff)
+                 : "memory");
+}
+
+// Transposing LDS read: of each 16 lanes, lane 2 r and 2 r + 1 name the two 8-byte halves of row r's 16 bytes,
+// and lane c gets byte c of the 8 rows.  (Not a template, like the two below: the host pass drops a kernel
+// template whose dependent code uses gfx950-only builtins.)
+__device__ __forceinline__ v2i read_transposed(const uint8_t *p)
+{
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(const_cast<uint8_t *>(p)));
+}
+
+// 8 codes of one channel to 8 bf16 numbers u 2^-133.
+__device__ __forceinline__ v8bf16 codes_to_bf16(v2i raw)
+{
+    const uint32_t lo = (uint32_t)raw[0] ^ 0x80808080u, hi = (uint32_t)raw[1] ^ 0x80808080u;
+    const v4u d = {__builtin_amdgcn_perm(0u, lo, 0x0c010c00u), __builtin_amdgcn_perm(0u, lo, 0x0c030c02u),
+                   __builtin_amdgcn_perm(0u, hi, 0x0c010c00u), __builtin_amdgcn_perm(0u, hi, 0x0c030c02u)};
+    return __builtin_bit_cast(v8bf16, d);
+}
+
+// s + the 8 values of v.
+__device__ __forceinline__ float add8(v8bf16 v, float s)
+{
+    const v4u d = __builtin_bit_cast(v4u, v);
+    const v2bf16 one = __builtin_bit_cast(v2bf16, 0x3f803f80u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t pair = d[i];                      // (a bit cast of d[i] itself takes d[0])
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf16, pair), one, s, false);
+    }
+    return s;
+}
+
+// The same for 64 tokens x 256 channels, for batches whose 256-token tiles would not fill the GPU or would mostly
+// compute padding: 256 threads, 72 KiB of LDS, two workgroups per CU; each of the 4 wavefronts takes 64
+// channels of all 64 tokens.  A step is short here against everything that is done once per step, so the
+// codes go to LDS as they are, both operands without passing registers, in three stages with two in
+// flight; a transposing read and the permute above make the fragments.
+//   codes   64 rows of 256 bytes as in memory, 16-byte chunk c of row n at c ^ n % 16, so that the rows
+//           of a transposing read (16 lanes: 8 rows x 16 bytes) fall on distinct banks;
+//   tokens  rows of 128 bytes (64 values), chunk c of row r at c ^ swz(r).
+// One barrier a step: it publishes the next stage and frees this one, which is refilled behind it.
+// (Against this kernel with the 256-token one's conversion through registers, us: 300 tokens 5376 x 2688 38 / 33,
+// 2688 x 2 * 5376 54 / 46; 512 tokens 5120 x 5120 62 / 52.  In 256-token tiles each wavefront would convert the
+// codes of 128 channels that three others convert too, and that one loses: 736 us against 682 at 4096 tokens,
+// 5376 x 16128.)
 __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 {
-    constexpr int TM = 64, WB = 256 * 128, TSTAGE = WB + TM * 128;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * TSTAGE];
+    constexpr int TM = 64, NST = 3;
+    constexpr int WB = BN * BC, TSTAGE = WB + TM * BN * 2;   // codes, then tokens
+    constexpr int XL = 2, WL = 4;                        // loads per step and wavefront
+    __shared__ __attribute__((aligned(16))) uint8_t smem[NST * TSTAGE];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int T = p.tiles_m * p.tiles_c, U = p.T_dp + (T - p.T_dp) * p.S;
@@ -394,83 +458,128 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
     tile_coords(tile, p.tiles_m, p.tiles_c, tm, tc);
     const int m0 = tm * TM, c0 = tc * BC;
 
-    // tokens: row 8 (4 i + w) + lane / 8, 16-byte chunk lane % 8
-    uint32_t offx[2];
+    // tokens: instruction i of wave w fills rows 8 (4 i + w) .. + 7 (lane -> row + lane / 8, position lane % 8);
+    // codes: rows 4 (4 i + w) .. + 3 (lane -> row + lane / 16, position lane % 16)
+    uint32_t offx[XL], offw[WL];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < XL; ++i) {
         const int r = 8 * (4 * i + w) + (lane >> 3);
-        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * (lane & 7)) : OOB;
+        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz(r))) : OOB;
     }
+#pragma unroll
+    for (int i = 0; i < WL; ++i) {
+        const int n = 4 * (4 * i + w) + (lane >> 4), c = 16 * ((lane & 15) ^ (n & 15));
+        offw[i] = c0 + c < K ? (uint32_t)(n * K + c) : OOB;
+    }
+    // The load side: the next step to issue, its codes' address and the rows left there, all in scalar
+    // registers.  Rows past N lie past the descriptor's end and read zeros, as everything past the last
+    // step does.
     const uint64_t xbase = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
-    const uint32_t offw = c0 + 4 * lane < K ? (uint32_t)(16 * w * K + 4 * lane) : OOB;
-    struct Set {
-        uint32_t w[16];
-        v4u x[2];
-    };
-    Set set0, set1;
-    auto load = [&](int t, Set &to) {
-        const int second = t >= p.nt1;
-        const int n0 = (t - (second ? p.nt1 : 0)) * BN;
-        const uint64_t base = reinterpret_cast<uint64_t>((second ? p.w2 : p.w1) + (int64_t)(t < ke ? n0 : 0) * K + c0);
-        const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(base, NUM_RECORDS), rx = uniform_rsrc(xbase, NUM_RECORDS);
-        const int rem = t < ke ? p.N - n0 - 16 * w : 0;
-        const uint32_t past = t < ke ? 0u : OOB;
-        const int k0 = __builtin_amdgcn_readfirstlane((t < ke ? t : 0) * (BN * 2));
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(const lds_void *)smem + (uint32_t)w * 1024u;
+    int ld_t = kb, ld_rows = p.N - (kb - (kb >= p.nt1 ? p.nt1 : 0)) * BN;
+    uint64_t ld_w = reinterpret_cast<uint64_t>((kb >= p.nt1 ? p.w2 : p.w1) +
+                                               (int64_t)(kb - (kb >= p.nt1 ? p.nt1 : 0)) * BN * K + c0);
+    uint32_t ld_lds = lds0;
+    auto issue = [&]() {
+        const int records = ld_t >= ke ? 0 : ld_rows >= BN ? NUM_RECORDS : ld_rows * K - c0;
+        const v4u rw = {(uint32_t)ld_w, (uint32_t)(ld_w >> 32) & 0xffffu, (uint32_t)records, 0x00020000u};
+        const v4u rx = {(uint32_t)xbase, (uint32_t)(xbase >> 32) & 0xffffu, ld_t < ke ? (uint32_t)NUM_RECORDS : 0u,
+                        0x00020000u};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) to.x[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, offx[i] | past, k0, 0);
+        for (int i = 0; i < WL; ++i) dma16(rw, ld_lds + 4096 * i, offw[i], 0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            to.w[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rw, offw | (i < rem ? 0u : OOB), i * K, 0);
-    };
-    auto store = [&](int t, const Set &from) {
-        uint8_t *stage = smem + ((t - kb) & 1) * TSTAGE;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 8 * (4 * i + w) + (lane >> 3);
-            *reinterpret_cast<v4u *>(stage + WB + r * 128 + 16 * ((lane & 7) ^ swz(r))) = from.x[i];
+        for (int i = 0; i < XL; ++i) dma16(rx, ld_lds + WB + 4096 * i, offx[i], (uint32_t)ld_t * (BN * 2));
+        ++ld_t;
+        ld_rows -= BN;
+        ld_w += (uint64_t)(BN * K);
+        if (ld_t == p.nt1) {
+            ld_rows = p.N;
+            ld_w = reinterpret_cast<uint64_t>(p.w2 + c0);
         }
-        transpose_to_lds(from.w, stage, lane, 2 * w);
-        transpose_to_lds(from.w + 8, stage, lane, 2 * w + 1);
+        ld_lds = ld_lds == lds0 + (NST - 1) * TSTAGE ? lds0 : ld_lds + TSTAGE;
     };
+
+    // codes: rows 32 kk + 8 fq + i / 2 for lane (fq, i), half i % 2 of chunk 4 w + b
     const int frow = lane & 15, fq = lane >> 4;
+    const int key = 8 * (fq & 1) + (frow >> 1);
+    int awhere[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        awhere[b] = (8 * fq + (frow >> 1)) * BC + 16 * ((4 * w + b) ^ key) + 8 * (frow & 1);
+    const int bwhere = WB + frow * 128;
+    const int bpos[2] = {16 * (fq ^ swz(frow)), 16 * ((4 + fq) ^ swz(frow))};
+    v2i raw[2][4];
+    v8bf16 fb[2][4];
+    auto read_codes = [&](int stage, int kk) {
+        const uint8_t *st = smem + stage * TSTAGE + kk * (32 * BC);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) raw[kk][b] = read_transposed(st + awhere[b]);
+    };
+    auto read_tokens = [&](int stage, int kk) {
+        const uint8_t *st = smem + stage * TSTAGE + bwhere + bpos[kk];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) fb[kk][b] = *reinterpret_cast<const v8bf16 *>(st + b * 2048);
+    };
     v4f acc[4][4];
+    float asum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int b = 0; b < 4; ++b) acc[a][b] = v4f{};
-    auto step = [&](int t, Set &next) {
-        const uint8_t *st = smem + ((t - kb) & 1) * TSTAGE;
+    auto mfma_range = [&](int kk, int a0, int a1) {
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            const int pos = (4 * kk + fq) ^ swz(frow);
-            v8bf16 fa[4], fb[4];
+        for (int a = a0; a < a1; ++a) {
+            const v8bf16 fa = codes_to_bf16(raw[kk][a]);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                fa[b] = *reinterpret_cast<const v8bf16 *>(st + (64 * w + 16 * b + frow) * 128 + 16 * (pos ^ (b & 1)));
-                fb[b] = *reinterpret_cast<const v8bf16 *>(st + WB + (16 * b + frow) * 128 + 16 * pos);
-            }
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[b], acc[a][b], 0, 0, 0);
+            for (int b = 0; b < 4; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, fb[kk][b], acc[a][b], 0, 0, 0);
         }
-        store(t + 1, next);
-        load(t + 3, next);
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+        for (int b = 0; b < (a0 ? 0 : 4); ++b) asum[b] = add8(fb[kk][b], asum[b]);
     };
-    load(kb, set0);
-    load(kb + 1, set1);
-    store(kb, set0);
-    load(kb + 2, set0);
-    __syncthreads();
-    for (int t = kb; t < ke; t += 2) {
-        step(t, set1);
-        step(t + 1, set0);
+    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+
+    issue();
+    issue();
+    issue();
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * (XL + WL)));
+    asm volatile("s_barrier" ::: "memory");
+    read_codes(0, 0);
+    read_tokens(0, 0);
+    int st = 0;                                          // this step's stage
+    for (int t = kb; t < ke; ++t) {
+        const int next = st == NST - 1 ? 0 : st + 1;
+        read_codes(st, 1);
+        read_tokens(st, 1);
+        mfma_range(0, 0, 4);
+        fence();
+        mfma_range(1, 0, 1);
+        fence();
+        // the next step has landed: only the one after it is still in flight
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(XL + WL));
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        issue();
+        read_codes(next, 0);
+        read_tokens(next, 0);
+        mfma_range(1, 1, 4);
+        fence();
+        st = next;
     }
+    // every load into LDS has landed and every wave is done reading before the epilogue reuses it
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
 
-    // lane: token lane % 16 of block b; channels 64 w + 16 a + 4 (lane / 16) + v
+    // lane: token lane % 16 of block b (all of its sum over the four fq), channels
+    // 16 (4 w + a) + 4 fq + v
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        asum[b] += __shfl_xor(asum[b], 16);
+        asum[b] += __shfl_xor(asum[b], 32);
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[a][b][v] = __builtin_fmaf(asum[b], -kOffset, acc[a][b][v]);
+    }
     if (slot >= 0) {
         float *dst = p.part + (int64_t)slot * (TM * BC);
 #pragma unroll
@@ -479,13 +588,13 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
             if (m0 + ml < p.M) {
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
-                    *reinterpret_cast<v4f *>(dst + ml * BC + 64 * w + 16 * a + 4 * fq) = acc[a][b];
+                    *reinterpret_cast<v4f *>(dst + ml * BC + 16 * (4 * w + a) + 4 * fq) = acc[a][b];
             }
         }
         return;
     }
-    // the rotation as in the kernel above: channel bits 0, 1 in v, 2, 3 across lanes, 4, 5 in a; 6 and 7
-    // across the four waves
+    // the rotation as in the kernel above: channel bits 0, 1 in v, 2, 3 across lanes, 4, 5 in a; 6 and 7 across the
+    // four waves
     const int lg = p.lg;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -531,41 +640,34 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
             }
         }
     }
-    // 16 tokens a round, in two buffers in turn: a thread takes one token's channels 4 cc .. + 3 of all
-    // four quarters
+    // through LDS, rows of 1 KiB with 16-byte chunk c at c ^ row % 16; then 32 threads per token, 8 channels each
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        uint8_t *buf = smem + (b & 1) * 16384;
+    for (int b = 0; b < 4; ++b)
 #pragma unroll
         for (int a = 0; a < 4; ++a)
-            *reinterpret_cast<v4f *>(buf + frow * 1024 + 16 * ((16 * w + 4 * a + fq) ^ frow)) = acc[a][b];
-        __syncthreads();
-        const int r = (int)threadIdx.x >> 4, cc = (int)threadIdx.x & 15;
-        const int m = m0 + 16 * b + r;
-        if (m >= p.M) continue;
-        v4f v[4];
+            *reinterpret_cast<v4f *>(smem + (16 * b + frow) * 1024 + 16 * ((4 * (4 * w + a) + fq) ^ frow)) = acc[a][b];
+    __syncthreads();
+    const int cc = (int)threadIdx.x & 31, c = c0 + 8 * cc;
+#pragma unroll 1
+    for (int it = 0; it < 8; ++it) {
+        const int row = 8 * it + ((int)threadIdx.x >> 5), m = m0 + row;
+        if (m >= p.M || c >= K) continue;
+        float v[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const v4f *>(buf + r * 1024 + 16 * ((16 * q + cc) ^ r));
-        if (lg > 6) {
-            const v4f x = v[0], y = v[2];
-            v[0] = x + v[1];
-            v[1] = x - v[1];
-            v[2] = y + v[3];
-            v[3] = y - v[3];
-        }
-        if (lg > 7) {
-            const v4f x = v[0], y = v[1];
-            v[0] = x + v[2];
-            v[2] = x - v[2];
-            v[1] = y + v[3];
-            v[3] = y - v[3];
-        }
+        for (int q = 0; q < 2; ++q) {
+            auto chunk = [&](int flip) {
+                return *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * (((2 * cc + q) ^ flip) ^ (row & 15)));
+            };
+            v4f x = chunk(0);
+            if (lg > 6) x = cc & 8 ? chunk(16) - x : x + chunk(16);
+            if (lg > 7) {
+                const v4f y = cc & 8 ? chunk(48) - chunk(32) : chunk(32) + chunk(48);
+                x = cc & 16 ? y - x : x + y;
+            }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int c = c0 + 64 * q + 4 * cc;
-            float out[4] = {v[q][0], v[q][1], v[q][2], v[q][3]};
-            if (c < K) finish<4>(p, m, c, out);
+            for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
         }
+        finish8(p, m, c, v);
     }
 }
 
@@ -612,7 +714,7 @@ __global__ void __launch_bounds__(256) grad_join_kernel(GradParams p, int rb)
                 v[e] = (l >> b) & 1 ? o - v[e] : v[e] + o;
             }
         }
-    if (row_ok && c < p.K) finish<8>(p, m, c, v);
+    if (row_ok && c < p.K) finish8(p, m, c, v);
 }
 
 struct PrepParams {
@@ -639,8 +741,8 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(PrepParams p)
     float s1[8], s2[8], sum1[8], sum2[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        s1[e] = n + e < p.N ? p.sw1[n + e] : 0.0f;
-        s2[e] = GATED && n + e < p.N ? p.sw2[n + e] : 0.0f;
+        s1[e] = n + e < p.N ? p.sw1[n + e] * kOperandScale : 0.0f;
+        s2[e] = GATED && n + e < p.N ? p.sw2[n + e] * kOperandScale : 0.0f;
         sum1[e] = sum2[e] = 0.0f;
     }
     auto load8 = [&](const uint16_t *base, int64_t m, float (&v)[8]) {
@@ -746,7 +848,7 @@ size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 void tile_plan(Plan &pl, int64_t M)
 {
     double best = 1e30;
-    for (int bm = 64; bm <= BM; bm *= 4) {
+    for (int bm = 64; bm <= 256; bm *= 4) {
         const int64_t tiles = (M + bm - 1) / bm * pl.tiles_c;
         if (tiles >= (int64_t)1 << 24) continue;
         const int T = (int)tiles, cap = (cu_count() & ~7) * (bm == 64 ? 2 : 1);
@@ -863,7 +965,7 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
     p.T_dp = pl.T_dp;
     p.S = pl.S;
     p.next = g.next;
-    p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g)));
+    p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g))) * (pl.bm == 64 ? kTileUnscale : 1.0f / kOperandScale);
     const int T = pl.tiles_m * pl.tiles_c, U = pl.T_dp + (T - pl.T_dp) * pl.S;
     const dim3 grid((unsigned)((U + 7) & ~7));
     if (pl.bm == 64) hipLaunchKernelGGL(grad_tile_kernel, grid, dim3(256), 0, stream, p);

@@ -3,7 +3,8 @@ differences of the forward calls, and in the ways a training loop calls them.
 
 Bounds.  With act none the matrix core's operand a = bf16(dz sw) is reproduced exactly (one fp32
 product, one rounding), so dx is off by fp32 sums alone: at most (N + 16) u of the sum of the absolute
-terms, then the bf16 rounding.  With an activation a's rounding (2^-8 of a term at most, uniform:
+terms, then the bf16 rounding.  The terms are a (q + 128), of which 128 sum(a) is taken back, itself a sum of
+N terms: |a| (|q| + 256) bounds both.  With an activation a's rounding (2^-8 of a term at most, uniform:
 2^-8 / sqrt 3 in the mean square) is independent over the terms, so it reaches dx with the same
 relative mean square, and the output's own rounding adds another: 0.82 * 2^-8 of |dx| together,
 held to 2^-8 in the 2-norm.  The slopes' fp32 errors are below 2^-18 for the inputs used here and vanish in that."""
@@ -75,7 +76,7 @@ def test_linear_backward_exact_operand(cr, M, N, K, g):
     a = (dy.float() * ws).bfloat16()
     q = _np(wq)
     ref = R.rotate(_np(a) @ q, g)
-    terms = R.rotate_abs(np.abs(_np(a)) @ np.abs(q), g)
+    terms = R.rotate_abs(np.abs(_np(a)) @ (np.abs(q) + 256), g)
     bound = (N + 16) * R.U * terms
     R.check(_np(dx), ref, R.rounded(ref, bound), "dx")
     dx2, db = cr.linear_act_backward(dy, wq, ws, group=g, dx_add=add, bias_grad=True)
