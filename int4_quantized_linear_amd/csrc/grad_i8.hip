@@ -842,23 +842,32 @@ struct Plan {
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// Tokens per tile and slices of the contraction, by estimated time.  Whole rounds of tiles run whole; the
-// rest of the last round may be split so that it fills the GPU.  Slices cost their partial sums' round
-// trip (8 bytes per element, counted at 2.5 TB/s) and the second launch.
-void tile_plan(Plan &pl, int64_t M)
+// Tokens per tile and slices of the contraction, by a model with measured constants.  Whole rounds of tiles run
+// whole; the rest of the last round may be split so that it fills the GPU.  A step takes 1.6 us of a CU in
+// 256-token tiles; in 64-token ones 0.72 us alone and 0.54 us when workgroups share the CU.  The codes stream at
+// 4.9 TB/s.  Slices cost their partial sums' round trip (8 bytes per element at 4.5 TB/s) and a launch.
+// Measured (us; K x N, 2 N for gate|up, all launches of the call), 256 tokens unsliced / in the best slices / 64
+// tokens unsliced / in the best slices:
+//   12 tokens 5120 x 8192: 178 / 28 / 84 / 20;      300 tokens 2688 x 2 * 5376: 241 / 56 / 118 / 48
+//   512 tokens 5120 x 5120: 131 / 54 / 67 / 53;    1024 tokens: 140 / 82 / 104 / 95
+void tile_plan(Plan &pl, int64_t M, int64_t N, int K, bool gated)
 {
+    const int cus = cu_count() & ~7;
+    const double stream = (double)N * K * (gated ? 2.0 : 1.0) / 4.9e12;
     double best = 1e30;
-    for (int bm = 64; bm <= 256; bm *= 4) {
+    for (int bm = 64; bm <= BM; bm *= 4) {
         const int64_t tiles = (M + bm - 1) / bm * pl.tiles_c;
         if (tiles >= (int64_t)1 << 24) continue;
-        const int T = (int)tiles, cap = (cu_count() & ~7) * (bm == 64 ? 2 : 1);
-        const double step = bm == 64 ? 1.0e-6 : 1.1e-6, rows = (double)(M < bm ? M : bm);
-        const int r = T % cap;
+        // 64 tokens: two workgroups per CU
+        const int T = (int)tiles, cap = cus * (bm == 64 ? 2 : 1), r = T % cap;
+        const double lone = bm == 64 ? 0.72e-6 : 1.6e-6, shared = bm == 64 ? 0.54e-6 : 1.6e-6;
         for (int S = 1; S <= (r ? MAX_SPLIT : 1); ++S) {
             if (S > 1 && pl.nt / S < 2) break;
-            const double rounds = (double)((r * S + cap - 1) / cap);
-            const double t = ((double)(T / cap) * pl.nt + rounds * ((pl.nt + S - 1) / S)) * step +
-                             (S > 1 ? (double)r * S * rows * BC * 8.0 / 2.5e12 + 4e-6 : 0.0);
+            const double per_cu = (double)(((int64_t)r * S + cus - 1) / cus) * shared;
+            const double math = (double)(T / cap) * (cap / cus) * pl.nt * shared +
+                                (r ? (double)((pl.nt + S - 1) / S) * (per_cu > lone ? per_cu : lone) : 0.0);
+            const double rows = (double)(M < bm ? M : bm);
+            const double t = (math > stream ? math : stream) + (S > 1 ? (double)r * S * rows * BC * 8.0 / 4.5e12 + 2e-6 : 0.0);
             if (t < best) {
                 best = t;
                 pl.bm = bm;
@@ -870,9 +879,9 @@ void tile_plan(Plan &pl, int64_t M)
     }
 }
 
-// Rows of a grad_prep workgroup: 8, one per thread, where no bias gradient needs its column sums.  With
-// one, a multiple of 8 that gives at most about 64 chunks of partial sums to add up.
-int prep_rows(int64_t M, bool bias) { return bias && M > 512 ? (int)((M + 511) / 512 * 8) : 8; }
+// Rows of a grad_prep workgroup: 8, one per thread, up to 512 tokens, and a multiple of 8 that gives at most about
+// 64 chunks beyond (2048 x 5120: 10 us, against 22 with 8 rows; and few partial column sums to add up).
+int prep_rows(int64_t M) { return M > 512 ? (int)((M + 511) / 512 * 8) : 8; }
 
 Plan make_plan(int64_t M, int64_t N, int K, bool gated)
 {
@@ -882,8 +891,8 @@ Plan make_plan(int64_t M, int64_t N, int K, bool gated)
     pl.nt1 = (int)(pl.Np / BN);
     pl.nt = (int)(pl.lda / BN);
     pl.tiles_c = (K + BC - 1) / BC;
-    tile_plan(pl, M);
-    const int rows = prep_rows(M, true);
+    tile_plan(pl, M, N, K, gated);
+    const int rows = prep_rows(M);
     pl.chunks = (int)((M + rows - 1) / rows);
     pl.a_bytes = round256((size_t)M * (size_t)pl.lda * 2);
     pl.sum_bytes = round256((size_t)pl.chunks * (size_t)N * (gated ? 8 : 4));
@@ -923,7 +932,7 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
             q.lda = pl.lda;
             q.act = g.act;
             q.col_blocks = (int)((pl.Np + 255) / 256);
-            q.rows = prep_rows(g.M, bias);
+            q.rows = prep_rows(g.M);
             const int64_t blocks = (g.M + q.rows - 1) / q.rows * q.col_blocks;
             if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
             const dim3 grid((unsigned)blocks);
