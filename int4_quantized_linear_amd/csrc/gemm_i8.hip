@@ -812,7 +812,11 @@ struct SplitPlan {
 // element of the tail and slice, counted at 2.5 TB/s: each unit's int32 stores leave in a burst at
 // its end, and a q|k|v-shaped tail of 64 tiles in 3 slices measured no faster than whole) and the
 // second launch.  A split is planned only if it saves at least 5% of the estimated GEMM time.
-SplitPlan plan_split(int64_t M, int64_t N, int K, int nf)
+// The fused epilogues plan with constants measured on weights that come from memory, as a layer's do, rather than
+// from the last-level cache: a K-tile takes 1.62 us also when few CUs run, and the partial sums move at 4.5
+// TB/s.  (2048 x 25600 x 5120, 160 tiles: 325 us whole, 286 in 3 slices, which the plain constants
+// decline; 1024 tokens: 327 whole, 146 in 3.)
+SplitPlan plan_split(int64_t M, int64_t N, int K, int nf, bool fused)
 {
     const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + nf - 1) / nf;
     const int64_t T = tiles_m * tiles_n;
@@ -822,7 +826,7 @@ SplitPlan plan_split(int64_t M, int64_t N, int K, int nf)
     // only the 16-byte-store variant (N % 8 == 0) has the partial-sum epilogue
     if (r == 0 || N % 8 != 0 || T >= ((int64_t)1 << 30)) return pl;
     const int KT = (K + BK - 1) / BK;
-    const double t_full = 1.84e-6, t_fast = 1.38e-6;
+    const double t_full = 1.84e-6, t_fast = fused ? 1.62e-6 : 1.38e-6, part_rate = fused ? 4.5e12 : 2.5e12;
     const double rows = (double)(M < BM ? M : BM);
     auto tail_time = [&](int S) {
         const double power = (double)r * KT * t_full / cap;
@@ -833,7 +837,7 @@ SplitPlan plan_split(int64_t M, int64_t N, int K, int nf)
     const double whole = (double)full * KT * t_full + tail_time(1);
     double best = tail_time(1);
     for (int S = 2; S <= MAX_SPLIT && KT / S >= 2; ++S) {
-        const double t = tail_time(S) + (double)(r * S) * rows * BN * 8.0 / 2.5e12 + 4e-6;
+        const double t = tail_time(S) + (double)(r * S) * rows * BN * 8.0 / part_rate + 4e-6;
         if (t < best && tail_time(1) - t >= 0.05 * whole) {
             best = t;
             pl = {(int)(full * cap), S, (size_t)(r * S) * BM * BN * sizeof(int32_t)};
@@ -853,22 +857,22 @@ double gemm_i8_seconds(int64_t M, int64_t N, int K, bool gated, bool split)
     const int64_t T = ((M + BM - 1) / BM) * ((N + nf - 1) / nf);
     const int cap = grid_capacity(), KT = (K + BK - 1) / BK;
     SplitPlan pl = {(int)T, 1, 0};
-    if (split) pl = plan_split(M, N, K, nf);
+    if (split) pl = plan_split(M, N, K, nf, true);
     const int64_t r = T % cap, full = T / cap;
-    const double t_full = 1.84e-6, t_fast = 1.38e-6;
+    const double t_full = 1.84e-6, t_fast = 1.62e-6;
     const double power = (double)r * KT * t_full / cap;
     const double clock = (double)((r * pl.S + cap - 1) / cap) * ((double)KT / pl.S) * t_fast;
     const double tail = power > clock ? power : clock;
-    const double joined = pl.S > 1 ? (double)r * pl.S * (double)(M < BM ? M : BM) * BN * 8.0 / 2.5e12 + 4e-6 : 0.0;
+    const double joined = pl.S > 1 ? (double)r * pl.S * (double)(M < BM ? M : BM) * BN * 8.0 / 4.5e12 + 4e-6 : 0.0;
     const double math = (double)full * KT * t_full + tail + joined;
     const double stream = (double)N * K * (gated ? 2.0 : 1.0) / 3.4e12;
     return (math > stream ? math : stream) + 8e-6;
 }
 
-size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K, bool gated)
+size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K, bool fused, bool gated)
 {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
-    return plan_split(M, N, K, gated ? tile_features<Epi::Gated>() : BN).bytes;
+    return plan_split(M, N, K, gated ? tile_features<Epi::Gated>() : BN, fused).bytes;
 }
 
 namespace {
@@ -909,7 +913,7 @@ hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
     // split-K tail (not for the int32 sums, and only with room for the partial sums)
     SplitPlan pl = {T, 1, 0};
     if (epi != Epi::Int32 && part) {
-        pl = plan_split(M, N, K, nf);
+        pl = plan_split(M, N, K, nf, epi != Epi::Bf16);
         if (pl.S > 1 && part_bytes < pl.bytes) pl = {T, 1, 0};
     }
     p.part = static_cast<int32_t *>(part);

@@ -313,7 +313,7 @@ TilePlan plan_gemm_i8_tile(int64_t M, int64_t N, int K, bool gated, bool split)
 {
     TilePlan best;
     double t_best = gemm_i8_seconds(M, N, K, gated, split);
-    best.part_bytes = split ? gemm_i8_split_bytes(M, N, K, gated) : 0;
+    best.part_bytes = split ? gemm_i8_split_bytes(M, N, K, true, gated) : 0;
     const int KT = (K + BK - 1) / BK;
     const double cols = (double)N * (gated ? 2.0 : 1.0);
     const double stream = cols * K / 4.9e12;

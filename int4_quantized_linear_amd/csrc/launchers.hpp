@@ -41,7 +41,7 @@ hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
                           void *y, Epi epi, int64_t M, int64_t N, int K, void *part, size_t part_bytes,
                           hipStream_t stream, const FusedEpi &fused = FusedEpi());
 // Bytes of `part` the split-K tail uses for this shape on the current device (0: no split).
-size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K, bool gated = false);
+size_t gemm_i8_split_bytes(int64_t M, int64_t N, int K, bool fused = false, bool gated = false);
 // Estimated seconds of launch_gemm_i8's fused epilogues, with or without `part`, for the choice below.
 double gemm_i8_seconds(int64_t M, int64_t N, int K, bool gated, bool split);
 
