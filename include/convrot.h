@@ -147,8 +147,8 @@ int convrot_linear(const void *x, int x_dtype, const int8_t *xq, const float *x_
  * All other arguments are convrot_linear's, and so are the workspace's rules with
  * convrot_workspace_bytes_act(M, N, K) bytes; with act NONE and no residual the outputs are its
  * outputs bit for bit.  For M > 16 the tiles and slices of K are chosen by size; they never change the
- * outputs.  residual may be y itself (added in place); any other overlap of y, pre and
- * residual returns CONVROT_ERR_OVERLAP.  residual, pre: 16-byte aligned.
+ * outputs.  residual may be y itself (added in place); any other overlap of y, pre, residual and
+ * xq returns CONVROT_ERR_OVERLAP.  residual, pre: 16-byte aligned.
  */
 int convrot_linear_act(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,
                        int64_t K, int group, const int8_t *wq, const float *w_scale, const float *bias, int act,
@@ -218,10 +218,10 @@ size_t convrot_workspace_bytes_ffn(int64_t M, int64_t F, int64_t K);
  *   dbias fp32 [N] or NULL.  The gradient of the residual is dy.
  * The products run on the bf16 matrix core: the codes are exact in bf16, and rounding dz * w_scale to
  * bf16 is the only rounding before the fp32 sums.  Sums are taken in a fixed order: the same call
- * gives the same bits.
+ * gives the same bits.  |dz * w_scale| must be below 2^47 (1.4e14): the kernels carry it times 2^80.
  *   M == 0: dbias is zeros.  N == 0 or K out of range: CONVROT_ERR_SHAPE (there is no gradient to
- *   form).  N < CONVROT_BACKWARD_MAX_N.  dx overlapping dx_add (other than dx == dx_add) or dbias:
- *   CONVROT_ERR_OVERLAP.
+ *   form).  N < CONVROT_BACKWARD_MAX_N.  An overlap of dx, dx_add and dbias other than dx == dx_add:
+ *   CONVROT_ERR_OVERLAP.  dx may be dy's own buffer.
  * workspace: convrot_workspace_bytes_backward(M, N, K) bytes, 256-byte aligned, required; scratch.
  */
 int convrot_linear_act_backward(const void *dy, const void *pre, int64_t M, int64_t N, int64_t K, int group,

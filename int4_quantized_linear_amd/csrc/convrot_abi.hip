@@ -255,6 +255,9 @@ int linear_i8(const char *who, const void *x, int x_dtype, const int8_t *xq, con
     if ((f.residual != y && overlap(f.residual, out_bytes, y, out_bytes)) || overlap(f.pre, pre_bytes, y, out_bytes) ||
         overlap(f.pre, pre_bytes, f.residual, out_bytes))
         return fail(CONVROT_ERR_OVERLAP, "%s: an output overlaps pre or residual (only residual == y is allowed)", who);
+    if (!x && epi != convrot::Epi::Bf16 &&
+        (overlap(xq, (size_t)M * (size_t)K, y, out_bytes) || overlap(xq, (size_t)M * (size_t)K, f.pre, pre_bytes)))
+        return fail(CONVROT_ERR_OVERLAP, "%s: an output overlaps xq", who);
     const WsLayout L = ws_layout(M, N, K, 8, epi);
     if (scratch_fn && x && workspace_bytes < L.part)
         return fail(CONVROT_ERR_WORKSPACE, "%s: M*K = %lld needs %zu bytes of scratch; the fixed scratch holds %zu "
@@ -347,7 +350,8 @@ int check_grad(const char *who, const convrot::GradArgs &g, int64_t K, int group
         return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
     const size_t dx_bytes = (size_t)g.M * (size_t)K * 2, db_bytes = (size_t)g.N * 4;
     if ((g.add != g.dx && overlap(g.add, dx_bytes, g.dx, dx_bytes)) || overlap(g.db1, db_bytes, g.dx, dx_bytes) ||
-        overlap(g.db2, db_bytes, g.dx, dx_bytes) || overlap(g.db1, db_bytes, g.db2, db_bytes))
+        overlap(g.db2, db_bytes, g.dx, dx_bytes) || overlap(g.db1, db_bytes, g.db2, db_bytes) ||
+        overlap(g.db1, db_bytes, g.add, dx_bytes) || overlap(g.db2, db_bytes, g.add, dx_bytes))
         return fail(CONVROT_ERR_OVERLAP, "%s: outputs overlap each other or dx_add (only dx_add == dx is allowed)", who);
     const size_t need = convrot::grad_workspace_bytes(g.M, g.N, (int)K, gated);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
@@ -626,6 +630,12 @@ int convrot_ffn_gated_backward(const void *dy, const void *pre, int64_t M, int64
     up.db2 = dup_bias;
     if ((rc = check_grad(who, up, K, group, true, workspace, L.steps_dh))) return rc;
     if ((rc = check_grad(who, down, F, group_h, false, workspace, L.steps_dh))) return rc;
+    const size_t dx_bytes = (size_t)M * (size_t)K * 2;
+    if (overlap(ddown_bias, (size_t)K * 4, dx, dx_bytes) || overlap(ddown_bias, (size_t)K * 4, dx_add, dx_bytes) ||
+        overlap(ddown_bias, (size_t)K * 4, dgate_bias, (size_t)F * 4) ||
+        overlap(ddown_bias, (size_t)K * 4, dup_bias, (size_t)F * 4) ||
+        overlap(ddown_bias, (size_t)K * 4, pre, (size_t)M * (size_t)F * 4))
+        return fail(CONVROT_ERR_OVERLAP, "%s: ddown_bias overlaps another array of the call", who);
     if (!sums) {
         down.next.pre = up.pre;
         down.next.sw_gate = gate_scale;

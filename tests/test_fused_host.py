@@ -48,7 +48,7 @@ CASES += [("convrot_linear_act", act_args(**kw), s) for kw, s in [
     (dict(wq=None), "NULL"), (dict(sw=None), "NULL"), (dict(y=None), "NULL"), (dict(y=MIS), "ALIGN"),
     (dict(bias=MIS - 1), "ALIGN"), (dict(res=MIS), "ALIGN"), (dict(res=D + 512), "OVERLAP"),
     (dict(res=D - 512), "OVERLAP"), (dict(res=G, pre=G), "OVERLAP"), (dict(N=1 << 24), "SHAPE"),
-    (dict(x=None, xq=A), "NULL")]]
+    (dict(x=None, xq=A), "NULL"), (dict(x=None, xq=D, xs=C), "OVERLAP"), (dict(x=None, xq=G, xs=C, pre=G), "OVERLAP")]]
 CASES += [("convrot_linear_gated", gated_args(**kw), s) for kw, s in [
     (dict(wu=None), "NULL"), (dict(su=None), "NULL"), (dict(wg=None), "NULL"), (dict(sg=None), "NULL"),
     (dict(h=None), "NULL"), (dict(wu=MIS), "ALIGN"), (dict(bu=MIS - 1), "ALIGN"),
@@ -85,13 +85,16 @@ CASES += [(n, f(**kw), s) for n, f in BACKWARD for kw, s in [
     (dict(dx=MIS), "ALIGN"), (dict(add=MIS), "ALIGN"), (dict(add=D + 256), "OVERLAP"), (dict(ws=None), "WORKSPACE"),
     (dict(ws=E + 16), "WORKSPACE"), (dict(wsb=100), "WORKSPACE")]]
 CASES += [("convrot_linear_act_backward", bwd_args(**kw), s) for kw, s in [
-    (dict(wq=None), "NULL"), (dict(sw=None), "NULL"), (dict(db=MIS - 1), "ALIGN"), (dict(db=D + 16), "OVERLAP")]]
+    (dict(wq=None), "NULL"), (dict(sw=None), "NULL"), (dict(db=MIS - 1), "ALIGN"), (dict(db=D + 16), "OVERLAP"),
+    (dict(db=H + 16, add=H), "OVERLAP")]]
 CASES += [("convrot_linear_gated_backward", gated_bwd_args(**kw), s) for kw, s in [
     (dict(wu=None), "NULL"), (dict(su=None), "NULL"), (dict(db1=H, db2=H + 512), "OVERLAP"), (dict(db2=D), "OVERLAP"),
     (dict(act=0, pre=None), "NULL")]]
 CASES += [("convrot_ffn_gated_backward", ffn_bwd_args(**kw), s) for kw, s in [
     (dict(wd=None), "NULL"), (dict(sd=None), "NULL"), (dict(wu=None), "NULL"), (dict(group_h=7), "GROUP"),
-    (dict(N=320, group_h=128), "SHAPE"), (dict(N=100), "SHAPE"), (dict(db3=MIS - 1), "ALIGN")]]
+    (dict(N=320, group_h=128), "SHAPE"), (dict(N=100), "SHAPE"), (dict(db3=MIS - 1), "ALIGN"),
+    (dict(db3=D), "OVERLAP"), (dict(db3=H, db1=H + 256), "OVERLAP"), (dict(db3=H, db2=H), "OVERLAP"),
+    (dict(db3=G), "OVERLAP"), (dict(db3=H, add=H), "OVERLAP")]]
 
 
 @pytest.mark.parametrize("i", range(len(CASES)))
@@ -102,29 +105,36 @@ def test_refusals(lib, i):
     assert rc == ERR["CONVROT_ERR_" + status] and name in msg, (name, args, rc, msg)
 
 
-@pytest.mark.parametrize("name,args", [
+# calls that pass every check and stop at the missing device
+VALID = [
     ("convrot_linear_act", act_args()), ("convrot_linear_act", act_args(res=D)),
     ("convrot_linear_act", act_args(M=4, N=1 << 24)),
     ("convrot_linear_act", act_args(x=None, xq=A, xs=C, ws=None, wsb=0, res=G, pre=H)),
+    ("convrot_linear_gated", gated_args(pre=G, bg=C, bu=C)), ("convrot_ffn_gated", ffn_args(res=D, pre=G)),
     ("convrot_linear_act_backward", bwd_args(act=0, pre=None)), ("convrot_linear_act_backward", bwd_args(add=D, db=H)),
+    ("convrot_linear_act_backward", bwd_args(M=0, db=H)),
     ("convrot_linear_gated_backward", gated_bwd_args(db1=H, db2=H + 1024)),
     ("convrot_ffn_gated_backward", ffn_bwd_args(add=A, db1=H, db2=H + 1024, db3=H + 2048)),
-    ("convrot_ffn_gated_backward", ffn_bwd_args(dx=A, add=A)),
-    ("convrot_linear_act_backward", bwd_args(M=0, db=H)),
-    ("convrot_linear_gated", gated_args(pre=G, bg=C, bu=C)), ("convrot_ffn_gated", ffn_args(res=D, pre=G))])
+    ("convrot_ffn_gated_backward", ffn_bwd_args(dx=A, add=A))]
+EMPTY = [
+    ("convrot_linear_act", (None, 1, None, None, 0, 256, 512, 256, *[None] * 3, 0, *[None] * 4, 0, None)),
+    ("convrot_linear_act", (None, 1, None, None, 5, 0, 512, 256, *[None] * 3, 0, *[None] * 4, 0, None)),
+    ("convrot_linear_gated", (None, 1, None, None, 0, 256, 512, 256, *[None] * 6, 2, None, None, None, 0, None)),
+    ("convrot_ffn_gated", (None, 1, 0, 256, 512, 256, 256, *[None] * 9, 2, *[None] * 4, 0, None)),
+    ("convrot_linear_act_backward", (None, None, 0, 256, 512, 256, None, None, 2, *[None] * 4, 0, None)),
+    ("convrot_linear_gated_backward", (None, None, 0, 256, 512, 256, *[None] * 4, 2, *[None] * 5, 0, None)),
+    ("convrot_ffn_gated_backward", (None, None, 0, 256, 512, 256, 256, *[None] * 6, 2, *[None] * 6, 0, None))]
+
+
+@pytest.mark.parametrize("name,args", VALID)
 def test_valid_calls_reach_the_device(lib, name, args):
     assert getattr(lib, name)(*args) == ERR["CONVROT_ERR_HIP"], lib.convrot_last_error().decode()
     assert "hipGetDevice" in lib.convrot_last_error().decode()
 
 
-def test_empty_inputs(lib):
-    assert lib.convrot_linear_act(None, 1, None, None, 0, 256, 512, 256, *[None] * 3, 0, *[None] * 4, 0, None) == 0
-    assert lib.convrot_linear_act(None, 1, None, None, 5, 0, 512, 256, *[None] * 3, 0, *[None] * 4, 0, None) == 0
-    assert lib.convrot_linear_gated(None, 1, None, None, 0, 256, 512, 256, *[None] * 6, 2, None, None, None, 0, None) == 0
-    assert lib.convrot_ffn_gated(None, 1, 0, 256, 512, 256, 256, *[None] * 9, 2, *[None] * 4, 0, None) == 0
-    assert lib.convrot_linear_act_backward(None, None, 0, 256, 512, 256, None, None, 2, *[None] * 4, 0, None) == 0
-    assert lib.convrot_linear_gated_backward(None, None, 0, 256, 512, 256, *[None] * 4, 2, *[None] * 5, 0, None) == 0
-    assert lib.convrot_ffn_gated_backward(None, None, 0, 256, 512, 256, 256, *[None] * 6, 2, *[None] * 6, 0, None) == 0
+@pytest.mark.parametrize("name,args", EMPTY)
+def test_empty_inputs(lib, name, args):
+    assert getattr(lib, name)(*args) == 0
 
 
 def test_backward_workspace_queries(lib):

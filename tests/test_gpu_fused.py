@@ -192,6 +192,24 @@ def test_large_and_extreme_values(cr):
             R.check(_np(y), ref, bound, act)
 
 
+def test_offsets_past_32_bits(cr):
+    """More than 2^31 outputs, through the GEMM and through the decode kernel: the last columns and tokens against
+    the same ones alone."""
+    K = 64
+    for M, N in ((300, 8000008), (16, 140000008)):
+        wq = torch.randint(-127, 128, (N, K), dtype=torch.int8, device=DEV)
+        ws = torch.rand(N, device=DEV) * 1e-3
+        xq, xs = cr.quantize_act(_tokens(M, K, 1), 64, 8)
+        y = cr.linear_act(None, wq, ws, act="silu", group=64, xq=xq, x_scale=xs)
+        tail = cr.linear_act(None, wq[-264:].clone(), ws[-264:].clone(), act="silu", group=64, xq=xq, x_scale=xs)
+        assert torch.equal(y[:, -264:], tail)
+        h = cr.linear_gated(None, wq, ws, wq, ws, act="relu", group=64, xq=xq, x_scale=xs)
+        tail = cr.linear_gated(None, wq[-264:].clone(), ws[-264:].clone(), wq[-264:].clone(), ws[-264:].clone(), act="relu",
+                               group=64, xq=xq, x_scale=xs)
+        assert torch.equal(h[:, -264:], tail)
+        del y, h
+
+
 def test_empty_batches(cr):
     gate, up, down = _weight(cr, 128, 64, 64, 1), _weight(cr, 128, 64, 64, 2), _weight(cr, 64, 128, 128, 3)
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)

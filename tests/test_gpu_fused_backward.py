@@ -62,7 +62,9 @@ def _slope_bound(z, act):
 # tile, several, none (g = 1), a last tile that is half empty
 SHAPES = [(1, 1, 64, 64), (1, 4096, 256, 256), (3, 65, 320, 64), (16, 520, 512, 2), (33, 1001, 2688, 128),
           (130, 264, 192, 1), (255, 63, 64, 16), (257, 136, 640, 32), (300, 2000, 1024, 256), (600, 72, 1280, 8),
-          (64, 192, 384, 4)]
+          (64, 192, 384, 4),
+          # 256-token tiles: whole, a sliced last round, all sliced (the sizes above run 64-token tiles, whole and sliced)
+          (1728, 65, 4864, 256), (1729, 64, 4864, 32), (3328, 384, 5120, 128), (2752, 3008, 1536, 256)]
 
 
 @pytest.mark.parametrize("M,N,K,g", SHAPES)
@@ -139,7 +141,8 @@ def test_linear_gated_backward(cr, M, N, K, g, act):
     assert torch.equal(cr.linear_gated_backward(dh, pre, *gate, *up, act=act, group=g, dx_add=add), dx)
 
 
-@pytest.mark.parametrize("M,K,F", [(1, 64, 64), (12, 512, 1344), (100, 2688, 1024), (260, 320, 640), (1, 5120, 2560)])
+@pytest.mark.parametrize("M,K,F", [(1, 64, 64), (12, 512, 1344), (100, 2688, 1024), (260, 320, 640), (1, 5120, 2560),
+                                   (1728, 64, 4864), (3328, 384, 5120), (2752, 3008, 1536)])
 def test_training_step(cr, M, K, F):
     """Forward with saved pre-activations, then the backward pass: one call is the two calls, and the
     chain is the formula's."""
@@ -204,6 +207,34 @@ def test_empty_batch_and_no_channels(cr):
     with pytest.raises(cr.ConvRotError, match="SHAPE"):
         none = (torch.empty((0, 64), dtype=torch.int8, device=DEV), torch.empty(0, device=DEV))
         cr.linear_act_backward(torch.empty((3, 0), dtype=torch.bfloat16, device=DEV), *none, group=64)
+
+
+def test_offsets_past_32_bits(cr):
+    """dy and the operand hold more than 2^31 elements; the last tokens are checked against the same tokens alone
+    (another tile choice: equal up to the order of fp32 sums)."""
+    M, N, K = 2100, 1048568, 64
+    wq = torch.randint(-127, 128, (N, K), dtype=torch.int8, device=DEV)
+    ws = torch.rand(N, device=DEV) * 1e-3
+    dy = torch.randn(M, N, device=DEV, dtype=torch.bfloat16)
+    dx, db = cr.linear_act_backward(dy, wq, ws, group=64, bias_grad=True)
+    few, _ = cr.linear_act_backward(dy[-5:].clone(), wq, ws, group=64)
+    _norm_check(_np(dx[-5:]), _np(few), "last tokens", 2 * R.BF16)
+    cols = dy[:, -8:].double().sum(0)
+    bound = (M + 8) * R.U * dy[:, -8:].double().abs().sum(0)
+    assert ((db[-8:].double() - cols).abs() <= bound).all()
+
+
+def test_extreme_gradients(cr):
+    """Gradients near both ends of the range the operand is carried in, and rows of zeros between them."""
+    M, N, K = 70, 200, 256
+    wq, ws = _weight(cr, N, K, 256, 1)
+    for scale in (1e-15, 1e-8, 1e8, 1e15):
+        dy = (_randn(M, N, seed=3, dtype=torch.float32) * scale).bfloat16()
+        dy[::3] = 0
+        dx, _ = cr.linear_act_backward(dy, wq, ws)
+        ref = R.rotate(_np((dy.float() * ws).bfloat16()) @ _np(wq), 256)
+        _norm_check(_np(dx), ref, "dx at %g" % scale)
+        assert not dx[::3].any()
 
 
 def test_streams_and_graph(cr):
