@@ -41,10 +41,27 @@ struct TileParams {
     FusedEpi f;
 };
 
-// Epilogue of 8 consecutive columns n.. of row m (VEC: N % 8 == 0, all exist and are 16-byte aligned):
-// v the scaled sums of the (gate) weight, u those of up.
+// The residual's 8 columns n.. of row m (zeros where there is none).
 template <Epi E, bool VEC>
-__device__ __forceinline__ void finish8(const TileParams &p, int m, int n, float (&v)[8], float (&u)[8])
+__device__ __forceinline__ v4u residual8(const TileParams &p, int m, int n)
+{
+    v4u d = {};
+    if (E != Epi::Act || !p.f.residual) return d;
+    const uint16_t *src = p.f.residual + (int64_t)m * p.N + n;
+    if constexpr (VEC) {
+        d = *reinterpret_cast<const v4u *>(src);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (n + e < p.N) d[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+    }
+    return d;
+}
+
+// Epilogue of 8 consecutive columns n.. of row m (VEC: N % 8 == 0, all exist and are 16-byte aligned):
+// v the scaled sums of the (gate) weight, u those of up, res the residual.
+template <Epi E, bool VEC>
+__device__ __forceinline__ void finish8(const TileParams &p, int m, int n, float (&v)[8], float (&u)[8], const v4u &res)
 {
     const int64_t o = (int64_t)m * p.N + n;
     auto store = [&](uint16_t *dst, const float (&a)[8]) {
@@ -64,22 +81,9 @@ __device__ __forceinline__ void finish8(const TileParams &p, int m, int n, float
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= u[e];
     } else {
-        float r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (p.f.residual) {
-            const uint16_t *src = p.f.residual + o;
-            if constexpr (VEC) {
-                const v4u d = *reinterpret_cast<const v4u *>(src);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) r[e] = e & 1 ? bf16hi_to_f32(d[e >> 1]) : bf16lo_to_f32(d[e >> 1]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (n + e < p.N) r[e] = bf16lo_to_f32(src[e]);
-            }
-        }
         act_values(v, p.f.act);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += r[e];
+        for (int e = 0; e < 8; ++e) v[e] += e & 1 ? bf16hi_to_f32(res[e >> 1]) : bf16lo_to_f32(res[e >> 1]);
     }
     store(p.y + o, v);
 }
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) gemm_i8_tile_kernel(TileParams p)
             float v[8], u[8];
             z8(ch, s1, b1, v);
             if constexpr (E == Epi::Gated) z8(ch + 4, s2, b2, u);
-            finish8<E, VEC>(p, m, n, v, u);
+            finish8<E, VEC>(p, m, n, v, u, residual8<E, VEC>(p, m, n));
         }
     }
 }
@@ -242,10 +246,16 @@ __global__ void __launch_bounds__(256) tile_reduce_kernel(TileParams p, int rb)
     tile_coords(i, p.tiles_m, p.tiles_n, tm, tn);
     const int m = tm * BM + ml, n = tn * NF + nl;
     if (ml >= BM || m >= p.M || n >= p.N) return;
-    auto sums = [&](int cl, const float *sw, const float *bias, float (&v)[8]) {
+    // everything is requested before the first sum is used: the kernel is one memory latency long
+    const float sxm = p.sx[m];
+    const v4u res = residual8<E, VEC>(p, m, n);
+    float s1[8], b1[8], s2[8], b2[8];
+    columns8<VEC>(p.sw, p.bias, n, p.N, s1, b1);
+    if constexpr (E == Epi::Gated) columns8<VEC>(p.f.sw2, p.f.bias2, n, p.N, s2, b2);
+    auto sums = [&](int cl, const float (&sc)[8], const float (&bi)[8], float (&v)[8]) {
         int32_t sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         const int32_t *src = p.part + (int64_t)i * (BM * BN) + ml * BN + cl;
-#pragma unroll 4
+#pragma unroll 8
         for (int s = 0; s < p.S; ++s, src += (int64_t)T * (BM * BN)) {
             const v4i a = *reinterpret_cast<const v4i *>(src), b = *reinterpret_cast<const v4i *>(src + 4);
 #pragma unroll
@@ -254,17 +264,14 @@ __global__ void __launch_bounds__(256) tile_reduce_kernel(TileParams p, int rb)
                 sum[e + 4] += b[e];
             }
         }
-        float sc[8], bi[8];
-        columns8<VEC>(sw, bias, n, p.N, sc, bi);
-        const float sxm = p.sx[m];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf((float)sum[e], sxm * sc[e], bi[e]);
     };
     const int cl = E == Epi::Gated ? 32 * (nl >> 4) + (nl & 15) : nl;
     float v[8], u[8];
-    sums(cl, p.sw, p.bias, v);
-    if constexpr (E == Epi::Gated) sums(cl + 16, p.f.sw2, p.f.bias2, u);
-    finish8<E, VEC>(p, m, n, v, u);
+    sums(cl, s1, b1, v);
+    if constexpr (E == Epi::Gated) sums(cl + 16, s2, b2, u);
+    finish8<E, VEC>(p, m, n, v, u, res);
 }
 
 template <Epi E, int BM, int NST, bool VEC>
