@@ -63,7 +63,8 @@ typedef enum convrot_status {
 enum { CONVROT_DTYPE_F32 = 0, CONVROT_DTYPE_BF16 = 1 };
 
 /* Activations of the fused linears: z;  max(z, 0);  z / (1 + e^-z);  z Phi(z) with the normal
- * distribution Phi;  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+ * distribution Phi;  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.  At z = -inf and +inf the
+ * last four and their slopes are the limits (0 and inf, 0 and 1), so a bias of -inf masks a channel. */
 enum {
     CONVROT_ACT_NONE = 0,
     CONVROT_ACT_RELU = 1,
@@ -147,8 +148,8 @@ int convrot_linear(const void *x, int x_dtype, const int8_t *xq, const float *x_
  * All other arguments are convrot_linear's, and so are the workspace's rules with
  * convrot_workspace_bytes_act(M, N, K) bytes; with act NONE and no residual the outputs are its
  * outputs bit for bit.  For M > 16 the tiles and slices of K are chosen by size; they never change the
- * outputs.  residual may be y itself (added in place); any other overlap of y, pre, residual and
- * xq returns CONVROT_ERR_OVERLAP.  residual, pre: 16-byte aligned.
+ * outputs.  residual may be y itself (added in place); any other overlap of y, pre, residual,
+ * xq and x_scale returns CONVROT_ERR_OVERLAP.  residual, pre: 16-byte aligned.
  */
 int convrot_linear_act(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,
                        int64_t K, int group, const int8_t *wq, const float *w_scale, const float *bias, int act,
@@ -168,8 +169,8 @@ size_t convrot_workspace_bytes_act(int64_t M, int64_t N, int64_t K);
  *   pre bf16 [2, M, N] or NULL: when given, receives bf16(g), then bf16(u), for
  *   convrot_linear_gated_backward; h is formed from the unrounded g and u.
  * x (or xq, x_scale) and the dispatch by M as in convrot_linear; the workspace is
- * convrot_workspace_bytes_gated(M, N, K) bytes under the same rules.  An overlap of h and pre
- * returns CONVROT_ERR_OVERLAP.
+ * convrot_workspace_bytes_gated(M, N, K) bytes under the same rules.  An overlap of h or pre
+ * with the other, xq or x_scale returns CONVROT_ERR_OVERLAP.
  */
 int convrot_linear_gated(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t M, int64_t N,
                          int64_t K, int group, const int8_t *wq_gate, const float *gate_scale, const float *gate_bias,
@@ -190,6 +191,8 @@ size_t convrot_workspace_bytes_gated(int64_t M, int64_t N, int64_t K);
  *   K % 64 == 0, F % 64 == 0, both in [64, CONVROT_MAX_K] and multiples of their groups.
  *   workspace: convrot_workspace_bytes_ffn(M, F, K) bytes, 256-byte aligned, required (the codes of x
  *   and h, h itself, the partial sums).
+ *   An overlap of y and residual other than y == residual, or of pre with y, residual or x, returns
+ *   CONVROT_ERR_OVERLAP.
  * The result is that of convrot_linear_gated followed by convrot_linear_act, bit for bit.
  */
 int convrot_ffn_gated(const void *x, int x_dtype, int64_t M, int64_t F, int64_t K, int group, int group_h,
@@ -218,7 +221,8 @@ size_t convrot_workspace_bytes_ffn(int64_t M, int64_t F, int64_t K);
  *   dbias fp32 [N] or NULL.  The gradient of the residual is dy.
  * The products run on the bf16 matrix core: the codes are exact in bf16, and rounding dz * w_scale to
  * bf16 is the only rounding before the fp32 sums.  Sums are taken in a fixed order: the same call
- * gives the same bits.  |dz * w_scale| must be below 2^47 (1.4e14): the kernels carry it times 2^80.
+ * gives the same bits.  |dz * w_scale| must be below 2^47 (1.4e14): the kernels carry it times 2^80;
+ * terms below 2^-73 (1e-22) lose precision.
  *   M == 0: dbias is zeros.  N == 0 or K out of range: CONVROT_ERR_SHAPE (there is no gradient to
  *   form).  N < CONVROT_BACKWARD_MAX_N.  An overlap of dx, dx_add and dbias other than dx == dx_add:
  *   CONVROT_ERR_OVERLAP.  dx may be dy's own buffer.

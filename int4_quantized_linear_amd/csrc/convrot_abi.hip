@@ -256,8 +256,9 @@ int linear_i8(const char *who, const void *x, int x_dtype, const int8_t *xq, con
         overlap(f.pre, pre_bytes, f.residual, out_bytes))
         return fail(CONVROT_ERR_OVERLAP, "%s: an output overlaps pre or residual (only residual == y is allowed)", who);
     if (!x && epi != convrot::Epi::Bf16 &&
-        (overlap(xq, (size_t)M * (size_t)K, y, out_bytes) || overlap(xq, (size_t)M * (size_t)K, f.pre, pre_bytes)))
-        return fail(CONVROT_ERR_OVERLAP, "%s: an output overlaps xq", who);
+        (overlap(xq, (size_t)M * (size_t)K, y, out_bytes) || overlap(xq, (size_t)M * (size_t)K, f.pre, pre_bytes) ||
+         overlap(x_scale, (size_t)M * 4, y, out_bytes) || overlap(x_scale, (size_t)M * 4, f.pre, pre_bytes)))
+        return fail(CONVROT_ERR_OVERLAP, "%s: an output overlaps xq or x_scale", who);
     const WsLayout L = ws_layout(M, N, K, 8, epi);
     if (scratch_fn && x && workspace_bytes < L.part)
         return fail(CONVROT_ERR_WORKSPACE, "%s: M*K = %lld needs %zu bytes of scratch; the fixed scratch holds %zu "

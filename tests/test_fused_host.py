@@ -48,7 +48,8 @@ CASES += [("convrot_linear_act", act_args(**kw), s) for kw, s in [
     (dict(wq=None), "NULL"), (dict(sw=None), "NULL"), (dict(y=None), "NULL"), (dict(y=MIS), "ALIGN"),
     (dict(bias=MIS - 1), "ALIGN"), (dict(res=MIS), "ALIGN"), (dict(res=D + 512), "OVERLAP"),
     (dict(res=D - 512), "OVERLAP"), (dict(res=G, pre=G), "OVERLAP"), (dict(N=1 << 24), "SHAPE"),
-    (dict(x=None, xq=A), "NULL"), (dict(x=None, xq=D, xs=C), "OVERLAP"), (dict(x=None, xq=G, xs=C, pre=G), "OVERLAP")]]
+    (dict(x=None, xq=A), "NULL"), (dict(x=None, xq=D, xs=C), "OVERLAP"), (dict(x=None, xq=G, xs=C, pre=G), "OVERLAP"),
+    (dict(x=None, xq=A, xs=D + 64), "OVERLAP"), (dict(x=None, xq=A, xs=G + 4, pre=G), "OVERLAP")]]
 CASES += [("convrot_linear_gated", gated_args(**kw), s) for kw, s in [
     (dict(wu=None), "NULL"), (dict(su=None), "NULL"), (dict(wg=None), "NULL"), (dict(sg=None), "NULL"),
     (dict(h=None), "NULL"), (dict(wu=MIS), "ALIGN"), (dict(bu=MIS - 1), "ALIGN"),
