@@ -5,7 +5,11 @@
 // silu(z) = z s(z) and the tanh form of gelu, z (1 + tanh v) / 2 = z s(2v), share the logistic
 // s(t) = 1 / (1 + e^-t), taken as one v_exp_f32 and one v_rcp_f32 (1 ulp each; e^-t rounds its
 // argument once, so the relative error is about |t| 2^-24 + 3 ulp, far below the bf16 the result is
-// rounded to).  At t -> -inf, e^-t is infinite and s is 0; at t -> +inf s is 1: no clamps needed.
+// rounded to).  At t -> -inf, e^-t is infinite and s is 0; at t -> +inf s is 1.
+// At z = -inf (a channel masked through its bias; the lowest fp32 numbers round to it in a bf16 pre) and
+// z = +inf every value and slope is its limit: a factor that would be infinite beside a zero is held
+// at the largest finite number.  Each such min or max stands beside a term that is NaN for a NaN z, so NaN
+// is kept.
 // gelu(z) = max(z, 0) - |z| h(|z|) with h(a) = erfc(a / sqrt 2) / 2 the normal distribution's tail, so
 // its negative side keeps its relative precision.  h(a) = e^(-a^2 / 2) t Q(t) with t = 1 / (1 + 0.28 a):
 // erfcx(a / sqrt 2) / 2 falls like 1 / a, and Q, a polynomial of degree 8 fitted here for the least
@@ -19,6 +23,7 @@ namespace convrot {
 
 constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4;
 
+constexpr float kMax = 3.40282347e38f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhA = 1.59576912160573071f;               // 2 sqrt(2 / pi)
@@ -50,12 +55,12 @@ __device__ __forceinline__ float act_value(float z, int act)
 {
     switch (act) {
     case kActRelu: return z < 0.0f ? 0.0f : z;                // keeps a NaN
-    case kActSilu: return z * logistic(z);
+    case kActSilu: return __builtin_fmaxf(z, -kMax) * logistic(z);
     case kActGelu: {
         float e;
-        return __builtin_fmaf(-__builtin_fabsf(z), normal_tail(z, e), z < 0.0f ? 0.0f : z);
+        return __builtin_fmaf(-__builtin_fminf(__builtin_fabsf(z), kMax), normal_tail(z, e), z < 0.0f ? 0.0f : z);
     }
-    case kActGeluTanh: return z * logistic(z * __builtin_fmaf(kTanhB * z, z, kTanhA));
+    case kActGeluTanh: return __builtin_fmaxf(z, -kMax) * logistic(z * __builtin_fmaf(kTanhB * z, z, kTanhA));
     default: return z;
     }
 }
@@ -81,7 +86,7 @@ __device__ __forceinline__ void act_values(float (&v)[8], int act)
 // act(z) and act'(z) together.
 //   silu': p + z p (1 - p);  gelu': Phi(z) + z phi(z);  gelu_tanh': p + z p (1 - p) (2v)'
 // with 1 - p = s(-t), so nothing cancels.  (2v)' grows as z^2 while p (1 - p) is 0 in fp32 beyond
-// |z| = 10, so the tanh form clamps z there before it could overflow to inf * 0.
+// |z| = 10, and z phi(z) beyond 15, so both hold z there before it could give inf * 0.
 __device__ __forceinline__ void act_value_slope(float z, int act, float &value, float &slope)
 {
     switch (act) {
@@ -91,22 +96,23 @@ __device__ __forceinline__ void act_value_slope(float z, int act, float &value, 
         break;
     case kActSilu: {
         const float p = logistic(z);
-        value = z * p;
-        slope = __builtin_fmaf(value, logistic(-z), p);
+        value = __builtin_fmaxf(z, -kMax) * p;
+        slope = __builtin_fmaf(__builtin_fminf(value, kMax), logistic(-z), p);
         break;
     }
     case kActGelu: {
         float e;
         const float h = normal_tail(z, e);
-        value = __builtin_fmaf(-__builtin_fabsf(z), h, z < 0.0f ? 0.0f : z);
-        slope = __builtin_fmaf(z * kInvSqrt2Pi, e, z < 0.0f ? h : 1.0f - h);
+        value = __builtin_fmaf(-__builtin_fminf(__builtin_fabsf(z), kMax), h, z < 0.0f ? 0.0f : z);
+        const float c = __builtin_fminf(__builtin_fmaxf(z, -16.0f), 16.0f);
+        slope = __builtin_fmaf(c * kInvSqrt2Pi, e, z < 0.0f ? h : 1.0f - h);
         break;
     }
     case kActGeluTanh: {
-        value = z * logistic(z * __builtin_fmaf(kTanhB * z, z, kTanhA));
+        const float p = logistic(z * __builtin_fmaf(kTanhB * z, z, kTanhA));
+        value = __builtin_fmaxf(z, -kMax) * p;
         const float c = __builtin_fminf(__builtin_fmaxf(z, -16.0f), 16.0f);
         const float t = c * __builtin_fmaf(kTanhB * c, c, kTanhA);
-        const float p = logistic(t);
         slope = __builtin_fmaf(c * p * logistic(-t), __builtin_fmaf(3.0f * kTanhB * c, c, kTanhA), p);
         break;
     }

@@ -192,6 +192,27 @@ def test_large_and_extreme_values(cr):
             R.check(_np(y), ref, bound, act)
 
 
+def test_infinite_and_nan_preactivations(cr):
+    """A bias of -inf, of fp32's lowest number or of +inf gives the activation's limit there, and a NaN stays one; the
+    other channels are not touched."""
+    N, K = 264, 256
+    (wq, ws), (up, us) = _weight(cr, N, K, 256, 3), _weight(cr, N, K, 256, 4)
+    b = torch.zeros(N, device=DEV)
+    b[0], b[9], b[18], b[27] = -torch.inf, torch.finfo(torch.float32).min, torch.inf, torch.nan
+    rest = [n for n in range(N) if n not in (0, 9, 18, 27)]
+    for m in (4, 40):
+        x = _tokens(m, K, m)
+        for act in R.ACTS[1:]:
+            y, pre = cr.linear_act(x, wq, ws, b, act=act, save_pre=True)
+            plain = cr.linear_act(x, wq, ws, act=act)
+            assert (y[:, 0] == 0).all() and (y[:, 9] == 0).all() and (y[:, 18] == torch.inf).all(), act
+            assert y[:, 27].isnan().all() and pre[:, 27].isnan().all(), act
+            assert torch.equal(y[:, rest], plain[:, rest]), act
+            h = cr.linear_gated(x, wq, ws, up, us, b, act=act)
+            assert (h[:, 0] == 0).all() and (h[:, 9] == 0).all() and h[:, 27].isnan().all(), act
+            assert torch.equal(h[:, rest], cr.linear_gated(x, wq, ws, up, us, act=act)[:, rest]), act
+
+
 def test_offsets_past_32_bits(cr):
     """More than 2^31 outputs, through the GEMM and through the decode kernel: the last columns and tokens against
     the same ones alone."""

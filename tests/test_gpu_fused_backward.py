@@ -120,6 +120,23 @@ def test_slopes_far_out(cr):
         assert np.abs(db.double().cpu().numpy() - ref).max() < 1e-4, act
 
 
+def test_slopes_at_infinity(cr):
+    """Pre-activations of -inf and +inf (a lowest fp32 number in bf16): slopes 0 and 1; a masked gate passes nothing
+    on to up."""
+    N, K = 264, 256
+    wq, ws = _weight(cr, N, K, 256, 3)
+    pre = _randn(2, N, seed=1)
+    pre[:, 0], pre[:, 9] = -torch.inf, torch.inf
+    dy = torch.ones(2, N, dtype=torch.bfloat16, device=DEV)
+    for act in R.ACTS[1:]:
+        dx, db = cr.linear_act_backward(dy, wq, ws, pre=pre, act=act, bias_grad=True)
+        assert db[0] == 0 and db[9] == 2 and db.isfinite().all() and dx.isfinite().all(), act
+        both = torch.stack([pre, _randn(2, N, seed=2)])
+        both[0, :, 9] = 0
+        dx, dg, du = cr.linear_gated_backward(dy, both, wq, ws, wq, ws, act=act, bias_grad=True)
+        assert dg[0] == 0 and du[0] == 0 and dx.isfinite().all(), act
+
+
 GATED = [(1, 64, 64, 64), (5, 33, 320, 64), (40, 1001, 640, 128), (257, 136, 192, 64), (300, 776, 1024, 256)]
 
 
