@@ -51,6 +51,7 @@ struct GemvParams {
 
 // Gated: the RB blocks alternate gate, up, gate, ...: block b is rows 16 (b / 2) .. of the
 // workgroup's 8 RB features of one weight, so a lane holds the gate and up sums of its features.
+// (2 x 25600 x 5120, 262 MB: 46 us with 1 token, 47 with 12, 5.6 TB/s, the weight stream.)
 template <Epi E>
 __host__ __device__ constexpr int features_per_block() { return E == Epi::Gated ? 8 : 16; }
 
