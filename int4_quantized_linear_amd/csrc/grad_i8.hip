@@ -733,10 +733,9 @@ struct PrepParams {
     int act, col_blocks, rows; // rows per chunk
 };
 
-// A workgroup takes 256 columns and a chunk of rows: 32 lanes of 8 columns, 8 rows at a time.  VEC:
-// N % 8 == 0, 16-byte loads; otherwise rows are not aligned and elements are read one by one.
+// A workgroup takes 256 columns and a chunk of rows: 32 lanes of 8 columns, 8 rows at a time.
 // Columns from N to Np are zeros.  Bound by memory: 4096 x 16128 with an activation 77 us (396 MB, 5.1 TB/s).
-template <bool GATED, bool VEC>
+template <bool GATED>
 __global__ void __launch_bounds__(256) grad_prep_kernel(PrepParams p)
 {
     __shared__ float red[GATED ? 2 : 1][8][256];
@@ -751,11 +750,14 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(PrepParams p)
         s2[e] = GATED && n + e < p.N ? p.sw2[n + e] * kOperandScale : 0.0f;
         sum1[e] = sum2[e] = 0.0f;
     }
+    // 16 bytes at any element: rows of an odd N start at odd ones, which a vector load takes.  (2001 x 14366: 49 us,
+    // element by element 101; 14368 columns 46.)
+    const bool whole = n + 8 <= p.N;
     auto load8 = [&](const uint16_t *base, int64_t m, float (&v)[8]) {
+        typedef v4u unaligned __attribute__((aligned(2)));
         const uint16_t *src = base + m * p.N + n;
-        if constexpr (VEC) {
-            v4u d = v4u{0, 0, 0, 0};
-            if (n < p.N) d = *reinterpret_cast<const v4u *>(src);
+        if (whole) {
+            const v4u d = *reinterpret_cast<const unaligned *>(src);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 v[2 * e] = bf16lo_to_f32(d[e]);
@@ -942,11 +944,8 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
             const int64_t blocks = (g.M + q.rows - 1) / q.rows * q.col_blocks;
             if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
             const dim3 grid((unsigned)blocks);
-            const bool vec = g.N % 8 == 0;
-            if (gated && vec) hipLaunchKernelGGL((grad_prep_kernel<true, true>), grid, dim3(256), 0, stream, q);
-            else if (gated) hipLaunchKernelGGL((grad_prep_kernel<true, false>), grid, dim3(256), 0, stream, q);
-            else if (vec) hipLaunchKernelGGL((grad_prep_kernel<false, true>), grid, dim3(256), 0, stream, q);
-            else hipLaunchKernelGGL((grad_prep_kernel<false, false>), grid, dim3(256), 0, stream, q);
+            if (gated) hipLaunchKernelGGL(grad_prep_kernel<true>, grid, dim3(256), 0, stream, q);
+            else hipLaunchKernelGGL(grad_prep_kernel<false>, grid, dim3(256), 0, stream, q);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
