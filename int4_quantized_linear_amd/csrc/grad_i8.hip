@@ -38,10 +38,6 @@ typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
 
 constexpr int BM = 256, BC = 256;             // tokens and channels of a tile
 constexpr int BN = 64;                        // contraction rows per step
-constexpr int OPB = 256 * BN * 2;             // bytes of one operand per stage (32 KiB)
-constexpr int STAGE = 2 * OPB;                // weights (by channel), then tokens
-constexpr int SMEM = 2 * STAGE;
-constexpr int NTHREADS = 512;
 constexpr int MAX_SPLIT = 64;
 
 struct GradParams {
@@ -118,269 +114,6 @@ __device__ __forceinline__ void swap16f(float &a, float &b)
     auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     a = __uint_as_float(r[0]);
     b = __uint_as_float(r[1]);
-}
-
-// The weights' rows are written 4 apart (a lane's 4 channels), so their position takes row bit 4 too:
-// 8 lanes then write 8 distinct chunks of one 128-byte window.
-__device__ __forceinline__ int swz_w(int row) { return swz(row) ^ ((row >> 4) & 1); }
-
-// Signed byte b of d.
-template <int B>
-__device__ __forceinline__ float byte_f32(uint32_t d)
-{
-    return (float)(int8_t)(d >> (8 * B));
-}
-
-// A step's weights of this wave in LDS order: raw holds 4 channels (4 lane .. + 3) of rows 8 chunk ..
-// 8 chunk + 7; each channel's 8 values become one 16-byte chunk of its row.
-__device__ __forceinline__ void transpose_to_lds(const uint32_t *raw, uint8_t *stage, int lane, int chunk)
-{
-    auto column = [&](auto byte, int j) {
-        const int r = 4 * lane + j;
-        v4u d;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = pack_bf16x2(byte(raw[2 * i]), byte(raw[2 * i + 1]));
-        *reinterpret_cast<v4u *>(stage + r * 128 + 16 * (chunk ^ swz_w(r))) = d;
-    };
-    column([](uint32_t d) { return byte_f32<0>(d); }, 0);
-    column([](uint32_t d) { return byte_f32<1>(d); }, 1);
-    column([](uint32_t d) { return byte_f32<2>(d); }, 2);
-    column([](uint32_t d) { return byte_f32<3>(d); }, 3);
-}
-
-// A 256 x 256 tile (tokens x channels) per workgroup, 8 wavefronts in 2 (channels) x 4 (tokens) of
-// 128 x 64 each: 8 x 4 blocks of 16x16x32, 128 accumulators per lane.  LDS holds two stages of 64
-// contraction rows, both operands with the contraction contiguous (128 bytes per row, 16-byte
-// chunks XOR-swizzled by row so that 16 consecutive rows' reads hit all banks).  The tokens go
-// global -> LDS directly.  The weights are stored the other way round ([n][channel]), so they pass
-// through registers: a lane loads 4 channels of 8 rows (8 dwords, 256 contiguous bytes per row and
-// wavefront), and the conversion to bf16 picks the bytes of one channel together, which is the
-// transposition: 4 chunks of 8 contraction values each.
-// During step g the next step's weights are converted and written, and the loads of the one after
-// are issued; the tokens of step g + 2 are issued once step g's stage is free (after the barrier).
-// 4096 tokens 5376 x 16128: 584 us, 1216 TFLOP/s, matrix core 59% busy at 2.1 GHz, LDS conflict-free (a plain
-// bf16 library product of that shape, operands ready in bf16: 887).  Without the weights' load, conversion
-// and write it takes 148 us less, of which the conversion's arithmetic is 15: the rest is the LDS writes
-// and the load's issue slots.  Tiles of 256 x 256 because the conversion is paid once per tile row.
-__global__ void __launch_bounds__(NTHREADS, 1) grad_gemm_kernel(GradParams p)
-{
-    __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
-    const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wn = w & 1, wm = w >> 1;
-    const int T = p.tiles_m * p.tiles_c, U = p.T_dp + (T - p.T_dp) * p.S;
-    const int K = p.K;
-    // the grid is rounded up to a multiple of 8
-    if ((int)blockIdx.x >= U) return;
-    const int u = unit_of((int)blockIdx.x, p.T_dp, U);
-    int tile = u, kb = 0, ke = p.nt, slot = -1;
-    if (u >= p.T_dp) {
-        const int r = T - p.T_dp, v = u - p.T_dp, sl = v / r;
-        tile = p.T_dp + v % r;
-        kb = (int)((int64_t)sl * p.nt / p.S);
-        ke = (int)((int64_t)(sl + 1) * p.nt / p.S);
-        slot = v;
-    }
-    int tm, tc;
-    tile_coords(tile, p.tiles_m, p.tiles_c, tm, tc);
-    const int m0 = tm * BM, c0 = tc * BC;
-
-    // tokens: instruction i of wave w fills rows 8 (8 i + w) .. + 7; lane -> row + lane / 8,
-    // position lane % 8
-    uint32_t offx[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 8 * (8 * i + w) + (lane >> 3);
-        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz(r))) : OOB;
-    }
-    const uint64_t xbase = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
-    auto issue_x = [&](int t) {
-        const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(xbase, NUM_RECORDS);
-        uint8_t *base = smem + ((t - kb) & 1) * STAGE + OPB + w * 1024;
-        const uint32_t past = t < ke ? 0u : OOB;
-        const int k0 = __builtin_amdgcn_readfirstlane((t < ke ? t : 0) * (BN * 2));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            load16_to_lds(rx, base + 8192 * i, offx[i] | past, k0);
-    };
-    // weights: wave w takes rows 8 w .. 8 w + 7 of a step, lane l channels c0 + 4 l .. + 3
-    const uint32_t offw = c0 + 4 * lane < K ? (uint32_t)(8 * w * K + 4 * lane) : OOB;
-    uint32_t raw[8];
-    auto load_w = [&](int t) {
-        const int second = t >= p.nt1;
-        const int n0 = (t - (second ? p.nt1 : 0)) * BN;
-        const uint64_t base = reinterpret_cast<uint64_t>((second ? p.w2 : p.w1) + (int64_t)(t < ke ? n0 : 0) * K + c0);
-        const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(base, NUM_RECORDS);
-        const int rem = t < ke ? p.N - n0 - 8 * w : 0;            // rows left from this wave's first
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            raw[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rw, offw | (i < rem ? 0u : OOB), i * K, 0);
-    };
-    auto convert_w = [&](int t) { transpose_to_lds(raw, smem + ((t - kb) & 1) * STAGE, lane, w); };
-
-    const int frow = lane & 15, fq = lane >> 4;
-    const int arow = (wn * 128 + frow) * 128, brow = OPB + (wm * 64 + frow) * 128;
-    v8bf16 fa[2][4], fb[2][4];
-    auto read_a = [&](int g, int kk, int h) {
-        const uint8_t *s0 = smem + (g & 1) * STAGE + arow;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-            fa[h][b] = *reinterpret_cast<const v8bf16 *>(s0 + (4 * h + b) * 2048 +
-                                                         16 * ((4 * kk + fq) ^ swz(frow) ^ (b & 1)));
-    };
-    auto read_b = [&](int g, int kk) {
-        const uint8_t *s0 = smem + (g & 1) * STAGE + brow + 16 * ((4 * kk + fq) ^ swz(frow));
-#pragma unroll
-        for (int b = 0; b < 4; ++b) fb[kk][b] = *reinterpret_cast<const v8bf16 *>(s0 + b * 2048);
-    };
-    v4f acc[8][4];
-#pragma unroll
-    for (int a = 0; a < 8; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[a][b] = v4f{};
-    auto mfma_range = [&](int kk, int h, int j0, int j1) {
-#pragma unroll
-        for (int j = j0; j < j1; ++j) {
-            const int bi = 4 * h + (j >> 2), bj = j & 3;
-            acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[h][j >> 2], fb[kk][bj], acc[bi][bj], 0, 0, 0);
-        }
-    };
-    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
-
-    load_w(kb);
-    issue_x(kb);
-    convert_w(kb);
-    load_w(kb + 1);
-    issue_x(kb + 1);
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(12));          // the tokens of step kb have landed
-    __syncthreads();
-    read_a(0, 0, 0);
-    read_b(0, 0);
-    for (int t = kb, g = 0; t < ke; ++t, ++g) {
-        read_a(g, 0, 1);
-        mfma_range(0, 0, 0, 16);
-        convert_w(t + 1);
-        fence();
-        load_w(t + 2);
-        read_a(g, 1, 0);
-        read_b(g, 1);
-        mfma_range(0, 1, 0, 16);
-        fence();
-        read_a(g, 1, 1);
-        mfma_range(1, 0, 0, 16);
-        fence();
-        mfma_range(1, 1, 0, 4);
-        fence();
-        // the tokens of step t + 1 have landed: only the 8 weight loads of step t + 2 are younger
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(8));
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        issue_x(t + 2);
-        read_a(g + 1, 0, 0);
-        read_b(g + 1, 0);
-        mfma_range(1, 1, 4, 16);
-        fence();
-    }
-    // every load into LDS has landed and every wave is done reading before the epilogue reuses it
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-    __syncthreads();
-
-    // lane: token lane % 16 of block bj; channels wn 128 + 16 bi + 4 (lane / 16) + v
-    if (slot >= 0) {
-        float *dst = p.part + (int64_t)slot * (BM * BC);
-#pragma unroll
-        for (int bj = 0; bj < 4; ++bj) {
-            const int ml = wm * 64 + 16 * bj + frow;
-            if (m0 + ml < p.M) {
-#pragma unroll
-                for (int bi = 0; bi < 8; ++bi)
-                    *reinterpret_cast<v4f *>(dst + ml * BC + wn * 128 + 16 * bi + 4 * fq) = acc[bi][bj];
-            }
-        }
-        return;
-    }
-    // Walsh-Hadamard over the channel bits below lg: 0, 1 in v, 4 .. 6 in bi, 2 and 3 across the
-    // lanes' 16-lane rows (a swap puts both partners of two registers into one lane), 7 across
-    // the two waves of a token range, through LDS
-    const int lg = p.lg;
-#pragma unroll
-    for (int bj = 0; bj < 4; ++bj) {
-#pragma unroll
-        for (int bi = 0; bi < 8; ++bi) {
-            v4f &v = acc[bi][bj];
-            if (lg > 0) {
-                float a = v[0], b = v[1], c = v[2], d = v[3];
-                bfly(a, b);
-                bfly(c, d);
-                if (lg > 1) {
-                    bfly(a, c);
-                    bfly(b, d);
-                }
-                v = v4f{a, b, c, d};
-            }
-        }
-#pragma unroll
-        for (int bi = 0; bi < 8; ++bi) {
-#pragma unroll
-            for (int v = 0; v < 4; v += 2) {
-                float a = acc[bi][bj][v], b = acc[bi][bj][v + 1];
-                if (lg > 2) {
-                    swap16f(a, b);
-                    bfly(a, b);
-                    swap16f(a, b);
-                }
-                if (lg > 3) {
-                    swap32f(a, b);
-                    bfly(a, b);
-                    swap32f(a, b);
-                }
-                acc[bi][bj][v] = a;
-                acc[bi][bj][v + 1] = b;
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < 3; ++s) {
-            if (lg > 4 + s) {
-#pragma unroll
-                for (int bi = 0; bi < 8; ++bi)
-                    if (!(bi & (1 << s))) {
-                        const v4f a = acc[bi][bj], b = acc[bi | (1 << s)][bj];
-                        acc[bi][bj] = a + b;
-                        acc[bi | (1 << s)][bj] = a - b;
-                    }
-            }
-        }
-    }
-    // 128 tokens (32 of each token range) a round, rows of 1 KiB with 16-byte chunk c at c ^ row % 16;
-    // then 32 threads per token, 8 channels each.  (The loop is rolled: finish8() appears twice, with 64
-    // accumulators live; unrolled over the accumulators' 16-token blocks it spilled 185 registers.)
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-        if (pass) __syncthreads();
-#pragma unroll
-        for (int b2 = 0; b2 < 2; ++b2)
-#pragma unroll
-            for (int bi = 0; bi < 8; ++bi)
-                *reinterpret_cast<v4f *>(smem + (wm * 32 + 16 * b2 + frow) * 1024 +
-                                         16 * ((32 * wn + 4 * bi + fq) ^ frow)) = acc[bi][2 * pass + b2];
-        __syncthreads();
-        const int cc = (int)threadIdx.x & 31, c = c0 + 8 * cc;
-#pragma unroll 1
-        for (int it = 0; it < 8; ++it) {
-            const int row = 16 * it + ((int)threadIdx.x >> 5);
-            const int m = m0 + (row >> 5) * 64 + 32 * pass + (row & 31);
-            if (m >= p.M || c >= K) continue;
-            float v[8];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const v4f own = *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * ((2 * cc + q) ^ (row & 15)));
-                const v4f other = *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * (((2 * cc + q) ^ 32) ^ (row & 15)));
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[4 * q + e] = lg <= 7 ? own[e] : cc & 16 ? other[e] - own[e] : own[e] + other[e];
-            }
-            finish8(p, m, c, v);
-        }
-    }
 }
 
 // 16 bytes per lane, global -> LDS (lane l to byte lds + 16 l).  Written out because the compiler, which knows the
@@ -673,6 +406,296 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
             for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
         }
         finish8(p, m, c, v);
+    }
+}
+
+// The same for 256 tokens x 256 channels, when there are enough of them: 512 threads, one workgroup per CU, 144 KiB of
+// LDS in three stages of the same layout.  Each of the 8 wavefronts takes 32 channels of all 256 tokens, so that
+// every code is converted once and by one wavefront; the tokens' fragments, which all eight read, come in
+// four groups of 8 a step (two halves of the contraction, 128 tokens each), one ahead of the products.  The barrier
+// stands before the last group: it publishes the next step, whose first group is read under those products, and
+// frees this one, whose last group is in registers by then.  The loads of step t + 2 go out two at a time during
+// three groups of products.  Wavefront w sums tokens 32 w .. + 31 for the correction.
+__global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
+{
+    constexpr int NST = 3, XL = 4, WL = 2, LPS = XL + WL;    // loads per step and wavefront
+    constexpr int WB = BN * BC, GSTAGE = WB + BM * BN * 2;   // codes, then tokens
+    __shared__ __attribute__((aligned(16))) uint8_t smem[NST * GSTAGE];
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int T = p.tiles_m * p.tiles_c, U = p.T_dp + (T - p.T_dp) * p.S;
+    const int K = p.K;
+    if ((int)blockIdx.x >= U) return;                    // the grid is rounded up to a multiple of 8
+    const int u = unit_of((int)blockIdx.x, p.T_dp, U);
+    int tile = u, kb = 0, ke = p.nt, slot = -1;
+    if (u >= p.T_dp) {
+        const int r = T - p.T_dp, v = u - p.T_dp, sl = v / r;
+        tile = p.T_dp + v % r;
+        kb = (int)((int64_t)sl * p.nt / p.S);
+        ke = (int)((int64_t)(sl + 1) * p.nt / p.S);
+        slot = v;
+    }
+    int tm, tc;
+    tile_coords(tile, p.tiles_m, p.tiles_c, tm, tc);
+    const int m0 = tm * BM, c0 = tc * BC;
+
+    // tokens: instruction i of wave w fills rows 8 (8 i + w) .. + 7; codes: rows 4 (8 i + w) .. + 3
+    uint32_t offx[XL], offw[WL];
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+        const int r = 8 * (8 * i + w) + (lane >> 3);
+        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz(r))) : OOB;
+    }
+#pragma unroll
+    for (int i = 0; i < WL; ++i) {
+        const int n = 4 * (8 * i + w) + (lane >> 4), c = 16 * ((lane & 15) ^ (n & 15));
+        offw[i] = c0 + c < K ? (uint32_t)(n * K + c) : OOB;
+    }
+    // the load side, as in the kernel above; load i of a step: its codes first
+    const uint64_t xbase = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(const lds_void *)smem + (uint32_t)w * 1024u;
+    int ld_t = kb, ld_rows = p.N - (kb - (kb >= p.nt1 ? p.nt1 : 0)) * BN;
+    uint64_t ld_w = reinterpret_cast<uint64_t>((kb >= p.nt1 ? p.w2 : p.w1) +
+                                               (int64_t)(kb - (kb >= p.nt1 ? p.nt1 : 0)) * BN * K + c0);
+    uint32_t ld_lds = lds0;
+    auto issue = [&](int i) {
+        if (i < WL) {
+            const int records = ld_t >= ke ? 0 : ld_rows >= BN ? NUM_RECORDS : ld_rows * K - c0;
+            const v4u rw = {(uint32_t)ld_w, (uint32_t)(ld_w >> 32) & 0xffffu, (uint32_t)records, 0x00020000u};
+            dma16(rw, ld_lds + 8192 * i, offw[i], 0);
+        } else {
+            const v4u rx = {(uint32_t)xbase, (uint32_t)(xbase >> 32) & 0xffffu, ld_t < ke ? (uint32_t)NUM_RECORDS : 0u,
+                            0x00020000u};
+            dma16(rx, ld_lds + WB + 8192 * (i - WL), offx[i - WL], (uint32_t)ld_t * (BN * 2));
+        }
+        if (i < LPS - 1) return;
+        ++ld_t;
+        ld_rows -= BN;
+        ld_w += (uint64_t)(BN * K);
+        if (ld_t == p.nt1) {
+            ld_rows = p.N;
+            ld_w = reinterpret_cast<uint64_t>(p.w2 + c0);
+        }
+        ld_lds = ld_lds == lds0 + (NST - 1) * GSTAGE ? lds0 : ld_lds + GSTAGE;
+    };
+
+    const int frow = lane & 15, fq = lane >> 4;
+    const int key = 8 * (fq & 1) + (frow >> 1);
+    int awhere[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+        awhere[a] = (8 * fq + (frow >> 1)) * BC + 16 * ((2 * w + a) ^ key) + 8 * (frow & 1);
+    const int bwhere = WB + frow * 128;
+    const int bpos[2] = {16 * (fq ^ swz(frow)), 16 * ((4 + fq) ^ swz(frow))};
+    v2i raw[2];
+    v8bf16 fb[2][8], fs[2];
+    auto read_codes = [&](int stage, int kk) {
+        const uint8_t *st = smem + stage * GSTAGE + kk * (32 * BC);
+#pragma unroll
+        for (int a = 0; a < 2; ++a) raw[a] = read_transposed(st + awhere[a]);
+    };
+    // group h of a step's half kk: tokens 128 h .. + 127
+    auto read_tokens = [&](int stage, int kk, int h) {
+        const uint8_t *st = smem + stage * GSTAGE + bwhere + bpos[kk] + h * 16384;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) fb[h][b] = *reinterpret_cast<const v8bf16 *>(st + b * 2048);
+    };
+    auto read_own = [&](int stage, int kk) {
+        const uint8_t *st = smem + stage * GSTAGE + bwhere + bpos[kk] + w * 4096;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) fs[b] = *reinterpret_cast<const v8bf16 *>(st + b * 2048);
+    };
+    v4f acc[2][16];
+    float asum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 16; ++b) acc[a][b] = v4f{};
+    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+    // the products of group h; loads i0, i0 + 1 after the first and third quarter (i0 < 0: none)
+    auto products = [&](const v8bf16 (&fa)[2], int h, int i0) {
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+                acc[a][8 * h + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[h][b], acc[a][8 * h + b], 0, 0, 0);
+            if (i0 >= 0 && (b == 1 || b == 5)) {
+                fence();
+                issue(i0 + (b >> 2));
+                fence();
+            }
+        }
+    };
+    auto sum_own = [&] {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) asum[b] = add8(fs[b], asum[b]);
+    };
+
+#pragma unroll
+    for (int i = 0; i < 2 * LPS + 2; ++i) issue(i % LPS);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(LPS + 2));
+    asm volatile("s_barrier" ::: "memory");
+    read_codes(0, 0);
+    read_tokens(0, 0, 0);
+    int st = 0;                                          // this step's stage
+    for (int t = kb; t < ke; ++t) {
+        const int next = st == NST - 1 ? 0 : st + 1;
+        v8bf16 fa[2];
+        read_tokens(st, 0, 1);
+        read_own(st, 0);
+        fence();
+#pragma unroll
+        for (int a = 0; a < 2; ++a) fa[a] = codes_to_bf16(raw[a]);
+        products(fa, 0, 2);
+        fence();
+        read_codes(st, 1);
+        read_tokens(st, 1, 0);
+        fence();
+        sum_own();
+        products(fa, 1, 4);
+        fence();
+        read_tokens(st, 1, 1);
+        read_own(st, 1);
+        fence();
+#pragma unroll
+        for (int a = 0; a < 2; ++a) fa[a] = codes_to_bf16(raw[a]);
+        products(fa, 0, -1);
+        fence();
+        // the next step has landed: only the one after it is still in flight
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(LPS));
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        read_codes(next, 0);
+        read_tokens(next, 0, 0);
+        fence();
+        sum_own();
+        products(fa, 1, 0);
+        fence();
+        st = next;
+    }
+    // every load into LDS has landed and every wave is done reading before the epilogue reuses it
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __syncthreads();
+
+    // the tokens' sums, each from its wave (the four fq together), to all of them
+    float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        asum[b] += __shfl_xor(asum[b], 16);
+        asum[b] += __shfl_xor(asum[b], 32);
+        if (fq == 0) sums[32 * w + 16 * b + frow] = asum[b];
+    }
+    __syncthreads();
+    // lane: token lane % 16 of block b, channels 32 w + 16 a + 4 fq + v
+#pragma unroll
+    for (int b = 0; b < 16; ++b) {
+        const float s = sums[16 * b + frow] * -kOffset;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[a][b][v] += s;
+    }
+    if (slot >= 0) {
+        float *dst = p.part + (int64_t)slot * (BM * BC);
+#pragma unroll
+        for (int b = 0; b < 16; ++b) {
+            const int ml = 16 * b + frow;
+            if (m0 + ml < p.M) {
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+                    *reinterpret_cast<v4f *>(dst + ml * BC + 32 * w + 16 * a + 4 * fq) = acc[a][b];
+            }
+        }
+        return;
+    }
+    // the rotation: channel bits 0, 1 in v, 2, 3 across lanes, 4 in a; 5 .. 7 across the eight waves, through LDS
+    const int lg = p.lg;
+#pragma unroll
+    for (int b = 0; b < 16; ++b) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            float x0 = acc[a][b][0], x1 = acc[a][b][1], x2 = acc[a][b][2], x3 = acc[a][b][3];
+            if (lg > 0) {
+                bfly(x0, x1);
+                bfly(x2, x3);
+            }
+            if (lg > 1) {
+                bfly(x0, x2);
+                bfly(x1, x3);
+            }
+            if (lg > 2) {
+                swap16f(x0, x1);
+                bfly(x0, x1);
+                swap16f(x0, x1);
+                swap16f(x2, x3);
+                bfly(x2, x3);
+                swap16f(x2, x3);
+            }
+            if (lg > 3) {
+                swap32f(x0, x1);
+                bfly(x0, x1);
+                swap32f(x0, x1);
+                swap32f(x2, x3);
+                bfly(x2, x3);
+                swap32f(x2, x3);
+            }
+            acc[a][b] = v4f{x0, x1, x2, x3};
+        }
+        if (lg > 4) {
+            const v4f x = acc[0][b], y = acc[1][b];
+            acc[0][b] = x + y;
+            acc[1][b] = x - y;
+        }
+    }
+    // 128 tokens a round, rows of 1 KiB with 16-byte chunk c at c ^ row % 16; then 32 threads per token, 8 channels each
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+                *reinterpret_cast<v4f *>(smem + (16 * b + frow) * 1024 + 16 * ((8 * w + 4 * a + fq) ^ frow)) =
+                    acc[a][8 * pass + b];
+        __syncthreads();
+        if (lg > 5) {
+            // thread: one row, 4 channels at 8 places 32 channels apart, twice
+            const int row = (int)threadIdx.x & 127;
+#pragma unroll 1
+            for (int j = (int)threadIdx.x >> 7; j < 8; j += 4) {
+                v4f x[8];
+#pragma unroll
+                for (int h = 0; h < 8; ++h) x[h] = *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * ((8 * h + j) ^ (row & 15)));
+#pragma unroll
+                for (int s = 0; s < 3; ++s) {
+                    if (lg > 5 + s) {
+#pragma unroll
+                        for (int h = 0; h < 8; ++h)
+                            if (!(h & (1 << s))) {
+                                const v4f a = x[h], b = x[h | (1 << s)];
+                                x[h] = a + b;
+                                x[h | (1 << s)] = a - b;
+                            }
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 8; ++h) *reinterpret_cast<v4f *>(smem + row * 1024 + 16 * ((8 * h + j) ^ (row & 15))) = x[h];
+            }
+            __syncthreads();
+        }
+        const int cc = (int)threadIdx.x & 31, c = c0 + 8 * cc;
+#pragma unroll 1
+        for (int it = 0; it < 8; ++it) {
+            const int row = 16 * it + ((int)threadIdx.x >> 5), m = m0 + 128 * pass + row;
+            if (m >= p.M || c >= K) continue;
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const v4f x = *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * ((2 * cc + q) ^ (row & 15)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
+            }
+            finish8(p, m, c, v);
+        }
     }
 }
 
@@ -979,11 +1002,11 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
     p.T_dp = pl.T_dp;
     p.S = pl.S;
     p.next = g.next;
-    p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g))) * (pl.bm == 64 ? kTileUnscale : 1.0f / kOperandScale);
+    p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g))) * kTileUnscale;
     const int T = pl.tiles_m * pl.tiles_c, U = pl.T_dp + (T - pl.T_dp) * pl.S;
     const dim3 grid((unsigned)((U + 7) & ~7));
     if (pl.bm == 64) hipLaunchKernelGGL(grad_tile_kernel, grid, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL(grad_gemm_kernel, grid, dim3(NTHREADS), 0, stream, p);
+    else hipLaunchKernelGGL(grad_gemm_kernel, grid, dim3(512), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.S == 1) return e;
     const int rb = (int)((g.M < pl.bm ? g.M : pl.bm) + 7) / 8;
