@@ -7,7 +7,7 @@
 // contraction over their stacked rows.  Three steps:
 //   1. grad_prep_kernel: dz from the incoming gradient, the saved pre-activations and the activation's
 //      slope; a[m,n] = bf16(dz sw) for the matrix core, fp32 column sums of dz for db.
-//   2. grad_gemm_kernel: a . wq with v_mfma_f32_16x16x32_bf16.  The codes are exact in bf16, so a's
+//   2. grad_gemm_kernel, or grad_tile_kernel for few tokens: a . wq with v_mfma_f32_16x16x32_bf16.  The codes are exact in bf16, so a's
 //      rounding (2^-8 of each term at most, what bf16 training rounds its gradients to anyway) is the
 //      only one before the fp32 sums.
 //   3. the rotation, dx_add and the one rounding to bf16: in the GEMM's epilogue (a tile spans 256
@@ -20,7 +20,7 @@
 namespace convrot {
 namespace {
 
-// Codes as bf16 without a conversion (grad_tile_kernel).  The 16 bits 0x00uu are the bf16 number uu * 2^-133 for
+// Codes as bf16 without a conversion.  The 16 bits 0x00uu are the bf16 number uu * 2^-133 for
 // every byte uu (below 128 a denormal, from 128 on the first binade, which continues the same grid; the
 // matrix core takes bf16 denormals as they are).  With u = q + 128 (the code's byte with its top bit
 // flipped), two codes become one register with a single byte permute, and
@@ -158,20 +158,18 @@ __device__ __forceinline__ float add8(v8bf16 v, float s)
     return s;
 }
 
-// The same for 64 tokens x 256 channels, for batches whose 256-token tiles would not fill the GPU or would mostly
-// compute padding: 256 threads, 72 KiB of LDS, two workgroups per CU; each of the 4 wavefronts takes 64
-// channels of all 64 tokens.  A step is short here against everything that is done once per step, so the
-// codes go to LDS as they are, both operands without passing registers, in three stages with two in
-// flight; a transposing read and the permute above make the fragments.
+// 64 tokens x 256 channels, for batches whose 256-token tiles would not fill the GPU or would mostly compute
+// padding: 256 threads, 72 KiB of LDS, two workgroups per CU; each of the 4 wavefronts takes 64 channels of all
+// 64 tokens.  The codes go to LDS as they are, both operands without passing registers, in three stages
+// with two in flight; a transposing read and the permute above make the fragments.
 //   codes   64 rows of 256 bytes as in memory, 16-byte chunk c of row n at c ^ n % 16, so that the rows
 //           of a transposing read (16 lanes: 8 rows x 16 bytes) fall on distinct banks;
 //   tokens  rows of 128 bytes (64 values), chunk c of row r at c ^ swz(r).
 // One barrier a step: it publishes the next stage and frees this one, which is refilled behind it.
-// (Against this kernel with the 256-token one's conversion through registers, us: 300 tokens 5376 x 2688 38 / 33,
-// 2688 x 2 * 5376 54 / 46; 512 tokens 5120 x 5120 62 / 52.  In 256-token tiles each wavefront would convert the
-// codes of 128 channels that three others convert too, and that one loses: 736 us against 682 at 4096 tokens,
-// 5376 x 16128.)  12 tokens 5120 x 8192: 13 us, the codes' stream and one load latency; 300 tokens
-// 5376 x 2688: 21 us, 2688 x 2 * 5376: 30 us, a step's LDS reads and barrier.
+// (With the codes converted and transposed in registers, then written to LDS as bf16, us: 300 tokens 5376 x 2688
+// 38 against 33, 2688 x 2 * 5376 54 / 46; 512 tokens 5120 x 5120 62 / 52.)  12 tokens 5120 x 8192: 13 us,
+// the codes' stream and one load latency; 300 tokens 5376 x 2688: 21 us, 2688 x 2 * 5376: 30 us, a step's
+// LDS reads and barrier.
 __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 {
     constexpr int TM = 64, NST = 3;
@@ -414,8 +412,15 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 // every code is converted once and by one wavefront; the tokens' fragments, which all eight read, come in
 // four groups of 8 a step (two halves of the contraction, 128 tokens each), one ahead of the products.  The barrier
 // stands before the last group: it publishes the next step, whose first group is read under those products, and
-// frees this one, whose last group is in registers by then.  The loads of step t + 2 go out two at a time during
-// three groups of products.  Wavefront w sums tokens 32 w .. + 31 for the correction.
+// frees this one, whose last group is in registers by then.  The loads of step t + 2 go out one by one, after
+// each half of three groups' products.  Wavefront w sums tokens 32 w .. + 31 for the correction.
+// 4096 tokens 5376 x 16128: 541 us, 1310 TFLOP/s, matrix core 61% busy at 2.05 GHz, LDS nearly conflict-free (a library's
+// bf16 product of that shape, operands ready in bf16: 887); without the loads (timing only) 14% less.
+// Alternatives, us for that call and for the gated block's at 2048 tokens 5120 x 25600 (593, 1311 as it is):
+// codes converted and transposed in registers and written to LDS as bf16 625, 1392; wavefronts of 64 channels x
+// 128 tokens, which read half as much LDS and convert twice as much, 602, 1335; the loads after
+// the first and third quarter of a group 603, 1337, or two at once at its end 600, 1321; their descriptors kept
+// ready instead of formed at each load 617, 1368.
 __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 {
     constexpr int NST = 3, XL = 4, WL = 2, LPS = XL + WL;    // loads per step and wavefront
@@ -519,7 +524,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 #pragma unroll
             for (int a = 0; a < 2; ++a)
                 acc[a][8 * h + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[h][b], acc[a][8 * h + b], 0, 0, 0);
-            if (i0 >= 0 && (b == 1 || b == 5)) {
+            if (i0 >= 0 && (b == 3 || b == 7)) {
                 fence();
                 issue(i0 + (b >> 2));
                 fence();
@@ -879,8 +884,8 @@ size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 // 4.9 TB/s.  Slices cost their partial sums' round trip (8 bytes per element at 4.5 TB/s) and a launch.
 // Measured (us; K x N, 2 N for gate|up, all launches of the call), 256 tokens unsliced / in the best slices / 64
 // tokens unsliced / in the best slices:
-//   12 tokens 5120 x 8192: 178 / 28 / 84 / 20;      300 tokens 2688 x 2 * 5376: 241 / 56 / 118 / 48
-//   512 tokens 5120 x 5120: 131 / 54 / 67 / 53;    1024 tokens: 140 / 82 / 104 / 95
+//   600 tokens 2048 x 8192: 185 / 50 / 93 / 47;    512 tokens 5120 x 5120: 127 / 54 / 71 / 55
+//   1024 tokens 5120 x 5120: 128 / 75 / 99 / 89;   2688 x 2 * 5376: 246 / 93 / 130 / 107
 void tile_plan(Plan &pl, int64_t M, int64_t N, int K, bool gated)
 {
     const int cus = cu_count() & ~7;
