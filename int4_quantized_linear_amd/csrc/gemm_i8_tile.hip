@@ -269,14 +269,25 @@ __global__ void __launch_bounds__(256) tile_reduce_kernel(TileParams p, int rb)
     auto sums = [&](int cl, const float (&sc)[8], const float (&bi)[8], float (&v)[8]) {
         int32_t sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         const int32_t *src = p.part + (int64_t)i * (BM * BN) + ml * BN + cl;
-#pragma unroll 8
-        for (int s = 0; s < p.S; ++s, src += (int64_t)T * (BM * BN)) {
-            const v4i a = *reinterpret_cast<const v4i *>(src), b = *reinterpret_cast<const v4i *>(src + 4);
+#pragma unroll 1
+        for (int s = 0; s < p.S; s += 8) {
+            v4i a[8], b[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sum[e] += a[e];
-                sum[e + 4] += b[e];
+            for (int i = 0; i < 8; ++i) {
+                a[i] = b[i] = v4i{};
+                if (s + i < p.S) {
+                    a[i] = *reinterpret_cast<const v4i *>(src);
+                    b[i] = *reinterpret_cast<const v4i *>(src + 4);
+                    src += (int64_t)T * (BM * BN);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum[e] += a[i][e];
+                    sum[e + 4] += b[i][e];
+                }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf((float)sum[e], sxm * sc[e], bi[e]);

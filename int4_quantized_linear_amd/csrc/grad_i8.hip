@@ -710,6 +710,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 // last round, 5 to 8 us (about two memory latencies) for a few hundred tokens.
 __global__ void __launch_bounds__(256) grad_join_kernel(GradParams p, int rb)
 {
+    constexpr int AHEAD = 8;                             // slices in flight (a remainder read one by one: 30 slices 9.1 us, 8.4 so)
     const int i = (int)blockIdx.x / rb;                                 // split tile
     const int ml = ((int)blockIdx.x % rb) * 8 + ((int)threadIdx.x >> 5);
     const int l = (int)threadIdx.x & 31;
@@ -722,14 +723,25 @@ __global__ void __launch_bounds__(256) grad_join_kernel(GradParams p, int rb)
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (row_ok) {
         const float *src = p.part + (int64_t)i * slot + ml * BC + 8 * l;
-#pragma unroll 4
-        for (int s = 0; s < p.S; ++s, src += (int64_t)r * slot) {
-            const v4f a = *reinterpret_cast<const v4f *>(src), b = *reinterpret_cast<const v4f *>(src + 4);
+#pragma unroll 1
+        for (int s = 0; s < p.S; s += AHEAD) {
+            v4f a[AHEAD], b[AHEAD];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] += a[e];
-                v[e + 4] += b[e];
+            for (int i = 0; i < AHEAD; ++i) {
+                a[i] = b[i] = v4f{};
+                if (s + i < p.S) {
+                    a[i] = *reinterpret_cast<const v4f *>(src);
+                    b[i] = *reinterpret_cast<const v4f *>(src + 4);
+                    src += (int64_t)r * slot;
+                }
             }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] += a[i][e];
+                    v[e + 4] += b[i][e];
+                }
         }
     }
 #pragma unroll
@@ -757,6 +769,7 @@ struct PrepParams {
     const float *sw1, *sw2;    // [N]
     uint16_t *a;               // [M, lda], columns Np on the second weight's
     float *sums;               // [chunks][N (2 N)] partial column sums, or null
+    float *db1, *db2;          // with one chunk and no sums: the column sums themselves (each may be null)
     int64_t M, N, Np, lda;
     int act, col_blocks, rows; // rows per chunk
 };
@@ -828,7 +841,7 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(PrepParams p)
         for (int e = 0; e < 8; ++e) sum1[e] += d[e];
         if (n < p.Np) store8(m, n, d, s1);
     }
-    if (!p.sums) return;
+    if (!p.sums && !p.db1 && !p.db2) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         red[0][tr][8 * tl + e] = sum1[e];
@@ -842,19 +855,21 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(PrepParams p)
         float s = 0.0f;
 #pragma unroll
         for (int r = 0; r < 8; ++r) s += red[q][r][threadIdx.x];
-        p.sums[((int64_t)chunk * (GATED ? 2 : 1) + q) * p.N + col] = s;
+        if (p.sums) p.sums[((int64_t)chunk * (GATED ? 2 : 1) + q) * p.N + col] = s;
+        else if (float *db = q ? p.db2 : p.db1) db[col] = s;
     }
 }
 
-// db[n] = sum of the chunks' partial sums, in chunk order (0 chunks: 0).
-__global__ void __launch_bounds__(256) grad_bias_kernel(const float *sums, int chunks, int which, int parts, int64_t N,
-                                                        float *db)
+// db[n] = sum of the chunks' partial sums, in chunk order (0 chunks: 0); the second weight's in the grid's second row.
+__global__ void __launch_bounds__(256) grad_bias_kernel(const float *sums, int chunks, int parts, int64_t N, float *db1,
+                                                        float *db2)
 {
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= N) return;
+    float *db = blockIdx.y ? db2 : db1;
+    if (n >= N || !db) return;
     float s = 0.0f;
 #pragma unroll 4
-    for (int c = 0; c < chunks; ++c) s += sums[((int64_t)c * parts + which) * N + n];
+    for (int c = 0; c < chunks; ++c) s += sums[((int64_t)c * parts + blockIdx.y) * N + n];
     db[n] = s;
 }
 
@@ -915,9 +930,10 @@ void tile_plan(Plan &pl, int64_t M, int64_t N, int K, bool gated)
     }
 }
 
-// Rows of a grad_prep workgroup: 8, one per thread, up to 512 tokens, and a multiple of 8 that gives at most about
-// 64 chunks beyond (2048 x 5120: 10 us, against 22 with 8 rows; and few partial column sums to add up).
-int prep_rows(int64_t M) { return M > 512 ? (int)((M + 511) / 512 * 8) : 8; }
+// Rows of a grad_prep workgroup: all up to 16 tokens, so that the column sums need no second launch (15 x 7497: 5.4 us
+// against 4.4 and 2.3); 8, one per thread, up to 512, and a multiple of 8 that gives at most about 64 chunks
+// beyond (2048 x 5120: 10 us, against 22 with 8 rows; and few partial column sums to add up).
+int prep_rows(int64_t M) { return M > 512 ? (int)((M + 511) / 512 * 8) : M > 16 ? 8 : 16; }
 
 Plan make_plan(int64_t M, int64_t N, int K, bool gated)
 {
@@ -961,7 +977,9 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
             q.sw1 = g.sw1;
             q.sw2 = g.sw2;
             q.a = reinterpret_cast<uint16_t *>(ws);
-            q.sums = bias ? sums : nullptr;
+            q.sums = bias && pl.chunks > 1 ? sums : nullptr;
+            q.db1 = pl.chunks > 1 ? nullptr : g.db1;
+            q.db2 = pl.chunks > 1 ? nullptr : g.db2;
             q.M = g.M;
             q.N = g.N;
             q.Np = pl.Np;
@@ -977,11 +995,9 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
-        for (int which = 0; which < 2; ++which) {
-            float *db = which ? g.db2 : g.db1;
-            if (!db) continue;
-            hipLaunchKernelGGL(grad_bias_kernel, dim3((unsigned)((g.N + 255) / 256)), dim3(256), 0, stream, sums,
-                               g.M > 0 ? pl.chunks : 0, which, gated ? 2 : 1, g.N, db);
+        if (bias && (g.M <= 0 || pl.chunks > 1)) {
+            hipLaunchKernelGGL(grad_bias_kernel, dim3((unsigned)((g.N + 255) / 256), g.db2 ? 2 : 1), dim3(256), 0, stream, sums,
+                               g.M > 0 ? pl.chunks : 0, gated ? 2 : 1, g.N, g.db1, g.db2);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
