@@ -177,3 +177,25 @@ def test_two_streams_at_once(cr):
                         c.run()
             torch.cuda.synchronize()
             assert all(c.same(w) for c, w in zip(pair, wants)), (op, M)
+
+
+@pytest.mark.parametrize("M", [0, 1, 16, 17, 600])
+def test_one_of_two_bias_gradients(cr, M):
+    """Either bias gradient of the gated linear alone, and neither, as with both."""
+    N, K, g = 1001, 320, 64
+    a, b = _weight(cr, N, K, g, 1), _weight(cr, N, K, g, 2)
+    dh, pre = _randn(M, N, seed=1), _randn(2, M, N, seed=2)
+    want = cr.linear_gated_backward(dh, pre, *a, *b, group=g, bias_grad=True)
+    ws = Guarded(max(cr.workspace_bytes_gated_backward(M, N, K), 256))
+    for first, second in ((True, False), (False, True), (False, False)):
+        dx, dg, du = Guarded(M * K * 2), Guarded(N * 4), Guarded(N * 4)
+        cr._call("convrot_linear_gated_backward", _p(dh), _p(pre), M, N, K, g, _p(a[0]), _p(a[1]), _p(b[0]), _p(b[1]),
+                 cr.ACTS["silu"], None, dx.ptr, dg.ptr if first else None, du.ptr if second else None, ws.ptr, ws.n,
+                 torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        for got, ref, asked in ((dx, want[0], True), (dg, want[1], first), (du, want[2], second)):
+            assert got.intact()
+            if asked:
+                assert torch.equal(got.bytes(), ref.contiguous().view(torch.uint8).flatten())
+            else:
+                assert (got.bytes() == 0xff).all()
