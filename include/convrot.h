@@ -219,10 +219,10 @@ size_t convrot_workspace_bytes_ffn(int64_t M, int64_t F, int64_t K);
  *   forward takes); dx bf16 [M, K]; dx_add bf16 [M, K] or NULL, added in fp32 before the rounding: the
  *   gradient of a residual path, or of other linears with the same input; may be dx itself;
  *   dbias fp32 [N] or NULL.  The gradient of the residual is dy.
- * The products run on the bf16 matrix core: the codes are exact in bf16, and rounding dz * w_scale to
- * bf16 is the only rounding before the fp32 sums.  Sums are taken in a fixed order: the same call
- * gives the same bits.  |dz * w_scale| must be below 2^47 (1.4e14): the kernels carry it times 2^80;
- * terms below 2^-73 (1e-22) lose precision.
+ * The products run on the bf16 matrix core: the codes are exact in bf16, rounding dz * w_scale to bf16 (by at
+ * most 2^-8 of it) is the only rounding before the sums, and the sums are plain fp32 sums of the products, whatever
+ * the gradients' signs.  They are taken in a fixed order: the same call gives the same bits.  The
+ * sums must be finite in fp32; terms |dz * w_scale| below 2^-126 lose precision.
  *   M == 0: dbias is zeros.  N == 0 or K out of range: CONVROT_ERR_SHAPE (there is no gradient to
  *   form).  N < CONVROT_BACKWARD_MAX_N.  An overlap of dx, dx_add and dbias other than dx == dx_add:
  *   CONVROT_ERR_OVERLAP.  dx may be dy's own buffer.

@@ -7,9 +7,10 @@
 // contraction over their stacked rows.  Three steps:
 //   1. grad_prep_kernel: dz from the incoming gradient, the saved pre-activations and the activation's
 //      slope; a[m,n] = bf16(dz sw) for the matrix core, fp32 column sums of dz for db.
-//   2. grad_gemm_kernel, or grad_tile_kernel for few tokens: a . wq with v_mfma_f32_16x16x32_bf16.  The codes are exact in bf16, so a's
-//      rounding (2^-8 of each term at most, what bf16 training rounds its gradients to anyway) is the
-//      only one before the fp32 sums.
+//   2. grad_gemm_kernel, or grad_tile_kernel for few tokens: a . wq with v_mfma_f32_16x16x32_bf16.  The codes
+//      are exact in bf16, so a's rounding (2^-8 of each term at most, what bf16 training rounds its gradients to
+//      anyway; dx's error is 1.3 to 1.5 times that of its own rounding alone) is the only one before
+//      the fp32 sums.
 //   3. the rotation, dx_add and the one rounding to bf16: in the GEMM's epilogue (a tile spans 256
 //      channels, whole groups), or in grad_join_kernel where tiles are split along n.
 #include "activation.hpp"
@@ -20,18 +21,6 @@
 namespace convrot {
 namespace {
 
-// Codes as bf16 without a conversion.  The 16 bits 0x00uu are the bf16 number uu * 2^-133 for
-// every byte uu (below 128 a denormal, from 128 on the first binade, which continues the same grid; the
-// matrix core takes bf16 denormals as they are).  With u = q + 128 (the code's byte with its top bit
-// flipped), two codes become one register with a single byte permute, and
-//   sum_n a q = 2^133 sum_n a (u 2^-133) - 128 sum_n a.
-// The second sum is taken from the operand itself (two values per v_dot2_f32_bf16) and subtracted in fp32.
-// a carries a factor 2^80 in both kernels, so that these products stay in fp32's normal range: |dz sw| has
-// to be below 2^47 (1.4e14), and sums keep full precision above 2^-73 (1e-22).
-constexpr float kOperandScale = 0x1p80f;
-constexpr float kOffset = 0x1p-126f;          // 128 * 2^-133
-constexpr float kTileUnscale = 0x1p53f;       // 2^133 / 2^80
-
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v2i lds_v2i;
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
@@ -41,7 +30,7 @@ constexpr int BN = 64;                        // contraction rows per step
 constexpr int MAX_SPLIT = 64;
 
 struct GradParams {
-    const uint16_t *a;         // [M, lda] bf16 times 2^80; columns [0, 64 nt1) the first weight's, then the second's
+    const uint16_t *a;         // [M, lda] bf16; columns [0, 64 nt1) the first weight's, then the second's
     const int8_t *w1, *w2;     // [N, K]
     const uint16_t *add;       // dx_add [M, K] or null
     uint16_t *dx;              // [M, K]
@@ -52,12 +41,12 @@ struct GradParams {
     int bm;                    // tokens per tile, 256 or 64
     int tiles_m, tiles_c;
     int T_dp, S;               // whole tiles, then the rest in S slices each
-    float norm;                // 2^(-lg / 2), and the operands' scales taken back
+    float norm;                // 2^(-lg / 2)
     GradNext next;             // next.a non-null: the gated product's gradient goes there, not to dx
 };
 
-// 8 channels c .. of token m, rotated but not yet normalised, to where the launch puts them:
-//   dx = bf16(v norm + add), or, for the hidden gradient of a gated block, dh = bf16(v norm) and on to
+// 8 rotated channels c .. of token m to where the launch puts them:
+//   dx = bf16(v + add), or, for the hidden gradient of a gated block, dh = bf16(v) and on to
 //   both operands of the next contraction, bf16(dh u act'(g) sw_gate) and bf16(dh act(g) sw_up), which
 //   saves writing dh and reading it back in a pass of its own.
 // (16 bytes each; K % 64 == 0, so all 8 exist.)
@@ -79,7 +68,7 @@ __device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float
         float add[8] = {};
         if (p.add) load(p.add + o, add);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], p.norm, add[e]);
+        for (int e = 0; e < 8; ++e) v[e] += add[e];
         store(p.dx + o, v);
         return;
     }
@@ -89,18 +78,20 @@ __device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float
     act_values_slopes(g, slope, p.next.act);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-        const uint32_t d = pack_bf16x2(v[e] * p.norm, v[e + 1] * p.norm);
+        const uint32_t d = pack_bf16x2(v[e], v[e + 1]);
         const float d0 = bf16lo_to_f32(d), d1 = bf16hi_to_f32(d);
-        u[e] = d0 * u[e] * slope[e] * (p.next.sw_gate[c + e] * kOperandScale);
-        u[e + 1] = d1 * u[e + 1] * slope[e + 1] * (p.next.sw_gate[c + e + 1] * kOperandScale);
-        g[e] = d0 * g[e] * (p.next.sw_up[c + e] * kOperandScale);
-        g[e + 1] = d1 * g[e + 1] * (p.next.sw_up[c + e + 1] * kOperandScale);
+        u[e] = d0 * u[e] * slope[e] * p.next.sw_gate[c + e];
+        u[e + 1] = d1 * u[e + 1] * slope[e + 1] * p.next.sw_gate[c + e + 1];
+        g[e] = d0 * g[e] * p.next.sw_up[c + e];
+        g[e + 1] = d1 * g[e + 1] * p.next.sw_up[c + e + 1];
     }
     uint16_t *a = p.next.a + (int64_t)m * 2 * p.K + c;       // K % 64 == 0: no padding between the two
     store(a, u);
     store(a + p.K, g);
 }
 
+// One step of the rotation.  Sums are normalised before the first: |a + b| or |a - b| is at least the larger of |a| and
+// |b|, so nothing on the way exceeds the group's largest result and only a result can overflow.
 __device__ __forceinline__ void bfly(float &a, float &b)
 {
     const float s = a + b;
@@ -136,32 +127,28 @@ __device__ __forceinline__ v2i read_transposed(const uint8_t *p)
     return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i *)(const_cast<uint8_t *>(p)));
 }
 
-// 8 codes of one channel to 8 bf16 numbers u 2^-133.
+// 8 codes of one channel to bf16, exactly: v_cvt_f32_i32 takes a byte with its sign, and an integer of 8 bits
+// leaves the low half of its fp32 empty.  (A byte u = q + 128 placed in a bf16 denormal, u 2^-133, needs one
+// permute for two codes and no conversion, but then every sum carries 128 times the sum of the tokens' own
+// values, to be taken back at the end.  For gradients of one sign that is most of the sum: a contraction of 51200
+// left an error of 3e-4 of dx before its rounding, against 2e-6 with these plain sums.  Of that contraction's time it
+// saved 1%.)
 __device__ __forceinline__ v8bf16 codes_to_bf16(v2i raw)
 {
-    const uint32_t lo = (uint32_t)raw[0] ^ 0x80808080u, hi = (uint32_t)raw[1] ^ 0x80808080u;
-    const v4u d = {__builtin_amdgcn_perm(0u, lo, 0x0c010c00u), __builtin_amdgcn_perm(0u, lo, 0x0c030c02u),
-                   __builtin_amdgcn_perm(0u, hi, 0x0c010c00u), __builtin_amdgcn_perm(0u, hi, 0x0c030c02u)};
-    return __builtin_bit_cast(v8bf16, d);
-}
-
-// s + the 8 values of v.
-__device__ __forceinline__ float add8(v8bf16 v, float s)
-{
-    const v4u d = __builtin_bit_cast(v4u, v);
-    const v2bf16 one = __builtin_bit_cast(v2bf16, 0x3f803f80u);
+    v4u d;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = d[i];                      // (a bit cast of d[i] itself takes d[0])
-        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf16, pair), one, s, false);
+        const uint32_t pair = (uint32_t)raw[i >> 1] >> (16 * (i & 1));
+        d[i] = __builtin_amdgcn_perm(__float_as_uint((float)(int8_t)(pair >> 8)), __float_as_uint((float)(int8_t)pair),
+                                     0x07060302u);
     }
-    return s;
+    return __builtin_bit_cast(v8bf16, d);
 }
 
 // 64 tokens x 256 channels, for batches whose 256-token tiles would not fill the GPU or would mostly compute
 // padding: 256 threads, 72 KiB of LDS, two workgroups per CU; each of the 4 wavefronts takes 64 channels of all
 // 64 tokens.  The codes go to LDS as they are, both operands without passing registers, in three stages
-// with two in flight; a transposing read and the permute above make the fragments.
+// with two in flight; a transposing read and the conversion above make the fragments.
 //   codes   64 rows of 256 bytes as in memory, 16-byte chunk c of row n at c ^ n % 16, so that the rows
 //           of a transposing read (16 lanes: 8 rows x 16 bytes) fall on distinct banks;
 //   tokens  rows of 128 bytes (64 values), chunk c of row r at c ^ swz(r).
@@ -257,7 +244,6 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
         for (int b = 0; b < 4; ++b) fb[kk][b] = *reinterpret_cast<const v8bf16 *>(st + b * 2048);
     };
     v4f acc[4][4];
-    float asum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
@@ -270,8 +256,6 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
             for (int b = 0; b < 4; ++b)
                 acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, fb[kk][b], acc[a][b], 0, 0, 0);
         }
-#pragma unroll
-        for (int b = 0; b < (a0 ? 0 : 4); ++b) asum[b] = add8(fb[kk][b], asum[b]);
     };
     auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
 
@@ -305,17 +289,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
 
-    // lane: token lane % 16 of block b (all of its sum over the four fq), channels
-    // 16 (4 w + a) + 4 fq + v
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        asum[b] += __shfl_xor(asum[b], 16);
-        asum[b] += __shfl_xor(asum[b], 32);
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[a][b][v] = __builtin_fmaf(asum[b], -kOffset, acc[a][b][v]);
-    }
+    // lane: token lane % 16 of block b, channels 16 (4 w + a) + 4 fq + v
     if (slot >= 0) {
         float *dst = p.part + (int64_t)slot * (TM * BC);
 #pragma unroll
@@ -329,14 +303,15 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
         }
         return;
     }
-    // the rotation as in the kernel above: channel bits 0, 1 in v, 2, 3 across lanes, 4, 5 in a; 6 and 7 across the
+    // the rotation: channel bits 0, 1 in v, 2, 3 across lanes, 4, 5 in a; 6 and 7 across the
     // four waves
     const int lg = p.lg;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-            float x0 = acc[a][b][0], x1 = acc[a][b][1], x2 = acc[a][b][2], x3 = acc[a][b][3];
+            float x0 = acc[a][b][0] * p.norm, x1 = acc[a][b][1] * p.norm, x2 = acc[a][b][2] * p.norm,
+                  x3 = acc[a][b][3] * p.norm;
             if (lg > 0) {
                 bfly(x0, x1);
                 bfly(x2, x3);
@@ -413,7 +388,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 // four groups of 8 a step (two halves of the contraction, 128 tokens each), one ahead of the products.  The barrier
 // stands before the last group: it publishes the next step, whose first group is read under those products, and
 // frees this one, whose last group is in registers by then.  The loads of step t + 2 go out one by one, after
-// each half of three groups' products.  Wavefront w sums tokens 32 w .. + 31 for the correction.
+// each half of three groups' products.
 // 4096 tokens 5376 x 16128: 541 us, 1310 TFLOP/s, matrix core 61% busy at 2.05 GHz, LDS nearly conflict-free (a library's
 // bf16 product of that shape, operands ready in bf16: 887); without the loads (timing only) 14% less.
 // Alternatives, us for that call and for the gated block's at 2048 tokens 5120 x 25600 (593, 1311 as it is):
@@ -493,7 +468,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
     const int bwhere = WB + frow * 128;
     const int bpos[2] = {16 * (fq ^ swz(frow)), 16 * ((4 + fq) ^ swz(frow))};
     v2i raw[2];
-    v8bf16 fb[2][8], fs[2];
+    v8bf16 fb[2][8];
     auto read_codes = [&](int stage, int kk) {
         const uint8_t *st = smem + stage * GSTAGE + kk * (32 * BC);
 #pragma unroll
@@ -505,13 +480,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 #pragma unroll
         for (int b = 0; b < 8; ++b) fb[h][b] = *reinterpret_cast<const v8bf16 *>(st + b * 2048);
     };
-    auto read_own = [&](int stage, int kk) {
-        const uint8_t *st = smem + stage * GSTAGE + bwhere + bpos[kk] + w * 4096;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) fs[b] = *reinterpret_cast<const v8bf16 *>(st + b * 2048);
-    };
     v4f acc[2][16];
-    float asum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -531,10 +500,6 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
             }
         }
     };
-    auto sum_own = [&] {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) asum[b] = add8(fs[b], asum[b]);
-    };
 
 #pragma unroll
     for (int i = 0; i < 2 * LPS + 2; ++i) issue(i % LPS);
@@ -547,7 +512,6 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
         const int next = st == NST - 1 ? 0 : st + 1;
         v8bf16 fa[2];
         read_tokens(st, 0, 1);
-        read_own(st, 0);
         fence();
 #pragma unroll
         for (int a = 0; a < 2; ++a) fa[a] = codes_to_bf16(raw[a]);
@@ -556,11 +520,9 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
         read_codes(st, 1);
         read_tokens(st, 1, 0);
         fence();
-        sum_own();
         products(fa, 1, 4);
         fence();
         read_tokens(st, 1, 1);
-        read_own(st, 1);
         fence();
 #pragma unroll
         for (int a = 0; a < 2; ++a) fa[a] = codes_to_bf16(raw[a]);
@@ -572,7 +534,6 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
         read_codes(next, 0);
         read_tokens(next, 0, 0);
         fence();
-        sum_own();
         products(fa, 1, 0);
         fence();
         st = next;
@@ -581,24 +542,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
 
-    // the tokens' sums, each from its wave (the four fq together), to all of them
-    float *sums = reinterpret_cast<float *>(smem);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        asum[b] += __shfl_xor(asum[b], 16);
-        asum[b] += __shfl_xor(asum[b], 32);
-        if (fq == 0) sums[32 * w + 16 * b + frow] = asum[b];
-    }
-    __syncthreads();
     // lane: token lane % 16 of block b, channels 32 w + 16 a + 4 fq + v
-#pragma unroll
-    for (int b = 0; b < 16; ++b) {
-        const float s = sums[16 * b + frow] * -kOffset;
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[a][b][v] += s;
-    }
     if (slot >= 0) {
         float *dst = p.part + (int64_t)slot * (BM * BC);
 #pragma unroll
@@ -618,7 +562,8 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
     for (int b = 0; b < 16; ++b) {
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-            float x0 = acc[a][b][0], x1 = acc[a][b][1], x2 = acc[a][b][2], x3 = acc[a][b][3];
+            float x0 = acc[a][b][0] * p.norm, x1 = acc[a][b][1] * p.norm, x2 = acc[a][b][2] * p.norm,
+                  x3 = acc[a][b][3] * p.norm;
             if (lg > 0) {
                 bfly(x0, x1);
                 bfly(x2, x3);
@@ -745,6 +690,8 @@ __global__ void __launch_bounds__(256) grad_join_kernel(GradParams p, int rb)
         }
     }
 #pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= p.norm;
+#pragma unroll
     for (int b = 0; b < 3; ++b)
         if (p.lg > b) {
 #pragma unroll
@@ -787,8 +734,8 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(PrepParams p)
     float s1[8], s2[8], sum1[8], sum2[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        s1[e] = n + e < p.N ? p.sw1[n + e] * kOperandScale : 0.0f;
-        s2[e] = GATED && n + e < p.N ? p.sw2[n + e] * kOperandScale : 0.0f;
+        s1[e] = n + e < p.N ? p.sw1[n + e] : 0.0f;
+        s2[e] = GATED && n + e < p.N ? p.sw2[n + e] : 0.0f;
         sum1[e] = sum2[e] = 0.0f;
     }
     // 16 bytes at any element: rows of an odd N start at odd ones, which a vector load takes.  (2001 x 14366: 49 us,
@@ -1023,7 +970,7 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
     p.T_dp = pl.T_dp;
     p.S = pl.S;
     p.next = g.next;
-    p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g))) * kTileUnscale;
+    p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g)));
     const int T = pl.tiles_m * pl.tiles_c, U = pl.T_dp + (T - pl.T_dp) * pl.S;
     const dim3 grid((unsigned)((U + 7) & ~7));
     if (pl.bm == 64) hipLaunchKernelGGL(grad_tile_kernel, grid, dim3(256), 0, stream, p);
