@@ -224,8 +224,8 @@ size_t convrot_workspace_bytes_ffn(int64_t M, int64_t F, int64_t K);
  * the gradients' signs.  They are taken in a fixed order: the same call gives the same bits.  The
  * sums must be finite in fp32; terms |dz * w_scale| below 2^-126 lose precision.
  *   M == 0: dbias is zeros.  N == 0 or K out of range: CONVROT_ERR_SHAPE (there is no gradient to
- *   form).  N < CONVROT_BACKWARD_MAX_N.  An overlap of dx, dx_add and dbias other than dx == dx_add:
- *   CONVROT_ERR_OVERLAP.  dx may be dy's own buffer.
+ *   form).  N < CONVROT_BACKWARD_MAX_N.  An overlap of dx and dx_add other than dx == dx_add, or of dbias with
+ *   dx, dx_add, dy or the pre that is read: CONVROT_ERR_OVERLAP.  dx may be dy's or pre's own buffer.
  * workspace: convrot_workspace_bytes_backward(M, N, K) bytes, 256-byte aligned, required; scratch.
  */
 int convrot_linear_act_backward(const void *dy, const void *pre, int64_t M, int64_t N, int64_t K, int group,

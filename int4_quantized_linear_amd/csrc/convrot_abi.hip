@@ -350,10 +350,16 @@ int check_grad(const char *who, const convrot::GradArgs &g, int64_t K, int group
         !aligned(g.sw2, 4) || !aligned(g.add, 16) || !aligned(g.dx, 16) || !aligned(g.db1, 4) || !aligned(g.db2, 4))
         return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
     const size_t dx_bytes = (size_t)g.M * (size_t)K * 2, db_bytes = (size_t)g.N * 4;
-    if ((g.add != g.dx && overlap(g.add, dx_bytes, g.dx, dx_bytes)) || overlap(g.db1, db_bytes, g.dx, dx_bytes) ||
-        overlap(g.db2, db_bytes, g.dx, dx_bytes) || overlap(g.db1, db_bytes, g.db2, db_bytes) ||
-        overlap(g.db1, db_bytes, g.add, dx_bytes) || overlap(g.db2, db_bytes, g.add, dx_bytes))
-        return fail(CONVROT_ERR_OVERLAP, "%s: outputs overlap each other or dx_add (only dx_add == dx is allowed)", who);
+    const size_t dy_bytes = (size_t)g.M * (size_t)g.N * 2, pre_bytes = dy_bytes * (gated ? 2 : 1);
+    // with few tokens a bias gradient is written while other workgroups still read dy and pre
+    auto shared = [&](const float *db) {
+        return overlap(db, db_bytes, g.dx, dx_bytes) || overlap(db, db_bytes, g.add, dx_bytes) ||
+               overlap(db, db_bytes, g.dy, dy_bytes) || overlap(db, db_bytes, g.pre, pre_bytes);
+    };
+    if ((g.add != g.dx && overlap(g.add, dx_bytes, g.dx, dx_bytes)) || shared(g.db1) || shared(g.db2) ||
+        overlap(g.db1, db_bytes, g.db2, db_bytes))
+        return fail(CONVROT_ERR_OVERLAP, "%s: dx overlaps dx_add (only dx_add == dx is allowed), or a bias gradient another "
+                    "array of the call", who);
     const size_t need = convrot::grad_workspace_bytes(g.M, g.N, (int)K, gated);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
         return fail(CONVROT_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of at least %zu bytes (got %zu)", who,
@@ -632,11 +638,13 @@ int convrot_ffn_gated_backward(const void *dy, const void *pre, int64_t M, int64
     if ((rc = check_grad(who, up, K, group, true, workspace, L.steps_dh))) return rc;
     if ((rc = check_grad(who, down, F, group_h, false, workspace, L.steps_dh))) return rc;
     const size_t dx_bytes = (size_t)M * (size_t)K * 2;
+    // what the two steps' own checks do not see: each step knows its own bias gradients only, and dy is the first's
     if (overlap(ddown_bias, (size_t)K * 4, dx, dx_bytes) || overlap(ddown_bias, (size_t)K * 4, dx_add, dx_bytes) ||
         overlap(ddown_bias, (size_t)K * 4, dgate_bias, (size_t)F * 4) ||
         overlap(ddown_bias, (size_t)K * 4, dup_bias, (size_t)F * 4) ||
-        overlap(ddown_bias, (size_t)K * 4, pre, (size_t)M * (size_t)F * 4))
-        return fail(CONVROT_ERR_OVERLAP, "%s: ddown_bias overlaps another array of the call", who);
+        overlap(ddown_bias, (size_t)K * 4, pre, (size_t)M * (size_t)F * 4) ||
+        overlap(dgate_bias, (size_t)F * 4, dy, dx_bytes) || overlap(dup_bias, (size_t)F * 4, dy, dx_bytes))
+        return fail(CONVROT_ERR_OVERLAP, "%s: a bias gradient overlaps another array of the call", who);
     if (!sums) {
         down.next.pre = up.pre;
         down.next.sw_gate = gate_scale;
