@@ -110,7 +110,8 @@ __device__ __forceinline__ void swap16f(float &a, float &b)
 // 16 bytes per lane, global -> LDS (lane l to byte lds + 16 l).  Written out because the compiler, which knows the
 // builtin to write LDS, waits for every such load in flight before each transposing read: one load latency
 // a step.  The kernel's own s_waitcnt and barrier order the two.  It has no output register, and a load the
-// compiler issues itself is only waited for longer than it counts.  (Nothing else in the kernel uses m0.)
+// compiler issues itself is only waited for longer than it counts.  It writes m0, which the compiler reserves and does
+// not let an asm declare, so nothing the compiler emits in these kernels may use m0 (tested on their assembly).
 __device__ __forceinline__ void dma16(v4u rsrc, uint32_t lds, uint32_t off, uint32_t soff)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
