@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 // 128 tokens, which read half as much LDS and convert twice as much, 602, 1335; the loads after
 // the first and third quarter of a group 603, 1337, or two at once at its end 600, 1321; their descriptors kept
 // ready instead of formed at each load 617, 1368.
+// The K loop holds everything in registers; the epilogue spills 26 of them (104 bytes a lane), once a tile.
 __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 {
     constexpr int NST = 3, XL = 4, WL = 2, LPS = XL + WL;    // loads per step and wavefront
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 #pragma unroll
         for (int b = 0; b < 16; ++b) acc[a][b] = v4f{};
     auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
-    // the products of group h; loads i0, i0 + 1 after the first and third quarter (i0 < 0: none)
+    // the products of group h; loads i0, i0 + 1 after its first and second half (i0 < 0: none)
     auto products = [&](const v8bf16 (&fa)[2], int h, int i0) {
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
