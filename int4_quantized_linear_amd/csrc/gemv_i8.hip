@@ -22,6 +22,7 @@
 #include "activation.hpp"
 #include "device_common.hpp"
 #include "launchers.hpp"
+#include "tile_common.hpp"
 
 namespace convrot {
 namespace {
@@ -32,10 +33,6 @@ constexpr int MAX_NW = 8;
 constexpr int TARGET_WAVES = 400;        // about 1.5 wavefronts per CU in all
 constexpr int MIN_CHUNKS = 5;            // per wavefront, to amortise its ramp-up and drain
 constexpr int LDS_BUDGET = 160 * 1024;
-constexpr uint32_t OOB = 0x80000000u;    // buffer offset past num_records -> loads return 0
-constexpr int NUM_RECORDS = 0x7ffffff0;
-
-typedef __attribute__((address_space(3))) void lds_void;
 
 struct GemvParams {
     const int8_t *xq;
@@ -54,9 +51,6 @@ struct GemvParams {
 // (2 x 25600 x 5120, 262 MB: 46 us with 1 token, 47 with 12, 5.6 TB/s, the weight stream.)
 template <Epi E>
 __host__ __device__ constexpr int features_per_block() { return E == Epi::Gated ? 8 : 16; }
-
-// s_waitcnt immediate waiting for vmcnt <= n only (gfx9 encoding)
-constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }
 
 template <int RB>
 constexpr int stage_bytes() { return (16 * RB + 16) * KC; }   // weight rows + 16 token rows

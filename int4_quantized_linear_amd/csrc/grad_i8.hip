@@ -107,6 +107,38 @@ __device__ __forceinline__ void swap16f(float &a, float &b)
     b = __uint_as_float(r[1]);
 }
 
+// A 16 x 16 block of sums (lane: channels 4 (lane / 16) + v of token lane % 16), normalised and rotated over its 16
+// channels: bits 0 and 1 in registers, 2 and 3 across lanes.
+__device__ __forceinline__ void rotate16(v4f &x, float norm, int lg)
+{
+    float x0 = x[0] * norm, x1 = x[1] * norm, x2 = x[2] * norm, x3 = x[3] * norm;
+    if (lg > 0) {
+        bfly(x0, x1);
+        bfly(x2, x3);
+    }
+    if (lg > 1) {
+        bfly(x0, x2);
+        bfly(x1, x3);
+    }
+    if (lg > 2) {
+        swap16f(x0, x1);
+        bfly(x0, x1);
+        swap16f(x0, x1);
+        swap16f(x2, x3);
+        bfly(x2, x3);
+        swap16f(x2, x3);
+    }
+    if (lg > 3) {
+        swap32f(x0, x1);
+        bfly(x0, x1);
+        swap32f(x0, x1);
+        swap32f(x2, x3);
+        bfly(x2, x3);
+        swap32f(x2, x3);
+    }
+    x = v4f{x0, x1, x2, x3};
+}
+
 // 16 bytes per lane, global -> LDS (lane l to byte lds + 16 l).  Written out because the compiler, which knows the
 // builtin to write LDS, waits for every such load in flight before each transposing read: one load latency
 // a step.  The kernel's own s_waitcnt and barrier order the two.  It has no output register, and a load the
@@ -119,6 +151,42 @@ __device__ __forceinline__ void dma16(v4u rsrc, uint32_t lds, uint32_t off, uint
                  : "s"(lds), "v"(off), "s"(rsrc), "s"(soff)
                  : "memory");
 }
+
+// The load side of a tile's K loop: the next step to request, its codes' address and the rows left there, all in
+// scalar registers.  Rows past N lie past the descriptor's end and read zeros, as everything past the last
+// step does.
+struct StepLoads {
+    int t, rows;
+    uint64_t w, x;             // codes of the step, tokens of the tile
+
+    __device__ __forceinline__ StepLoads(const GradParams &p, int kb, int m0, int c0)
+    {
+        const int first = kb >= p.nt1 ? p.nt1 : 0;
+        t = kb;
+        rows = p.N - (kb - first) * BN;
+        w = reinterpret_cast<uint64_t>((first ? p.w2 : p.w1) + (int64_t)(kb - first) * BN * p.K + c0);
+        x = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
+    }
+    __device__ __forceinline__ v4u codes(int ke, int K, int c0) const
+    {
+        const int records = t >= ke ? 0 : rows >= BN ? NUM_RECORDS : rows * K - c0;
+        return v4u{(uint32_t)w, (uint32_t)(w >> 32) & 0xffffu, (uint32_t)records, 0x00020000u};
+    }
+    __device__ __forceinline__ v4u tokens(int ke) const
+    {
+        return v4u{(uint32_t)x, (uint32_t)(x >> 32) & 0xffffu, t < ke ? (uint32_t)NUM_RECORDS : 0u, 0x00020000u};
+    }
+    __device__ __forceinline__ void advance(const GradParams &p, int c0)
+    {
+        ++t;
+        rows -= BN;
+        w += (uint64_t)(BN * p.K);
+        if (t == p.nt1) {
+            rows = p.N;
+            w = reinterpret_cast<uint64_t>(p.w2 + c0);
+        }
+    }
+};
 
 // Transposing LDS read: of each 16 lanes, lane 2 r and 2 r + 1 name the two 8-byte halves of row r's 16 bytes,
 // and lane c gets byte c of the 8 rows.  (Not a template, like the two below: the host pass drops a kernel
@@ -195,31 +263,16 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
         const int n = 4 * (4 * i + w) + (lane >> 4), c = 16 * ((lane & 15) ^ (n & 15));
         offw[i] = c0 + c < K ? (uint32_t)(n * K + c) : OOB;
     }
-    // The load side: the next step to issue, its codes' address and the rows left there, all in scalar
-    // registers.  Rows past N lie past the descriptor's end and read zeros, as everything past the last
-    // step does.
-    const uint64_t xbase = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(const lds_void *)smem + (uint32_t)w * 1024u;
-    int ld_t = kb, ld_rows = p.N - (kb - (kb >= p.nt1 ? p.nt1 : 0)) * BN;
-    uint64_t ld_w = reinterpret_cast<uint64_t>((kb >= p.nt1 ? p.w2 : p.w1) +
-                                               (int64_t)(kb - (kb >= p.nt1 ? p.nt1 : 0)) * BN * K + c0);
+    StepLoads ld(p, kb, m0, c0);
     uint32_t ld_lds = lds0;
     auto issue = [&]() {
-        const int records = ld_t >= ke ? 0 : ld_rows >= BN ? NUM_RECORDS : ld_rows * K - c0;
-        const v4u rw = {(uint32_t)ld_w, (uint32_t)(ld_w >> 32) & 0xffffu, (uint32_t)records, 0x00020000u};
-        const v4u rx = {(uint32_t)xbase, (uint32_t)(xbase >> 32) & 0xffffu, ld_t < ke ? (uint32_t)NUM_RECORDS : 0u,
-                        0x00020000u};
+        const v4u rw = ld.codes(ke, K, c0), rx = ld.tokens(ke);
 #pragma unroll
         for (int i = 0; i < WL; ++i) dma16(rw, ld_lds + 4096 * i, offw[i], 0);
 #pragma unroll
-        for (int i = 0; i < XL; ++i) dma16(rx, ld_lds + WB + 4096 * i, offx[i], (uint32_t)ld_t * (BN * 2));
-        ++ld_t;
-        ld_rows -= BN;
-        ld_w += (uint64_t)(BN * K);
-        if (ld_t == p.nt1) {
-            ld_rows = p.N;
-            ld_w = reinterpret_cast<uint64_t>(p.w2 + c0);
-        }
+        for (int i = 0; i < XL; ++i) dma16(rx, ld_lds + WB + 4096 * i, offx[i], (uint32_t)ld.t * (BN * 2));
+        ld.advance(p, c0);
         ld_lds = ld_lds == lds0 + (NST - 1) * TSTAGE ? lds0 : ld_lds + TSTAGE;
     };
 
@@ -310,35 +363,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            float x0 = acc[a][b][0] * p.norm, x1 = acc[a][b][1] * p.norm, x2 = acc[a][b][2] * p.norm,
-                  x3 = acc[a][b][3] * p.norm;
-            if (lg > 0) {
-                bfly(x0, x1);
-                bfly(x2, x3);
-            }
-            if (lg > 1) {
-                bfly(x0, x2);
-                bfly(x1, x3);
-            }
-            if (lg > 2) {
-                swap16f(x0, x1);
-                bfly(x0, x1);
-                swap16f(x0, x1);
-                swap16f(x2, x3);
-                bfly(x2, x3);
-                swap16f(x2, x3);
-            }
-            if (lg > 3) {
-                swap32f(x0, x1);
-                bfly(x0, x1);
-                swap32f(x0, x1);
-                swap32f(x2, x3);
-                bfly(x2, x3);
-                swap32f(x2, x3);
-            }
-            acc[a][b] = v4f{x0, x1, x2, x3};
-        }
+        for (int a = 0; a < 4; ++a) rotate16(acc[a][b], p.norm, lg);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             if (lg > 4 + s) {
@@ -433,31 +458,15 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
         const int n = 4 * (8 * i + w) + (lane >> 4), c = 16 * ((lane & 15) ^ (n & 15));
         offw[i] = c0 + c < K ? (uint32_t)(n * K + c) : OOB;
     }
-    // the load side, as in the kernel above; load i of a step: its codes first
-    const uint64_t xbase = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
+    // load i of a step: its codes first
     const uint32_t lds0 = (uint32_t)(uintptr_t)(const lds_void *)smem + (uint32_t)w * 1024u;
-    int ld_t = kb, ld_rows = p.N - (kb - (kb >= p.nt1 ? p.nt1 : 0)) * BN;
-    uint64_t ld_w = reinterpret_cast<uint64_t>((kb >= p.nt1 ? p.w2 : p.w1) +
-                                               (int64_t)(kb - (kb >= p.nt1 ? p.nt1 : 0)) * BN * K + c0);
+    StepLoads ld(p, kb, m0, c0);
     uint32_t ld_lds = lds0;
     auto issue = [&](int i) {
-        if (i < WL) {
-            const int records = ld_t >= ke ? 0 : ld_rows >= BN ? NUM_RECORDS : ld_rows * K - c0;
-            const v4u rw = {(uint32_t)ld_w, (uint32_t)(ld_w >> 32) & 0xffffu, (uint32_t)records, 0x00020000u};
-            dma16(rw, ld_lds + 8192 * i, offw[i], 0);
-        } else {
-            const v4u rx = {(uint32_t)xbase, (uint32_t)(xbase >> 32) & 0xffffu, ld_t < ke ? (uint32_t)NUM_RECORDS : 0u,
-                            0x00020000u};
-            dma16(rx, ld_lds + WB + 8192 * (i - WL), offx[i - WL], (uint32_t)ld_t * (BN * 2));
-        }
+        if (i < WL) dma16(ld.codes(ke, K, c0), ld_lds + 8192 * i, offw[i], 0);
+        else dma16(ld.tokens(ke), ld_lds + WB + 8192 * (i - WL), offx[i - WL], (uint32_t)ld.t * (BN * 2));
         if (i < LPS - 1) return;
-        ++ld_t;
-        ld_rows -= BN;
-        ld_w += (uint64_t)(BN * K);
-        if (ld_t == p.nt1) {
-            ld_rows = p.N;
-            ld_w = reinterpret_cast<uint64_t>(p.w2 + c0);
-        }
+        ld.advance(p, c0);
         ld_lds = ld_lds == lds0 + (NST - 1) * GSTAGE ? lds0 : ld_lds + GSTAGE;
     };
 
@@ -563,35 +572,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 #pragma unroll
     for (int b = 0; b < 16; ++b) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            float x0 = acc[a][b][0] * p.norm, x1 = acc[a][b][1] * p.norm, x2 = acc[a][b][2] * p.norm,
-                  x3 = acc[a][b][3] * p.norm;
-            if (lg > 0) {
-                bfly(x0, x1);
-                bfly(x2, x3);
-            }
-            if (lg > 1) {
-                bfly(x0, x2);
-                bfly(x1, x3);
-            }
-            if (lg > 2) {
-                swap16f(x0, x1);
-                bfly(x0, x1);
-                swap16f(x0, x1);
-                swap16f(x2, x3);
-                bfly(x2, x3);
-                swap16f(x2, x3);
-            }
-            if (lg > 3) {
-                swap32f(x0, x1);
-                bfly(x0, x1);
-                swap32f(x0, x1);
-                swap32f(x2, x3);
-                bfly(x2, x3);
-                swap32f(x2, x3);
-            }
-            acc[a][b] = v4f{x0, x1, x2, x3};
-        }
+        for (int a = 0; a < 2; ++a) rotate16(acc[a][b], p.norm, lg);
         if (lg > 4) {
             const v4f x = acc[0][b], y = acc[1][b];
             acc[0][b] = x + y;
