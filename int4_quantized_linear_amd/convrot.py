@@ -3,12 +3,16 @@ linear runs in the library's HIP kernels; torch provides device memory and the c
 
 Raises ``ConvRotError`` when the library rejects a call and ``ImportError``-style
 ``RuntimeError`` when the built library is missing -- there is no fallback path.
+
+Returned tensors carry no autograd history.  The fused linears' gradients are calls of their own
+(``linear_act_backward`` and so on); a training loop pairs the two in a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+import warnings
 
 import torch
 
@@ -232,6 +236,17 @@ def _tokens(x, xq, x_scale, K: int, dev: torch.device) -> int:
     return M
 
 
+def _no_history(name: str, *inputs: torch.Tensor | None):
+    """Warns where autograd would take the result for a constant: inputs that require a gradient, outside
+    torch.no_grad() and torch.autograd.Function (which turns recording off in its forward)."""
+    for t in inputs:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            warnings.warn("%s returns a tensor without autograd history, so no gradient reaches its inputs; pair it with "
+                          "%s_backward in a torch.autograd.Function, or call it under torch.no_grad()" % (name, name),
+                          stacklevel=3)
+            return
+
+
 def linear_act(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, bias: torch.Tensor | None = None,
                act: str = "none", residual: torch.Tensor | None = None, group: int = 256,
                xq: torch.Tensor | None = None, x_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -239,7 +254,9 @@ def linear_act(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, 
     """INT8 ConvRot linear with its activation and residual in the epilogue:
     z = (q(xR) . q(wR)^T) * sx * sw + bias,  y = bf16(act(z) + residual).  x (or xq, x_scale) and the
     weight as in linear(); act one of ACTS; residual bf16 [M, N], may be ``out`` (added in place).
-    save_pre=True returns (y, pre) with pre = bf16(z) [M, N] for linear_act_backward."""
+    save_pre=True returns (y, pre) with pre = bf16(z) [M, N] for linear_act_backward; the result itself has no
+    autograd history."""
+    _no_history("linear_act", x, bias, residual)
     code = _act_code(act)
     N, K = wq.shape
     dev = wq.device
@@ -265,7 +282,8 @@ def linear_gated(x: torch.Tensor | None, wq_gate: torch.Tensor, gate_scale: torc
                  x_scale: torch.Tensor | None = None, out: torch.Tensor | None = None, save_pre: bool = False):
     """Gate and up projections of one input, the activation and the product in one kernel:
     h = bf16(act(g) * u) with g and u the INT8 ConvRot linears of x.  save_pre=True returns (h, pre)
-    with pre = bf16 [2, M, N], g then u, for linear_gated_backward."""
+    with pre = bf16 [2, M, N], g then u, for linear_gated_backward; the result itself has no autograd history."""
+    _no_history("linear_gated", x, bias_gate, bias_up)
     code = _act_code(act)
     N, K = wq_gate.shape
     dev = wq_gate.device
@@ -295,7 +313,9 @@ def ffn_gated(x: torch.Tensor, wq_gate: torch.Tensor, gate_scale: torch.Tensor, 
     """Gated feed-forward block on INT8 ConvRot weights: h = bf16(act(g) * u) as in linear_gated
     (gate, up [F, K], prepared with ``group``), then y = bf16(linear(h) + bias_down + residual) (down
     [K, F], prepared with ``group_h``).  residual bf16 [M, K], may be ``out``.  save_pre=True returns
-    (y, pre) with pre = bf16 [2, M, F], g then u, for ffn_gated_backward."""
+    (y, pre) with pre = bf16 [2, M, F], g then u, for ffn_gated_backward; the result itself has no autograd
+    history."""
+    _no_history("ffn_gated", x, bias_gate, bias_up, bias_down, residual)
     code = _act_code(act)
     F, K = wq_gate.shape
     dev = wq_gate.device
