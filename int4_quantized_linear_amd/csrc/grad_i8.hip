@@ -223,9 +223,9 @@ __device__ __forceinline__ v8bf16 codes_to_bf16(v2i raw)
 //   tokens  rows of 128 bytes (64 values), chunk c of row r at c ^ swz(r).
 // One barrier a step: it publishes the next stage and frees this one, which is refilled behind it.
 // (With the codes converted and transposed in registers, then written to LDS as bf16, us: 300 tokens 5376 x 2688
-// 38 against 33, 2688 x 2 * 5376 54 / 46; 512 tokens 5120 x 5120 62 / 52.)  12 tokens 5120 x 8192: 13 us,
-// the codes' stream and one load latency; 300 tokens 5376 x 2688: 21 us, 2688 x 2 * 5376: 30 us, a step's
-// LDS reads and barrier.
+// 38 against 33, 2688 x 2 * 5376 54 / 46; 512 tokens 5120 x 5120 62 / 52.)  12 tokens 5120 x 8192: 12 us,
+// the codes' stream and one load latency, 5120 x 2 * 25600: 54 us, 4.8 TB/s; 300 tokens 5376 x 2688: 20 us, matrix core 13%
+// busy, 2688 x 2 * 5376: 28 us, 23%: a step's LDS reads and barrier.
 __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 {
     constexpr int TM = 64, NST = 3;
@@ -415,9 +415,10 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 // stands before the last group: it publishes the next step, whose first group is read under those products, and
 // frees this one, whose last group is in registers by then.  The loads of step t + 2 go out one by one, after
 // each half of three groups' products.
-// 4096 tokens 5376 x 16128: 541 us, 1310 TFLOP/s, matrix core 61% busy at 2.05 GHz, LDS nearly conflict-free (a library's
+// 4096 tokens 5376 x 16128: 553 us, 1280 TFLOP/s, matrix core 62% busy at 1.97 GHz, LDS nearly conflict-free (a library's
 // bf16 product of that shape, operands ready in bf16: 887); without the loads (timing only) 14% less.
-// Alternatives, us for that call and for the gated block's at 2048 tokens 5120 x 25600 (593, 1311 as it is):
+// Alternatives, us for that call and for the gated block's at 2048 tokens 5120 x 25600 (593, 1311 as it was, on a faster
+// card and with the codes as denormals):
 // codes converted and transposed in registers and written to LDS as bf16 625, 1392; wavefronts of 64 channels x
 // 128 tokens, which read half as much LDS and convert twice as much, 602, 1335; the loads after
 // the first and third quarter of a group 603, 1337, or two at once at its end 600, 1321; their descriptors kept
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 
 // Split tiles: the S partial sums of a token's 256 channels, added in slice order (the same order at
 // every call), then the rotation, dx_add and the rounding.  32 lanes per token, 8 channels each:
-// channel bits 0 .. 2 in registers, 3 .. 7 across lanes.  Bound by the partial sums' read: 12 us for 4096 x 5376's
+// channel bits 0 .. 2 in registers, 3 .. 7 across lanes.  Bound by the partial sums' read: 14 us for 4096 x 5376's
 // last round, 5 to 8 us (about two memory latencies) for a few hundred tokens.
 __global__ void __launch_bounds__(256) grad_join_kernel(GradParams p, int rb)
 {
@@ -705,7 +706,7 @@ struct PrepParams {
 };
 
 // A workgroup takes 256 columns and a chunk of rows: 32 lanes of 8 columns, 8 rows at a time.
-// Columns from N to Np are zeros.  Bound by memory: 4096 x 16128 with an activation 77 us (396 MB, 5.1 TB/s).
+// Columns from N to Np are zeros.  Bound by memory: 4096 x 16128 with an activation 76 us (396 MB, 5.2 TB/s).
 template <bool GATED>
 __global__ void __launch_bounds__(256) grad_prep_kernel(PrepParams p)
 {
