@@ -57,7 +57,8 @@ typedef enum convrot_status {
     CONVROT_ERR_HIP = 8,       /* a HIP runtime call or kernel launch failed                     */
     CONVROT_ERR_DEVICE = 9,    /* the current device is not gfx950                               */
     CONVROT_ERR_ACT = 10,      /* unknown activation code                                        */
-    CONVROT_ERR_OVERLAP = 11   /* an output overlaps another array it must not (see the call)   */
+    CONVROT_ERR_OVERLAP = 11,  /* an output overlaps another array it must not (see the call)   */
+    CONVROT_ERR_SCORE = 12     /* unknown router score code                                      */
 } convrot_status;
 
 enum { CONVROT_DTYPE_F32 = 0, CONVROT_DTYPE_BF16 = 1 };
@@ -261,6 +262,127 @@ int convrot_ffn_gated_backward(const void *dy, const void *pre, int64_t M, int64
 size_t convrot_workspace_bytes_backward(int64_t M, int64_t N, int64_t K);
 size_t convrot_workspace_bytes_gated_backward(int64_t M, int64_t N, int64_t K);
 size_t convrot_workspace_bytes_ffn_backward(int64_t M, int64_t F, int64_t K);
+
+/*
+ * Mixture of experts.  A router picks `top` experts for each token; the layer runs each token through its experts'
+ * gated blocks and adds up the results.  Weights of E experts are stacked: int8 [E, N, K] and fp32 [E, N], as
+ * convrot_prepare_weight(bits = 8) gives them for the [E N, K] rows.
+ * E (and the groups of convrot_linear_grouped) is 1 .. CONVROT_MAX_GROUPS, top 1 .. min(E, CONVROT_MOE_MAX_TOP), and M top (the
+ * rows of the grouped calls) below CONVROT_GROUPED_MAX_ROWS; else CONVROT_ERR_SHAPE.  The calls need nothing from the
+ * host that depends on the routing, so they can be captured into a graph and replayed on other routings.
+ */
+#define CONVROT_MAX_GROUPS 1024
+#define CONVROT_MOE_MAX_TOP 32
+#define CONVROT_GROUPED_MAX_ROWS 67108864
+
+enum { CONVROT_SCORE_SOFTMAX = 0, CONVROT_SCORE_SIGMOID = 1 };
+
+/*
+ * Router: logits [M, E] fp32 or bf16 -> experts int32 [M, top] and weights fp32 [M, top].
+ *   s = softmax(logits) or sigmoid(logits) over the E experts (score CONVROT_SCORE_*)
+ *   key = the logit, or with bias (fp32 [E] or NULL, for instance one that balances the experts' load) s + bias
+ *   experts = the top largest keys, in falling order, ties to the lowest index; keys are compared exactly (in 64 bits with a
+ *   bias).  weights[j] = scale * s[experts[j]], or with normalize != 0  scale * s[experts[j]] / (their sum over j).
+ * A logit of -inf (or a bias of -inf) masks its expert.  Where fewer than top are left, the rest of the row is expert -1 with
+ * weight 0.  A NaN among a row's logits makes the row's weights NaN, as does +inf under a softmax; its experts stay
+ * distinct and in range.
+ * Pointers need only their elements' alignment here and in the backward call.  M == 0 is a no-op.
+ */
+int convrot_moe_route(const void *logits, int dtype, int64_t M, int64_t E, int top, int score, int normalize,
+                      float scale, const float *bias, int32_t *experts, float *weights, hipStream_t stream);
+
+/*
+ * Gradient of the logits from that of the weights, the choice held fixed (the bias has none):
+ *   dlogits [M, E] in the logits' type, from dweights fp32 [M, top] and the experts the forward call chose (-1, or any
+ *   other value outside [0, E): no part; the same expert twice in a row: both parts).
+ * dlogits may be logits' own buffer; any other overlap of it with an input returns CONVROT_ERR_OVERLAP.
+ */
+int convrot_moe_route_backward(const float *dweights, const void *logits, int dtype, int64_t M, int64_t E, int top,
+                               int score, int normalize, float scale, const int32_t *experts, void *dlogits,
+                               hipStream_t stream);
+
+/*
+ * INT8 ConvRot linear of rows sorted by group, each group through a weight of its own:
+ *   y[r] = convrot_linear(x[r]) with wq[e], w_scale[e]   for offsets[e] <= r < offsets[e + 1],  bit for bit
+ *   x bf16/fp32 [rows, K], or x = NULL and xq int8 [rows, K], x_scale fp32 [rows], as in convrot_linear;
+ *   offsets int32 [groups + 1] in device memory, non-decreasing; groups may be empty.  Rows before offsets[0] and from
+ *   offsets[groups] on belong to no group: their rows of y are left as they were.  (Values outside [0, rows] count as the
+ *   nearer end, a group that starts behind its end is empty, and where groups share rows any of them may give the result.)
+ *   wq int8 [groups, N, K], w_scale fp32 [groups, N]; y bf16 [rows, N]; 1 <= N < CONVROT_GEMM_MAX_N.
+ * workspace: convrot_workspace_bytes_grouped(rows, groups, N, K) bytes, 256-byte aligned; with x = NULL it may be NULL.
+ * An overlap of y with xq, x_scale or offsets returns CONVROT_ERR_OVERLAP.
+ */
+int convrot_linear_grouped(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t rows, int64_t N,
+                           int64_t K, int group, const int32_t *offsets, int64_t groups, const int8_t *wq,
+                           const float *w_scale, void *y, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of convrot_linear_grouped; 0 on invalid arguments. */
+size_t convrot_workspace_bytes_grouped(int64_t rows, int64_t groups, int64_t N, int64_t K);
+
+/*
+ * Input gradient of convrot_linear_grouped, as convrot_linear_act_backward takes it (act NONE):
+ *   dx[r] = bf16( ( sum_n bf16(dy[r,n] * w_scale[e,n]) * wq[e,n,:] ) R + dx_add[r] )
+ *   dy bf16 [rows, N]; dx bf16 [rows, K]; dx_add bf16 [rows, K] or NULL, may be dx itself; rows of no group are left as they were.
+ *   1 <= N < CONVROT_BACKWARD_MAX_N.  workspace: convrot_workspace_bytes_grouped_backward bytes, required.
+ * An overlap of dx and dx_add other than dx == dx_add, or of dx and offsets, returns CONVROT_ERR_OVERLAP.
+ */
+int convrot_linear_grouped_backward(const void *dy, int64_t rows, int64_t N, int64_t K, int group,
+                                    const int32_t *offsets, int64_t groups, const int8_t *wq, const float *w_scale,
+                                    const void *dx_add, void *dx, void *workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
+
+/* Workspace bytes of convrot_linear_grouped_backward; 0 on invalid arguments (and for rows == 0). */
+size_t convrot_workspace_bytes_grouped_backward(int64_t rows, int64_t groups, int64_t N, int64_t K);
+
+/*
+ * Gated expert layer: for the slots (m, j) with an expert e = experts[m, j] in [0, E)
+ *   g, u = the gate and up linears of x[m] with expert e's weights;  h = bf16( act(g) * u )
+ *   d[m, j] = linear(h) with expert e's down weight (h rotated in groups of group_h and quantized per slot)
+ *   y[m] = bf16( sum_j weights[m, j] * d[m, j] + residual[m] )    in fp32, j in order
+ * A slot without an expert (one outside [0, E): dropped, or another GPU's) adds nothing; a token with none gets its
+ * residual.  The same expert may stand in several slots of a token.
+ *   x bf16/fp32 [M, K], M K < 2^31; experts int32 [M, top]; weights fp32 [M, top];
+ *   wq_gate, wq_up int8 [E, F, K] (prepared with group), wq_down int8 [E, K, F] (prepared with group_h), their scales
+ *   fp32 [E, F], [E, F], [E, K]; residual bf16 [M, K] or NULL, may be y itself; y bf16 [M, K].
+ *   pre bf16 [2, M, top, F] (g, then u) and d bf16 [M, top, K], or NULL: when given, receive bf16 copies for the
+ *   backward call; rows of slots without an expert are left as they were.  y is the same with and without them.
+ *   F % 64 == 0, K % 64 == 0, both in [64, CONVROT_MAX_K] and multiples of their groups.
+ * workspace: convrot_workspace_bytes_moe_ffn(M, top, E, F, K) bytes, 256-byte aligned, required.
+ * An overlap of y (other than with residual == y), pre or d with each other, x (y may overlap x), residual,
+ * experts or weights returns CONVROT_ERR_OVERLAP.
+ */
+int convrot_moe_ffn_gated(const void *x, int x_dtype, const int32_t *experts, const float *weights, int64_t M, int top,
+                          int64_t E, int64_t F, int64_t K, int group, int group_h, const int8_t *wq_gate,
+                          const float *gate_scale, const int8_t *wq_up, const float *up_scale, const int8_t *wq_down,
+                          const float *down_scale, int act, const void *residual, void *pre, void *d, void *y,
+                          void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of convrot_moe_ffn_gated; 0 on invalid arguments. */
+size_t convrot_workspace_bytes_moe_ffn(int64_t M, int top, int64_t E, int64_t F, int64_t K);
+
+/*
+ * Gradients of convrot_moe_ffn_gated through the frozen experts, the quantizers as the identity:
+ *   dweights[m, j] = sum_k dy[m,k] * d[m,j,k]   (fp32; 0 for a slot without an expert)
+ *   dh = bf16( (bf16(weights[m, j] dy[m] * down_scale) . wq_down) R_h ),  dg = dh * u * act'(g),  du = dh * act(g)
+ *   dx[m] = bf16( sum_j (bf16(dg * gate_scale) . wq_gate + bf16(du * up_scale) . wq_up) R + dx_add[m] )
+ * with the sums in fp32 and in a fixed order (the same call gives the same bits).
+ *   dy bf16 [M, K]; pre, d as the forward call saved them (d may be NULL where dweights is); experts, weights
+ *   and the expert weights as there; dx bf16 [M, K]; dx_add bf16 [M, K] or NULL, may be dx itself (where the forward's residual
+ *   was x, pass dx_add = dy); dweights fp32 [M, top] or NULL.
+ *   F, K < CONVROT_BACKWARD_MAX_N.  M == 0 is a no-op.
+ * workspace: convrot_workspace_bytes_moe_ffn_backward(M, top, E, F, K) bytes, 256-byte aligned, required.
+ * An overlap of dx and dx_add other than dx == dx_add, or of dweights with any other array of the call, returns
+ * CONVROT_ERR_OVERLAP.
+ */
+int convrot_moe_ffn_gated_backward(const void *dy, const void *pre, const void *d, const int32_t *experts,
+                                   const float *weights, int64_t M, int top, int64_t E, int64_t F, int64_t K, int group,
+                                   int group_h, const int8_t *wq_gate, const float *gate_scale, const int8_t *wq_up,
+                                   const float *up_scale, const int8_t *wq_down, const float *down_scale, int act,
+                                   const void *dx_add, void *dx, float *dweights, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of convrot_moe_ffn_gated_backward; 0 on invalid arguments (and for M == 0). */
+size_t convrot_workspace_bytes_moe_ffn_backward(int64_t M, int top, int64_t E, int64_t F, int64_t K);
 
 /* Size of the fixed scratch array convrot_linear_noalloc uses on each GPU (32 MiB). */
 #define CONVROT_NOALLOC_SCRATCH_BYTES 33554432

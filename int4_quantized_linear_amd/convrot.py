@@ -22,11 +22,13 @@ LIB_PATH = os.path.join(_HERE, "libconvrot.so")
 CONVROT_DTYPE_F32, CONVROT_DTYPE_BF16 = 0, 1
 STATUS = {0: "CONVROT_OK", 1: "CONVROT_ERR_NULL", 2: "CONVROT_ERR_SHAPE", 3: "CONVROT_ERR_GROUP",
           4: "CONVROT_ERR_ALIGN", 5: "CONVROT_ERR_DTYPE", 6: "CONVROT_ERR_BITS", 7: "CONVROT_ERR_WORKSPACE",
-          8: "CONVROT_ERR_HIP", 9: "CONVROT_ERR_DEVICE", 10: "CONVROT_ERR_ACT", 11: "CONVROT_ERR_OVERLAP"}
+          8: "CONVROT_ERR_HIP", 9: "CONVROT_ERR_DEVICE", 10: "CONVROT_ERR_ACT", 11: "CONVROT_ERR_OVERLAP",
+          12: "CONVROT_ERR_SCORE"}
+SCORES = {"softmax": 0, "sigmoid": 1}
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 # name -> (argtypes, restype); mirrors include/convrot.h
-P, I64, I, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+P, I64, I, SZ, F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "convrot_prepare_weight": ([P, I, I64, I64, I, I, P, P, P], I),
     "convrot_quantize_act": ([P, I, I64, I64, I, I, P, P, P], I),
@@ -57,6 +59,17 @@ SIGNATURES = {
     "convrot_workspace_bytes_w4a8": ([I64, I64, I64], SZ),
     "convrot_gemm_i8_i32": ([P, P, I64, I64, I64, P, P, SZ, P], I),
     "convrot_gemm_i4_i32": ([P, P, I64, I64, I64, P, P, SZ, P], I),
+    "convrot_moe_route": ([P, I, I64, I64, I, I, I, F32, P, P, P, P], I),
+    "convrot_moe_route_backward": ([P, P, I, I64, I64, I, I, I, F32, P, P, P], I),
+    "convrot_linear_grouped": ([P, I, P, P, I64, I64, I64, I, P, I64, P, P, P, P, SZ, P], I),
+    "convrot_workspace_bytes_grouped": ([I64, I64, I64, I64], SZ),
+    "convrot_linear_grouped_backward": ([P, I64, I64, I64, I, P, I64, P, P, P, P, P, SZ, P], I),
+    "convrot_workspace_bytes_grouped_backward": ([I64, I64, I64, I64], SZ),
+    "convrot_moe_ffn_gated": ([P, I, P, P, I64, I, I64, I64, I64, I, I, P, P, P, P, P, P, I, P, P, P, P, P, SZ, P], I),
+    "convrot_workspace_bytes_moe_ffn": ([I64, I, I64, I64, I64], SZ),
+    "convrot_moe_ffn_gated_backward": ([P, P, P, P, P, I64, I, I64, I64, I64, I, I, P, P, P, P, P, P, I, P, P, P, P, SZ,
+                                        P], I),
+    "convrot_workspace_bytes_moe_ffn_backward": ([I64, I, I64, I64, I64], SZ),
     "convrot_dynamic_group": ([I64, I], I),
     "convrot_last_error": ([], ctypes.c_char_p),
     "convrot_status_string": ([I], ctypes.c_char_p),
@@ -415,6 +428,158 @@ def ffn_gated_backward(dy: torch.Tensor, pre: torch.Tensor, wq_gate: torch.Tenso
              _ptr(gate_scale), _ptr(wq_up), _ptr(up_scale), _ptr(wq_down), _ptr(down_scale), code, _ptr(dx_add),
              _ptr(dx), _ptr(db[0]), _ptr(db[1]), _ptr(db[2]), _ptr(ws), ws.numel())
     return (dx, *db) if bias_grad else dx
+
+
+def _score_code(score: str) -> int:
+    if score not in SCORES:
+        raise ValueError("score is one of %s, got %r" % (", ".join(SCORES), score))
+    return SCORES[score]
+
+
+def moe_route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, score: str = "softmax",
+              normalize: bool = True, scale: float = 1.0):
+    """Router of a mixture of experts: logits [M, E] fp32 or bf16 -> (experts int32 [M, top], weights fp32
+    [M, top]).  The experts are the top scores' (s = softmax or sigmoid of the logits; with bias fp32 [E] those of s +
+    bias), in falling order, ties to the lowest index; the weights scale * s, divided by the chosen ones' sum with
+    normalize.  A logit of -inf masks its expert; slots that find none get expert -1 and weight 0.  The weights have no
+    autograd history: moe_route_backward."""
+    _no_history("moe_route", logits)
+    code = _score_code(score)
+    M, E = logits.shape
+    dev = logits.device
+    _check(dev, logits=(logits, (M, E), _X_DTYPES), bias=(bias, (E,), torch.float32))
+    experts = torch.empty((M, top), dtype=torch.int32, device=dev)
+    weights = torch.empty((M, top), dtype=torch.float32, device=dev)
+    _call_on(dev, "convrot_moe_route", _ptr(logits), _dtype_code(logits), M, E, top, code, int(normalize), scale, _ptr(bias),
+             _ptr(experts), _ptr(weights))
+    return experts, weights
+
+
+def moe_route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, score: str = "softmax",
+                       normalize: bool = True, scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of moe_route's logits (in their type) from that of its weights, dweights fp32 [M, top], the chosen
+    experts held fixed.  out may be logits itself."""
+    code = _score_code(score)
+    M, E = logits.shape
+    top = experts.shape[1]
+    dev = logits.device
+    _check(dev, logits=(logits, (M, E), _X_DTYPES), dweights=(dweights, (M, top), torch.float32),
+           experts=(experts, (M, top), torch.int32), out=(out, (M, E), logits.dtype))
+    dlogits = out if out is not None else torch.empty_like(logits)
+    _call_on(dev, "convrot_moe_route_backward", _ptr(dweights), _ptr(logits), _dtype_code(logits), M, E, top, code,
+             int(normalize), scale, _ptr(experts), _ptr(dlogits))
+    return dlogits
+
+
+def workspace_bytes_grouped(rows: int, groups: int, N: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_grouped(rows, groups, N, K))
+
+
+def linear_grouped(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, offsets: torch.Tensor,
+                   group: int = 256, xq: torch.Tensor | None = None, x_scale: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """INT8 ConvRot linear of rows sorted by group, each group through its own weight: y[r] = linear(x[r]) with
+    wq[e] for offsets[e] <= r < offsets[e + 1].  x (or xq, x_scale) [rows, K] as in linear(); wq int8 [groups, N, K],
+    w_scale fp32 [groups, N]; offsets int32 [groups + 1] on the GPU (the host never reads them).  Rows of no group
+    are not written: pass ``out`` where they matter."""
+    _no_history("linear_grouped", x)
+    groups, N, K = wq.shape
+    dev = wq.device
+    rows = _tokens(x, xq, x_scale, K, dev)
+    _check(dev, wq=(wq, (groups, N, K), torch.int8), w_scale=(w_scale, (groups, N), torch.float32),
+           offsets=(offsets, (groups + 1,), torch.int32), out=(out, (rows, N), torch.bfloat16))
+    y = out if out is not None else torch.empty((rows, N), dtype=torch.bfloat16, device=dev)
+    ws = torch.empty(max(workspace_bytes_grouped(rows, groups, N, K), 256), dtype=torch.uint8, device=dev)
+    _call_on(dev, "convrot_linear_grouped", _ptr(x), _dtype_code(x) if x is not None else 0, _ptr(xq), _ptr(x_scale), rows,
+             N, K, group, _ptr(offsets), groups, _ptr(wq), _ptr(w_scale), _ptr(y), _ptr(ws), ws.numel())
+    return y
+
+
+def workspace_bytes_grouped_backward(rows: int, groups: int, N: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_grouped_backward(rows, groups, N, K))
+
+
+def linear_grouped_backward(dy: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, offsets: torch.Tensor,
+                            group: int = 256, dx_add: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None) -> torch.Tensor:
+    """Input gradient of linear_grouped through its frozen weights, as linear_act_backward takes it: dy bf16
+    [rows, N] -> dx bf16 [rows, K]; dx_add bf16 [rows, K], may be ``out``.  Rows of no group are not written."""
+    groups, N, K = wq.shape
+    rows = dy.shape[0]
+    dev, bf16 = wq.device, torch.bfloat16
+    _check(dev, dy=(dy, (rows, N), bf16), wq=(wq, (groups, N, K), torch.int8), w_scale=(w_scale, (groups, N), torch.float32),
+           offsets=(offsets, (groups + 1,), torch.int32), dx_add=(dx_add, (rows, K), bf16), out=(out, (rows, K), bf16))
+    dx, ws = _backward_buffers(rows, K, workspace_bytes_grouped_backward(rows, groups, N, K), out, dev)
+    _call_on(dev, "convrot_linear_grouped_backward", _ptr(dy), rows, N, K, group, _ptr(offsets), groups, _ptr(wq),
+             _ptr(w_scale), _ptr(dx_add), _ptr(dx), _ptr(ws), ws.numel())
+    return dx
+
+
+def workspace_bytes_moe_ffn(M: int, top: int, E: int, F: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_moe_ffn(M, top, E, F, K))
+
+
+def _check_experts(dev, M, top, E, F, K, experts, weights, wq_gate, gate_scale, wq_up, up_scale, wq_down, down_scale):
+    f32, i8 = torch.float32, torch.int8
+    _check(dev, experts=(experts, (M, top), torch.int32), weights=(weights, (M, top), f32),
+           wq_gate=(wq_gate, (E, F, K), i8), gate_scale=(gate_scale, (E, F), f32), wq_up=(wq_up, (E, F, K), i8),
+           up_scale=(up_scale, (E, F), f32), wq_down=(wq_down, (E, K, F), i8), down_scale=(down_scale, (E, K), f32))
+
+
+def moe_ffn_gated(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, wq_gate: torch.Tensor,
+                  gate_scale: torch.Tensor, wq_up: torch.Tensor, up_scale: torch.Tensor, wq_down: torch.Tensor,
+                  down_scale: torch.Tensor, act: str = "silu", residual: torch.Tensor | None = None, group: int = 256,
+                  group_h: int = 256, out: torch.Tensor | None = None, save: bool = False):
+    """Gated expert layer on INT8 ConvRot weights: each token through the gated blocks of its experts (experts int32
+    and weights fp32 [M, top], as moe_route gives them), y = bf16(sum_j weights[:, j] * block(x) + residual).
+    gate, up [E, F, K] (prepared with ``group``), down [E, K, F] (with ``group_h``).  Slots with an expert outside [0, E) add
+    nothing.  residual bf16 [M, K], may be ``out``.  save=True returns (y, pre, d) for moe_ffn_gated_backward: pre = bf16
+    [2, M, top, F], g then u, and d = bf16 [M, top, K], the blocks' results; their rows of slots without an expert are
+    not written.  The result itself has no autograd history."""
+    _no_history("moe_ffn_gated", x, weights, residual)
+    code = _act_code(act)
+    E, F, K = wq_gate.shape
+    dev, bf16 = wq_gate.device, torch.bfloat16
+    M = _tokens(x, None, None, K, dev)
+    top = experts.shape[1]
+    _check_experts(dev, M, top, E, F, K, experts, weights, wq_gate, gate_scale, wq_up, up_scale, wq_down, down_scale)
+    _check(dev, residual=(residual, (M, K), bf16), out=(out, (M, K), bf16))
+    y = out if out is not None else torch.empty((M, K), dtype=bf16, device=dev)
+    pre = torch.empty((2, M, top, F), dtype=bf16, device=dev) if save else None
+    d = torch.empty((M, top, K), dtype=bf16, device=dev) if save else None
+    ws = torch.empty(max(workspace_bytes_moe_ffn(M, top, E, F, K), 256), dtype=torch.uint8, device=dev)
+    _call_on(dev, "convrot_moe_ffn_gated", _ptr(x), _dtype_code(x), _ptr(experts), _ptr(weights), M, top, E, F, K, group,
+             group_h, _ptr(wq_gate), _ptr(gate_scale), _ptr(wq_up), _ptr(up_scale), _ptr(wq_down), _ptr(down_scale), code,
+             _ptr(residual), _ptr(pre), _ptr(d), _ptr(y), _ptr(ws), ws.numel())
+    return (y, pre, d) if save else y
+
+
+def workspace_bytes_moe_ffn_backward(M: int, top: int, E: int, F: int, K: int) -> int:
+    return int(load().convrot_workspace_bytes_moe_ffn_backward(M, top, E, F, K))
+
+
+def moe_ffn_gated_backward(dy: torch.Tensor, pre: torch.Tensor, d: torch.Tensor | None, experts: torch.Tensor,
+                           weights: torch.Tensor, wq_gate: torch.Tensor, gate_scale: torch.Tensor, wq_up: torch.Tensor,
+                           up_scale: torch.Tensor, wq_down: torch.Tensor, down_scale: torch.Tensor, act: str = "silu",
+                           group: int = 256, group_h: int = 256, dx_add: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None):
+    """Gradients of moe_ffn_gated: dy bf16 [M, K] through down, the product, gate and up of each slot's expert (pre as
+    the forward saved it), summed over a token's slots; dx_add = dy where the residual was x.  Returns (dx, dweights),
+    dweights fp32 [M, top] = dy . d of each slot (0 without an expert), or None where d is None."""
+    code = _act_code(act)
+    E, F, K = wq_gate.shape
+    M = dy.shape[0]
+    top = experts.shape[1]
+    dev, bf16 = wq_gate.device, torch.bfloat16
+    _check_experts(dev, M, top, E, F, K, experts, weights, wq_gate, gate_scale, wq_up, up_scale, wq_down, down_scale)
+    _check(dev, dy=(dy, (M, K), bf16), pre=(pre, (2, M, top, F), bf16), d=(d, (M, top, K), bf16), dx_add=(dx_add, (M, K), bf16),
+           out=(out, (M, K), bf16))
+    dx, ws = _backward_buffers(M, K, workspace_bytes_moe_ffn_backward(M, top, E, F, K), out, dev)
+    dw = torch.empty((M, top), dtype=torch.float32, device=dev) if d is not None else None
+    _call_on(dev, "convrot_moe_ffn_gated_backward", _ptr(dy), _ptr(pre), _ptr(d), _ptr(experts), _ptr(weights), M, top, E, F,
+             K, group, group_h, _ptr(wq_gate), _ptr(gate_scale), _ptr(wq_up), _ptr(up_scale), _ptr(wq_down),
+             _ptr(down_scale), code, _ptr(dx_add), _ptr(dx), _ptr(dw), _ptr(ws), ws.numel())
+    return dx, dw
 
 
 def linear_noalloc(x: torch.Tensor | None, wq: torch.Tensor, w_scale: torch.Tensor, bias: torch.Tensor | None = None,

@@ -186,6 +186,7 @@ const char *convrot_status_string(int s)
     case CONVROT_ERR_DEVICE: return "CONVROT_ERR_DEVICE";
     case CONVROT_ERR_ACT: return "CONVROT_ERR_ACT";
     case CONVROT_ERR_OVERLAP: return "CONVROT_ERR_OVERLAP";
+    case CONVROT_ERR_SCORE: return "CONVROT_ERR_SCORE";
     default: return "CONVROT_ERR_UNKNOWN";
     }
 }
@@ -889,6 +890,467 @@ int convrot_gemm_i4_i32(const uint8_t *xq, const uint8_t *wq, int64_t M, int64_t
     return hip_status(convrot::launch_gemm_w4a4(xq, false, wq, false, nullptr, nullptr, nullptr, acc, convrot::Epi::Int32, M, N,
                                                 (int)K, 256, static_cast<uint8_t *>(workspace) + L.tiles, stream),
                       "gemm_w4a4");
+}
+
+} // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// Mixture of experts
+namespace {
+
+int check_route(const char *who, int dtype, int64_t M, int64_t E, int top, int score)
+{
+    if (M < 0 || M >= CONVROT_GROUPED_MAX_ROWS || E < 1 || E > CONVROT_MAX_GROUPS || top < 1 || top > E ||
+        top > CONVROT_MOE_MAX_TOP || M * top >= CONVROT_GROUPED_MAX_ROWS)
+        return fail(CONVROT_ERR_SHAPE, "%s: M=%lld E=%lld top=%d: E must be in [1, %d], top in [1, min(E, %d)], M * top in "
+                    "[0, %d)", who, (long long)M, (long long)E, top, CONVROT_MAX_GROUPS, CONVROT_MOE_MAX_TOP,
+                    CONVROT_GROUPED_MAX_ROWS);
+    if (dtype != CONVROT_DTYPE_F32 && dtype != CONVROT_DTYPE_BF16) return fail(CONVROT_ERR_DTYPE, "%s: dtype=%d", who, dtype);
+    if (score != CONVROT_SCORE_SOFTMAX && score != CONVROT_SCORE_SIGMOID)
+        return fail(CONVROT_ERR_SCORE, "%s: score=%d is not one of CONVROT_SCORE_*", who, score);
+    return CONVROT_OK;
+}
+
+convrot::RouteArgs route_args(const void *logits, int dtype, const float *bias, int64_t M, int64_t E, int top, int score,
+                              int normalize, float scale)
+{
+    convrot::RouteArgs a;
+    a.logits = logits;
+    a.f32 = dtype == CONVROT_DTYPE_F32;
+    a.bias = bias;
+    a.M = M;
+    a.E = (int)E;
+    a.top = top;
+    a.score = score;
+    a.normalize = normalize != 0;
+    a.scale = scale;
+    return a;
+}
+
+// Rows sorted by group: the rules of check_shape, the limits of the group table, and units (of 64 rows and, forward, 64
+// features) that int can count.
+bool grouped_shape_ok(int64_t rows, int64_t groups, int64_t N, int64_t K, bool backward)
+{
+    if (rows < 0 || rows >= CONVROT_GROUPED_MAX_ROWS || groups < 1 || groups > CONVROT_MAX_GROUPS || N < 1 ||
+        N >= (backward ? CONVROT_BACKWARD_MAX_N : CONVROT_GEMM_MAX_N) || K < 64 || K > CONVROT_MAX_K || K % 64)
+        return false;
+    return (rows / 64 + groups) * (((backward ? K : N) + 63) / 64) < ((int64_t)1 << 30);
+}
+
+int check_grouped(const char *who, int64_t rows, int64_t groups, int64_t N, int64_t K, int group, bool backward)
+{
+    int rc = check_shape(0, N, K, group, who);
+    if (rc) return rc;
+    if (!grouped_shape_ok(rows, groups, N, K, backward))
+        return fail(CONVROT_ERR_SHAPE, "%s: rows=%lld groups=%lld N=%lld: rows must be in [0, %d), groups in [1, %d], N in "
+                    "[1, %d), and the tiles fewer than 2^30", who, (long long)rows, (long long)groups, (long long)N,
+                    CONVROT_GROUPED_MAX_ROWS, CONVROT_MAX_GROUPS, backward ? CONVROT_BACKWARD_MAX_N : CONVROT_GEMM_MAX_N);
+    return CONVROT_OK;
+}
+
+// [xq int8 rows*K][x_scale fp32 rows]
+size_t grouped_bytes(int64_t rows, int64_t K) { return round256((size_t)rows * (size_t)K) + round256((size_t)rows * 4); }
+
+size_t grouped_backward_bytes(int64_t rows, int64_t N)
+{
+    return round256((size_t)rows * (size_t)convrot::grouped_grad_lda(N) * 2);
+}
+
+int check_workspace(const char *who, const void *workspace, size_t bytes, size_t need)
+{
+    if (!workspace || bytes < need || !aligned(workspace, 256))
+        return fail(CONVROT_ERR_WORKSPACE, "%s: need a 256-byte aligned workspace of at least %zu bytes (got %zu)", who, need,
+                    workspace ? bytes : (size_t)0);
+    return CONVROT_OK;
+}
+
+// The expert layer's workspace: the sort's arrays, then, forward, the codes and scales of x, h, its codes and
+// scales, and d in fp32; backward, the two contractions' operands, and dx's parts in fp32 in the place of the first.
+struct MoeLayout {
+    size_t offsets = 0, slot_of = 0, token_of = 0, row_of = 0;
+    size_t xq = 0, xs = 0, h = 0, hq = 0, hs = 0;
+    size_t a = 0, a2 = 0;
+    size_t part = 0, total = 0;
+};
+
+MoeLayout moe_layout(int64_t M, int top, int64_t E, int64_t F, int64_t K, bool backward)
+{
+    MoeLayout L;
+    const size_t S = (size_t)M * (size_t)top;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += round256(bytes);
+        return at;
+    };
+    L.offsets = take((size_t)(E + 1) * 4);
+    L.slot_of = take(S * 4);
+    L.token_of = take(S * 4);
+    L.row_of = take(S * 4);
+    if (backward) {
+        L.a2 = take(S * (size_t)F * 4);
+        L.a = L.part = take(S * (size_t)K * 4);
+    } else {
+        L.xq = take((size_t)M * (size_t)K);
+        L.xs = take((size_t)M * 4);
+        L.h = take(S * (size_t)F * 2);
+        L.hq = take(S * (size_t)F);
+        L.hs = take(S * 4);
+        L.part = take(S * (size_t)K * 4);
+    }
+    L.total = off;
+    return L;
+}
+
+bool moe_shape_ok(int64_t M, int top, int64_t E, int64_t F, int64_t K, bool backward)
+{
+    if (M < 0 || M >= CONVROT_GROUPED_MAX_ROWS || E < 1 || E > CONVROT_MAX_GROUPS || top < 1 || top > E ||
+        top > CONVROT_MOE_MAX_TOP)
+        return false;
+    return grouped_shape_ok(M * top, E, F, K, backward) && grouped_shape_ok(M * top, E, K, F, backward) &&
+           M * K < ((int64_t)1 << 31);
+}
+
+int check_moe(const char *who, int64_t M, int top, int64_t E, int64_t F, int64_t K, int group, int group_h, int act,
+              bool backward)
+{
+    int rc = check_shape(M, F, K, group, who);
+    if (rc) return rc;
+    if ((rc = check_shape(M, K, F, group_h, who))) return rc;
+    if ((rc = check_act(act, who))) return rc;
+    if (!moe_shape_ok(M, top, E, F, K, backward))
+        return fail(CONVROT_ERR_SHAPE, "%s: M=%lld top=%d E=%lld F=%lld K=%lld: E must be in [1, %d], top in [1, min(E, %d)], "
+                    "M * top below %d, M * K below 2^31", who, (long long)M, top, (long long)E, (long long)F, (long long)K,
+                    CONVROT_MAX_GROUPS, CONVROT_MOE_MAX_TOP, CONVROT_GROUPED_MAX_ROWS);
+    return CONVROT_OK;
+}
+
+convrot::MoeOrder moe_order(uint8_t *ws, const MoeLayout &L)
+{
+    convrot::MoeOrder o;
+    o.offsets = reinterpret_cast<int32_t *>(ws + L.offsets);
+    o.slot_of = reinterpret_cast<int32_t *>(ws + L.slot_of);
+    o.token_of = reinterpret_cast<int32_t *>(ws + L.token_of);
+    o.row_of = reinterpret_cast<int32_t *>(ws + L.row_of);
+    return o;
+}
+
+} // namespace
+
+extern "C" {
+
+int convrot_moe_route(const void *logits, int dtype, int64_t M, int64_t E, int top, int score, int normalize,
+                      float scale, const float *bias, int32_t *experts, float *weights, hipStream_t stream)
+{
+    const char *who = "convrot_moe_route";
+    int rc = check_route(who, dtype, M, E, top, score);
+    if (rc) return rc;
+    if (M == 0) return CONVROT_OK;
+    if (!logits || !experts || !weights) return fail(CONVROT_ERR_NULL, "%s: logits, experts and weights must be non-NULL", who);
+    if (!aligned(logits, dtype == CONVROT_DTYPE_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(experts, 4) || !aligned(weights, 4))
+        return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+    const size_t out = (size_t)M * (size_t)top * 4, in = (size_t)M * (size_t)E * (dtype == CONVROT_DTYPE_F32 ? 4 : 2);
+    if (overlap(experts, out, weights, out) || overlap(experts, out, logits, in) || overlap(weights, out, logits, in) ||
+        overlap(experts, out, bias, (size_t)E * 4) || overlap(weights, out, bias, (size_t)E * 4))
+        return fail(CONVROT_ERR_OVERLAP, "%s: an output overlaps another array of the call", who);
+    if ((rc = check_device())) return rc;
+    return hip_status(convrot::launch_moe_route(route_args(logits, dtype, bias, M, E, top, score, normalize, scale), experts,
+                                                weights, stream),
+                      "moe_route");
+}
+
+int convrot_moe_route_backward(const float *dweights, const void *logits, int dtype, int64_t M, int64_t E, int top,
+                               int score, int normalize, float scale, const int32_t *experts, void *dlogits,
+                               hipStream_t stream)
+{
+    const char *who = "convrot_moe_route_backward";
+    int rc = check_route(who, dtype, M, E, top, score);
+    if (rc) return rc;
+    if (M == 0) return CONVROT_OK;
+    if (!dweights || !logits || !experts || !dlogits)
+        return fail(CONVROT_ERR_NULL, "%s: dweights, logits, experts and dlogits must be non-NULL", who);
+    const uintptr_t es = dtype == CONVROT_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, es) || !aligned(dlogits, es) || !aligned(experts, 4) || !aligned(dweights, 4))
+        return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+    const size_t small = (size_t)M * (size_t)top * 4, in = (size_t)M * (size_t)E * es;
+    if ((dlogits != logits && overlap(dlogits, in, logits, in)) || overlap(dlogits, in, experts, small) ||
+        overlap(dlogits, in, dweights, small))
+        return fail(CONVROT_ERR_OVERLAP, "%s: dlogits overlaps an input (only dlogits == logits is allowed)", who);
+    if ((rc = check_device())) return rc;
+    return hip_status(convrot::launch_moe_route_backward(route_args(logits, dtype, nullptr, M, E, top, score, normalize, scale),
+                                                         dweights, experts, dlogits, stream),
+                      "moe_route_backward");
+}
+
+size_t convrot_workspace_bytes_grouped(int64_t rows, int64_t groups, int64_t N, int64_t K)
+{
+    return grouped_shape_ok(rows, groups, N, K, false) ? grouped_bytes(rows, K) : 0;
+}
+
+int convrot_linear_grouped(const void *x, int x_dtype, const int8_t *xq, const float *x_scale, int64_t rows, int64_t N,
+                           int64_t K, int group, const int32_t *offsets, int64_t groups, const int8_t *wq,
+                           const float *w_scale, void *y, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const char *who = "convrot_linear_grouped";
+    int rc = check_grouped(who, rows, groups, N, K, group, false);
+    if (rc) return rc;
+    if (rows == 0) return CONVROT_OK;
+    if (!offsets || !wq || !w_scale || !y) return fail(CONVROT_ERR_NULL, "%s: offsets, wq, w_scale and y must be non-NULL", who);
+    if (!x && (!xq || !x_scale)) return fail(CONVROT_ERR_NULL, "%s: give x, or both xq and x_scale", who);
+    if (x && x_dtype != CONVROT_DTYPE_F32 && x_dtype != CONVROT_DTYPE_BF16)
+        return fail(CONVROT_ERR_DTYPE, "%s: x_dtype=%d", who, x_dtype);
+    if ((x && !aligned(x, 16)) || (!x && (!aligned(xq, 16) || !aligned(x_scale, 4))) || !aligned(offsets, 4) ||
+        !aligned(wq, 16) || !aligned(w_scale, 4) || !aligned(y, 16))
+        return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+    const size_t y_bytes = (size_t)rows * (size_t)N * 2;
+    if (overlap(y, y_bytes, offsets, (size_t)(groups + 1) * 4) ||
+        (!x && (overlap(y, y_bytes, xq, (size_t)rows * (size_t)K) || overlap(y, y_bytes, x_scale, (size_t)rows * 4))))
+        return fail(CONVROT_ERR_OVERLAP, "%s: y overlaps xq, x_scale or offsets", who);
+    if (x && (rc = check_workspace(who, workspace, workspace_bytes, grouped_bytes(rows, K)))) return rc;
+    if ((rc = check_device())) return rc;
+    if (x) {
+        int8_t *qx = static_cast<int8_t *>(workspace);
+        float *sx = reinterpret_cast<float *>(qx + round256((size_t)rows * (size_t)K));
+        rc = hip_status(convrot::launch_rotate_quant(x, x_dtype == CONVROT_DTYPE_F32, rows, (int)K, log2i(group), 8, qx, sx,
+                                                     stream),
+                        "rotate_quant");
+        if (rc) return rc;
+        xq = qx;
+        x_scale = sx;
+    }
+    convrot::GroupedArgs g;
+    g.xq = xq;
+    g.sx = x_scale;
+    g.offsets = offsets;
+    g.wq = wq;
+    g.sw = w_scale;
+    g.y = static_cast<uint16_t *>(y);
+    g.rows = rows;
+    g.N = N;
+    g.groups = (int)groups;
+    g.K = (int)K;
+    return hip_status(convrot::launch_grouped_i8(g, convrot::GroupedEpi::Plain, stream), "grouped_i8");
+}
+
+size_t convrot_workspace_bytes_grouped_backward(int64_t rows, int64_t groups, int64_t N, int64_t K)
+{
+    return grouped_shape_ok(rows, groups, N, K, true) ? grouped_backward_bytes(rows, N) : 0;
+}
+
+int convrot_linear_grouped_backward(const void *dy, int64_t rows, int64_t N, int64_t K, int group,
+                                    const int32_t *offsets, int64_t groups, const int8_t *wq, const float *w_scale,
+                                    const void *dx_add, void *dx, void *workspace, size_t workspace_bytes,
+                                    hipStream_t stream)
+{
+    const char *who = "convrot_linear_grouped_backward";
+    int rc = check_grouped(who, rows, groups, N, K, group, true);
+    if (rc) return rc;
+    if (rows == 0) return CONVROT_OK;
+    if (!dy || !offsets || !wq || !w_scale || !dx)
+        return fail(CONVROT_ERR_NULL, "%s: dy, offsets, wq, w_scale and dx must be non-NULL", who);
+    if (!aligned(dy, 16) || !aligned(offsets, 4) || !aligned(wq, 16) || !aligned(w_scale, 4) || !aligned(dx_add, 16) ||
+        !aligned(dx, 16))
+        return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+    const size_t dx_bytes = (size_t)rows * (size_t)K * 2;
+    if ((dx_add != dx && overlap(dx_add, dx_bytes, dx, dx_bytes)) || overlap(dx, dx_bytes, offsets, (size_t)(groups + 1) * 4))
+        return fail(CONVROT_ERR_OVERLAP, "%s: dx overlaps dx_add (only dx_add == dx is allowed) or offsets", who);
+    if ((rc = check_workspace(who, workspace, workspace_bytes, grouped_backward_bytes(rows, N)))) return rc;
+    if ((rc = check_device())) return rc;
+    convrot::GroupedRowsArgs r;
+    r.dy = static_cast<const uint16_t *>(dy);
+    r.sw = w_scale;
+    r.offsets = offsets;
+    r.a = static_cast<uint16_t *>(workspace);
+    r.rows = rows;
+    r.N = N;
+    r.groups = (int)groups;
+    if ((rc = hip_status(convrot::launch_grouped_rows(r, stream), "grouped_rows"))) return rc;
+    convrot::GroupedGradArgs g;
+    g.a = r.a;
+    g.offsets = offsets;
+    g.wq1 = wq;
+    g.add = static_cast<const uint16_t *>(dx_add);
+    g.dx = static_cast<uint16_t *>(dx);
+    g.rows = rows;
+    g.N = N;
+    g.groups = (int)groups;
+    g.K = (int)K;
+    g.log2g = log2i(group);
+    return hip_status(convrot::launch_grouped_grad(g, stream), "grouped_grad");
+}
+
+size_t convrot_workspace_bytes_moe_ffn(int64_t M, int top, int64_t E, int64_t F, int64_t K)
+{
+    return moe_shape_ok(M, top, E, F, K, false) ? moe_layout(M, top, E, F, K, false).total : 0;
+}
+
+int convrot_moe_ffn_gated(const void *x, int x_dtype, const int32_t *experts, const float *weights, int64_t M, int top,
+                          int64_t E, int64_t F, int64_t K, int group, int group_h, const int8_t *wq_gate,
+                          const float *gate_scale, const int8_t *wq_up, const float *up_scale, const int8_t *wq_down,
+                          const float *down_scale, int act, const void *residual, void *pre, void *d, void *y,
+                          void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const char *who = "convrot_moe_ffn_gated";
+    int rc = check_moe(who, M, top, E, F, K, group, group_h, act, false);
+    if (rc) return rc;
+    if (M == 0) return CONVROT_OK;
+    if (!x || !experts || !weights || !wq_gate || !gate_scale || !wq_up || !up_scale || !wq_down || !down_scale || !y)
+        return fail(CONVROT_ERR_NULL, "%s: x, experts, weights, the expert weights, their scales and y must be non-NULL", who);
+    if (x_dtype != CONVROT_DTYPE_F32 && x_dtype != CONVROT_DTYPE_BF16)
+        return fail(CONVROT_ERR_DTYPE, "%s: x_dtype=%d", who, x_dtype);
+    if (!aligned(x, 16) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(wq_gate, 16) || !aligned(wq_up, 16) ||
+        !aligned(wq_down, 16) || !aligned(gate_scale, 4) || !aligned(up_scale, 4) || !aligned(down_scale, 4) ||
+        !aligned(residual, 16) || !aligned(pre, 16) || !aligned(d, 16) || !aligned(y, 16))
+        return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+    const size_t S = (size_t)M * (size_t)top, y_bytes = (size_t)M * (size_t)K * 2, small = S * 4;
+    const size_t x_bytes = (size_t)M * (size_t)K * (x_dtype == CONVROT_DTYPE_F32 ? 4 : 2);
+    const size_t pre_bytes = S * (size_t)F * 4, d_bytes = S * (size_t)K * 2;
+    // y is written last, when only weights, residual and the workspace are still read; pre and d before that
+    auto saved = [&](const void *q, size_t n) {
+        return overlap(q, n, y, y_bytes) || overlap(q, n, residual, y_bytes) || overlap(q, n, x, x_bytes) ||
+               overlap(q, n, experts, small) || overlap(q, n, weights, small);
+    };
+    if ((residual != y && overlap(residual, y_bytes, y, y_bytes)) || overlap(y, y_bytes, experts, small) ||
+        overlap(y, y_bytes, weights, small) || saved(pre, pre_bytes) || saved(d, d_bytes) || overlap(pre, pre_bytes, d, d_bytes))
+        return fail(CONVROT_ERR_OVERLAP, "%s: y, pre or d overlaps another array of the call (only residual == y is allowed)",
+                    who);
+    const MoeLayout L = moe_layout(M, top, E, F, K, false);
+    if ((rc = check_workspace(who, workspace, workspace_bytes, L.total))) return rc;
+    if ((rc = check_device())) return rc;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const convrot::MoeOrder o = moe_order(ws, L);
+    int8_t *xq = reinterpret_cast<int8_t *>(ws + L.xq), *hq = reinterpret_cast<int8_t *>(ws + L.hq);
+    float *xs = reinterpret_cast<float *>(ws + L.xs), *hs = reinterpret_cast<float *>(ws + L.hs);
+    uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h);
+    float *part = reinterpret_cast<float *>(ws + L.part);
+    rc = hip_status(convrot::launch_rotate_quant(x, x_dtype == CONVROT_DTYPE_F32, M, (int)K, log2i(group), 8, xq, xs, stream),
+                    "rotate_quant");
+    if (rc) return rc;
+    if ((rc = hip_status(convrot::launch_moe_order(experts, (int64_t)S, (int)E, top, o, stream), "moe_order"))) return rc;
+    convrot::GroupedArgs g;
+    g.xq = xq;
+    g.sx = xs;
+    g.offsets = o.offsets;
+    g.source = o.token_of;
+    g.slot_of = o.slot_of;
+    g.wq = wq_gate;
+    g.wq2 = wq_up;
+    g.sw = gate_scale;
+    g.sw2 = up_scale;
+    g.y = h;
+    g.pre = static_cast<uint16_t *>(pre);
+    g.rows = (int64_t)S;
+    g.N = F;
+    g.groups = (int)E;
+    g.K = (int)K;
+    g.act = act;
+    if ((rc = hip_status(convrot::launch_grouped_i8(g, convrot::GroupedEpi::Gated, stream), "grouped_i8"))) return rc;
+    // (rows past the last slot with an expert hold anything; their codes are never read)
+    if ((rc = hip_status(convrot::launch_rotate_quant(h, false, (int64_t)S, (int)F, log2i(group_h), 8, hq, hs, stream),
+                         "rotate_quant")))
+        return rc;
+    convrot::GroupedArgs w;
+    w.xq = hq;
+    w.sx = hs;
+    w.offsets = o.offsets;
+    w.slot_of = o.slot_of;
+    w.wq = wq_down;
+    w.sw = down_scale;
+    w.part = part;
+    w.d = static_cast<uint16_t *>(d);
+    w.rows = (int64_t)S;
+    w.N = K;
+    w.groups = (int)E;
+    w.K = (int)F;
+    if ((rc = hip_status(convrot::launch_grouped_i8(w, convrot::GroupedEpi::Part, stream), "grouped_i8"))) return rc;
+    return hip_status(convrot::launch_moe_combine(part, o.row_of, weights, static_cast<const uint16_t *>(residual),
+                                                  static_cast<uint16_t *>(y), M, (int)K, top, stream),
+                      "moe_combine");
+}
+
+size_t convrot_workspace_bytes_moe_ffn_backward(int64_t M, int top, int64_t E, int64_t F, int64_t K)
+{
+    return M > 0 && moe_shape_ok(M, top, E, F, K, true) ? moe_layout(M, top, E, F, K, true).total : 0;
+}
+
+int convrot_moe_ffn_gated_backward(const void *dy, const void *pre, const void *d, const int32_t *experts,
+                                   const float *weights, int64_t M, int top, int64_t E, int64_t F, int64_t K, int group,
+                                   int group_h, const int8_t *wq_gate, const float *gate_scale, const int8_t *wq_up,
+                                   const float *up_scale, const int8_t *wq_down, const float *down_scale, int act,
+                                   const void *dx_add, void *dx, float *dweights, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream)
+{
+    const char *who = "convrot_moe_ffn_gated_backward";
+    int rc = check_moe(who, M, top, E, F, K, group, group_h, act, true);
+    if (rc) return rc;
+    if (M == 0) return CONVROT_OK;
+    if (!dy || !pre || !experts || !weights || !wq_gate || !gate_scale || !wq_up || !up_scale || !wq_down || !down_scale ||
+        !dx || (dweights && !d))
+        return fail(CONVROT_ERR_NULL, "%s: dy, pre, experts, weights, the expert weights, their scales, dx and, with dweights, "
+                    "d must be non-NULL", who);
+    if (!aligned(dy, 16) || !aligned(pre, 16) || !aligned(d, 16) || !aligned(experts, 4) || !aligned(weights, 4) ||
+        !aligned(wq_gate, 16) || !aligned(wq_up, 16) || !aligned(wq_down, 16) || !aligned(gate_scale, 4) ||
+        !aligned(up_scale, 4) || !aligned(down_scale, 4) || !aligned(dx_add, 16) || !aligned(dx, 16) || !aligned(dweights, 4))
+        return fail(CONVROT_ERR_ALIGN, "%s: misaligned pointer", who);
+    const size_t S = (size_t)M * (size_t)top, x_bytes = (size_t)M * (size_t)K * 2, small = S * 4;
+    if ((dx_add != dx && overlap(dx_add, x_bytes, dx, x_bytes)) || overlap(dweights, small, dx, x_bytes) ||
+        overlap(dweights, small, dx_add, x_bytes) || overlap(dweights, small, dy, x_bytes) ||
+        overlap(dweights, small, pre, S * (size_t)F * 4) || overlap(dweights, small, d, S * (size_t)K * 2) ||
+        overlap(dweights, small, experts, small) || overlap(dweights, small, weights, small))
+        return fail(CONVROT_ERR_OVERLAP, "%s: dx overlaps dx_add (only dx_add == dx is allowed), or dweights another array of "
+                    "the call", who);
+    const MoeLayout L = moe_layout(M, top, E, F, K, true);
+    if ((rc = check_workspace(who, workspace, workspace_bytes, L.total))) return rc;
+    if ((rc = check_device())) return rc;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const convrot::MoeOrder o = moe_order(ws, L);
+    float *part = reinterpret_cast<float *>(ws + L.part);
+    if ((rc = hip_status(convrot::launch_moe_order(experts, (int64_t)S, (int)E, top, o, stream), "moe_order"))) return rc;
+    convrot::GroupedRowsArgs r;
+    r.dy = static_cast<const uint16_t *>(dy);
+    r.sw = down_scale;
+    r.experts = experts;
+    r.row_of = o.row_of;
+    r.weights = weights;
+    r.d = dweights ? static_cast<const uint16_t *>(d) : nullptr;
+    r.dweights = dweights;
+    r.a = reinterpret_cast<uint16_t *>(ws + L.a);
+    r.rows = (int64_t)S;
+    r.N = K;
+    r.groups = (int)E;
+    r.top = top;
+    if ((rc = hip_status(convrot::launch_grouped_rows(r, stream), "grouped_rows"))) return rc;
+    convrot::GroupedGradArgs down;
+    down.a = r.a;
+    down.offsets = o.offsets;
+    down.slot_of = o.slot_of;
+    down.wq1 = wq_down;
+    down.next.pre = static_cast<const uint16_t *>(pre);
+    down.next.sw_gate = gate_scale;
+    down.next.sw_up = up_scale;
+    down.next.act = act;
+    down.next.a = reinterpret_cast<uint16_t *>(ws + L.a2);
+    down.rows = (int64_t)S;
+    down.N = K;
+    down.groups = (int)E;
+    down.K = (int)F;
+    down.log2g = log2i(group_h);
+    if ((rc = hip_status(convrot::launch_grouped_grad(down, stream), "grouped_grad"))) return rc;
+    convrot::GroupedGradArgs up;
+    up.a = down.next.a;
+    up.offsets = o.offsets;
+    up.wq1 = wq_gate;
+    up.wq2 = wq_up;
+    up.rows_out = part;
+    up.rows = (int64_t)S;
+    up.N = F;
+    up.groups = (int)E;
+    up.K = (int)K;
+    up.log2g = log2i(group);
+    if ((rc = hip_status(convrot::launch_grouped_grad(up, stream), "grouped_grad"))) return rc;
+    return hip_status(convrot::launch_moe_combine(part, o.row_of, nullptr, static_cast<const uint16_t *>(dx_add),
+                                                  static_cast<uint16_t *>(dx), M, (int)K, top, stream),
+                      "moe_combine");
 }
 
 } // extern "C"

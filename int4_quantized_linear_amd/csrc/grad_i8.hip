@@ -13,8 +13,12 @@
 //      the fp32 sums.
 //   3. the rotation, dx_add and the one rounding to bf16: in the GEMM's epilogue (a tile spans 256
 //      channels, whole groups), or in grad_join_kernel where tiles are split along n.
+// Grouped: rows sorted by group (expert), each through its own group's weight.  The operand then comes from
+// grad_rows_kernel, a tile holds rows of one group, nothing is split, and the result may also go to
+// fp32 rows that moe_combine_kernel adds up.
 #include "activation.hpp"
 #include "device_common.hpp"
+#include "grouped_common.hpp"
 #include "launchers.hpp"
 #include "tile_common.hpp"
 
@@ -43,6 +47,11 @@ struct GradParams {
     int T_dp, S;               // whole tiles, then the rest in S slices each
     float norm;                // 2^(-lg / 2)
     GradNext next;             // next.a non-null: the gated product's gradient goes there, not to dx
+    // Grouped (M rows in all, w1, w2 [groups, N, K], next's scales [groups, K]; tiles_m, T_dp and S unused):
+    const int32_t *offsets;
+    const int32_t *slot_of;    // the row of next.pre that a row has, or null: its own
+    float *rows_out;           // non-null: fp32 [M, K] instead of dx
+    int groups;
 };
 
 // 8 rotated channels c .. of token m to where the launch puts them:
@@ -50,7 +59,8 @@ struct GradParams {
 //   both operands of the next contraction, bf16(dh u act'(g) sw_gate) and bf16(dh act(g) sw_up), which
 //   saves writing dh and reading it back in a pass of its own.
 // (16 bytes each; K % 64 == 0, so all 8 exist.)
-__device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float (&v)[8])
+template <bool GROUPED>
+__device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float (&v)[8], int group = 0)
 {
     auto load = [](const uint16_t *src, float (&to)[8]) {
         const v4u d = *reinterpret_cast<const v4u *>(src);
@@ -63,7 +73,12 @@ __device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float
         for (int e = 0; e < 4; ++e) d[e] = pack_bf16x2(from[2 * e], from[2 * e + 1]);
         *reinterpret_cast<v4u *>(dst) = d;
     };
-    const int64_t o = (int64_t)m * p.K + c;
+    int64_t o = (int64_t)m * p.K + c;
+    if (GROUPED && p.rows_out) {
+        *reinterpret_cast<v4f *>(p.rows_out + o) = v4f{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<v4f *>(p.rows_out + o + 4) = v4f{v[4], v[5], v[6], v[7]};
+        return;
+    }
     if (!p.next.a) {
         float add[8] = {};
         if (p.add) load(p.add + o, add);
@@ -72,6 +87,9 @@ __device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float
         store(p.dx + o, v);
         return;
     }
+    if (GROUPED && p.slot_of) o = (int64_t)p.slot_of[m] * p.K + c;
+    const float *sw_gate = p.next.sw_gate + (GROUPED ? (int64_t)group * p.K : 0);
+    const float *sw_up = p.next.sw_up + (GROUPED ? (int64_t)group * p.K : 0);
     float g[8], u[8], slope[8];
     load(p.next.pre + o, g);
     load(p.next.pre + (int64_t)p.M * p.K + o, u);
@@ -80,10 +98,10 @@ __device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float
     for (int e = 0; e < 8; e += 2) {
         const uint32_t d = pack_bf16x2(v[e], v[e + 1]);
         const float d0 = bf16lo_to_f32(d), d1 = bf16hi_to_f32(d);
-        u[e] = d0 * u[e] * slope[e] * p.next.sw_gate[c + e];
-        u[e + 1] = d1 * u[e + 1] * slope[e + 1] * p.next.sw_gate[c + e + 1];
-        g[e] = d0 * g[e] * p.next.sw_up[c + e];
-        g[e + 1] = d1 * g[e + 1] * p.next.sw_up[c + e + 1];
+        u[e] = d0 * u[e] * slope[e] * sw_gate[c + e];
+        u[e + 1] = d1 * u[e + 1] * slope[e + 1] * sw_gate[c + e + 1];
+        g[e] = d0 * g[e] * sw_up[c + e];
+        g[e + 1] = d1 * g[e + 1] * sw_up[c + e + 1];
     }
     uint16_t *a = p.next.a + (int64_t)m * 2 * p.K + c;       // K % 64 == 0: no padding between the two
     store(a, u);
@@ -158,13 +176,15 @@ __device__ __forceinline__ void dma16(v4u rsrc, uint32_t lds, uint32_t off, uint
 struct StepLoads {
     int t, rows;
     uint64_t w, x;             // codes of the step, tokens of the tile
+    int64_t own;               // where the group's weights begin (0 but for rows sorted by group)
 
-    __device__ __forceinline__ StepLoads(const GradParams &p, int kb, int m0, int c0)
+    __device__ __forceinline__ StepLoads(const GradParams &p, int kb, int m0, int c0, int group)
     {
+        own = (int64_t)group * p.N * p.K;
         const int first = kb >= p.nt1 ? p.nt1 : 0;
         t = kb;
         rows = p.N - (kb - first) * BN;
-        w = reinterpret_cast<uint64_t>((first ? p.w2 : p.w1) + (int64_t)(kb - first) * BN * p.K + c0);
+        w = reinterpret_cast<uint64_t>((first ? p.w2 : p.w1) + own + (int64_t)(kb - first) * BN * p.K + c0);
         x = reinterpret_cast<uint64_t>(p.a + (int64_t)m0 * p.lda);
     }
     __device__ __forceinline__ v4u codes(int ke, int K, int c0) const
@@ -183,7 +203,7 @@ struct StepLoads {
         w += (uint64_t)(BN * p.K);
         if (t == p.nt1) {
             rows = p.N;
-            w = reinterpret_cast<uint64_t>(p.w2 + c0);
+            w = reinterpret_cast<uint64_t>(p.w2 + own + c0);
         }
     }
 };
@@ -226,6 +246,7 @@ __device__ __forceinline__ v8bf16 codes_to_bf16(v2i raw)
 // 38 against 33, 2688 x 2 * 5376 54 / 46; 512 tokens 5120 x 5120 62 / 52.)  12 tokens 5120 x 8192: 12 us,
 // the codes' stream and one load latency, 5120 x 2 * 25600: 54 us, 4.8 TB/s; 300 tokens 5376 x 2688: 20 us, matrix core 13%
 // busy, 2688 x 2 * 5376: 28 us, 23%: a step's LDS reads and barrier.
+template <bool GROUPED>
 __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 {
     constexpr int TM = 64, NST = 3;
@@ -234,21 +255,37 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
     __shared__ __attribute__((aligned(16))) uint8_t smem[NST * TSTAGE];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int T = p.tiles_m * p.tiles_c, U = p.T_dp + (T - p.T_dp) * p.S;
     const int K = p.K;
-    if ((int)blockIdx.x >= U) return;                    // the grid is rounded up to a multiple of 8
-    const int u = unit_of((int)blockIdx.x, p.T_dp, U);
-    int tile = u, kb = 0, ke = p.nt, slot = -1;
-    if (u >= p.T_dp) {
-        const int r = T - p.T_dp, v = u - p.T_dp, sl = v / r;
-        tile = p.T_dp + v % r;
-        kb = (int)((int64_t)sl * p.nt / p.S);
-        ke = (int)((int64_t)(sl + 1) * p.nt / p.S);
-        slot = v;
+    int m0, c0, group = 0, end = p.M, kb = 0, ke = p.nt, slot = -1;
+    if constexpr (GROUPED) {
+        __shared__ int starts[MAX_GROUPS];
+        const int tiles = group_tiles<256>(p.offsets, p.groups, p.M, TM, starts, reinterpret_cast<int *>(smem));
+        const int units = (int)min((int64_t)tiles * p.tiles_c, (int64_t)0x7fffff00);
+        if ((int)blockIdx.x >= units) return;            // the grid holds the most units there could be
+        int tm, tc;
+        tile_coords(unit_of((int)blockIdx.x, 0, units), tiles, p.tiles_c, tm, tc);
+        const GroupRows gr = group_of_tile(p.offsets, p.M, TM, starts, tm);
+        m0 = gr.first;
+        end = gr.end;
+        group = gr.group;
+        c0 = tc * BC;
+    } else {
+        const int T = p.tiles_m * p.tiles_c, U = p.T_dp + (T - p.T_dp) * p.S;
+        if ((int)blockIdx.x >= U) return;                // the grid is rounded up to a multiple of 8
+        const int u = unit_of((int)blockIdx.x, p.T_dp, U);
+        int tile = u;
+        if (u >= p.T_dp) {
+            const int r = T - p.T_dp, v = u - p.T_dp, sl = v / r;
+            tile = p.T_dp + v % r;
+            kb = (int)((int64_t)sl * p.nt / p.S);
+            ke = (int)((int64_t)(sl + 1) * p.nt / p.S);
+            slot = v;
+        }
+        int tm, tc;
+        tile_coords(tile, p.tiles_m, p.tiles_c, tm, tc);
+        m0 = tm * TM;
+        c0 = tc * BC;
     }
-    int tm, tc;
-    tile_coords(tile, p.tiles_m, p.tiles_c, tm, tc);
-    const int m0 = tm * TM, c0 = tc * BC;
 
     // tokens: instruction i of wave w fills rows 8 (4 i + w) .. + 7 (lane -> row + lane / 8, position lane % 8);
     // codes: rows 4 (4 i + w) .. + 3 (lane -> row + lane / 16, position lane % 16)
@@ -256,7 +293,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
         const int r = 8 * (4 * i + w) + (lane >> 3);
-        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz(r))) : OOB;
+        offx[i] = m0 + r < end ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz(r))) : OOB;
     }
 #pragma unroll
     for (int i = 0; i < WL; ++i) {
@@ -264,7 +301,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
         offw[i] = c0 + c < K ? (uint32_t)(n * K + c) : OOB;
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(const lds_void *)smem + (uint32_t)w * 1024u;
-    StepLoads ld(p, kb, m0, c0);
+    StepLoads ld(p, kb, m0, c0, group);
     uint32_t ld_lds = lds0;
     auto issue = [&]() {
         const v4u rw = ld.codes(ke, K, c0), rx = ld.tokens(ke);
@@ -344,12 +381,12 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
     __syncthreads();
 
     // lane: token lane % 16 of block b, channels 16 (4 w + a) + 4 fq + v
-    if (slot >= 0) {
+    if (!GROUPED && slot >= 0) {
         float *dst = p.part + (int64_t)slot * (TM * BC);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const int ml = 16 * b + frow;
-            if (m0 + ml < p.M) {
+            if (m0 + ml < end) {
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
                     *reinterpret_cast<v4f *>(dst + ml * BC + 16 * (4 * w + a) + 4 * fq) = acc[a][b];
@@ -388,7 +425,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 #pragma unroll 1
     for (int it = 0; it < 8; ++it) {
         const int row = 8 * it + ((int)threadIdx.x >> 5), m = m0 + row;
-        if (m >= p.M || c >= K) continue;
+        if (m >= end || c >= K) continue;
         float v[8];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -404,7 +441,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
         }
-        finish8(p, m, c, v);
+        finish8<GROUPED>(p, m, c, v, group);
     }
 }
 
@@ -424,6 +461,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
 // the first and third quarter of a group 603, 1337, or two at once at its end 600, 1321; their descriptors kept
 // ready instead of formed at each load 617, 1368.
 // The K loop holds everything in registers; the epilogue spills 26 of them (104 bytes a lane), once a tile.
+template <bool GROUPED>
 __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 {
     constexpr int NST = 3, XL = 4, WL = 2, LPS = XL + WL;    // loads per step and wavefront
@@ -431,28 +469,44 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
     __shared__ __attribute__((aligned(16))) uint8_t smem[NST * GSTAGE];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int T = p.tiles_m * p.tiles_c, U = p.T_dp + (T - p.T_dp) * p.S;
     const int K = p.K;
-    if ((int)blockIdx.x >= U) return;                    // the grid is rounded up to a multiple of 8
-    const int u = unit_of((int)blockIdx.x, p.T_dp, U);
-    int tile = u, kb = 0, ke = p.nt, slot = -1;
-    if (u >= p.T_dp) {
-        const int r = T - p.T_dp, v = u - p.T_dp, sl = v / r;
-        tile = p.T_dp + v % r;
-        kb = (int)((int64_t)sl * p.nt / p.S);
-        ke = (int)((int64_t)(sl + 1) * p.nt / p.S);
-        slot = v;
+    int m0, c0, group = 0, end = p.M, kb = 0, ke = p.nt, slot = -1;
+    if constexpr (GROUPED) {
+        __shared__ int starts[MAX_GROUPS];
+        const int tiles = group_tiles<512>(p.offsets, p.groups, p.M, BM, starts, reinterpret_cast<int *>(smem));
+        const int units = (int)min((int64_t)tiles * p.tiles_c, (int64_t)0x7fffff00);
+        if ((int)blockIdx.x >= units) return;            // the grid holds the most units there could be
+        int tm, tc;
+        tile_coords(unit_of((int)blockIdx.x, 0, units), tiles, p.tiles_c, tm, tc);
+        const GroupRows gr = group_of_tile(p.offsets, p.M, BM, starts, tm);
+        m0 = gr.first;
+        end = gr.end;
+        group = gr.group;
+        c0 = tc * BC;
+    } else {
+        const int T = p.tiles_m * p.tiles_c, U = p.T_dp + (T - p.T_dp) * p.S;
+        if ((int)blockIdx.x >= U) return;                // the grid is rounded up to a multiple of 8
+        const int u = unit_of((int)blockIdx.x, p.T_dp, U);
+        int tile = u;
+        if (u >= p.T_dp) {
+            const int r = T - p.T_dp, v = u - p.T_dp, sl = v / r;
+            tile = p.T_dp + v % r;
+            kb = (int)((int64_t)sl * p.nt / p.S);
+            ke = (int)((int64_t)(sl + 1) * p.nt / p.S);
+            slot = v;
+        }
+        int tm, tc;
+        tile_coords(tile, p.tiles_m, p.tiles_c, tm, tc);
+        m0 = tm * BM;
+        c0 = tc * BC;
     }
-    int tm, tc;
-    tile_coords(tile, p.tiles_m, p.tiles_c, tm, tc);
-    const int m0 = tm * BM, c0 = tc * BC;
 
     // tokens: instruction i of wave w fills rows 8 (8 i + w) .. + 7; codes: rows 4 (8 i + w) .. + 3
     uint32_t offx[XL], offw[WL];
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
         const int r = 8 * (8 * i + w) + (lane >> 3);
-        offx[i] = m0 + r < p.M ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz(r))) : OOB;
+        offx[i] = m0 + r < end ? (uint32_t)(r * (int)p.lda * 2 + 16 * ((lane & 7) ^ swz(r))) : OOB;
     }
 #pragma unroll
     for (int i = 0; i < WL; ++i) {
@@ -461,7 +515,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
     }
     // load i of a step: its codes first
     const uint32_t lds0 = (uint32_t)(uintptr_t)(const lds_void *)smem + (uint32_t)w * 1024u;
-    StepLoads ld(p, kb, m0, c0);
+    StepLoads ld(p, kb, m0, c0, group);
     uint32_t ld_lds = lds0;
     auto issue = [&](int i) {
         if (i < WL) dma16(ld.codes(ke, K, c0), ld_lds + 8192 * i, offw[i], 0);
@@ -555,12 +609,12 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
     __syncthreads();
 
     // lane: token lane % 16 of block b, channels 32 w + 16 a + 4 fq + v
-    if (slot >= 0) {
+    if (!GROUPED && slot >= 0) {
         float *dst = p.part + (int64_t)slot * (BM * BC);
 #pragma unroll
         for (int b = 0; b < 16; ++b) {
             const int ml = 16 * b + frow;
-            if (m0 + ml < p.M) {
+            if (m0 + ml < end) {
 #pragma unroll
                 for (int a = 0; a < 2; ++a)
                     *reinterpret_cast<v4f *>(dst + ml * BC + 32 * w + 16 * a + 4 * fq) = acc[a][b];
@@ -620,7 +674,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 #pragma unroll 1
         for (int it = 0; it < 8; ++it) {
             const int row = 16 * it + ((int)threadIdx.x >> 5), m = m0 + 128 * pass + row;
-            if (m >= p.M || c >= K) continue;
+            if (m >= end || c >= K) continue;
             float v[8];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -628,7 +682,7 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
             }
-            finish8(p, m, c, v);
+            finish8<GROUPED>(p, m, c, v, group);
         }
     }
 }
@@ -691,7 +745,7 @@ __global__ void __launch_bounds__(256) grad_join_kernel(GradParams p, int rb)
                 v[e] = (l >> b) & 1 ? o - v[e] : v[e] + o;
             }
         }
-    if (row_ok && c < p.K) finish8(p, m, c, v);
+    if (row_ok && c < p.K) finish8<false>(p, m, c, v);
 }
 
 struct PrepParams {
@@ -802,6 +856,86 @@ __global__ void __launch_bounds__(256) grad_bias_kernel(const float *sums, int c
 #pragma unroll 4
     for (int c = 0; c < chunks; ++c) s += sums[((int64_t)c * parts + blockIdx.y) * N + n];
     db[n] = s;
+}
+
+// The operand of a grouped contraction: a[row] = bf16(share dy[source] sw[group]) and, for the slots of a
+// mixture-of-experts layer, the gradient of their weights, dweight = sum_n dy[source, n] d[slot, n] in fp32.
+// A workgroup takes one row.  MoE (experts non-null): workgroup = slot, its group the slot's expert, its source the
+// slot's token, its row where the sort put it; slots without an expert get dweight 0 and no row.  Otherwise the
+// workgroup's row itself, and the first group whose offsets hold it.  Columns from N to lda are zeros.  Bound by memory.
+struct RowsParams {
+    const uint16_t *dy;        // [., N]
+    const float *sw;           // [groups, N]
+    const int32_t *offsets;
+    const int32_t *experts, *row_of;   // [slots]
+    const float *weights;      // [slots]
+    const uint16_t *d;         // bf16 [slots, N] or null
+    float *dweights;           // [slots] or null
+    uint16_t *a;               // [rows, lda]
+    int64_t lda;
+    int rows, groups, N, top;
+};
+
+__global__ void __launch_bounds__(256) grad_rows_kernel(RowsParams p)
+{
+    __shared__ float red[4];
+    typedef v4u unaligned __attribute__((aligned(2)));
+    const int s = (int)blockIdx.x, t = (int)threadIdx.x;
+    int64_t row = s, source = s;
+    int group = -1;
+    float share = 1.0f;
+    if (p.experts) {
+        row = p.row_of[s];
+        if (row < 0) {
+            if (p.dweights && t == 0) p.dweights[s] = 0.0f;
+            return;
+        }
+        group = p.experts[s];
+        source = s / p.top;
+        share = p.weights[s];
+    } else {
+        for (int b = 0; b < p.groups && group < 0; b += 64) {
+            const int e = b + (t & 63);
+            int lo = 0, hi = 0;
+            if (e < p.groups) group_range(p.offsets, e, p.rows, lo, hi);
+            const uint64_t in = __builtin_amdgcn_ballot_w64(lo <= s && s < hi);
+            if (in) group = b + __builtin_ctzll(in);
+        }
+        if (group < 0) return;                           // a row of no group
+    }
+    const uint16_t *dy = p.dy + source * p.N, *d = p.d ? p.d + (int64_t)s * p.N : nullptr;
+    const float *sw = p.sw + (int64_t)group * p.N;
+    uint16_t *a = p.a + row * p.lda;
+    float sum = 0.0f;
+    for (int n = 8 * t; n < p.lda; n += 8 * 256) {
+        float v[8], e[8];
+        auto load8 = [&](const uint16_t *src, float (&to)[8]) {
+            if (n + 8 <= p.N) {
+                const v4u x = *reinterpret_cast<const unaligned *>(src + n);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) to[i] = i & 1 ? bf16hi_to_f32(x[i >> 1]) : bf16lo_to_f32(x[i >> 1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) to[i] = n + i < p.N ? bf16lo_to_f32(src[n + i]) : 0.0f;
+            }
+        };
+        load8(dy, v);
+        if (d) {
+            load8(d, e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(v[i], e[i], sum);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = n + i < p.N ? v[i] * share * sw[n + i] : 0.0f;
+        *reinterpret_cast<v4u *>(a + n) =
+            v4u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
+    if (!p.dweights || !d) return;
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) sum += __shfl_xor(sum, k);
+    if ((t & 63) == 0) red[t >> 6] = sum;
+    __syncthreads();
+    if (t == 0) p.dweights[s] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
 int cu_count()
@@ -934,7 +1068,7 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
         }
     }
     if (g.M <= 0) return hipSuccess;
-    GradParams p;
+    GradParams p = {};
     p.a = g.a ? g.a : reinterpret_cast<const uint16_t *>(ws);
     p.w1 = g.wq1;
     p.w2 = gated ? g.wq2 : g.wq1;
@@ -957,12 +1091,71 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
     p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g)));
     const int T = pl.tiles_m * pl.tiles_c, U = pl.T_dp + (T - pl.T_dp) * pl.S;
     const dim3 grid((unsigned)((U + 7) & ~7));
-    if (pl.bm == 64) hipLaunchKernelGGL(grad_tile_kernel, grid, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL(grad_gemm_kernel, grid, dim3(512), 0, stream, p);
+    if (pl.bm == 64) hipLaunchKernelGGL(grad_tile_kernel<false>, grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(grad_gemm_kernel<false>, grid, dim3(512), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || pl.S == 1) return e;
     const int rb = (int)((g.M < pl.bm ? g.M : pl.bm) + 7) / 8;
     hipLaunchKernelGGL(grad_join_kernel, dim3((unsigned)(T - pl.T_dp) * (unsigned)rb), dim3(256), 0, stream, p, rb);
+    return hipGetLastError();
+}
+
+int64_t grouped_grad_lda(int64_t N) { return (N + BN - 1) / BN * BN; }
+
+hipError_t launch_grouped_rows(const GroupedRowsArgs &g, hipStream_t stream)
+{
+    if (g.rows <= 0) return hipSuccess;
+    RowsParams p;
+    p.dy = g.dy;
+    p.sw = g.sw;
+    p.offsets = g.offsets;
+    p.experts = g.experts;
+    p.row_of = g.row_of;
+    p.weights = g.weights;
+    p.d = g.d;
+    p.dweights = g.dweights;
+    p.a = g.a;
+    p.lda = grouped_grad_lda(g.N);
+    p.rows = (int)g.rows;
+    p.groups = g.groups;
+    p.N = (int)g.N;
+    p.top = g.top;
+    hipLaunchKernelGGL(grad_rows_kernel, dim3((unsigned)g.rows), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_grouped_grad(const GroupedGradArgs &g, hipStream_t stream)
+{
+    if (g.rows <= 0) return hipSuccess;
+    GradParams p = {};
+    p.a = g.a;
+    p.w1 = g.wq1;
+    p.w2 = g.wq2 ? g.wq2 : g.wq1;
+    p.add = g.add;
+    p.dx = g.dx;
+    p.rows_out = g.rows_out;
+    p.lda = grouped_grad_lda(g.N) * (g.wq2 ? 2 : 1);
+    p.M = (int)g.rows;
+    p.N = (int)g.N;
+    p.K = g.K;
+    p.lg = g.log2g;
+    p.nt1 = (int)(grouped_grad_lda(g.N) / BN);
+    p.nt = p.nt1 * (g.wq2 ? 2 : 1);
+    p.tiles_c = (g.K + BC - 1) / BC;
+    p.norm = (float)(1.0 / __builtin_sqrt((double)(1 << g.log2g)));
+    p.next = g.next;
+    p.offsets = g.offsets;
+    p.slot_of = g.slot_of;
+    p.groups = g.groups;
+    // A step takes 0.54 us of a CU in 64-row tiles, 1.6 us in 256-row ones (tile_plan), and a group's last tile is half
+    // empty on average: equal at about 240 rows per group.
+    const int64_t used = g.groups < g.rows ? g.groups : g.rows;
+    const int bm = g.rows > 240 * used ? BM : 64;
+    const int64_t most = most_group_tiles(g.rows, g.groups, bm) * p.tiles_c;
+    if (most >= ((int64_t)1 << 31) - 8) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)((most + 7) & ~7));
+    if (bm == 64) hipLaunchKernelGGL(grad_tile_kernel<true>, grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(grad_gemm_kernel<true>, grid, dim3(512), 0, stream, p);
     return hipGetLastError();
 }
 

@@ -1,0 +1,424 @@
+// grouped_i8.hip -- products of rows sorted by group (expert) with their group's INT8 weight, and what a
+// mixture-of-experts layer needs around them (gfx950).
+//
+//   moe_order_kernel    slots sorted by expert: the groups' offsets, slot and token of each row, row of each slot
+//   grouped_tile_kernel acc[r, n] = sum_k xq[src(r), k] wq[group(r), n, k] with one of three epilogues
+//   moe_combine_kernel  y[m] = bf16(sum_j weight[m, j] part[row(m, j)] + residual[m])
+#include "activation.hpp"
+#include "device_common.hpp"
+#include "grouped_common.hpp"
+#include "launchers.hpp"
+#include "tile_common.hpp"
+
+namespace convrot {
+namespace {
+
+// ---------------------------------------------------------------------------------------------
+// Slots sorted by expert, in their own order within an expert (a counting sort).  Workgroup e of E + 1 reads all
+// slots, counts those of smaller experts, which is where its rows begin, and then writes the rows of its own; the
+// last one takes the slots without an expert and the total.  Workgroups need nothing from one another, so this is one
+// launch with the same result at every call.  Bound by each workgroup's read of all slots.
+struct OrderParams {
+    const int32_t *experts;    // [S]
+    int32_t *offsets;          // [E + 1]
+    int32_t *slot_of, *token_of;   // [S] of each row
+    int32_t *row_of;           // [S] of each slot, -1 without an expert
+    int S, E, top;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
+{
+    __shared__ int2 part[NT / 64];
+    const int t = (int)threadIdx.x, lane = t & 63, e = (int)blockIdx.x;
+    const int chunk = (((p.S + NT - 1) / NT) + 3) & ~3;
+    const int s0 = min(t * (int64_t)chunk, (int64_t)p.S), s1 = min(s0 + chunk, p.S);
+    const bool none = e == p.E;
+    // mine: of this expert (or of none); less: with a smaller one
+    auto mine = [&](int x) { return none ? (unsigned)x >= (unsigned)p.E : x == e; };
+    auto less = [&](int x) { return (unsigned)x < (unsigned)e; };
+    int n_mine = 0, n_less = 0;
+    typedef v4i v4i_any __attribute__((aligned(4)));
+    auto each = [&](auto f) {
+        int s = s0;
+        for (; s + 4 <= s1; s += 4) {
+            const v4i x = *reinterpret_cast<const v4i_any *>(p.experts + s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f(s + i, x[i]);
+        }
+        for (; s < s1; ++s) f(s, p.experts[s]);
+    };
+    each([&](int, int x) {
+        n_mine += mine(x);
+        n_less += less(x);
+    });
+    int before = n_mine, all = n_less;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(before, d);
+        if (lane >= d) before += o;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) all += __shfl_xor(all, d);
+    if (lane == 63) part[t >> 6] = int2{before, all};
+    __syncthreads();
+    int row = before - n_mine, first = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) {
+        if (i < (t >> 6)) row += part[i].x;
+        first += part[i].y;
+    }
+    if (t == 0) p.offsets[e] = first;
+    row += first;
+    if (n_mine == 0) return;
+    each([&](int s, int x) {
+        if (!mine(x)) return;
+        p.row_of[s] = none ? -1 : row;
+        if (none) return;
+        p.slot_of[row] = s;
+        p.token_of[row] = s / p.top;
+        ++row;
+    });
+}
+
+// ---------------------------------------------------------------------------------------------
+// The product, BM (64 or 128) rows x 128 weight rows per unit: the structure of gemm_i8_tile_kernel (K in tiles of 128
+// bytes through NST LDS stages, one barrier per K-tile, 4 wavefronts in 2 x 2, two workgroups per CU), walking
+// units blockIdx.x, blockIdx.x + gridDim.x, ... of a count that only the GPU knows.
+constexpr int BN = 128, BK = 128;
+constexpr int NTHREADS = 256;
+
+struct GroupedParams {
+    const int8_t *xq;          // codes of the source rows
+    const float *sx;
+    const int32_t *offsets;
+    const int32_t *source;     // source row of a row, or null: the row itself
+    const int32_t *slot_of;    // where pre and d keep a row, or null: the row itself
+    const int8_t *wq, *wq2;    // [groups, N, K]
+    const float *sw, *sw2;     // [groups, N]
+    uint16_t *y;               // Plain: bf16 [rows, N]; Gated: bf16(act(g) u) [rows, N]
+    float *part;               // Part: fp32 [rows, N]
+    uint16_t *pre;             // Gated: bf16 [2, pre_rows, N] or null
+    uint16_t *d;               // Part: bf16 [slots, N] or null
+    int64_t pre_rows;
+    int rows, groups, N, K, tiles_n, act;
+};
+
+typedef v4u v4u_any __attribute__((aligned(2)));         // 16 bytes at any element (an odd N)
+
+template <GroupedEpi E>
+constexpr int features() { return E == GroupedEpi::Gated ? BN / 2 : BN; }
+
+// Rows of 8 columns n.. to dst, clipped at N (VEC: N % 8 == 0, all exist).
+template <bool VEC>
+__device__ __forceinline__ void store8(uint16_t *dst, int n, int N, const float (&a)[8])
+{
+    const v4u d = {pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7])};
+    if (VEC || n + 8 <= N) {
+        *reinterpret_cast<v4u_any *>(dst) = d;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (n + e < N) dst[e] = (uint16_t)(e & 1 ? d[e >> 1] >> 16 : d[e >> 1] & 0xffffu);
+    }
+}
+
+template <GroupedEpi E, int BM, int NST, bool VEC>
+__global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams p)
+{
+    constexpr int NF = features<E>();
+    constexpr int STAGE = (BN + BM) * BK;
+    constexpr int LPK = (BN + BM) / 32;                  // loads per K-tile and wave
+    constexpr int MB = BM / 32;                          // 16-row blocks per wave
+    __shared__ __attribute__((aligned(16))) uint8_t smem[NST * STAGE];
+    __shared__ int starts[MAX_GROUPS];
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = w & 1, wm = w >> 1;
+    const int K = p.K, KT = (K + BK - 1) / BK;
+    const int tiles = group_tiles<NTHREADS>(p.offsets, p.groups, p.rows, BM, starts, reinterpret_cast<int *>(smem));
+    // (offsets out of order may give more than the host counted: held to what int can number)
+    const int units = (int)min((int64_t)tiles * p.tiles_n, (int64_t)0x7fffff00);
+    const int frow = lane & 15, fq = lane >> 4;
+    const uint32_t half = K % BK && ((lane & 7) ^ swz(8 * w + (lane >> 3))) >= 4 ? OOB : 0u;
+
+    for (uint32_t v = blockIdx.x; v < (uint32_t)units; v += gridDim.x) {
+        int tm, tn;
+        tile_coords(unit_of((int)v, 0, units), tiles, p.tiles_n, tm, tn);
+        const GroupRows gr = group_of_tile(p.offsets, p.rows, BM, starts, tm);
+        const int m0 = gr.first, left = gr.end - gr.first;   // rows of this tile: min(left, BM)
+        const int n0 = tn * NF;
+        // instruction i of wave w fills LDS rows 8 (4 i + w) .. + 7 (weight rows 0 .. 127, then rows of x);
+        // lane -> row + lane / 8 at position lane % 8
+        uint32_t off[LPK];
+#pragma unroll
+        for (int i = 0; i < LPK; ++i) {
+            const int r = 8 * (4 * i + w) + (lane >> 3), c = 16 * ((lane & 7) ^ swz(r));
+            if (i < 4) {
+                const int wr = E == GroupedEpi::Gated ? 16 * (r >> 5) + (r & 15) : r;
+                off[i] = n0 + wr < p.N ? (uint32_t)(wr * K + c) : OOB;
+            } else {
+                const int rr = r - BN;
+                if (p.source) off[i] = rr < left ? (uint32_t)(p.source[m0 + rr] * K + c) : OOB;
+                else off[i] = rr < left ? (uint32_t)(rr * K + c) : OOB;
+            }
+        }
+        const int8_t *wsrc = E == GroupedEpi::Gated && (w & 2) ? p.wq2 : p.wq;   // rows 16..31 of each 32: up
+        const uint64_t wbase = reinterpret_cast<uint64_t>(wsrc + ((int64_t)gr.group * p.N + n0) * K);
+        const uint64_t xbase = reinterpret_cast<uint64_t>(p.source ? p.xq : p.xq + (int64_t)m0 * K);
+        auto issue = [&](int t) {
+            const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(wbase, NUM_RECORDS), rx = uniform_rsrc(xbase, NUM_RECORDS);
+            uint8_t *base = smem + (t % NST) * STAGE + w * 1024;
+            const uint32_t skip = t >= KT ? OOB : t == KT - 1 ? half : 0u;
+            const int k0 = __builtin_amdgcn_readfirstlane(t < KT ? t * BK : 0);
+#pragma unroll
+            for (int i = 0; i < LPK; ++i) load16_to_lds(i < 4 ? rw : rx, base + 4096 * i, off[i] | skip, k0);
+        };
+
+        v4i acc[4][MB];
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int b = 0; b < MB; ++b) acc[a][b] = v4i{};
+#pragma unroll
+        for (int j = 0; j < NST - 1; ++j) issue(j);
+        for (int t = 0; t < KT; ++t) {
+            // K-tile t has landed once only the NST - 2 after it are in flight
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * LPK));
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            issue(t + NST - 1);
+            const uint8_t *st = smem + (t % NST) * STAGE;
+            const uint8_t *ar = st + (wn * 64 + frow) * BK, *br = st + (BN + wm * (BM / 2) + frow) * BK;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                const int pos = 16 * ((4 * kk + fq) ^ swz(frow));
+                v4i fa[4], fb[MB];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) fa[b] = *reinterpret_cast<const v4i *>(ar + 16 * b * BK + pos);
+#pragma unroll
+                for (int b = 0; b < MB; ++b) fb[b] = *reinterpret_cast<const v4i *>(br + 16 * b * BK + pos);
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int b = 0; b < MB; ++b)
+                        acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[a], fb[b], acc[a][b], 0, 0, 0);
+            }
+        }
+        // lane: row lane % 16 of block b, weight rows 16 a + 4 (lane / 16) + v of the wave's 64.  Each wave passes
+        // its 16-row blocks through its own 4 KiB (rows of 64 sums, 16-byte chunk c at c ^ row), then takes row pieces
+        // of 8 output columns per lane.
+        constexpr int LPR = NF / 2 / 8, RPI = 64 / LPR;  // lanes per row, rows at a time
+        const int lrow = lane / LPR, lcol = lane % LPR;
+        const int n = n0 + wn * (NF / 2) + 8 * lcol;
+        const int ch = E == GroupedEpi::Gated ? 8 * (lcol >> 1) + 2 * (lcol & 1) : 2 * lcol;
+        float s1[8], s2[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t i = (int64_t)gr.group * p.N + min(n + e, p.N - 1);
+            s1[e] = p.sw[i];
+            if constexpr (E == GroupedEpi::Gated) s2[e] = p.sw2[i];
+        }
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        __syncthreads();
+        uint8_t *reg = smem + w * 4096;
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+                *reinterpret_cast<v4i *>(reg + frow * 256 + 16 * ((4 * a + fq) ^ frow)) = acc[a][b];
+#pragma unroll 1
+            for (int q = 0; q < 16 / RPI; ++q) {
+                const int r = RPI * q + lrow, rl = wm * (BM / 2) + 16 * b + r;
+                if (rl >= left || n >= p.N) continue;
+                const int64_t row = m0 + rl;
+                const float sxm = p.sx[p.source ? p.source[row] : row];
+                auto z8 = [&](int chunk, const float (&s)[8], float (&z)[8]) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const v4i d = *reinterpret_cast<const v4i *>(reg + r * 256 + 16 * ((chunk + h) ^ r));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z[4 * h + i] = __builtin_fmaf((float)d[i], sxm * s[4 * h + i], 0.0f);
+                    }
+                };
+                float z[8], u[8];
+                z8(ch, s1, z);
+                if constexpr (E == GroupedEpi::Plain) store8<VEC>(p.y + row * p.N + n, n, p.N, z);
+                if constexpr (E == GroupedEpi::Part) {
+                    float *dst = p.part + row * p.N + n;
+                    *reinterpret_cast<v4f *>(dst) = v4f{z[0], z[1], z[2], z[3]};
+                    *reinterpret_cast<v4f *>(dst + 4) = v4f{z[4], z[5], z[6], z[7]};
+                    if (p.d) store8<VEC>(p.d + (int64_t)p.slot_of[row] * p.N + n, n, p.N, z);
+                }
+                if constexpr (E == GroupedEpi::Gated) {
+                    z8(ch + 4, s2, u);
+                    if (p.pre) {
+                        uint16_t *dst = p.pre + (int64_t)p.slot_of[row] * p.N + n;
+                        store8<VEC>(dst, n, p.N, z);
+                        store8<VEC>(dst + p.pre_rows * p.N, n, p.N, u);
+                    }
+                    act_values(z, p.act);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] *= u[e];
+                    store8<VEC>(p.y + row * p.N + n, n, p.N, z);
+                }
+            }
+        }
+        __syncthreads();                                 // the next unit's loads refill what was read here
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// A thread takes 8 channels of one token; all slots' parts are requested before the first is added, in slot
+// order.  Slots without an expert add nothing.
+struct CombineParams {
+    const float *part;         // [rows, K]
+    const int32_t *row_of;     // [M, top]
+    const float *weights;      // [M, top], or null: 1
+    const uint16_t *residual;  // bf16 [M, K] or null
+    uint16_t *y;
+    int64_t units;             // M K / 8
+    int K, top;
+};
+
+__global__ void __launch_bounds__(256) moe_combine_kernel(CombineParams p)
+{
+    constexpr int AHEAD = 8;
+    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (u >= p.units) return;
+    const int per = p.K / 8;
+    const int64_t m = u / per;
+    const int c = 8 * (int)(u - m * per);
+    v4u res = {};
+    if (p.residual) res = *reinterpret_cast<const v4u *>(p.residual + m * p.K + c);
+    float v[8] = {};
+#pragma unroll 1
+    for (int j = 0; j < p.top; j += AHEAD) {
+        v4f a[AHEAD], b[AHEAD];
+        float w[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            a[i] = b[i] = v4f{};
+            w[i] = 0.0f;
+            if (j + i < p.top) {
+                const int row = p.row_of[m * p.top + j + i];
+                if (row >= 0) {
+                    const float *src = p.part + (int64_t)row * p.K + c;
+                    a[i] = *reinterpret_cast<const v4f *>(src);
+                    b[i] = *reinterpret_cast<const v4f *>(src + 4);
+                    w[i] = p.weights ? p.weights[m * p.top + j + i] : 1.0f;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = __builtin_fmaf(w[i], a[i][e], v[e]);
+                v[e + 4] = __builtin_fmaf(w[i], b[i][e], v[e + 4]);
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += e & 1 ? bf16hi_to_f32(res[e >> 1]) : bf16lo_to_f32(res[e >> 1]);
+    *reinterpret_cast<v4u *>(p.y + m * p.K + c) =
+        v4u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+constexpr int GRID = 512;                                // two workgroups per CU
+
+template <GroupedEpi E, int BM, int NST, bool VEC>
+void launch_tiles(const GroupedParams &p, hipStream_t stream)
+{
+    // a multiple of 8, so that a workgroup's units stay on its XCD
+    const int64_t most = most_group_tiles(p.rows, p.groups, BM) * p.tiles_n;
+    const unsigned grid = most < GRID ? (unsigned)((most + 7) & ~7) : (unsigned)GRID;
+    hipLaunchKernelGGL((grouped_tile_kernel<E, BM, NST, VEC>), dim3(grid), dim3(NTHREADS), 0, stream, p);
+}
+
+template <GroupedEpi E, bool VEC>
+void launch_rows(const GroupedParams &p, hipStream_t stream)
+{
+    const int used = p.groups < p.rows ? p.groups : p.rows;
+    if (p.rows <= 64 * (int64_t)used) launch_tiles<E, 64, 3, VEC>(p, stream);
+    else launch_tiles<E, 128, 2, VEC>(p, stream);
+}
+
+} // namespace
+
+hipError_t launch_moe_order(const int32_t *experts, int64_t S, int E, int top, const MoeOrder &o, hipStream_t stream)
+{
+    OrderParams p;
+    p.experts = experts;
+    p.offsets = o.offsets;
+    p.slot_of = o.slot_of;
+    p.token_of = o.token_of;
+    p.row_of = o.row_of;
+    p.S = (int)S;
+    p.E = E;
+    p.top = top;
+    if (S <= 2048) hipLaunchKernelGGL(moe_order_kernel<256>, dim3(E + 1), dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(moe_order_kernel<1024>, dim3(E + 1), dim3(1024), 0, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_grouped_i8(const GroupedArgs &g, GroupedEpi epi, hipStream_t stream)
+{
+    if (g.rows <= 0 || g.N <= 0) return hipSuccess;
+    GroupedParams p;
+    p.xq = g.xq;
+    p.sx = g.sx;
+    p.offsets = g.offsets;
+    p.source = g.source;
+    p.slot_of = g.slot_of;
+    p.wq = g.wq;
+    p.wq2 = g.wq2;
+    p.sw = g.sw;
+    p.sw2 = g.sw2;
+    p.y = g.y;
+    p.part = g.part;
+    p.pre = g.pre;
+    p.d = g.d;
+    p.pre_rows = g.rows;
+    p.rows = (int)g.rows;
+    p.groups = g.groups;
+    p.N = (int)g.N;
+    p.K = g.K;
+    p.act = g.act;
+    const int nf = epi == GroupedEpi::Gated ? BN / 2 : BN;
+    p.tiles_n = (int)((g.N + nf - 1) / nf);
+    const bool vec = g.N % 8 == 0;
+    switch (epi) {
+    case GroupedEpi::Plain:
+        if (vec) launch_rows<GroupedEpi::Plain, true>(p, stream);
+        else launch_rows<GroupedEpi::Plain, false>(p, stream);
+        break;
+    case GroupedEpi::Gated:
+        if (!vec) return hipErrorInvalidValue;
+        launch_rows<GroupedEpi::Gated, true>(p, stream);
+        break;
+    default:
+        if (!vec) return hipErrorInvalidValue;
+        launch_rows<GroupedEpi::Part, true>(p, stream);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const float *part, const int32_t *row_of, const float *weights, const uint16_t *residual,
+                              uint16_t *y, int64_t M, int K, int top, hipStream_t stream)
+{
+    if (M <= 0) return hipSuccess;
+    CombineParams p;
+    p.part = part;
+    p.row_of = row_of;
+    p.weights = weights;
+    p.residual = residual;
+    p.y = y;
+    p.units = M * (K / 8);
+    p.K = K;
+    p.top = top;
+    const int64_t blocks = (p.units + 255) / 256;
+    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+} // namespace convrot

@@ -91,6 +91,85 @@ struct GradArgs {
 size_t grad_workspace_bytes(int64_t M, int64_t N, int K, bool gated, bool a_given = false);
 hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream);
 
+// ---- mixture of experts (grouped_common.hpp says what offsets hold)
+//
+// Where the slots (token, j) of M tokens with `top` experts each go when sorted by expert, E <= MAX_GROUPS: rows
+// offsets[e] .. offsets[e + 1] - 1 are expert e's, in slot order; slots with an expert outside [0, E) have row -1 and
+// take no row.  All in device memory, S = M top entries (offsets: E + 1).
+struct MoeOrder {
+    int32_t *offsets = nullptr, *slot_of = nullptr, *token_of = nullptr, *row_of = nullptr;
+};
+hipError_t launch_moe_order(const int32_t *experts, int64_t S, int E, int top, const MoeOrder &o, hipStream_t stream);
+
+// Products of rows sorted by group with their group's weight, z = acc sx sw:
+//   Plain: y = bf16(z);   Gated: y = bf16(act(g) u), pre = bf16([g; u]);   Part: part = z (fp32), d = bf16(z)
+// Rows of no group are neither read nor written.  Gated and Part: N % 8 == 0.
+enum class GroupedEpi { Plain = 0, Gated = 1, Part = 2 };
+struct GroupedArgs {
+    const int8_t *xq = nullptr;           // [rows, K], or with `source` any rows, of fewer than 2^31 bytes in all
+    const float *sx = nullptr;
+    const int32_t *offsets = nullptr;
+    const int32_t *source = nullptr;      // the row of xq and sx that a row takes; null: its own
+    const int32_t *slot_of = nullptr;     // the row of pre and d that a row goes to (with pre or d)
+    const int8_t *wq = nullptr, *wq2 = nullptr;   // [groups, N, K]
+    const float *sw = nullptr, *sw2 = nullptr;    // [groups, N]
+    uint16_t *y = nullptr, *pre = nullptr, *d = nullptr;   // pre [2, rows, N] (or null), d [rows, N] (or null)
+    float *part = nullptr;
+    int64_t rows = 0, N = 0;
+    int groups = 0, K = 0, act = 0;
+};
+hipError_t launch_grouped_i8(const GroupedArgs &g, GroupedEpi epi, hipStream_t stream);
+
+// Gradients of grouped products through the frozen weights, in two steps (contractions of grouped_grad_lda(N) columns
+// per weight):
+//   rows:  a[row] = bf16(share dy[source] sw[group]);  with `experts` (one workgroup per slot) share, source and row are the
+//          slot's weight, token and place in the sort, and dweights[slot] = sum dy[token] d[slot] (0 without an expert)
+//   grad:  v = (a . wq[group]) R;  to dx = bf16(v + add), to rows_out = v in fp32, or on to next.a (GradNext, its pre
+//          [2, rows, K] read at row slot_of[row], its scales [groups, K])
+int64_t grouped_grad_lda(int64_t N);
+struct GroupedRowsArgs {
+    const uint16_t *dy = nullptr;
+    const float *sw = nullptr;
+    const int32_t *offsets = nullptr, *experts = nullptr, *row_of = nullptr;
+    const float *weights = nullptr;
+    const uint16_t *d = nullptr;
+    float *dweights = nullptr;
+    uint16_t *a = nullptr;
+    int64_t rows = 0, N = 0;
+    int groups = 0, top = 1;
+};
+hipError_t launch_grouped_rows(const GroupedRowsArgs &g, hipStream_t stream);
+struct GroupedGradArgs {
+    const uint16_t *a = nullptr;
+    const int32_t *offsets = nullptr, *slot_of = nullptr;
+    const int8_t *wq1 = nullptr, *wq2 = nullptr;
+    const uint16_t *add = nullptr;
+    uint16_t *dx = nullptr;
+    float *rows_out = nullptr;
+    GradNext next;
+    int64_t rows = 0, N = 0;
+    int groups = 0, K = 0, log2g = 0;
+};
+hipError_t launch_grouped_grad(const GroupedGradArgs &g, hipStream_t stream);
+
+// y[m] = bf16(sum_j weights[m, j] part[row_of[m, j]] + residual[m])  (weights null: 1; K % 8 == 0).
+hipError_t launch_moe_combine(const float *part, const int32_t *row_of, const float *weights, const uint16_t *residual,
+                              uint16_t *y, int64_t M, int K, int top, hipStream_t stream);
+
+// Router: see convrot_moe_route and convrot_moe_route_backward.
+struct RouteArgs {
+    const void *logits = nullptr;         // [M, E]
+    bool f32 = false;
+    const float *bias = nullptr;
+    int64_t M = 0;
+    int E = 0, top = 0, score = 0;
+    bool normalize = false;
+    float scale = 1.0f;
+};
+hipError_t launch_moe_route(const RouteArgs &a, int32_t *experts, float *weights, hipStream_t stream);
+hipError_t launch_moe_route_backward(const RouteArgs &a, const float *dweights, const int32_t *experts, void *dlogits,
+                                     hipStream_t stream);
+
 // W4A4: y = bf16(sum_g acc_g * sx[m,g] * sw[n,g] + bias[n]) with packed int4 operands and
 // fp16 group scales (group = 256 or 128, K % group == 0, K >= 256), or the unscaled int32 total
 // sum_k cx*cw (scales ignored).

@@ -1,0 +1,294 @@
+// moe_route.hip -- the router of a mixture-of-experts layer: the top experts of each token and their weights, and the
+// gradient of the logits (gfx950).
+//
+//   s = softmax(l) or sigmoid(l) over the E experts;   key = l, or with a bias s + bias
+//   experts = the `top` largest keys (ties to the lowest index), never a key of -inf (a masked expert)
+//   w_j = scale s_j,  or with normalize  scale s_j / sum over the chosen of s
+// Without a bias the logits themselves order the experts (both scores grow with them), exactly; with one the keys
+// are taken in 64 bits, since two of them may be closer than fp32 can tell.
+// Normalised weights come from the chosen logits alone: a softmax over log s (l itself, up to a constant, for
+// softmax), so they stay defined where every s is 0 in fp32.  They and their gradients are formed in 64 bits:
+// a handful of values per token, next to differences that cancel.
+//
+// One wavefront per token, PER logits per lane.  A choice is the largest (key, lowest index) over the wavefront, six
+// exchanges; the winner's lane drops it.  Bound by those exchanges: memory would take a quarter of the time.
+#include "device_common.hpp"
+#include "launchers.hpp"
+
+namespace convrot {
+namespace {
+
+constexpr int WAVES = 4;
+
+struct RouteParams {
+    const void *logits;
+    const float *bias;
+    int32_t *experts;
+    float *weights;
+    int64_t M;
+    int E, top;
+    float scale;
+    bool f32, sigmoid, normalize;
+};
+
+__device__ __forceinline__ float load_logit(const void *p, bool f32, int64_t i)
+{
+    return f32 ? static_cast<const float *>(p)[i] : bf16lo_to_f32(static_cast<const uint16_t *>(p)[i]);
+}
+
+__device__ __forceinline__ float wave_max(float v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v = __builtin_fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+
+// Unsigned integers in the order of the floats (-0 as 0; 0 for NaN and -inf, which no choice takes).
+__device__ __forceinline__ uint32_t ordered(float v)
+{
+    if (!(v > -__builtin_inff())) return 0u;
+    const uint32_t b = __float_as_uint(v == 0.0f ? 0.0f : v);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t ordered(double v)
+{
+    if (!(v > -__builtin_inf())) return 0u;
+    const uint64_t b = __builtin_bit_cast(uint64_t, v == 0.0 ? 0.0 : v);
+    return b & 0x8000000000000000u ? ~b : b | 0x8000000000000000u;
+}
+
+// log sigmoid(l), whose exponential is the score up to rounding for every l.
+__device__ __forceinline__ double log_sigmoid(double l) { return l < 0.0 ? l - log1p(exp(l)) : -log1p(exp(-l)); }
+
+// The weights' common part for lane j < n, which holds the chosen logit l (other lanes: nothing): with normalize the
+// softmax of log s, else s itself.  zmax, z: the row's largest logit and sum of exponentials (softmax scores).
+__device__ __forceinline__ double chosen_share(bool sigmoid, bool normalize, double l, bool valid, float zmax, double z)
+{
+    if (!normalize) {
+        if (!valid) return 0.0;
+        return sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)zmax) / z;
+    }
+    const double v = sigmoid ? log_sigmoid(l) : l;
+    double most = valid ? v : -__builtin_inf();
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) most = fmax(most, __shfl_xor(most, d));
+    const double e = valid ? exp(v - most) : 0.0;
+    return e / wave_sum(e);
+}
+
+template <typename KEY, int PER>
+__global__ void __launch_bounds__(64 * WAVES) moe_route_kernel(RouteParams p)
+{
+    constexpr bool BIAS = sizeof(KEY) == 8;
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
+    if (m >= p.M) return;
+    float l[PER];
+    bool bad = false;
+    float most = -__builtin_inff();
+#pragma unroll
+    for (int r = 0; r < PER; ++r) {
+        const int i = 64 * r + lane;
+        l[r] = i < p.E ? load_logit(p.logits, p.f32, m * p.E + i) : -__builtin_inff();
+        bad |= l[r] != l[r];
+        most = __builtin_fmaxf(most, l[r]);
+    }
+    bad = __builtin_amdgcn_ballot_w64(bad) != 0;
+    double z = 1.0;
+    if (!p.sigmoid && (BIAS || !p.normalize)) {
+        most = wave_max(most);
+        double sum = 0.0;
+#pragma unroll
+        for (int r = 0; r < PER; ++r)
+            if (l[r] > -__builtin_inff()) sum += BIAS ? exp((double)l[r] - (double)most) : (double)expf(l[r] - most);
+        z = wave_sum(sum);
+    }
+    KEY key[PER];
+#pragma unroll
+    for (int r = 0; r < PER; ++r) {
+        if constexpr (BIAS) {
+            const int i = 64 * r + lane;
+            key[r] = 0u;
+            if (i < p.E && l[r] > -__builtin_inff()) {
+                const double x = (double)l[r];
+                const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)most) / z;
+                key[r] = ordered(s + (double)p.bias[i]);
+            }
+        } else {
+            key[r] = ordered(l[r]);
+        }
+    }
+    int chosen = -1;                                     // lane j: the j-th expert
+    float value = 0.0f;                                  // and its logit
+    for (int j = 0; j < p.top; ++j) {
+        KEY best = 0u;
+        int at = 0;
+#pragma unroll
+        for (int r = 0; r < PER; ++r)
+            if (key[r] > best) {                         // the lowest index of equal ones
+                best = key[r];
+                at = 64 * r + lane;
+            }
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const KEY other = __shfl_xor(best, d);
+            const int oat = __shfl_xor(at, d);
+            if (other > best || (other == best && oat < at)) {
+                best = other;
+                at = oat;
+            }
+        }
+        if (best == 0u) break;                           // nothing left that may be chosen
+        float v = 0.0f;
+#pragma unroll
+        for (int r = 0; r < PER; ++r)
+            if (at == 64 * r + lane) {
+                key[r] = 0u;
+                v = l[r];
+            }
+        v = __shfl(v, at & 63);
+        if (lane == j) {
+            chosen = at;
+            value = v;
+        }
+    }
+    const double share = chosen_share(p.sigmoid, p.normalize, (double)value, chosen >= 0, most, z);
+    if (lane < p.top) {
+        p.experts[m * p.top + lane] = chosen;
+        p.weights[m * p.top + lane] = bad ? __builtin_nanf("") : chosen < 0 ? 0.0f : (float)(share * (double)p.scale);
+    }
+}
+
+struct RouteGradParams {
+    const void *logits;
+    const int32_t *experts;    // [M, top]
+    const float *dweights;     // [M, top]
+    void *dlogits;             // logits' type
+    int64_t M;
+    int E, top;
+    float scale;
+    bool f32, sigmoid, normalize;
+};
+
+// With q the shares above and g = scale dweights:
+//   softmax:  dl_i = s_i ((sum of g over the slots that chose i) - sum_j g_j s_j)
+//   softmax normalised: dl_t = q_t (g_t - sum_j g_j q_j);   sigmoid: dl_t = s_t (1 - s_t) g_t, normalised
+//   q_t (1 - s_t) (g_t - sum_j g_j q_j);   the logits that no slot chose get 0.
+// An expert chosen twice gets the sum.
+template <int PER>
+__global__ void __launch_bounds__(64 * WAVES) moe_route_backward_kernel(RouteGradParams p)
+{
+    const bool all = !p.sigmoid && !p.normalize;         // every logit has a gradient
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
+    if (m >= p.M) return;
+    int chosen = -1;
+    double g = 0.0, l = 0.0;
+    if (lane < p.top) {
+        chosen = p.experts[m * p.top + lane];
+        if ((unsigned)chosen >= (unsigned)p.E) chosen = -1;
+        if (chosen >= 0) {
+            g = (double)p.dweights[m * p.top + lane] * (double)p.scale;
+            l = (double)load_logit(p.logits, p.f32, m * p.E + chosen);
+            if (l == -__builtin_inf()) chosen = -1;      // masked: its weight is a constant 0
+        }
+    }
+    float s[PER] = {}, most = -__builtin_inff();
+    double z = 1.0;
+    if (all) {
+#pragma unroll
+        for (int r = 0; r < PER; ++r) {
+            const int i = 64 * r + lane;
+            s[r] = i < p.E ? load_logit(p.logits, p.f32, m * p.E + i) : -__builtin_inff();
+            most = __builtin_fmaxf(most, s[r]);
+        }
+        most = wave_max(most);
+        double sum = 0.0;
+#pragma unroll
+        for (int r = 0; r < PER; ++r) {
+            s[r] = s[r] == -__builtin_inff() ? 0.0f : expf(s[r] - most);   // a NaN stays one
+            sum += (double)s[r];
+        }
+        z = wave_sum(sum);
+    }
+    const bool valid = chosen >= 0;
+    const double share = chosen_share(p.sigmoid, p.normalize, l, valid, most, z);
+    const double inner = wave_sum(valid ? share * g : 0.0);
+    double d = share * (p.normalize ? g - inner : g);
+    if (p.sigmoid) d *= 1.0 / (1.0 + exp(l));            // 1 - s
+    if (!valid) d = 0.0;
+    // every logit's part: 0 where a row is masked whole (z == 0), NaN in a row with one
+    const float rest = !all || z == 0.0 ? 0.0f : (float)(-inner / z);
+    float out[PER];
+#pragma unroll
+    for (int r = 0; r < PER; ++r) out[r] = s[r] * rest;
+    // in slot order, so that an expert chosen twice gets the same sum at every call
+    const float df = (float)d;
+    for (int j = 0; j < p.top; ++j) {
+        const int at = __shfl(chosen, j);
+        const float add = __shfl(df, j);
+#pragma unroll
+        for (int r = 0; r < PER; ++r)
+            if (at == 64 * r + lane) out[r] += add;
+    }
+#pragma unroll
+    for (int r = 0; r < PER; ++r) {
+        const int i = 64 * r + lane;
+        if (i >= p.E) continue;
+        if (p.f32) static_cast<float *>(p.dlogits)[m * p.E + i] = out[r];
+        else static_cast<uint16_t *>(p.dlogits)[m * p.E + i] = (uint16_t)(pack_bf16x2(out[r], 0.0f) & 0xffffu);
+    }
+}
+
+int per_lane(int E) { return E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16; }
+
+template <typename KEY>
+void route_per(const RouteParams &p, dim3 grid, hipStream_t stream)
+{
+    const dim3 block(64 * WAVES);
+    switch (per_lane(p.E)) {
+    case 1: hipLaunchKernelGGL((moe_route_kernel<KEY, 1>), grid, block, 0, stream, p); break;
+    case 2: hipLaunchKernelGGL((moe_route_kernel<KEY, 2>), grid, block, 0, stream, p); break;
+    case 4: hipLaunchKernelGGL((moe_route_kernel<KEY, 4>), grid, block, 0, stream, p); break;
+    case 8: hipLaunchKernelGGL((moe_route_kernel<KEY, 8>), grid, block, 0, stream, p); break;
+    default: hipLaunchKernelGGL((moe_route_kernel<KEY, 16>), grid, block, 0, stream, p);
+    }
+}
+
+} // namespace
+
+hipError_t launch_moe_route(const RouteArgs &a, int32_t *experts, float *weights, hipStream_t stream)
+{
+    if (a.M <= 0) return hipSuccess;
+    const RouteParams p = {a.logits, a.bias, experts, weights, a.M, a.E, a.top, a.scale, a.f32, a.score != 0, a.normalize};
+    const dim3 grid((unsigned)((a.M + WAVES - 1) / WAVES));
+    if (a.bias) route_per<uint64_t>(p, grid, stream);
+    else route_per<uint32_t>(p, grid, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_route_backward(const RouteArgs &a, const float *dweights, const int32_t *experts, void *dlogits,
+                                     hipStream_t stream)
+{
+    if (a.M <= 0) return hipSuccess;
+    const RouteGradParams p = {a.logits, experts, dweights, dlogits, a.M, a.E, a.top, a.scale, a.f32, a.score != 0, a.normalize};
+    const dim3 grid((unsigned)((a.M + WAVES - 1) / WAVES));
+    const dim3 block(64 * WAVES);
+    switch (per_lane(a.E)) {
+    case 1: hipLaunchKernelGGL(moe_route_backward_kernel<1>, grid, block, 0, stream, p); break;
+    case 2: hipLaunchKernelGGL(moe_route_backward_kernel<2>, grid, block, 0, stream, p); break;
+    case 4: hipLaunchKernelGGL(moe_route_backward_kernel<4>, grid, block, 0, stream, p); break;
+    case 8: hipLaunchKernelGGL(moe_route_backward_kernel<8>, grid, block, 0, stream, p); break;
+    default: hipLaunchKernelGGL(moe_route_backward_kernel<16>, grid, block, 0, stream, p);
+    }
+    return hipGetLastError();
+}
+
+} // namespace convrot
