@@ -306,8 +306,8 @@ int convrot_moe_route_backward(const float *dweights, const void *logits, int dt
  *   y[r] = convrot_linear(x[r]) with wq[e], w_scale[e]   for offsets[e] <= r < offsets[e + 1],  bit for bit
  *   x bf16/fp32 [rows, K], or x = NULL and xq int8 [rows, K], x_scale fp32 [rows], as in convrot_linear;
  *   offsets int32 [groups + 1] in device memory, non-decreasing; groups may be empty.  Rows before offsets[0] and from
- *   offsets[groups] on belong to no group: their rows of y are left as they were.  (Values outside [0, rows] count as the
- *   nearer end, a group that starts behind its end is empty, and where groups share rows any of them may give the result.)
+ *   offsets[groups] on belong to no group: their rows of y are left as they were.  (A value outside [0, rows] counts as the
+ *   nearer end, and one below an earlier one as that one.)
  *   wq int8 [groups, N, K], w_scale fp32 [groups, N]; y bf16 [rows, N]; 1 <= N < CONVROT_GEMM_MAX_N.
  * workspace: convrot_workspace_bytes_grouped(rows, groups, N, K) bytes, 256-byte aligned; with x = NULL it may be NULL.
  * An overlap of y with xq, x_scale or offsets returns CONVROT_ERR_OVERLAP.

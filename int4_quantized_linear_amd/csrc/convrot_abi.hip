@@ -964,11 +964,11 @@ int check_workspace(const char *who, const void *workspace, size_t bytes, size_t
     return CONVROT_OK;
 }
 
-// The expert layer's workspace: the sort's arrays, then, forward, the codes and scales of x, h, its codes and
+// The expert layer's workspace: the sort's arrays, then, forward, the codes and scales of x, each row's scale, h, its codes and
 // scales, and d in fp32; backward, the two contractions' operands, and dx's parts in fp32 in the place of the first.
 struct MoeLayout {
     size_t offsets = 0, slot_of = 0, token_of = 0, row_of = 0;
-    size_t xq = 0, xs = 0, h = 0, hq = 0, hs = 0;
+    size_t xq = 0, xs = 0, rs = 0, h = 0, hq = 0, hs = 0;
     size_t a = 0, a2 = 0;
     size_t part = 0, total = 0;
 };
@@ -993,6 +993,7 @@ MoeLayout moe_layout(int64_t M, int top, int64_t E, int64_t F, int64_t K, bool b
     } else {
         L.xq = take((size_t)M * (size_t)K);
         L.xs = take((size_t)M * 4);
+        L.rs = take(S * 4);
         L.h = take(S * (size_t)F * 2);
         L.hq = take(S * (size_t)F);
         L.hs = take(S * 4);
@@ -1129,7 +1130,7 @@ int convrot_linear_grouped(const void *x, int x_dtype, const int8_t *xq, const f
     g.N = N;
     g.groups = (int)groups;
     g.K = (int)K;
-    return hip_status(convrot::launch_grouped_i8(g, convrot::GroupedEpi::Plain, stream), "grouped_i8");
+    return hip_status(convrot::launch_grouped_i8(g, convrot::Epi::Bf16, stream), "grouped_i8");
 }
 
 size_t convrot_workspace_bytes_grouped_backward(int64_t rows, int64_t groups, int64_t N, int64_t K)
@@ -1218,18 +1219,20 @@ int convrot_moe_ffn_gated(const void *x, int x_dtype, const int32_t *experts, co
     if ((rc = check_workspace(who, workspace, workspace_bytes, L.total))) return rc;
     if ((rc = check_device())) return rc;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const convrot::MoeOrder o = moe_order(ws, L);
+    convrot::MoeOrder o = moe_order(ws, L);
     int8_t *xq = reinterpret_cast<int8_t *>(ws + L.xq), *hq = reinterpret_cast<int8_t *>(ws + L.hq);
     float *xs = reinterpret_cast<float *>(ws + L.xs), *hs = reinterpret_cast<float *>(ws + L.hs);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h);
     float *part = reinterpret_cast<float *>(ws + L.part);
+    o.sx = xs;
+    o.sx_of = reinterpret_cast<float *>(ws + L.rs);
     rc = hip_status(convrot::launch_rotate_quant(x, x_dtype == CONVROT_DTYPE_F32, M, (int)K, log2i(group), 8, xq, xs, stream),
                     "rotate_quant");
     if (rc) return rc;
     if ((rc = hip_status(convrot::launch_moe_order(experts, (int64_t)S, (int)E, top, o, stream), "moe_order"))) return rc;
     convrot::GroupedArgs g;
     g.xq = xq;
-    g.sx = xs;
+    g.sx = o.sx_of;
     g.offsets = o.offsets;
     g.source = o.token_of;
     g.slot_of = o.slot_of;
@@ -1244,7 +1247,7 @@ int convrot_moe_ffn_gated(const void *x, int x_dtype, const int32_t *experts, co
     g.groups = (int)E;
     g.K = (int)K;
     g.act = act;
-    if ((rc = hip_status(convrot::launch_grouped_i8(g, convrot::GroupedEpi::Gated, stream), "grouped_i8"))) return rc;
+    if ((rc = hip_status(convrot::launch_grouped_i8(g, convrot::Epi::Gated, stream), "grouped_i8"))) return rc;
     // (rows past the last slot with an expert hold anything; their codes are never read)
     if ((rc = hip_status(convrot::launch_rotate_quant(h, false, (int64_t)S, (int)F, log2i(group_h), 8, hq, hs, stream),
                          "rotate_quant")))
@@ -1262,7 +1265,7 @@ int convrot_moe_ffn_gated(const void *x, int x_dtype, const int32_t *experts, co
     w.N = K;
     w.groups = (int)E;
     w.K = (int)F;
-    if ((rc = hip_status(convrot::launch_grouped_i8(w, convrot::GroupedEpi::Part, stream), "grouped_i8"))) return rc;
+    if ((rc = hip_status(convrot::launch_grouped_i8(w, convrot::Epi::Part, stream), "grouped_i8"))) return rc;
     return hip_status(convrot::launch_moe_combine(part, o.row_of, weights, static_cast<const uint16_t *>(residual),
                                                   static_cast<uint16_t *>(y), M, (int)K, top, stream),
                       "moe_combine");

@@ -44,6 +44,7 @@
 
 #include "activation.hpp"
 #include "device_common.hpp"
+#include "grouped_common.hpp"
 #include "launchers.hpp"
 #include "tile_common.hpp"
 
@@ -80,6 +81,12 @@ struct GemmParams {
     int32_t *part;
     int T_dp, S;
     FusedEpi f;                // Act and Gated epilogues
+    // Rows sorted by group (M rows in all, weights [groups, N, K] and scales [groups, N]; no split):
+    const int32_t *offsets;
+    const int32_t *source;     // the row of xq that a row takes, or null: its own
+    const int32_t *slot_of;    // the row of f.pre, or of d, that a row goes to
+    uint16_t *d;               // Part: bf16 [M, N] or null
+    int groups;
 };
 
 // Gated: a tile's 256 weight rows are 128 features of both weights, in alternating 16-row blocks
@@ -92,16 +99,31 @@ struct GemmParams {
 template <Epi E>
 constexpr int tile_features() { return E == Epi::Gated ? BN / 2 : BN; }
 
-template <Epi E, bool VEC>
+// Grouped: the same walk over the tiles of rows sorted by group (grouped_common.hpp), each with its group's weight.  Only
+// where a tile's rows begin and end, its weight and, where rows are taken from elsewhere, the addresses of its rows
+// differ.  Those rows' numbers are requested one tile ahead, each wavefront its own 32, into its part of LDS: waiting
+// for them at the tile's start would drain the K-tiles in flight.
+struct GroupedLds {
+    GroupTable table;
+    int source[8][64];
+};
+
+template <Epi E, bool VEC, bool GROUPED = false>
 __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams p)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM + (GROUPED ? sizeof(GroupedLds) : 0)];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = w & 1, wm = w >> 1;   // wn: 128-row half of N, wm: 64-row quarter of M
     const int K = p.K;
     constexpr int NF = tile_features<E>();     // output columns per tile
     const int KT = (K + BK - 1) / BK;          // the last K-tile may be half (K % 128 == 64)
+    GroupedLds &gl = *reinterpret_cast<GroupedLds *>(smem + SMEM);   // Grouped only
+    int last = 0;
+    if constexpr (GROUPED) {
+        p.tiles_m = group_tiles<NTHREADS>(p.offsets, p.groups, p.M, BM, gl.table, reinterpret_cast<int *>(smem), last);
+        p.T_dp = p.tiles_m * p.tiles_n;
+    }
     const int T = p.tiles_m * p.tiles_n;
     const int U = p.T_dp + (T - p.T_dp) * p.S;
     // jobs of this workgroup: virtual ids blockIdx.x + j*gridDim.x < U.  Job j is a unit: tile
@@ -109,6 +131,7 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
     const int njobs = (U - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
     struct Job {
         int tm, tn, kb, ke, slot;
+        GroupRows g;                           // Grouped
     };
     auto job = [&](int j) {
         Job J;
@@ -127,6 +150,7 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
             J.slot = v;
         }
         tile_coords(q, p.tiles_m, p.tiles_n, J.tm, J.tn);
+        if constexpr (GROUPED) J.g = group_of_tile(gl.table, BM, last, J.tm);
         return J;
     };
     // Per-lane load geometry (independent of the tile): instruction i (0..3) of wave w fills
@@ -145,19 +169,26 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
     // the loop's job switch could otherwise be placed in VGPRs, which turns every load into a
     // waterfall loop.
     int ld_tm = 0, ld_tn = 0;
+    GroupRows ld_g = {0, 0, 0};
     uint64_t wbase_addr = 0, xbase_addr = 0;
     uint32_t offw[4], offx[4];
-    auto set_load_tile = [&](int tm, int tn) {
-        ld_tm = tm;
-        ld_tn = tn;
-        const int64_t m0 = (int64_t)ld_tm * BM, n0 = (int64_t)ld_tn * NF;
+    auto load_m0 = [&]() { return GROUPED ? (int64_t)ld_g.first : (int64_t)ld_tm * BM; };
+    // rows left from the tile's first on
+    auto load_mrem = [&]() { return GROUPED ? ld_g.end - ld_g.first : p.M - ld_tm * BM; };
+    auto group_n = [&](int group) { return GROUPED ? (int64_t)group * p.N : (int64_t)0; };
+    auto set_load_tile = [&](const Job &J) {
+        ld_tm = J.tm;
+        ld_tn = J.tn;
+        if constexpr (GROUPED) ld_g = J.g;
+        const int64_t m0 = load_m0(), n0 = (int64_t)ld_tn * NF;
         const int8_t *wsrc = p.wq;
         if constexpr (E == Epi::Gated) wsrc = (w & 2) ? p.f.wq2 : p.wq;   // lrow / 16 is odd where w & 2
+        if constexpr (GROUPED) wsrc += group_n(ld_g.group) * K;
         wbase_addr = reinterpret_cast<uint64_t>(wsrc + n0 * K);
-        xbase_addr = reinterpret_cast<uint64_t>(p.xq + m0 * K);
+        xbase_addr = reinterpret_cast<uint64_t>(GROUPED && p.source ? p.xq : p.xq + m0 * K);
         // rows left in the operands past the tile's first row (32-bit: N, M < 2^31)
         const int nrem = __builtin_amdgcn_readfirstlane(p.N - ld_tn * NF);
-        const int mrem = __builtin_amdgcn_readfirstlane(p.M - ld_tm * BM);
+        const int mrem = __builtin_amdgcn_readfirstlane(load_mrem());
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t o = (uint32_t)(lrow[i] * K + 16 * lchunk[i]);
@@ -167,8 +198,19 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
             } else {
                 offw[i] = lrow[i] < nrem ? o : OOB;
             }
-            offx[i] = lrow[i] < mrem ? o : OOB;
+            if (GROUPED && p.source)
+                offx[i] = lrow[i] < mrem ? (uint32_t)(gl.source[w][8 * i + (lane >> 3)] * K + 16 * lchunk[i]) : OOB;
+            else offx[i] = lrow[i] < mrem ? o : OOB;
         }
+    };
+    // Grouped, rows from elsewhere: the source rows of job j's rows 8 (8 i + w) + l at gl.source[w][8 i + l].  Read by
+    // set_load_tile(job j), at least one K-tile and its wait later.
+    auto request_sources = [&](int j) {
+        const Job J = job(j);
+        const int l = lane & 31, r = 8 * (8 * (l >> 3) + w) + (l & 7);
+        const __amdgpu_buffer_rsrc_t rs =
+            uniform_rsrc(reinterpret_cast<uint64_t>(p.source + J.g.first), 4 * min(J.g.end - J.g.first, BM));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)gl.source[w], 4, (uint32_t)(4 * r), 0, 0, 0);
     };
     // The tile's sw, bias and sx (256 floats each) go to LDS scale buffer (t & 3) with the
     // tile's first K-tile: 12 dword load-to-LDS instructions, 2 on each of waves 0-5.
@@ -177,12 +219,12 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
         if constexpr (E == Epi::Gated) {
             // the same 1 KiB arrays, gate in the first half and up in the second: the odd waves of
             // arrays 0 and 1 take the up half
-            const int64_t m0 = (int64_t)ld_tm * BM, n0 = (int64_t)ld_tn * NF;
-            const int nb = (int)(4 * (p.N - n0 < NF ? p.N - n0 : NF)), mb = (int)(4 * (p.M - m0 < BM ? p.M - m0 : BM));
+            const int64_t m0 = load_m0(), n0 = (int64_t)ld_tn * NF;
+            const int nb = (int)(4 * (p.N - n0 < NF ? p.N - n0 : NF)), mb = 4 * (load_mrem() < BM ? load_mrem() : BM);
             uint8_t *sb = smem + SCALE_OFF + (t & (NSCALE - 1)) * SCALE_BYTES;
             if (w < 6) {
                 const int arr = w >> 1, up = w & 1;
-                const float *scl = up ? p.f.sw2 : p.sw, *bia = up ? p.f.bias2 : p.bias;
+                const float *scl = (up ? p.f.sw2 : p.sw) + group_n(ld_g.group), *bia = up ? p.f.bias2 : p.bias;
                 const float *src = arr == 0 ? scl + n0 : arr == 1 ? (bia ? bia + n0 : scl) : p.sx + m0;
                 const int bytes = arr == 0 ? nb : arr == 1 ? (bia ? nb : 0) : mb;
                 const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(reinterpret_cast<uint64_t>(src), bytes);
@@ -193,14 +235,15 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                                                              (uint32_t)(skip + j * 256 + 4 * lane), 0, 0, 0);
             }
         } else if constexpr (E != Epi::Int32) {
-            const int64_t m0 = (int64_t)ld_tm * BM, n0 = (int64_t)ld_tn * BN;
-            const int nb = (int)(4 * (p.N - n0 < BN ? p.N - n0 : BN)), mb = (int)(4 * (p.M - m0 < BM ? p.M - m0 : BM));
+            const int64_t m0 = load_m0(), n0 = (int64_t)ld_tn * BN;
+            const int nb = (int)(4 * (p.N - n0 < BN ? p.N - n0 : BN)), mb = 4 * (load_mrem() < BM ? load_mrem() : BM);
             uint8_t *sb = smem + SCALE_OFF + (t & (NSCALE - 1)) * SCALE_BYTES;
             if (w < 6) {
                 // array arr = w / 2 (0 sw, 1 bias, 2 sx), picked with wave-uniform scalars so the
                 // descriptor stays in SGPRs
                 const int arr = w >> 1;
-                const float *src = arr == 0 ? p.sw + n0 : arr == 1 ? (p.bias ? p.bias + n0 : p.sw) : p.sx + m0;
+                const float *src =
+                    arr == 0 ? p.sw + group_n(ld_g.group) + n0 : arr == 1 ? (p.bias ? p.bias + n0 : p.sw) : p.sx + m0;
                 const int bytes = arr == 0 ? nb : arr == 1 ? (p.bias ? nb : 0) : mb;
                 const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(reinterpret_cast<uint64_t>(src), bytes);
 #pragma unroll
@@ -235,8 +278,16 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
         ld_done = ld_j < njobs ? 0u : OOB;
         if (ld_j < njobs) {
             const Job J = job(ld_j);
-            set_load_tile(J.tm, J.tn);
+            // (with one K-tile per tile, the prologue gets here without having waited for the request)
+            if (GROUPED && p.source && KT == 1) __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+            set_load_tile(J);
             issue_scales(ld_j);
+            if constexpr (GROUPED) {
+                if (p.source && ld_j + 1 < njobs) {
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this job's have been read
+                    request_sources(ld_j + 1);
+                }
+            }
             ld_kt = __builtin_amdgcn_readfirstlane(J.kb);
             ld_ke = __builtin_amdgcn_readfirstlane(J.ke);
         }
@@ -321,8 +372,8 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
         if (ld_kt == ld_ke) next_job();
     };
     auto epilogue = [&](const Job &J, int j, int g) {
-        const int m0 = J.tm * BM, n0 = J.tn * NF;
-        const int Mi = p.M, Ni = p.N;
+        const int m0 = GROUPED ? J.g.first : J.tm * BM, n0 = J.tn * NF;
+        const int Mi = GROUPED ? J.g.end : p.M, Ni = p.N;
         // lane-dependent bases laundered so the addresses below are formed here, not hoisted out
         // of the tile loop (where they would stay live through the main loop): the lane's token
         // row in a 16-row block and its first weight column in a 16-column block
@@ -382,7 +433,7 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                 }
                 fence();
             }
-        } else if constexpr (E == Epi::Act || E == Epi::Gated) {
+        } else if constexpr (E == Epi::Act || E == Epi::Gated || E == Epi::Part) {
             // Two phases per 16-token block, so that the activation's code exists once and not per
             // accumulator register.  (Applied where the accumulators are, fully unrolled, it spilled
             // 64 (Gated) and 145 (Act) registers.)  First the block's int32 sums go to the wave's own 8 KiB
@@ -408,11 +459,19 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                 return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(base) + (int64_t)mw * p.N, (short)0,
                                                          base ? NUM_RECORDS : 0, 0x00020000);
             };
-            const __amdgpu_buffer_rsrc_t ry = rows_of(static_cast<uint16_t *>(p.y));
+            const __amdgpu_buffer_rsrc_t ry = E == Epi::Part
+                ? __builtin_amdgcn_make_buffer_rsrc(static_cast<float *>(p.y) + (int64_t)mw * p.N, (short)0, NUM_RECORDS, 0x00020000)
+                : rows_of(static_cast<uint16_t *>(p.y));
             const __amdgpu_buffer_rsrc_t rres = rows_of(E == Epi::Act ? p.f.residual : nullptr);
-            const __amdgpu_buffer_rsrc_t rpre = rows_of(p.f.pre);
+            const __amdgpu_buffer_rsrc_t rpre = rows_of(GROUPED ? nullptr : p.f.pre);
             const __amdgpu_buffer_rsrc_t rpre2 =
-                rows_of(E == Epi::Gated && p.f.pre ? p.f.pre + (int64_t)Mi * p.N : nullptr);
+                rows_of(E == Epi::Gated && !GROUPED && p.f.pre ? p.f.pre + (int64_t)Mi * p.N : nullptr);
+            // Grouped: pre and d go to the row's slot
+            auto store_slot = [&](const float (&v)[8], uint16_t *to, int r) {
+                if (mw + r < Mi && n < Ni)
+                    *reinterpret_cast<v4u *>(to + (int64_t)p.slot_of[mw + r] * p.N + n) = v4u{
+                        pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+            };
             const int act = p.f.act;
             auto offset = [&](int r) {                                 // r: row in the wave's 64
                 return (r < 64 && mw + r < Mi && n < Ni) ? (uint32_t)(r * Ni + n) * 2u : OOB;
@@ -473,11 +532,24 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                     const uint32_t off = offset(r);
                     float v[8];
                     z8(ch, cl, v);
-                    if (p.f.pre) store8(v, rpre, off);
+                    if constexpr (E == Epi::Part) {
+                        const uint32_t off4 = off == OOB ? OOB : 2u * off;
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, ry,
+                            off4, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            v4u{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])}, ry,
+                            off4, 16, 0);
+                        if (p.d) store_slot(v, p.d, r);
+                        continue;
+                    }
+                    if (!GROUPED && p.f.pre) store8(v, rpre, off);
+                    if (GROUPED && E == Epi::Gated && p.f.pre) store_slot(v, p.f.pre, r);
                     if constexpr (E == Epi::Gated) {
                         float u[8];
                         z8(ch + 4, cl + NF, u);
-                        if (p.f.pre) store8(u, rpre2, off);
+                        if (!GROUPED && p.f.pre) store8(u, rpre2, off);
+                        if (GROUPED && p.f.pre) store_slot(u, p.f.pre + (int64_t)p.M * p.N, r);
                         act_values(v, act);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[i] *= u[i];
@@ -607,6 +679,12 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
         __builtin_amdgcn_sched_group_barrier(0x008, 16 - decltype(nreads)::value, 0);
     };
     // prologue: K-tile 0 (and job 0's scales) visible, K-tile 1 in flight, first fragments
+    if constexpr (GROUPED) {
+        if (p.source) {
+            request_sources(0);
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        }
+    }
     next_job();
     issue_ktile(0, true);
     if (ld_kt == ld_ke) next_job();
@@ -622,11 +700,28 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
         // only the K-tile count of the job stays live through its K loop; the epilogue recomputes
         // the rest (scalar registers are scarce here)
         int nkt, first = 1;
+        bool rows = true;
         {
             const Job J = job(j);
             nkt = __builtin_amdgcn_readfirstlane(J.ke - J.kb);
+            if constexpr (GROUPED) rows = J.g.first + 64 * wm < J.g.end;
         }
-        for (int kt = 0; kt < nkt; ++kt, ++g, first = 0) {
+        // Grouped: the wavefronts whose 64 rows all lie past the group's end only take part in the loads (a group's last
+        // tile is half empty on average, and products of rows that are not there cost power that others lack)
+        for (int kt = 0; GROUPED && !rows && kt < nkt; ++kt, ++g, first = 0) {
+            if (VEC && j > 0 && first) __builtin_amdgcn_s_waitcnt(waitcnt_vm(EPI_STORES));
+            else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            issue_ktile(g, kt + 1 < nkt);
+            if (kt + 1 == nkt) {                         // the next tile's first fragments
+                read_a(g + 1, 0, 0);
+                read_b(g + 1, 0);
+            }
+            fence();
+            if (ld_kt == ld_ke) next_job();
+            fence();
+        }
+        for (int kt = 0; rows && kt < nkt; ++kt, ++g, first = 0) {
             // sub-steps (0,0), (0,1), (1,0): MFMAs on the fragments read one sub-step earlier, the
             // next sub-step's fragments read between them
             read_a(g, 0, 1);
@@ -897,7 +992,7 @@ hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
     // the epilogue's byte offset within a 32-row output block, 32 * N * 4 bytes at most, is 32-bit
     if (N >= ((int64_t)1 << 24)) return hipErrorInvalidValue;
     const int nf = epi == Epi::Gated ? tile_features<Epi::Gated>() : BN;
-    GemmParams p;
+    GemmParams p = {};
     p.xq = xq;
     p.wq = wq;
     p.sx = sx;
@@ -957,6 +1052,45 @@ hipError_t launch_gemm_i8(const int8_t *xq, const int8_t *wq, const float *sx, c
     case Epi::Gated: hipLaunchKernelGGL((split_reduce_kernel<Epi::Gated>), dim3(rgrid), dim3(256), 0, stream, r); break;
     default: hipLaunchKernelGGL((split_reduce_kernel<Epi::Bf16>), dim3(rgrid), dim3(256), 0, stream, r);
     }
+    return hipGetLastError();
+}
+
+hipError_t launch_grouped_gemm_i8(const GroupedArgs &g, Epi epi, hipStream_t stream)
+{
+    if (g.rows <= 0 || g.N <= 0) return hipSuccess;
+    if (g.N >= ((int64_t)1 << 24)) return hipErrorInvalidValue;
+    const int nf = epi == Epi::Gated ? tile_features<Epi::Gated>() : BN;
+    GemmParams p = {};
+    p.xq = g.xq;
+    p.wq = g.wq;
+    p.sx = g.sx;
+    p.sw = g.sw;
+    p.y = epi == Epi::Part ? static_cast<void *>(g.part) : g.y;
+    p.M = (int)g.rows;
+    p.N = (int)g.N;
+    p.K = g.K;
+    p.tiles_n = (int)((g.N + nf - 1) / nf);
+    p.S = 1;
+    p.f.act = g.act;
+    p.f.pre = g.pre;
+    p.f.wq2 = g.wq2;
+    p.f.sw2 = g.sw2;
+    p.offsets = g.offsets;
+    p.source = g.source;
+    p.slot_of = g.slot_of;
+    p.d = g.d;
+    p.groups = g.groups;
+    const int64_t most = most_group_tiles(g.rows, g.groups, BM) * p.tiles_n;
+    if (most >= ((int64_t)1 << 31) - 1024) return hipErrorInvalidValue;
+    int grid = grid_capacity();
+    if (most < grid) grid = (int)((most + 7) & ~7);
+    const dim3 blocks((unsigned)grid), threads(NTHREADS);
+    const bool vec = g.N % 8 == 0;
+    if (epi == Epi::Gated && vec) hipLaunchKernelGGL((gemm_i8_kernel<Epi::Gated, true, true>), blocks, threads, 0, stream, p);
+    else if (epi == Epi::Part && vec) hipLaunchKernelGGL((gemm_i8_kernel<Epi::Part, true, true>), blocks, threads, 0, stream, p);
+    else if (epi == Epi::Bf16 && vec) hipLaunchKernelGGL((gemm_i8_kernel<Epi::Bf16, true, true>), blocks, threads, 0, stream, p);
+    else if (epi == Epi::Bf16) hipLaunchKernelGGL((gemm_i8_kernel<Epi::Bf16, false, true>), blocks, threads, 0, stream, p);
+    else return hipErrorInvalidValue;
     return hipGetLastError();
 }
 

@@ -258,13 +258,14 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
     const int K = p.K;
     int m0, c0, group = 0, end = p.M, kb = 0, ke = p.nt, slot = -1;
     if constexpr (GROUPED) {
-        __shared__ int starts[MAX_GROUPS];
-        const int tiles = group_tiles<256>(p.offsets, p.groups, p.M, TM, starts, reinterpret_cast<int *>(smem));
-        const int units = (int)min((int64_t)tiles * p.tiles_c, (int64_t)0x7fffff00);
+        __shared__ GroupTable table;
+        int last;
+        const int tiles = group_tiles<256>(p.offsets, p.groups, p.M, TM, table, reinterpret_cast<int *>(smem), last);
+        const int units = tiles * p.tiles_c;
         if ((int)blockIdx.x >= units) return;            // the grid holds the most units there could be
         int tm, tc;
         tile_coords(unit_of((int)blockIdx.x, 0, units), tiles, p.tiles_c, tm, tc);
-        const GroupRows gr = group_of_tile(p.offsets, p.M, TM, starts, tm);
+        const GroupRows gr = group_of_tile(table, TM, last, tm);
         m0 = gr.first;
         end = gr.end;
         group = gr.group;
@@ -472,13 +473,14 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
     const int K = p.K;
     int m0, c0, group = 0, end = p.M, kb = 0, ke = p.nt, slot = -1;
     if constexpr (GROUPED) {
-        __shared__ int starts[MAX_GROUPS];
-        const int tiles = group_tiles<512>(p.offsets, p.groups, p.M, BM, starts, reinterpret_cast<int *>(smem));
-        const int units = (int)min((int64_t)tiles * p.tiles_c, (int64_t)0x7fffff00);
+        __shared__ GroupTable table;
+        int last;
+        const int tiles = group_tiles<512>(p.offsets, p.groups, p.M, BM, table, reinterpret_cast<int *>(smem), last);
+        const int units = tiles * p.tiles_c;
         if ((int)blockIdx.x >= units) return;            // the grid holds the most units there could be
         int tm, tc;
         tile_coords(unit_of((int)blockIdx.x, 0, units), tiles, p.tiles_c, tm, tc);
-        const GroupRows gr = group_of_tile(p.offsets, p.M, BM, starts, tm);
+        const GroupRows gr = group_of_tile(table, BM, last, tm);
         m0 = gr.first;
         end = gr.end;
         group = gr.group;
@@ -862,7 +864,7 @@ __global__ void __launch_bounds__(256) grad_bias_kernel(const float *sums, int c
 // mixture-of-experts layer, the gradient of their weights, dweight = sum_n dy[source, n] d[slot, n] in fp32.
 // A workgroup takes one row.  MoE (experts non-null): workgroup = slot, its group the slot's expert, its source the
 // slot's token, its row where the sort put it; slots without an expert get dweight 0 and no row.  Otherwise the
-// workgroup's row itself, and the first group whose offsets hold it.  Columns from N to lda are zeros.  Bound by memory.
+// workgroup's row itself, and the group whose offsets hold it.  Columns from N to lda are zeros.  Bound by memory.
 struct RowsParams {
     const uint16_t *dy;        // [., N]
     const float *sw;           // [groups, N]
@@ -894,12 +896,12 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(RowsParams p)
         source = s / p.top;
         share = p.weights[s];
     } else {
-        for (int b = 0; b < p.groups && group < 0; b += 64) {
+        // the group before the first offset past the row
+        group = -2;
+        for (int b = 0; b <= p.groups && group == -2; b += 64) {
             const int e = b + (t & 63);
-            int lo = 0, hi = 0;
-            if (e < p.groups) group_range(p.offsets, e, p.rows, lo, hi);
-            const uint64_t in = __builtin_amdgcn_ballot_w64(lo <= s && s < hi);
-            if (in) group = b + __builtin_ctzll(in);
+            const uint64_t past = __builtin_amdgcn_ballot_w64(e <= p.groups && p.offsets[min(e, p.groups)] > s);
+            if (past) group = b + __builtin_ctzll(past) - 1;
         }
         if (group < 0) return;                           // a row of no group
     }

@@ -23,6 +23,8 @@ struct OrderParams {
     int32_t *offsets;          // [E + 1]
     int32_t *slot_of, *token_of;   // [S] of each row
     int32_t *row_of;           // [S] of each slot, -1 without an expert
+    const float *sx;           // [tokens] or null
+    float *sx_of;              // [S] of each row
     int S, E, top;
 };
 
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
         if (none) return;
         p.slot_of[row] = s;
         p.token_of[row] = s / p.top;
+        if (p.sx) p.sx_of[row] = p.sx[s / p.top];
         ++row;
     });
 }
@@ -106,8 +109,8 @@ struct GroupedParams {
 
 typedef v4u v4u_any __attribute__((aligned(2)));         // 16 bytes at any element (an odd N)
 
-template <GroupedEpi E>
-constexpr int features() { return E == GroupedEpi::Gated ? BN / 2 : BN; }
+template <Epi E>
+constexpr int features() { return E == Epi::Gated ? BN / 2 : BN; }
 
 // Rows of 8 columns n.. to dst, clipped at N (VEC: N % 8 == 0, all exist).
 template <bool VEC>
@@ -123,7 +126,7 @@ __device__ __forceinline__ void store8(uint16_t *dst, int n, int N, const float 
     }
 }
 
-template <GroupedEpi E, int BM, int NST, bool VEC>
+template <Epi E, int BM, int NST, bool VEC>
 __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams p)
 {
     constexpr int NF = features<E>();
@@ -131,21 +134,21 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
     constexpr int LPK = (BN + BM) / 32;                  // loads per K-tile and wave
     constexpr int MB = BM / 32;                          // 16-row blocks per wave
     __shared__ __attribute__((aligned(16))) uint8_t smem[NST * STAGE];
-    __shared__ int starts[MAX_GROUPS];
+    __shared__ GroupTable table;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = w & 1, wm = w >> 1;
     const int K = p.K, KT = (K + BK - 1) / BK;
-    const int tiles = group_tiles<NTHREADS>(p.offsets, p.groups, p.rows, BM, starts, reinterpret_cast<int *>(smem));
-    // (offsets out of order may give more than the host counted: held to what int can number)
-    const int units = (int)min((int64_t)tiles * p.tiles_n, (int64_t)0x7fffff00);
+    int last;
+    const int tiles = group_tiles<NTHREADS>(p.offsets, p.groups, p.rows, BM, table, reinterpret_cast<int *>(smem), last);
+    const int units = tiles * p.tiles_n;
     const int frow = lane & 15, fq = lane >> 4;
     const uint32_t half = K % BK && ((lane & 7) ^ swz(8 * w + (lane >> 3))) >= 4 ? OOB : 0u;
 
-    for (uint32_t v = blockIdx.x; v < (uint32_t)units; v += gridDim.x) {
+    for (int v = blockIdx.x; v < units; v += gridDim.x) {
         int tm, tn;
-        tile_coords(unit_of((int)v, 0, units), tiles, p.tiles_n, tm, tn);
-        const GroupRows gr = group_of_tile(p.offsets, p.rows, BM, starts, tm);
+        tile_coords(unit_of(v, 0, units), tiles, p.tiles_n, tm, tn);
+        const GroupRows gr = group_of_tile(table, BM, last, tm);
         const int m0 = gr.first, left = gr.end - gr.first;   // rows of this tile: min(left, BM)
         const int n0 = tn * NF;
         // instruction i of wave w fills LDS rows 8 (4 i + w) .. + 7 (weight rows 0 .. 127, then rows of x);
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
         for (int i = 0; i < LPK; ++i) {
             const int r = 8 * (4 * i + w) + (lane >> 3), c = 16 * ((lane & 7) ^ swz(r));
             if (i < 4) {
-                const int wr = E == GroupedEpi::Gated ? 16 * (r >> 5) + (r & 15) : r;
+                const int wr = E == Epi::Gated ? 16 * (r >> 5) + (r & 15) : r;
                 off[i] = n0 + wr < p.N ? (uint32_t)(wr * K + c) : OOB;
             } else {
                 const int rr = r - BN;
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
                 else off[i] = rr < left ? (uint32_t)(rr * K + c) : OOB;
             }
         }
-        const int8_t *wsrc = E == GroupedEpi::Gated && (w & 2) ? p.wq2 : p.wq;   // rows 16..31 of each 32: up
+        const int8_t *wsrc = E == Epi::Gated && (w & 2) ? p.wq2 : p.wq;   // rows 16..31 of each 32: up
         const uint64_t wbase = reinterpret_cast<uint64_t>(wsrc + ((int64_t)gr.group * p.N + n0) * K);
         const uint64_t xbase = reinterpret_cast<uint64_t>(p.source ? p.xq : p.xq + (int64_t)m0 * K);
         auto issue = [&](int t) {
@@ -210,13 +213,13 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
         constexpr int LPR = NF / 2 / 8, RPI = 64 / LPR;  // lanes per row, rows at a time
         const int lrow = lane / LPR, lcol = lane % LPR;
         const int n = n0 + wn * (NF / 2) + 8 * lcol;
-        const int ch = E == GroupedEpi::Gated ? 8 * (lcol >> 1) + 2 * (lcol & 1) : 2 * lcol;
+        const int ch = E == Epi::Gated ? 8 * (lcol >> 1) + 2 * (lcol & 1) : 2 * lcol;
         float s1[8], s2[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int64_t i = (int64_t)gr.group * p.N + min(n + e, p.N - 1);
             s1[e] = p.sw[i];
-            if constexpr (E == GroupedEpi::Gated) s2[e] = p.sw2[i];
+            if constexpr (E == Epi::Gated) s2[e] = p.sw2[i];
         }
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
         __syncthreads();
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
                 const int r = RPI * q + lrow, rl = wm * (BM / 2) + 16 * b + r;
                 if (rl >= left || n >= p.N) continue;
                 const int64_t row = m0 + rl;
-                const float sxm = p.sx[p.source ? p.source[row] : row];
+                const float sxm = p.sx[row];
                 auto z8 = [&](int chunk, const float (&s)[8], float (&z)[8]) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -242,14 +245,14 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
                 };
                 float z[8], u[8];
                 z8(ch, s1, z);
-                if constexpr (E == GroupedEpi::Plain) store8<VEC>(p.y + row * p.N + n, n, p.N, z);
-                if constexpr (E == GroupedEpi::Part) {
+                if constexpr (E == Epi::Bf16) store8<VEC>(p.y + row * p.N + n, n, p.N, z);
+                if constexpr (E == Epi::Part) {
                     float *dst = p.part + row * p.N + n;
                     *reinterpret_cast<v4f *>(dst) = v4f{z[0], z[1], z[2], z[3]};
                     *reinterpret_cast<v4f *>(dst + 4) = v4f{z[4], z[5], z[6], z[7]};
                     if (p.d) store8<VEC>(p.d + (int64_t)p.slot_of[row] * p.N + n, n, p.N, z);
                 }
-                if constexpr (E == GroupedEpi::Gated) {
+                if constexpr (E == Epi::Gated) {
                     z8(ch + 4, s2, u);
                     if (p.pre) {
                         uint16_t *dst = p.pre + (int64_t)p.slot_of[row] * p.N + n;
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(CombineParams p)
 
 constexpr int GRID = 512;                                // two workgroups per CU
 
-template <GroupedEpi E, int BM, int NST, bool VEC>
+template <Epi E, int BM, int NST, bool VEC>
 void launch_tiles(const GroupedParams &p, hipStream_t stream)
 {
     // a multiple of 8, so that a workgroup's units stay on its XCD
@@ -334,7 +337,7 @@ void launch_tiles(const GroupedParams &p, hipStream_t stream)
     hipLaunchKernelGGL((grouped_tile_kernel<E, BM, NST, VEC>), dim3(grid), dim3(NTHREADS), 0, stream, p);
 }
 
-template <GroupedEpi E, bool VEC>
+template <Epi E, bool VEC>
 void launch_rows(const GroupedParams &p, hipStream_t stream)
 {
     const int used = p.groups < p.rows ? p.groups : p.rows;
@@ -352,6 +355,8 @@ hipError_t launch_moe_order(const int32_t *experts, int64_t S, int E, int top, c
     p.slot_of = o.slot_of;
     p.token_of = o.token_of;
     p.row_of = o.row_of;
+    p.sx = o.sx;
+    p.sx_of = o.sx_of;
     p.S = (int)S;
     p.E = E;
     p.top = top;
@@ -360,9 +365,11 @@ hipError_t launch_moe_order(const int32_t *experts, int64_t S, int E, int top, c
     return hipGetLastError();
 }
 
-hipError_t launch_grouped_i8(const GroupedArgs &g, GroupedEpi epi, hipStream_t stream)
+hipError_t launch_grouped_i8(const GroupedArgs &g, Epi epi, hipStream_t stream)
 {
     if (g.rows <= 0 || g.N <= 0) return hipSuccess;
+    const int used = (int)(g.groups < g.rows ? g.groups : g.rows);
+    if (g.rows > 160 * (int64_t)used) return launch_grouped_gemm_i8(g, epi, stream);
     GroupedParams p;
     p.xq = g.xq;
     p.sx = g.sx;
@@ -383,21 +390,21 @@ hipError_t launch_grouped_i8(const GroupedArgs &g, GroupedEpi epi, hipStream_t s
     p.N = (int)g.N;
     p.K = g.K;
     p.act = g.act;
-    const int nf = epi == GroupedEpi::Gated ? BN / 2 : BN;
+    const int nf = epi == Epi::Gated ? BN / 2 : BN;
     p.tiles_n = (int)((g.N + nf - 1) / nf);
     const bool vec = g.N % 8 == 0;
     switch (epi) {
-    case GroupedEpi::Plain:
-        if (vec) launch_rows<GroupedEpi::Plain, true>(p, stream);
-        else launch_rows<GroupedEpi::Plain, false>(p, stream);
+    case Epi::Bf16:
+        if (vec) launch_rows<Epi::Bf16, true>(p, stream);
+        else launch_rows<Epi::Bf16, false>(p, stream);
         break;
-    case GroupedEpi::Gated:
+    case Epi::Gated:
         if (!vec) return hipErrorInvalidValue;
-        launch_rows<GroupedEpi::Gated, true>(p, stream);
+        launch_rows<Epi::Gated, true>(p, stream);
         break;
     default:
         if (!vec) return hipErrorInvalidValue;
-        launch_rows<GroupedEpi::Part, true>(p, stream);
+        launch_rows<Epi::Part, true>(p, stream);
     }
     return hipGetLastError();
 }

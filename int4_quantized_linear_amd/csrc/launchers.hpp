@@ -19,7 +19,8 @@ hipError_t launch_rotate_quant_fp6(const void *x, bool x_f32, int64_t rows, int 
 // Epilogue selector of the integer GEMM / GEMV kernels.
 //   Act:   z = acc * sx[m] * sw[n] + bias[n];  y = bf16(act(z) + residual);  pre = bf16(z)
 //   Gated: two weights share the tokens: g, u as z;  y = bf16(act(g) * u);  pre = bf16([g; u])
-enum class Epi { Bf16 = 0, Int32 = 1, Act = 2, Gated = 3 };
+//   Part:  part = z in fp32, d = bf16(z)  (rows sorted by group only)
+enum class Epi { Bf16 = 0, Int32 = 1, Act = 2, Gated = 3, Part = 4 };
 
 // What the Act and Gated epilogues take besides the plain one's arguments (activation.hpp holds
 // the codes of act).  residual, pre, bias2: may be null.  residual may be y itself.
@@ -96,20 +97,22 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream);
 // Where the slots (token, j) of M tokens with `top` experts each go when sorted by expert, E <= MAX_GROUPS: rows
 // offsets[e] .. offsets[e + 1] - 1 are expert e's, in slot order; slots with an expert outside [0, E) have row -1 and
 // take no row.  All in device memory, S = M top entries (offsets: E + 1).
+// With sx (fp32 [M]) also each row's token's scale, in sx_of [S].
 struct MoeOrder {
     int32_t *offsets = nullptr, *slot_of = nullptr, *token_of = nullptr, *row_of = nullptr;
+    const float *sx = nullptr;
+    float *sx_of = nullptr;
 };
 hipError_t launch_moe_order(const int32_t *experts, int64_t S, int E, int top, const MoeOrder &o, hipStream_t stream);
 
 // Products of rows sorted by group with their group's weight, z = acc sx sw:
-//   Plain: y = bf16(z);   Gated: y = bf16(act(g) u), pre = bf16([g; u]);   Part: part = z (fp32), d = bf16(z)
+//   Bf16: y = bf16(z);   Gated: y = bf16(act(g) u), pre = bf16([g; u]);   Part: part = z (fp32), d = bf16(z)
 // Rows of no group are neither read nor written.  Gated and Part: N % 8 == 0.
-enum class GroupedEpi { Plain = 0, Gated = 1, Part = 2 };
 struct GroupedArgs {
     const int8_t *xq = nullptr;           // [rows, K], or with `source` any rows, of fewer than 2^31 bytes in all
-    const float *sx = nullptr;
+    const float *sx = nullptr;            // [rows]
     const int32_t *offsets = nullptr;
-    const int32_t *source = nullptr;      // the row of xq and sx that a row takes; null: its own
+    const int32_t *source = nullptr;      // the row of xq that a row takes; null: its own
     const int32_t *slot_of = nullptr;     // the row of pre and d that a row goes to (with pre or d)
     const int8_t *wq = nullptr, *wq2 = nullptr;   // [groups, N, K]
     const float *sw = nullptr, *sw2 = nullptr;    // [groups, N]
@@ -118,7 +121,9 @@ struct GroupedArgs {
     int64_t rows = 0, N = 0;
     int groups = 0, K = 0, act = 0;
 };
-hipError_t launch_grouped_i8(const GroupedArgs &g, GroupedEpi epi, hipStream_t stream);
+hipError_t launch_grouped_i8(const GroupedArgs &g, Epi epi, hipStream_t stream);
+// The same in 256 x 256 tiles (gemm_i8.hip), for launch_grouped_i8.
+hipError_t launch_grouped_gemm_i8(const GroupedArgs &g, Epi epi, hipStream_t stream);
 
 // Gradients of grouped products through the frozen weights, in two steps (contractions of grouped_grad_lda(N) columns
 // per weight):

@@ -92,7 +92,7 @@ def test_linear_grouped_all_rows_of_no_group(cr):
 
 
 def test_linear_grouped_offsets_are_held_to_the_rows(cr):
-    """Offsets outside the rows count as the nearer end; one behind the next makes its group empty."""
+    """Offsets outside the rows count as the nearer end; one below an earlier one as that one."""
     wq, ws = _weights(cr, 3, 64, 64, 64, 1)
     x, dy = _randn(20, 64, seed=1), _randn(20, 64, seed=2)
     want = torch.tensor([0, 5, 5, 20], dtype=torch.int32, device=DEV)
@@ -101,10 +101,12 @@ def test_linear_grouped_offsets_are_held_to_the_rows(cr):
         assert torch.equal(cr.linear_grouped(x, wq, ws, o, group=64), cr.linear_grouped(x, wq, ws, want, group=64))
         assert torch.equal(cr.linear_grouped_backward(dy, wq, ws, o, group=64),
                            cr.linear_grouped_backward(dy, wq, ws, want, group=64))
-    o = torch.tensor([8, 3, 3, 20], dtype=torch.int32, device=DEV)    # group 0 is empty, rows 0 .. 2 belong to none
-    out = torch.full((20, 64), 3.0, dtype=torch.bfloat16, device=DEV)
-    cr.linear_grouped(x, wq, ws, o, group=64, out=out)
-    assert (out[:3] == 3).all() and torch.equal(out[3:], cr.linear(x[3:].clone(), wq[2], ws[2], group=64))
+    o = torch.tensor([8, 3, 3, 20], dtype=torch.int32, device=DEV)    # groups 0 and 1 are empty, rows 0 .. 7 belong to none
+    for call, v in ((cr.linear_grouped, x), (cr.linear_grouped_backward, dy)):
+        out = torch.full((20, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+        call(v, wq, ws, o, group=64, out=out)
+        want = call(v, wq, ws, torch.tensor([8, 8, 8, 20], dtype=torch.int32, device=DEV), group=64)
+        assert (out[:8] == 3).all() and torch.equal(out[8:], want[8:])
 
 
 @pytest.mark.parametrize("counts,N,K,g", GROUPED + [([257, 0, 700, 256], 72, 1280, 256), ([1024, 511], 321, 512, 32),
