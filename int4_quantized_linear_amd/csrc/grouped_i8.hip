@@ -85,9 +85,11 @@ __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
 }
 
 // ---------------------------------------------------------------------------------------------
-// The product, BM (64 or 128) rows x 128 weight rows per unit: the structure of gemm_i8_tile_kernel (K in tiles of 128
-// bytes through NST LDS stages, one barrier per K-tile, 4 wavefronts in 2 x 2, two workgroups per CU), walking
-// units blockIdx.x, blockIdx.x + gridDim.x, ... of a count that only the GPU knows.
+// The product, BM (64 or 128) rows x 128 weight rows per unit: gemm_i8_tile_kernel's tiles (K in tiles of 128 bytes through
+// NST LDS stages, one barrier per K-tile, 4 wavefronts in 2 x 2, two workgroups per CU), walking units blockIdx.x,
+// blockIdx.x + gridDim.x, ... of a count that only the GPU knows.  The loads run NST - 1 K-tiles ahead across
+// units, so a unit's epilogue (in the stage of its last K-tile) runs while the next one's first K-tiles arrive; what a
+// unit's start needs from memory, its source rows, scales and slots, is requested one unit ahead, into registers.
 constexpr int BN = 128, BK = 128;
 constexpr int NTHREADS = 256;
 
@@ -132,66 +134,128 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
     constexpr int NF = features<E>();
     constexpr int STAGE = (BN + BM) * BK;
     constexpr int LPK = (BN + BM) / 32;                  // loads per K-tile and wave
+    constexpr int XL = LPK - 4;                          // of them rows of x
     constexpr int MB = BM / 32;                          // 16-row blocks per wave
     __shared__ __attribute__((aligned(16))) uint8_t smem[NST * STAGE];
     __shared__ GroupTable table;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = w & 1, wm = w >> 1;
-    const int K = p.K, KT = (K + BK - 1) / BK;
+    const int K = p.K;
+    const int KT = max((K + BK - 1) / BK, NST - 1);      // at least the K-tiles in flight (past K: zeros)
     int last;
     const int tiles = group_tiles<NTHREADS>(p.offsets, p.groups, p.rows, BM, table, reinterpret_cast<int *>(smem), last);
     const int units = tiles * p.tiles_n;
+    if ((int)blockIdx.x >= units) return;
     const int frow = lane & 15, fq = lane >> 4;
-    const uint32_t half = K % BK && ((lane & 7) ^ swz(8 * w + (lane >> 3))) >= 4 ? OOB : 0u;
+    // epilogue: rows of 8 output columns per lane
+    constexpr int LPR = NF / 2 / 8, RPI = 64 / LPR;      // lanes per row, rows at a time
+    const int lrow = lane / LPR, lcol = lane % LPR;
 
-    for (int v = blockIdx.x; v < units; v += gridDim.x) {
+    struct Unit {
+        GroupRows g;
+        int n0;
+    };
+    auto locate = [&](int v) {
+        Unit u;
         int tm, tn;
         tile_coords(unit_of(v, 0, units), tiles, p.tiles_n, tm, tn);
-        const GroupRows gr = group_of_tile(table, BM, last, tm);
-        const int m0 = gr.first, left = gr.end - gr.first;   // rows of this tile: min(left, BM)
-        const int n0 = tn * NF;
-        // instruction i of wave w fills LDS rows 8 (4 i + w) .. + 7 (weight rows 0 .. 127, then rows of x);
-        // lane -> row + lane / 8 at position lane % 8
-        uint32_t off[LPK];
+        u.g = group_of_tile(table, BM, last, tm);
+        u.n0 = tn * NF;
+        return u;
+    };
+    // The load side.  Instruction i of wave w fills LDS rows 8 (4 i + w) .. + 7 (weight rows 0 .. 127, then rows of x);
+    // lane -> row + lane / 8 at position lane % 8.
+    const int ldr = 8 * w + (lane >> 3), ldc = 16 * ((lane & 7) ^ swz(ldr));   // swz(row) is swz(ldr) for every i
+    const uint32_t half = K % BK && ldc >= 64 ? OOB : 0u;
+    int src[XL] = {};                                    // source rows of the unit that the load side takes next
+    auto request = [&](int v) {
+        if (!p.source || v >= units) return;
+        const Unit u = locate(v);
+#pragma unroll
+        for (int i = 0; i < XL; ++i) src[i] = p.source[min(u.g.first + 32 * i + ldr, u.g.end - 1)];
+    };
+    uint32_t off[LPK], none = 0u;                        // none: OOB past the last unit
+    uint64_t wbase = 0, xbase = 0;
+    int ld_t = 0;
+    // what the epilogue of the load side's unit will need, requested with its first K-tile
+    float s1[8], s2[8], sx;
+    int slot = 0;
+    auto load_unit = [&](int v) {
+        ld_t = 0;
+        none = v < units ? 0u : OOB;
+        if (v >= units) return;
+        const Unit u = locate(v);
+        const int left = u.g.end - u.g.first;
 #pragma unroll
         for (int i = 0; i < LPK; ++i) {
-            const int r = 8 * (4 * i + w) + (lane >> 3), c = 16 * ((lane & 7) ^ swz(r));
+            const int r = 32 * i + ldr;
             if (i < 4) {
                 const int wr = E == Epi::Gated ? 16 * (r >> 5) + (r & 15) : r;
-                off[i] = n0 + wr < p.N ? (uint32_t)(wr * K + c) : OOB;
+                off[i] = u.n0 + wr < p.N ? (uint32_t)(wr * K + ldc) : OOB;
             } else {
                 const int rr = r - BN;
-                if (p.source) off[i] = rr < left ? (uint32_t)(p.source[m0 + rr] * K + c) : OOB;
-                else off[i] = rr < left ? (uint32_t)(rr * K + c) : OOB;
+                off[i] = rr < left ? (uint32_t)((p.source ? src[i - 4] : rr) * K + ldc) : OOB;
             }
         }
+        const int64_t g0 = (int64_t)u.g.group * p.N;
         const int8_t *wsrc = E == Epi::Gated && (w & 2) ? p.wq2 : p.wq;   // rows 16..31 of each 32: up
-        const uint64_t wbase = reinterpret_cast<uint64_t>(wsrc + ((int64_t)gr.group * p.N + n0) * K);
-        const uint64_t xbase = reinterpret_cast<uint64_t>(p.source ? p.xq : p.xq + (int64_t)m0 * K);
-        auto issue = [&](int t) {
-            const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(wbase, NUM_RECORDS), rx = uniform_rsrc(xbase, NUM_RECORDS);
-            uint8_t *base = smem + (t % NST) * STAGE + w * 1024;
-            const uint32_t skip = t >= KT ? OOB : t == KT - 1 ? half : 0u;
-            const int k0 = __builtin_amdgcn_readfirstlane(t < KT ? t * BK : 0);
+        wbase = reinterpret_cast<uint64_t>(wsrc + (g0 + u.n0) * K);
+        xbase = reinterpret_cast<uint64_t>(p.source ? p.xq : p.xq + (int64_t)u.g.first * K);
+        const int n = u.n0 + wn * (NF / 2) + 8 * lcol;
 #pragma unroll
-            for (int i = 0; i < LPK; ++i) load16_to_lds(i < 4 ? rw : rx, base + 4096 * i, off[i] | skip, k0);
-        };
+        for (int e = 0; e < 8; ++e) {
+            const int64_t i = g0 + min(n + e, p.N - 1);
+            s1[e] = p.sw[i];
+            if constexpr (E == Epi::Gated) s2[e] = p.sw2[i];
+        }
+        const int row = min(u.g.first + wm * (BM / 2) + lane % (BM / 2), u.g.end - 1);   // lane l: row l of the wave's
+        sx = p.sx[row];
+        if (E != Epi::Bf16 && p.slot_of) slot = p.slot_of[row];
+        request(v + (int)gridDim.x);
+    };
+    int st = 0;                                          // stage of the compute side's K-tile
+    auto issue = [&](int stage) {
+        const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(wbase, NUM_RECORDS), rx = uniform_rsrc(xbase, NUM_RECORDS);
+        uint8_t *base = smem + stage * STAGE + w * 1024;
+        const int k0 = ld_t * BK;
+        const uint32_t skip = none | (k0 >= K ? OOB : k0 + BK > K ? half : 0u);
+#pragma unroll
+        for (int i = 0; i < LPK; ++i)
+            load16_to_lds(i < 4 ? rw : rx, base + 4096 * i, off[i] | skip, __builtin_amdgcn_readfirstlane(k0));
+        ++ld_t;
+    };
 
+    request((int)blockIdx.x);
+    load_unit((int)blockIdx.x);
+#pragma unroll
+    for (int j = 0; j < NST - 1; ++j) issue(j);
+    for (int v = blockIdx.x; v < units; v += gridDim.x) {
+        const Unit u = locate(v);
+        float c1[8], c2[8], csx = 0.0f;                  // this unit's, while the load side moves on
+        int cslot = 0;
         v4i acc[4][MB];
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
             for (int b = 0; b < MB; ++b) acc[a][b] = v4i{};
-#pragma unroll
-        for (int j = 0; j < NST - 1; ++j) issue(j);
         for (int t = 0; t < KT; ++t) {
             // K-tile t has landed once only the NST - 2 after it are in flight
             __builtin_amdgcn_s_waitcnt(waitcnt_vm((NST - 2) * LPK));
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            issue(t + NST - 1);
-            const uint8_t *st = smem + (t % NST) * STAGE;
-            const uint8_t *ar = st + (wn * 64 + frow) * BK, *br = st + (BN + wm * (BM / 2) + frow) * BK;
+            if (t == KT - (NST - 1)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    c1[e] = s1[e];
+                    if constexpr (E == Epi::Gated) c2[e] = s2[e];
+                }
+                csx = sx;
+                cslot = slot;
+                load_unit(v + (int)gridDim.x);
+            }
+            issue(st == 0 ? NST - 1 : st - 1);           // the stage read before this one
+            const uint8_t *base = smem + st * STAGE;
+            const uint8_t *ar = base + (wn * 64 + frow) * BK, *br = base + (BN + wm * (BM / 2) + frow) * BK;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 const int pos = 16 * ((4 * kk + fq) ^ swz(frow));
@@ -206,24 +270,15 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
                     for (int b = 0; b < MB; ++b)
                         acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[a], fb[b], acc[a][b], 0, 0, 0);
             }
+            if (t + 1 < KT) st = st == NST - 1 ? 0 : st + 1;
         }
-        // lane: row lane % 16 of block b, weight rows 16 a + 4 (lane / 16) + v of the wave's 64.  Each wave passes
-        // its 16-row blocks through its own 4 KiB (rows of 64 sums, 16-byte chunk c at c ^ row), then takes row pieces
-        // of 8 output columns per lane.
-        constexpr int LPR = NF / 2 / 8, RPI = 64 / LPR;  // lanes per row, rows at a time
-        const int lrow = lane / LPR, lcol = lane % LPR;
-        const int n = n0 + wn * (NF / 2) + 8 * lcol;
+        // Lane: row lane % 16 of block b, weight rows 16 a + 4 (lane / 16) + v of the wave's 64.  Each wave passes
+        // its 16-row blocks through 4 KiB of the last K-tile's stage (rows of 64 sums, 16-byte chunk c at c ^ row), which every
+        // wave has read by now and the loads leave alone until the next unit's first barrier.
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        uint8_t *reg = smem + st * STAGE + w * 4096;
+        const int n = u.n0 + wn * (NF / 2) + 8 * lcol, left = u.g.end - u.g.first;
         const int ch = E == Epi::Gated ? 8 * (lcol >> 1) + 2 * (lcol & 1) : 2 * lcol;
-        float s1[8], s2[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t i = (int64_t)gr.group * p.N + min(n + e, p.N - 1);
-            s1[e] = p.sw[i];
-            if constexpr (E == Epi::Gated) s2[e] = p.sw2[i];
-        }
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-        __syncthreads();
-        uint8_t *reg = smem + w * 4096;
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
 #pragma unroll
@@ -231,10 +286,11 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
                 *reinterpret_cast<v4i *>(reg + frow * 256 + 16 * ((4 * a + fq) ^ frow)) = acc[a][b];
 #pragma unroll 1
             for (int q = 0; q < 16 / RPI; ++q) {
-                const int r = RPI * q + lrow, rl = wm * (BM / 2) + 16 * b + r;
+                const int r = RPI * q + lrow, rw = 16 * b + r, rl = wm * (BM / 2) + rw;
+                const float sxm = __shfl(csx, rw);
+                const int64_t to = E != Epi::Bf16 ? __shfl(cslot, rw) : 0;
                 if (rl >= left || n >= p.N) continue;
-                const int64_t row = m0 + rl;
-                const float sxm = p.sx[row];
+                const int64_t row = u.g.first + rl;
                 auto z8 = [&](int chunk, const float (&s)[8], float (&z)[8]) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -243,31 +299,32 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
                         for (int i = 0; i < 4; ++i) z[4 * h + i] = __builtin_fmaf((float)d[i], sxm * s[4 * h + i], 0.0f);
                     }
                 };
-                float z[8], u[8];
-                z8(ch, s1, z);
+                float z[8], g[8];
+                z8(ch, c1, z);
                 if constexpr (E == Epi::Bf16) store8<VEC>(p.y + row * p.N + n, n, p.N, z);
                 if constexpr (E == Epi::Part) {
                     float *dst = p.part + row * p.N + n;
                     *reinterpret_cast<v4f *>(dst) = v4f{z[0], z[1], z[2], z[3]};
                     *reinterpret_cast<v4f *>(dst + 4) = v4f{z[4], z[5], z[6], z[7]};
-                    if (p.d) store8<VEC>(p.d + (int64_t)p.slot_of[row] * p.N + n, n, p.N, z);
+                    if (p.d) store8<VEC>(p.d + to * p.N + n, n, p.N, z);
                 }
                 if constexpr (E == Epi::Gated) {
-                    z8(ch + 4, s2, u);
+                    z8(ch + 4, c2, g);
                     if (p.pre) {
-                        uint16_t *dst = p.pre + (int64_t)p.slot_of[row] * p.N + n;
+                        uint16_t *dst = p.pre + to * p.N + n;
                         store8<VEC>(dst, n, p.N, z);
-                        store8<VEC>(dst + p.pre_rows * p.N, n, p.N, u);
+                        store8<VEC>(dst + p.pre_rows * p.N, n, p.N, g);
                     }
                     act_values(z, p.act);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] *= u[e];
+                    for (int e = 0; e < 8; ++e) z[e] *= g[e];
                     store8<VEC>(p.y + row * p.N + n, n, p.N, z);
                 }
             }
         }
-        __syncthreads();                                 // the next unit's loads refill what was read here
+        st = st == NST - 1 ? 0 : st + 1;
     }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));           // the last loads into LDS
 }
 
 // ---------------------------------------------------------------------------------------------
