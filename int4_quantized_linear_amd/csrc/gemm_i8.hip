@@ -459,6 +459,8 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                 return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(base) + (int64_t)mw * p.N, (short)0,
                                                          base ? NUM_RECORDS : 0, 0x00020000);
             };
+            // (Part's sums stored straight from the accumulators, 64 bytes of a row at a time: 443 us for the expert layer
+            // of 4096 tokens, 435 so.)
             const __amdgpu_buffer_rsrc_t ry = E == Epi::Part
                 ? __builtin_amdgcn_make_buffer_rsrc(static_cast<float *>(p.y) + (int64_t)mw * p.N, (short)0, NUM_RECORDS, 0x00020000)
                 : rows_of(static_cast<uint16_t *>(p.y));

@@ -394,11 +394,43 @@ void launch_tiles(const GroupedParams &p, hipStream_t stream)
     hipLaunchKernelGGL((grouped_tile_kernel<E, BM, NST, VEC>), dim3(grid), dim3(NTHREADS), 0, stream, p);
 }
 
-template <Epi E, bool VEC>
-void launch_rows(const GroupedParams &p, hipStream_t stream)
+// Rows per tile, 64, 128 or 256, by a model with measured constants (us).  A CU takes `step` per K-tile and `end` per
+// unit of several, a lone workgroup `lone` per K-tile; a group's last tile is half empty; the weights stream at 4.9 TB/s.
+// Measured, whole calls, 64 / 128 / 256 rows:
+//   linear_grouped, rows, groups, K x N:  2500, 6, 2688 x 1001: 38 / 42 / 67;   2000, 8, 2048 x 2048: 39 / 29 / 36
+//     4000, 8, 2688 x 5376: 149 / 107 / 95;   8192, 16, 5376 x 5376: 595 / 389 / 325
+//   expert layer, tokens, top of E, K x F:  12, 6 of 64, 2048 x 1408: 101 / 107 / 134;  1000, 4 of 32, the same: 160 / 149 / 154
+//     4096, 6 of 64, the same: 623 / 494 / 438
+int rows_per_tile(int64_t rows, int groups, int64_t N, int K, Epi epi)
 {
-    const int used = p.groups < p.rows ? p.groups : p.rows;
-    if (p.rows <= 64 * (int64_t)used) launch_tiles<E, 64, 3, VEC>(p, stream);
+    const double cols = (double)N * (epi == Epi::Gated ? 2.0 : 1.0), used = (double)(groups < rows ? groups : rows);
+    const double stream = used * cols * K / 4.9e6;
+    const int KT = (K + BK - 1) / BK;
+    int best_bm = 64;
+    double best = 1e30;
+    for (int bm = 64; bm <= 256; bm *= 2) {
+        const double width = bm == 256 ? 256.0 : 128.0;
+        const double step = bm == 64 ? 0.55 : bm == 128 ? 0.72 : 1.72, lone = bm == 64 ? 0.85 : bm == 128 ? 1.1 : 1.72;
+        const double end = bm == 64 ? 1.5 : bm == 128 ? 2.5 : epi == Epi::Bf16 ? 5.0 : 10.0;
+        const double tiles = (double)rows / bm + 0.5 * used;
+        const double units = (tiles > used ? tiles : used) * __builtin_ceil(cols / width);
+        // rounds: the last one is half full on average, unless the tiles are surely no more than the CUs
+        const double rounds = units < 220.0 ? 1.0 : units / 256.0 + 0.5;
+        const double many = rounds * (KT * step + end), one = KT * lone + end;
+        double t = many > one ? many : one;
+        if (t < stream) t = stream + end;
+        if (t < best) {
+            best = t;
+            best_bm = bm;
+        }
+    }
+    return best_bm;
+}
+
+template <Epi E, bool VEC>
+void launch_rows(const GroupedParams &p, int bm, hipStream_t stream)
+{
+    if (bm == 64) launch_tiles<E, 64, 3, VEC>(p, stream);
     else launch_tiles<E, 128, 2, VEC>(p, stream);
 }
 
@@ -425,8 +457,8 @@ hipError_t launch_moe_order(const int32_t *experts, int64_t S, int E, int top, c
 hipError_t launch_grouped_i8(const GroupedArgs &g, Epi epi, hipStream_t stream)
 {
     if (g.rows <= 0 || g.N <= 0) return hipSuccess;
-    const int used = (int)(g.groups < g.rows ? g.groups : g.rows);
-    if (g.rows > 160 * (int64_t)used) return launch_grouped_gemm_i8(g, epi, stream);
+    const int bm = rows_per_tile(g.rows, g.groups, g.N, g.K, epi);
+    if (bm == 256) return launch_grouped_gemm_i8(g, epi, stream);
     GroupedParams p;
     p.xq = g.xq;
     p.sx = g.sx;
@@ -452,16 +484,16 @@ hipError_t launch_grouped_i8(const GroupedArgs &g, Epi epi, hipStream_t stream)
     const bool vec = g.N % 8 == 0;
     switch (epi) {
     case Epi::Bf16:
-        if (vec) launch_rows<Epi::Bf16, true>(p, stream);
-        else launch_rows<Epi::Bf16, false>(p, stream);
+        if (vec) launch_rows<Epi::Bf16, true>(p, bm, stream);
+        else launch_rows<Epi::Bf16, false>(p, bm, stream);
         break;
     case Epi::Gated:
         if (!vec) return hipErrorInvalidValue;
-        launch_rows<Epi::Gated, true>(p, stream);
+        launch_rows<Epi::Gated, true>(p, bm, stream);
         break;
     default:
         if (!vec) return hipErrorInvalidValue;
-        launch_rows<Epi::Part, true>(p, stream);
+        launch_rows<Epi::Part, true>(p, bm, stream);
     }
     return hipGetLastError();
 }
