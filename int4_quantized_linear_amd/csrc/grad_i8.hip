@@ -882,6 +882,7 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(RowsParams p)
 {
     __shared__ float red[4];
     typedef v4u unaligned __attribute__((aligned(2)));
+    typedef v4f v4f_any __attribute__((aligned(4)));
     const int s = (int)blockIdx.x, t = (int)threadIdx.x;
     int64_t row = s, source = s;
     int group = -1;
@@ -927,8 +928,14 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(RowsParams p)
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(v[i], e[i], sum);
         }
+        if (n + 8 <= p.N) {
+            const v4f lo = *reinterpret_cast<const v4f_any *>(sw + n), hi = *reinterpret_cast<const v4f_any *>(sw + n + 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = n + i < p.N ? v[i] * share * sw[n + i] : 0.0f;
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * share * (i < 4 ? lo[i & 3] : hi[i & 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = n + i < p.N ? v[i] * share * sw[n + i] : 0.0f;
+        }
         *reinterpret_cast<v4u *>(a + n) =
             v4u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
     }
@@ -1102,6 +1109,27 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Rows per tile, 64 or 256, by a model with measured constants (us): a CU takes `step` per contraction step and `end` per
+// unit; a group's last tile is half empty, and so is the last round unless the tiles are surely no more than the CUs.
+// Measured, whole calls, 64 / 256 rows:
+//   linear_grouped_backward, rows, groups, N x K:  1000, 4, 2048 x 2688: 37 / 66;   3000, 12, 2048 x 2048: 52 / 66
+//     2000, 8, 2688 x 5376: 90 / 82;   4097, 8, 5376 x 2688: 167 / 151;   8000, 8, 2688 x 2688: 161 / 160
+//   expert layer, tokens, top of E, K x F:  2048, 4 of 32, 2048 x 1408: 288 / 359;   4096, 2 of 16, 2688 x 2688: 537 / 515
+int grouped_rows_per_tile(int64_t rows, int groups, int tiles_c, int nt)
+{
+    const double used = (double)(groups < rows ? groups : rows);
+    double t[2];
+    for (int i = 0; i < 2; ++i) {
+        const int bm = i ? BM : 64;
+        const double step = i ? 1.6 : 0.57, lone = i ? 1.6 : 0.75, end = i ? 12.0 : 3.0;
+        const double tiles = (double)rows / bm + 0.5 * used, units = (tiles > used ? tiles : used) * tiles_c;
+        const double rounds = units < 235.0 ? 1.0 : units / 256.0 + 0.5;
+        const double many = rounds * (nt * step + end), one = nt * lone + end;
+        t[i] = many > one ? many : one;
+    }
+    return t[1] < t[0] ? BM : 64;
+}
+
 int64_t grouped_grad_lda(int64_t N) { return (N + BN - 1) / BN * BN; }
 
 hipError_t launch_grouped_rows(const GroupedRowsArgs &g, hipStream_t stream)
@@ -1149,10 +1177,7 @@ hipError_t launch_grouped_grad(const GroupedGradArgs &g, hipStream_t stream)
     p.offsets = g.offsets;
     p.slot_of = g.slot_of;
     p.groups = g.groups;
-    // A step takes 0.54 us of a CU in 64-row tiles, 1.6 us in 256-row ones (tile_plan), and a group's last tile is half
-    // empty on average: equal at about 240 rows per group.
-    const int64_t used = g.groups < g.rows ? g.groups : g.rows;
-    const int bm = g.rows > 240 * used ? BM : 64;
+    const int bm = grouped_rows_per_tile(g.rows, g.groups, p.tiles_c, p.nt);
     const int64_t most = most_group_tiles(g.rows, g.groups, bm) * p.tiles_c;
     if (most >= ((int64_t)1 << 31) - 8) return hipErrorInvalidValue;
     const dim3 grid((unsigned)((most + 7) & ~7));
