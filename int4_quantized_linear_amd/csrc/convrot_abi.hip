@@ -1224,6 +1224,44 @@ int convrot_moe_ffn_gated(const void *x, int x_dtype, const int32_t *experts, co
     float *xs = reinterpret_cast<float *>(ws + L.xs), *hs = reinterpret_cast<float *>(ws + L.hs);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h);
     float *part = reinterpret_cast<float *>(ws + L.part);
+    convrot::MoeFew few;
+    if (!pre && !d && convrot::plan_moe_few(M, top, (int)K, (int)F, few)) {
+        convrot::MoeFewArgs a;
+        a.x = x;
+        a.x_f32 = x_dtype == CONVROT_DTYPE_F32;
+        a.xq = xq;
+        a.xs = xs;
+        a.hq = hq;
+        a.hs = hs;
+        a.experts = experts;
+        a.weights = weights;
+        a.wq_gate = wq_gate;
+        a.gate_scale = gate_scale;
+        a.wq_up = wq_up;
+        a.up_scale = up_scale;
+        a.wq_down = wq_down;
+        a.down_scale = down_scale;
+        a.residual = static_cast<const uint16_t *>(residual);
+        a.h = h;
+        a.y = static_cast<uint16_t *>(y);
+        a.M = M;
+        a.top = top;
+        a.E = (int)E;
+        a.K = (int)K;
+        a.F = (int)F;
+        a.act = act;
+        a.log2g = log2i(group);
+        a.log2g_h = log2i(group_h);
+        if (!few.fuse_x &&
+            (rc = hip_status(convrot::launch_rotate_quant(x, a.x_f32, M, (int)K, a.log2g, 8, xq, xs, stream), "rotate_quant")))
+            return rc;
+        if ((rc = hip_status(convrot::launch_moe_few_gate(a, few, stream), "moe_few_gate"))) return rc;
+        if (!few.fuse_h &&
+            (rc = hip_status(convrot::launch_rotate_quant(h, false, (int64_t)S, (int)F, a.log2g_h, 8, hq, hs, stream),
+                             "rotate_quant")))
+            return rc;
+        return hip_status(convrot::launch_moe_few_down(a, few, stream), "moe_few_down");
+    }
     o.sx = xs;
     o.sx_of = reinterpret_cast<float *>(ws + L.rs);
     rc = hip_status(convrot::launch_rotate_quant(x, x_dtype == CONVROT_DTYPE_F32, M, (int)K, log2i(group), 8, xq, xs, stream),

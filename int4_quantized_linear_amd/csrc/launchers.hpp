@@ -161,6 +161,30 @@ hipError_t launch_grouped_grad(const GroupedGradArgs &g, hipStream_t stream);
 hipError_t launch_moe_combine(const float *part, const int32_t *row_of, const float *weights, const uint16_t *residual,
                               uint16_t *y, int64_t M, int K, int top, hipStream_t stream);
 
+// The expert layer for at most 128 slots (moe_few.hip), nothing saved: plan_moe_few says whether it takes the call and which of
+// the two kernels quantizes its rows itself; where one does not, its codes and scales (xq, xs of the tokens; hq, hs of h's
+// slots) are made by launch_rotate_quant before it.
+struct MoeFew {
+    bool fuse_x = false, fuse_h = false;
+};
+struct MoeFewArgs {
+    const void *x = nullptr;
+    bool x_f32 = false;
+    const int8_t *xq = nullptr, *hq = nullptr;
+    const float *xs = nullptr, *hs = nullptr;
+    const int32_t *experts = nullptr;
+    const float *weights = nullptr;
+    const int8_t *wq_gate = nullptr, *wq_up = nullptr, *wq_down = nullptr;
+    const float *gate_scale = nullptr, *up_scale = nullptr, *down_scale = nullptr;
+    const uint16_t *residual = nullptr;
+    uint16_t *h = nullptr, *y = nullptr;  // h [S, F] by slot
+    int64_t M = 0;
+    int top = 0, E = 0, K = 0, F = 0, act = 0, log2g = 0, log2g_h = 0;
+};
+bool plan_moe_few(int64_t M, int top, int K, int F, MoeFew &plan);
+hipError_t launch_moe_few_gate(const MoeFewArgs &a, const MoeFew &plan, hipStream_t stream);
+hipError_t launch_moe_few_down(const MoeFewArgs &a, const MoeFew &plan, hipStream_t stream);
+
 // Router: see convrot_moe_route and convrot_moe_route_backward.
 struct RouteArgs {
     const void *logits = nullptr;         // [M, E]

@@ -1,0 +1,571 @@
+// moe_few.hip -- the gated expert layer for a few tokens (at most 128 slots): two kernels, or up to two more that quantize
+// (gfx950).
+//
+// With few tokens the layer is its experts' weights streamed once, and the launches around that.  Here
+//   moe_few_gate_kernel  h[slot] = bf16(act(g) u):  a workgroup per 16 features and expert
+//   moe_few_down_kernel  y = bf16(sum_j weight d + residual):  a workgroup per 16 output channels, all experts
+// find the experts' slots from the table of experts themselves (two slots per lane, ballots), and rotate and
+// quantize the rows they use themselves, into LDS, where that repeated work is short (FUSED): it runs while the
+// workgroup's first weights arrive.  Otherwise the codes come from launch_rotate_quant.
+// The weights go from memory to the matrix core's operand registers: v_mfma_i32_16x16x64_i8 takes 16 rows (lane % 16) of 64
+// bytes (16 per lane / 16), so four loads per 16 rows fetch 256 contiguous bytes of each; P such chunks are in
+// flight per wavefront.  Columns are the rows of x or h of one expert, at most 16 a pass.
+// Integer sums are exact and the epilogues are those of the other kernels, so the results are the same bits.
+#include "activation.hpp"
+#include "device_common.hpp"
+#include "launchers.hpp"
+#include "rotate_common.hpp"
+#include "tile_common.hpp"
+
+namespace convrot {
+namespace {
+
+constexpr int MAX_SLOTS = 128;
+constexpr int KC = 256;                                  // bytes of a row per chunk
+
+// The table of experts, two slots per lane: slot l in a lane's first, slot 64 + l in its second entry (-1: none).
+struct Slots {
+    int e0, e1;
+    uint64_t v0, v1;                                     // slots with an expert
+
+    __device__ __forceinline__ Slots(const int32_t *experts, int S, int E)
+    {
+        const int lane = threadIdx.x & 63;
+        e0 = lane < S ? experts[lane] : -1;
+        e1 = lane + 64 < S ? experts[lane + 64] : -1;
+        if ((unsigned)e0 >= (unsigned)E) e0 = -1;
+        if ((unsigned)e1 >= (unsigned)E) e1 = -1;
+        v0 = __builtin_amdgcn_ballot_w64(e0 >= 0);
+        v1 = __builtin_amdgcn_ballot_w64(e1 >= 0);
+    }
+    __device__ __forceinline__ int expert(int slot) const
+    {
+        const int a = __builtin_amdgcn_readlane(e0, slot & 63), b = __builtin_amdgcn_readlane(e1, slot & 63);
+        return slot < 64 ? a : b;
+    }
+};
+
+// Index of the set bit number i (from 0) of m0, then m1, for i < their count, in lane i; any number in other lanes.
+// Every set bit's lane sends its own number to the lane of its rank (from 64 on: nowhere that is read).
+__device__ __forceinline__ int slot_of_rank(uint64_t m0, uint64_t m1, int first)
+{
+    const int lane = threadIdx.x & 63;
+    const int below0 = __builtin_amdgcn_mbcnt_hi((uint32_t)(m0 >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m0, 0));
+    const int below1 = __builtin_amdgcn_mbcnt_hi((uint32_t)(m1 >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m1, 0));
+    const int n0 = __builtin_popcountll(m0);
+    const int r0 = below0 - first, r1 = n0 + below1 - first;
+    const bool in0 = (m0 >> lane & 1) && r0 >= 0 && r0 < 16, in1 = (m1 >> lane & 1) && r1 >= 0 && r1 < 16;
+    const int a = __builtin_amdgcn_ds_permute(4 * (in0 ? r0 : 63), lane);
+    const int b = __builtin_amdgcn_ds_permute(4 * (in1 ? r1 : 63), lane + 64);
+    return lane + first < n0 ? a : b;
+}
+
+// One unit of rotation, 256 channels jj of a row, in the 8 lanes of a slot (rotate_common.hpp).
+template <bool F32, int LG>
+__device__ __forceinline__ void rotated(const void *x, int64_t row0, int K, int jj, bool ok, float (&v)[4][8])
+{
+    const int lane = threadIdx.x & 63, qd = lane & 3, h = lane >> 5;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int k = 256 * jj + 64 * r + 32 * h + 8 * qd;
+        const bool in = ok && k < K;
+        const int64_t at = in ? row0 + k : 0;
+        if constexpr (F32) {
+            const v4f *src = reinterpret_cast<const v4f *>(static_cast<const float *>(x) + at);
+            const v4f a = src[0], b = src[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[r][e] = in ? a[e] : 0.0f;
+                v[r][e + 4] = in ? b[e] : 0.0f;
+            }
+        } else {
+            v4u d = *reinterpret_cast<const v4u *>(static_cast<const uint16_t *>(x) + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t p = in ? d[e] : 0u;
+                v[r][2 * e] = bf16lo_to_f32(p);
+                v[r][2 * e + 1] = bf16hi_to_f32(p);
+            }
+        }
+    }
+    fwht_slot<LG>(v, qd);
+}
+
+__device__ __forceinline__ float slot_max(const float (&v)[4][8])
+{
+    float a = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a = __builtin_fmaxf(a, __builtin_fabsf(v[r][e]));
+    a = __builtin_fmaxf(a, dpp_xor1(a));
+    a = __builtin_fmaxf(a, dpp_xor2(a));
+    uint32_t lo = __float_as_uint(a), hi = lo;
+    swap32(lo, hi);
+    return __builtin_fmaxf(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+struct Rotation {
+    float cg, cg_lo;
+    double root;
+};
+
+template <int LG>
+__device__ __forceinline__ float row_scale(float amax, const Rotation &g)
+{
+    return (LG % 2 == 0 ? amax * g.cg : (float)((double)amax / g.root)) / 127.0f;
+}
+
+// Rows of codes in LDS: `stride` bytes each, 16-byte chunk c of every 256 at c ^ row % 16, so that the 16 rows of a fragment
+// read fall on distinct banks.
+__device__ __forceinline__ uint32_t code_at(int row, int stride, int jj, int chunk)
+{
+    return (uint32_t)(row * stride + KC * jj + 16 * (chunk ^ (row & 15)));
+}
+
+template <int LG>
+__device__ __forceinline__ void store_codes(float (&v)[4][8], float sc, const Rotation &g, uint8_t *codes, int row, int stride, int jj)
+{
+    const int lane = threadIdx.x & 63, qd = lane & 3, h = lane >> 5;
+    const float lsign = (((LG > 3 ? qd : 0) ^ (LG > 4 ? qd >> 1 : 0)) & 1) ? -1.0f : 1.0f;
+    QuotientRN k = quotient_consts<LG>(sc, lsign, g.cg);
+    const bool tiny = sc > 0.0f && sc < 0x1p-100f;       // 1 / sc could overflow: both scaled by 2^64, exactly
+    if (__builtin_amdgcn_ballot_w64(tiny) != 0 && tiny) {
+        k = quotient_consts<LG>(sc * 0x1p64f, lsign, g.cg);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[r][e] *= 0x1p64f;
+    }
+    uint32_t c[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        uint32_t t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = rne_bits(quotient_rn<LG>(v[r][e], k, g.cg, g.cg_lo), 1.0f);
+        c[r][0] = pack4_i8(t[0], t[1], t[2], t[3]);
+        c[r][1] = pack4_i8(t[4], t[5], t[6], t[7]);
+    }
+    if constexpr (LG > 5) {
+#pragma unroll
+        for (int r1 = 0; r1 < 2; ++r1) {
+            swap32(c[2 * r1][0], c[2 * r1 + 1][0]);
+            swap32(c[2 * r1][1], c[2 * r1 + 1][1]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<v2u *>(codes + code_at(row, stride, jj, 4 * r + 2 * h + (qd >> 1)) + 8 * (qd & 1)) = v2u{c[r][0], c[r][1]};
+}
+
+// Rows 0 .. n - 1 (row r from element start(r) of x) to codes and scales in LDS, by a workgroup of NW wavefronts; all of it
+// calls.  maxima: n words, zeroed.  A wavefront rotates 8 units at a time; its first stay in registers until the
+// rows' maxima are known, later ones are rotated again.
+template <bool F32, int LG, int NW, typename Start>
+__device__ __forceinline__ void quantize_rows(const void *x, Start start, int n, int K, const Rotation &g, uint8_t *codes, int stride,
+                                              uint32_t *maxima, float *scales)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, sl = (lane >> 2) & 7;
+    const bool lead = (lane & 3) == 0 && lane < 32;
+    const int SL = (K + KC - 1) / KC, units = n * SL;
+    float kept[4][8];
+    for (int u0 = 8 * w; u0 < units; u0 += 8 * NW) {
+        const int u = u0 + sl, row = u < units ? u / SL : 0;
+        float v[4][8];
+        rotated<F32, LG>(x, start(row), K, u - row * SL, u < units, v);
+        const float m = slot_max(v);
+        if (lead && u < units) atomicMax(&maxima[row], __float_as_uint(m));
+        if (u0 == 8 * w) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) kept[r][e] = v[r][e];
+        }
+    }
+    __syncthreads();
+    for (int u0 = 8 * w; u0 < units; u0 += 8 * NW) {
+        const int u = u0 + sl, row = u < units ? u / SL : 0, jj = u - row * SL;
+        if (u0 != 8 * w) rotated<F32, LG>(x, start(row), K, jj, u < units, kept);
+        const float sc = row_scale<LG>(__uint_as_float(maxima[row]), g);
+        if (u < units) {
+            store_codes<LG>(kept, sc, g, codes, row, stride, jj);
+            if (jj == 0 && lead) scales[row] = sc;
+        }
+    }
+    __syncthreads();
+}
+
+struct FewParams {
+    const int32_t *experts;    // [S]
+    const float *weights;      // [S]
+    const void *x;             // FUSED: the rows to quantize, [tokens, K] (down: h [S, F])
+    const int8_t *q;           // otherwise their codes
+    const float *qs;           // and scales
+    const int8_t *w1, *w2;     // gate, up [E, F, K]; down [E, K, F]
+    const float *s1, *s2;
+    const uint16_t *residual;  // bf16 [tokens, K] or null
+    uint16_t *out;             // h [S, F]; y [tokens, K]
+    Rotation g;
+    int S, E, top, K, F, act, rmax;
+};
+
+// ---------------------------------------------------------------------------------------------
+// h: workgroup (feature tile, slot); the first slot of each expert does the expert's work, the others end.  4 wavefronts take
+// every fourth chunk of K for 16 rows of gate and 16 of up; their sums meet in LDS.
+constexpr int GNW = 4, GP = 3;
+
+template <bool FUSED, bool F32, int LG>
+__global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];       // codes, then the sums
+    __shared__ uint32_t maxima[16];
+    __shared__ float scales[16];
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    const int K = p.K, SL = (K + KC - 1) / KC, stride = KC * SL;
+    const Slots t(p.experts, p.S, p.E);
+    const int s = blockIdx.y, e = t.expert(s);
+    if (e < 0) return;
+    const uint64_t m0 = __builtin_amdgcn_ballot_w64(t.e0 == e), m1 = __builtin_amdgcn_ballot_w64(t.e1 == e);
+    if ((m0 ? __builtin_ctzll(m0) : 64 + __builtin_ctzll(m1)) != s) return;
+    const int count = __builtin_popcountll(m0) + __builtin_popcountll(m1);
+    const int f0 = 16 * (int)blockIdx.x;
+    // this thread's output: row r of the pass, feature f0 + 4 q + w
+    const int64_t fs = (int64_t)e * p.F + f0 + 4 * q + w;
+    const float sg = p.s1[fs], su = p.s2[fs];
+    const int64_t w0 = ((int64_t)e * p.F + f0) * K;
+    const __amdgpu_buffer_rsrc_t rg = uniform_rsrc(reinterpret_cast<uint64_t>(p.w1 + w0), 16 * K);
+    const __amdgpu_buffer_rsrc_t ru = uniform_rsrc(reinterpret_cast<uint64_t>(p.w2 + w0), 16 * K);
+    const __amdgpu_buffer_rsrc_t rq = uniform_rsrc(reinterpret_cast<uint64_t>(p.q), NUM_RECORDS);
+    // chunk c's operands: rows r, bytes 256 c + 64 kk + 16 q (past K: zeros)
+    auto load_weights = [&](v4u (&b)[2][4], int c) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const int k = KC * c + 64 * kk;
+            const uint32_t off = k < K ? (uint32_t)(r * K + k + 16 * q) : OOB;
+            b[0][kk] = __builtin_amdgcn_raw_buffer_load_b128(rg, off, 0, 2);
+            b[1][kk] = __builtin_amdgcn_raw_buffer_load_b128(ru, off, 0, 2);
+        }
+    };
+    for (int first = 0; first < count; first += p.rmax) {
+        const int n = min(count - first, p.rmax);
+        const int slots = slot_of_rank(m0, m1, first);
+        const int slot = __shfl(slots, min(r, n - 1));   // of this lane's column
+        v4u wb[GP][2][4], xb[GP][4];
+#pragma unroll
+        for (int i = 0; i < GP; ++i) load_weights(wb[i], w + GNW * i);
+        const uint32_t xrow = (uint32_t)(slot / p.top) * (uint32_t)K;
+        auto load_rows = [&](v4u (&b)[4], int c) {       // from memory; FUSED reads LDS when the chunk's turn comes
+            if constexpr (!FUSED) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const int k = KC * c + 64 * kk;
+                    b[kk] = __builtin_amdgcn_raw_buffer_load_b128(rq, k < K ? xrow + (uint32_t)(k + 16 * q) : OOB, 0, 0);
+                }
+            }
+        };
+        float sx;
+        if constexpr (FUSED) {
+            if (threadIdx.x < 16) maxima[threadIdx.x] = 0u;
+            __syncthreads();
+            quantize_rows<F32, LG, GNW>(p.x, [&](int row) { return (int64_t)(__shfl(slots, row) / p.top) * K; }, n, K, p.g, smem,
+                                        stride, maxima, scales);
+            sx = scales[min(r, n - 1)];
+        } else {
+#pragma unroll
+            for (int i = 0; i < GP; ++i) load_rows(xb[i], w + GNW * i);
+            sx = p.qs[slot / p.top];
+        }
+        v4i acc[2] = {};
+        for (int c0 = w; c0 < SL; c0 += GNW * GP) {
+#pragma unroll
+            for (int i = 0; i < GP; ++i) {
+                const int c = min(c0 + GNW * i, SL - 1); // past the end: weights are zeros
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if constexpr (FUSED)
+                        xb[i][kk] = *reinterpret_cast<const v4u *>(smem + code_at(min(r, n - 1), stride, c, 4 * kk + q));
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, wb[i][b][kk]),
+                                                                       __builtin_bit_cast(v4i, xb[i][kk]), acc[b], 0, 0, 0);
+                }
+                load_weights(wb[i], c0 + GNW * (i + GP));
+                load_rows(xb[i], c0 + GNW * (i + GP));
+            }
+        }
+        // lane: column r, features 4 q + v
+        __syncthreads();                                 // the codes have been read
+        int32_t *red = reinterpret_cast<int32_t *>(smem);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) red[((w * 2 + b) * 4 + v) * 64 + lane] = acc[b][v];
+        __syncthreads();
+        int32_t ga = 0, ua = 0;
+#pragma unroll
+        for (int i = 0; i < GNW; ++i) {
+            ga += red[((i * 2 + 0) * 4 + w) * 64 + lane];
+            ua += red[((i * 2 + 1) * 4 + w) * 64 + lane];
+        }
+        if (r < n) {
+            const float gv = __builtin_fmaf((float)ga, sx * sg, 0.0f), uv = __builtin_fmaf((float)ua, sx * su, 0.0f);
+            p.out[(int64_t)slot * p.F + f0 + 4 * q + w] = (uint16_t)(pack_bf16x2(act_value(gv, p.act) * uv, 0.0f) & 0xffffu);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// y: workgroup = 16 output channels.  The experts' products are items, cut into `parts` along F where there are fewer than
+// wavefronts; wavefront w takes items w, w + NW, ...  and adds its int32 sums to the slots' in LDS (exact in any order).  Then a
+// thread per token and channel scales, weighs and adds up its slots in their order.
+constexpr int DNW = 8, DP = 4;
+
+template <bool FUSED, int LG>
+__global__ void __launch_bounds__(64 * DNW) moe_few_down_kernel(FewParams p)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];       // FUSED: codes of h
+    __shared__ int32_t sums[MAX_SLOTS][16];
+    __shared__ uint32_t maxima[MAX_SLOTS];
+    __shared__ float scales[MAX_SLOTS];
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    const int F = p.F, SL = (F + KC - 1) / KC, stride = KC * SL;
+    const int n0 = 16 * (int)blockIdx.x;
+    const Slots t(p.experts, p.S, p.E);
+    for (int i = threadIdx.x; i < p.S * 16; i += 64 * DNW) sums[0][i] = 0;
+    if constexpr (FUSED) {
+        if ((int)threadIdx.x < p.S) maxima[threadIdx.x] = 0u;
+    }
+
+    // Walks this wavefront's chunks: of every expert in order of first slot, each block of 16 of its slots, each part.
+    struct Walk {
+        uint64_t r0, r1, m0, m1;                         // slots not yet walked; the expert's
+        int e, first, count, item, part, c, end;         // c >= end: done
+    };
+    int parts = 1;
+    auto next_item = [&](Walk &k) {
+        do {
+            if (++k.part == parts) {
+                k.part = 0;
+                k.first += 16;
+            }
+            if (k.first >= k.count) {
+                if (!(k.r0 | k.r1)) {
+                    k.c = k.end = 0;
+                    return;
+                }
+                k.e = t.expert(k.r0 ? __builtin_ctzll(k.r0) : 64 + __builtin_ctzll(k.r1));
+                k.m0 = __builtin_amdgcn_ballot_w64(t.e0 == k.e);
+                k.m1 = __builtin_amdgcn_ballot_w64(t.e1 == k.e);
+                k.r0 &= ~k.m0;
+                k.r1 &= ~k.m1;
+                k.first = 0;
+                k.count = __builtin_popcountll(k.m0) + __builtin_popcountll(k.m1);
+            }
+        } while (k.item++ % DNW != w);
+        k.c = SL * k.part / parts;
+        k.end = SL * (k.part + 1) / parts;
+    };
+    auto start = [&] {
+        Walk k = {t.v0, t.v1, 0, 0, 0, 0, 0, 0, parts - 1, 0, 0};
+        next_item(k);
+        return k;
+    };
+    {
+        int distinct = 0;
+        for (uint64_t r0 = t.v0, r1 = t.v1; r0 | r1; ++distinct) {
+            const int e = t.expert(r0 ? __builtin_ctzll(r0) : 64 + __builtin_ctzll(r1));
+            r0 &= ~__builtin_amdgcn_ballot_w64(t.e0 == e);
+            r1 &= ~__builtin_amdgcn_ballot_w64(t.e1 == e);
+        }
+        while (distinct * parts < DNW && 2 * parts <= SL) parts *= 2;
+    }
+    const __amdgpu_buffer_rsrc_t rq = uniform_rsrc(reinterpret_cast<uint64_t>(p.q), NUM_RECORDS);
+    Walk ld = start();
+    int ld_slot = 0;                                     // of this lane's column
+    auto load = [&](v4u (&wb)[4], v4u (&xb)[4]) {
+        const bool any = ld.c < ld.end;
+        const __amdgpu_buffer_rsrc_t rw =
+            uniform_rsrc(reinterpret_cast<uint64_t>(p.w1 + ((int64_t)ld.e * p.K + n0) * F), any ? 16 * F : 0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const int k = KC * ld.c + 64 * kk;
+            const uint32_t off = k < F ? (uint32_t)(k + 16 * q) : OOB;
+            wb[kk] = __builtin_amdgcn_raw_buffer_load_b128(rw, (uint32_t)(r * F) + off, 0, 2);
+            if constexpr (!FUSED)
+                xb[kk] = __builtin_amdgcn_raw_buffer_load_b128(rq, any ? (uint32_t)(ld_slot * F) + off : OOB, 0, 0);
+        }
+        if (any && ++ld.c == ld.end) {
+            next_item(ld);
+            if (!FUSED && ld.c < ld.end)
+                ld_slot = __shfl(slot_of_rank(ld.m0, ld.m1, ld.first), min(r, min(ld.count - ld.first, 16) - 1));
+        }
+    };
+    v4u wb[DP][4], xb[DP][4];
+    Walk at = ld;
+    int n_at = 0, slot = 0;
+    auto enter = [&] {                                   // the compute side's next item
+        n_at = min(at.count - at.first, 16);
+        if (at.c < at.end) slot = __shfl(slot_of_rank(at.m0, at.m1, at.first), min(r, n_at - 1));
+    };
+    enter();
+    ld_slot = slot;
+#pragma unroll
+    for (int i = 0; i < DP; ++i) load(wb[i], xb[i]);
+    __syncthreads();
+    if constexpr (FUSED) quantize_rows<false, LG, DNW>(p.x, [&](int row) { return (int64_t)row * F; }, p.S, F, p.g, smem, stride,
+                                                       maxima, scales);
+    v4i acc = {};
+    while (at.c < at.end) {
+#pragma unroll
+        for (int i = 0; i < DP; ++i) {
+            const bool any = at.c < at.end;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                if constexpr (FUSED)
+                    xb[i][kk] = *reinterpret_cast<const v4u *>(smem + code_at(slot, stride, any ? at.c : 0, 4 * kk + q));
+                acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, wb[i][kk]), __builtin_bit_cast(v4i, xb[i][kk]),
+                                                            acc, 0, 0, 0);
+            }
+            load(wb[i], xb[i]);
+            if (any && ++at.c == at.end) {
+                if (r < n_at) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) atomicAdd(&sums[slot][4 * q + v], acc[v]);
+                }
+                acc = v4i{};
+                next_item(at);
+                enter();
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.S / p.top * 16; i += 64 * DNW) {
+        const int m = i >> 4, n = i & 15;
+        float v = 0.0f;
+        for (int j = 0; j < p.top; ++j) {
+            const int s = m * p.top + j, e = p.experts[s];
+            if ((unsigned)e >= (unsigned)p.E) continue;
+            const float sh = FUSED ? scales[s] : p.qs[s];
+            const float d = __builtin_fmaf((float)sums[s][n], sh * p.s1[(int64_t)e * p.K + n0 + n], 0.0f);
+            v = __builtin_fmaf(p.weights[s], d, v);
+        }
+        const int64_t o = (int64_t)m * p.K + n0 + n;
+        if (p.residual) v += bf16lo_to_f32(p.residual[o]);
+        p.out[o] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
+    }
+}
+
+Rotation rotation(int log2g)
+{
+    Rotation g;
+    g.root = __builtin_sqrt((double)(1 << log2g));
+    g.cg = (float)(1.0 / g.root);
+    g.cg_lo = (float)(1.0 / g.root - (double)g.cg);
+    return g;
+}
+
+template <bool F32, int LG>
+void launch_gate(const FewParams &p, dim3 grid, size_t lds, hipStream_t stream)
+{
+    hipLaunchKernelGGL((moe_few_gate_kernel<true, F32, LG>), grid, dim3(64 * GNW), lds, stream, p);
+}
+
+#define CONVROT_LOG2G(fn, ...)           \
+    switch (log2g) {                     \
+    case 0: fn(0, __VA_ARGS__); break;   \
+    case 1: fn(1, __VA_ARGS__); break;   \
+    case 2: fn(2, __VA_ARGS__); break;   \
+    case 3: fn(3, __VA_ARGS__); break;   \
+    case 4: fn(4, __VA_ARGS__); break;   \
+    case 5: fn(5, __VA_ARGS__); break;   \
+    case 6: fn(6, __VA_ARGS__); break;   \
+    case 7: fn(7, __VA_ARGS__); break;   \
+    default: fn(8, __VA_ARGS__);         \
+    }
+
+} // namespace
+
+bool plan_moe_few(int64_t M, int top, int K, int F, MoeFew &plan)
+{
+    if (M * top > MAX_SLOTS) return false;
+    const int rows = M < 16 ? (int)M : 16, slk = (K + KC - 1) / KC, slf = (F + KC - 1) / KC;
+    plan.fuse_x = (int)M * slk <= 64 && rows * slk * KC <= 64 * 1024;
+    plan.fuse_h = (int)M * top * slf <= 64;
+    return true;
+}
+
+hipError_t launch_moe_few_gate(const MoeFewArgs &a, const MoeFew &plan, hipStream_t stream)
+{
+    FewParams p = {};
+    p.experts = a.experts;
+    p.x = a.x;
+    p.q = a.xq;
+    p.qs = a.xs;
+    p.w1 = a.wq_gate;
+    p.w2 = a.wq_up;
+    p.s1 = a.gate_scale;
+    p.s2 = a.up_scale;
+    p.out = a.h;
+    p.S = (int)a.M * a.top;
+    p.E = a.E;
+    p.top = a.top;
+    p.K = a.K;
+    p.F = a.F;
+    p.act = a.act;
+    p.rmax = a.M < 16 ? (int)a.M : 16;
+    const int log2g = a.log2g;
+    p.g = rotation(log2g);
+    const dim3 grid((unsigned)(a.F / 16), (unsigned)p.S);
+    const size_t sums = GNW * 2 * 4 * 64 * 4, codes = plan.fuse_x ? (size_t)p.rmax * ((a.K + KC - 1) / KC) * KC : 0;
+    const size_t lds = codes > sums ? codes : sums;
+    if (!plan.fuse_x) {
+        hipLaunchKernelGGL((moe_few_gate_kernel<false, false, 0>), grid, dim3(64 * GNW), lds, stream, p);
+        return hipGetLastError();
+    }
+#define CONVROT_GATE(lg, f32)                                   \
+    if (f32) launch_gate<true, lg>(p, grid, lds, stream);       \
+    else launch_gate<false, lg>(p, grid, lds, stream)
+    CONVROT_LOG2G(CONVROT_GATE, a.x_f32)
+#undef CONVROT_GATE
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_few_down(const MoeFewArgs &a, const MoeFew &plan, hipStream_t stream)
+{
+    FewParams p = {};
+    p.experts = a.experts;
+    p.weights = a.weights;
+    p.x = a.h;
+    p.q = a.hq;
+    p.qs = a.hs;
+    p.w1 = a.wq_down;
+    p.s1 = a.down_scale;
+    p.residual = a.residual;
+    p.out = a.y;
+    p.S = (int)a.M * a.top;
+    p.E = a.E;
+    p.top = a.top;
+    p.K = a.K;
+    p.F = a.F;
+    const int log2g = a.log2g_h;
+    p.g = rotation(log2g);
+    const dim3 grid((unsigned)(a.K / 16)), block(64 * DNW);
+    const size_t lds = plan.fuse_h ? (size_t)p.S * ((a.F + KC - 1) / KC) * KC : 0;
+    if (!plan.fuse_h) {
+        hipLaunchKernelGGL((moe_few_down_kernel<false, 0>), grid, block, 0, stream, p);
+        return hipGetLastError();
+    }
+#define CONVROT_DOWN(lg, unused) hipLaunchKernelGGL((moe_few_down_kernel<true, lg>), grid, block, lds, stream, p)
+    CONVROT_LOG2G(CONVROT_DOWN, 0)
+#undef CONVROT_DOWN
+    return hipGetLastError();
+}
+
+#undef CONVROT_LOG2G
+
+} // namespace convrot

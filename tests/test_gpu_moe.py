@@ -220,6 +220,34 @@ def test_moe_ffn_gated(cr, M, top, E, F, K, gh, g, kind):
                 assert torch.equal(y[M // 2], res[M // 2])
 
 
+FEW = [(1, 8, 64), (2, 8, 16), (3, 4, 4), (4, 32, 40), (8, 8, 64), (16, 8, 24), (13, 1, 3), (128, 1, 5), (64, 2, 2), (43, 3, 700)]
+
+
+@pytest.mark.parametrize("kind", ["mixed", "twice", "one", "dropped", "none"])
+@pytest.mark.parametrize("M,top,E", FEW)
+def test_moe_ffn_gated_few_slots(cr, M, top, E, kind):
+    """At most 128 slots take kernels of their own; nothing saved, they give the other path's bits.  The rotation groups
+    go through all sizes, the widths through whole and part 256-channel pieces and more pieces than wavefronts."""
+    experts, w = _experts(M, top, E, M + top, kind)
+    for i, (F, K, gh, g) in enumerate([(64, 64, 1, 2), (128, 320, 4, 8), (192, 1088, 16, 32), (320, 2688, 64, 128), (2304, 512, 256, 256)]):
+        if E > 100 and i != M % 5:
+            continue
+        P.say("moe few M=%d top=%d E=%d F=%d K=%d %s" % (M, top, E, F, K, kind))
+        gate, up, down = _layer(cr, E, F, K, gh, g)
+        for dtype in (torch.bfloat16, torch.float32):
+            x, res = _randn(M, K, seed=M + i, dtype=dtype), _randn(M, K, seed=M + 1, std=0.5)
+            x[M // 2] *= 1e-37 if dtype is torch.float32 else 1.0
+            x[M // 3] = 0
+            call = dict(act=R.ACTS[i % 5], group=g, group_h=gh)
+            for r in (res, None):
+                want = cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, residual=r, save=True, **call)[0]
+                assert torch.equal(cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, residual=r, **call), want)
+        place = x.bfloat16()                                     # y in the place of x
+        want = cr.moe_ffn_gated(place, experts, w, *gate, *up, *down, residual=res, save=True, **call)[0]
+        assert cr.moe_ffn_gated(place, experts, w, *gate, *up, *down, residual=res, out=place, **call) is place
+        assert torch.equal(place, want)
+
+
 def test_moe_ffn_gated_keeps_rows_without_an_expert(cr):
     """pre and d of slots without an expert are left as they were."""
     M, top, E, F, K = 20, 3, 4, 64, 128
