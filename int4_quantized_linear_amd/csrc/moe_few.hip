@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
         for (int kk = 0; kk < 4; ++kk) {
             const int k = KC * c + 64 * kk;
             const uint32_t off = k < K ? (uint32_t)(r * K + k + 16 * q) : OOB;
-            b[0][kk] = __builtin_amdgcn_raw_buffer_load_b128(rg, off, 0, 2);
-            b[1][kk] = __builtin_amdgcn_raw_buffer_load_b128(ru, off, 0, 2);
+            b[0][kk] = __builtin_amdgcn_raw_buffer_load_b128(rg, off, 0, 0);
+            b[1][kk] = __builtin_amdgcn_raw_buffer_load_b128(ru, off, 0, 0);
         }
     };
     for (int first = 0; first < count; first += p.rmax) {
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
                 }
             }
         };
-        float sx;
+        float sx = FUSED ? 0.0f : p.qs[slot / p.top];
         if constexpr (FUSED) {
             if (threadIdx.x < 16) maxima[threadIdx.x] = 0u;
             __syncthreads();
@@ -275,7 +275,6 @@ __global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
         } else {
 #pragma unroll
             for (int i = 0; i < GP; ++i) load_rows(xb[i], w + GNW * i);
-            sx = p.qs[slot / p.top];
         }
         v4i acc[2] = {};
         for (int c0 = w; c0 < SL; c0 += GNW * GP) {
@@ -293,6 +292,7 @@ __global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
                 }
                 load_weights(wb[i], c0 + GNW * (i + GP));
                 load_rows(xb[i], c0 + GNW * (i + GP));
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         // lane: column r, features 4 q + v
@@ -318,9 +318,10 @@ __global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
 }
 
 // ---------------------------------------------------------------------------------------------
-// y: workgroup = 16 output channels.  The experts' products are items, cut into `parts` along F where there are fewer than
-// wavefronts; wavefront w takes items w, w + NW, ...  and adds its int32 sums to the slots' in LDS (exact in any order).  Then a
-// thread per token and channel scales, weighs and adds up its slots in their order.
+// y: workgroup = 16 output channels, all experts.  A list in LDS holds the experts' products, at most 16 slots each; each
+// is cut along F into `parts` of CP chunks, so that 8 wavefronts have about 4 each, and wavefront w takes pieces w, w + 8, ...
+// It adds its int32 sums to the slots' in LDS (exact in any order).  Then a thread per token and channel scales,
+// weighs and adds up its slots in their order; what that needs from memory is requested at the start.
 constexpr int DNW = 8, DP = 4;
 
 template <bool FUSED, int LG>
@@ -328,135 +329,136 @@ __global__ void __launch_bounds__(64 * DNW) moe_few_down_kernel(FewParams p)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];       // FUSED: codes of h
     __shared__ int32_t sums[MAX_SLOTS][16];
+    __shared__ float factor[MAX_SLOTS][16];              // down scales of each slot's expert
     __shared__ uint32_t maxima[MAX_SLOTS];
-    __shared__ float scales[MAX_SLOTS];
+    __shared__ float scales[MAX_SLOTS], share[MAX_SLOTS];
+    __shared__ int expert_of[MAX_SLOTS];                 // of a slot
+    __shared__ int list_expert[MAX_SLOTS], list_count[MAX_SLOTS];
+    __shared__ uint8_t list_slot[MAX_SLOTS][16];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int F = p.F, SL = (F + KC - 1) / KC, stride = KC * SL;
     const int n0 = 16 * (int)blockIdx.x;
     const Slots t(p.experts, p.S, p.E);
-    for (int i = threadIdx.x; i < p.S * 16; i += 64 * DNW) sums[0][i] = 0;
-    if constexpr (FUSED) {
-        if ((int)threadIdx.x < p.S) maxima[threadIdx.x] = 0u;
-    }
-
-    // Walks this wavefront's chunks: of every expert in order of first slot, each block of 16 of its slots, each part.
-    struct Walk {
-        uint64_t r0, r1, m0, m1;                         // slots not yet walked; the expert's
-        int e, first, count, item, part, c, end;         // c >= end: done
-    };
-    int parts = 1;
-    auto next_item = [&](Walk &k) {
-        do {
-            if (++k.part == parts) {
-                k.part = 0;
-                k.first += 16;
-            }
-            if (k.first >= k.count) {
-                if (!(k.r0 | k.r1)) {
-                    k.c = k.end = 0;
-                    return;
+    // the list: every wavefront walks the experts in the order of their first slots, wavefront 0 writes
+    int items = 0;
+    for (uint64_t r0 = t.v0, r1 = t.v1; r0 | r1;) {
+        const int e = t.expert(r0 ? __builtin_ctzll(r0) : 64 + __builtin_ctzll(r1));
+        const uint64_t m0 = __builtin_amdgcn_ballot_w64(t.e0 == e), m1 = __builtin_amdgcn_ballot_w64(t.e1 == e);
+        r0 &= ~m0;
+        r1 &= ~m1;
+        const int count = __builtin_popcountll(m0) + __builtin_popcountll(m1);
+        for (int first = 0; first < count; first += 16, ++items) {
+            if (w == 0) {
+                const int n = min(count - first, 16), slot = __shfl(slot_of_rank(m0, m1, first), min(r, n - 1));
+                if (lane < 16) list_slot[items][lane] = (uint8_t)slot;
+                if (lane == 0) {
+                    list_expert[items] = e;
+                    list_count[items] = n;
                 }
-                k.e = t.expert(k.r0 ? __builtin_ctzll(k.r0) : 64 + __builtin_ctzll(k.r1));
-                k.m0 = __builtin_amdgcn_ballot_w64(t.e0 == k.e);
-                k.m1 = __builtin_amdgcn_ballot_w64(t.e1 == k.e);
-                k.r0 &= ~k.m0;
-                k.r1 &= ~k.m1;
-                k.first = 0;
-                k.count = __builtin_popcountll(k.m0) + __builtin_popcountll(k.m1);
             }
-        } while (k.item++ % DNW != w);
-        k.c = SL * k.part / parts;
-        k.end = SL * (k.part + 1) / parts;
-    };
-    auto start = [&] {
-        Walk k = {t.v0, t.v1, 0, 0, 0, 0, 0, 0, parts - 1, 0, 0};
-        next_item(k);
-        return k;
-    };
-    {
-        int distinct = 0;
-        for (uint64_t r0 = t.v0, r1 = t.v1; r0 | r1; ++distinct) {
-            const int e = t.expert(r0 ? __builtin_ctzll(r0) : 64 + __builtin_ctzll(r1));
-            r0 &= ~__builtin_amdgcn_ballot_w64(t.e0 == e);
-            r1 &= ~__builtin_amdgcn_ballot_w64(t.e1 == e);
         }
-        while (distinct * parts < DNW && 2 * parts <= SL) parts *= 2;
     }
+    if (w == 0) {
+        expert_of[lane] = t.e0;
+        expert_of[64 + lane] = t.e1;
+    }
+    for (int i = threadIdx.x; i < p.S * 16; i += 64 * DNW) sums[0][i] = 0;
+    if ((int)threadIdx.x < p.S) {
+        share[threadIdx.x] = p.weights[threadIdx.x];
+        if constexpr (FUSED) maxima[threadIdx.x] = 0u;
+        else scales[threadIdx.x] = p.qs[threadIdx.x];
+    }
+    __syncthreads();
+    int CP = (items * SL + 4 * DNW - 1) / (4 * DNW);
+    CP = min(max(CP, 1), SL);
+    const int parts = (SL + CP - 1) / CP, pieces = items * parts;
+
     const __amdgpu_buffer_rsrc_t rq = uniform_rsrc(reinterpret_cast<uint64_t>(p.q), NUM_RECORDS);
-    Walk ld = start();
-    int ld_slot = 0;                                     // of this lane's column
+    // A place in this wavefront's walk: piece (item, part) and chunk of the part; past the last piece: nothing.
+    struct Place {
+        int item, part, c;
+    };
+    auto step = [&](Place &k) {
+        if (++k.c < CP) return;
+        k.c = 0;
+        k.part += DNW;
+        while (k.part >= parts && k.item < items) {
+            k.part -= parts;
+            ++k.item;
+        }
+    };
+    Place at = {0, w, 0};
+    while (at.part >= parts && at.item < items) {
+        at.part -= parts;
+        ++at.item;
+    }
+    Place ld = at;
     auto load = [&](v4u (&wb)[4], v4u (&xb)[4]) {
-        const bool any = ld.c < ld.end;
+        const bool any = ld.item < items;
+        const int i = any ? ld.item : 0, c = ld.part * CP + ld.c;
+        const int e = __builtin_amdgcn_readfirstlane(list_expert[i]);
         const __amdgpu_buffer_rsrc_t rw =
-            uniform_rsrc(reinterpret_cast<uint64_t>(p.w1 + ((int64_t)ld.e * p.K + n0) * F), any ? 16 * F : 0);
+            uniform_rsrc(reinterpret_cast<uint64_t>(p.w1 + ((int64_t)e * p.K + n0) * F), any ? 16 * F : 0);
+        const uint32_t row = FUSED ? 0u : (uint32_t)list_slot[i][r] * (uint32_t)F;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-            const int k = KC * ld.c + 64 * kk;
+            const int k = KC * c + 64 * kk;
             const uint32_t off = k < F ? (uint32_t)(k + 16 * q) : OOB;
-            wb[kk] = __builtin_amdgcn_raw_buffer_load_b128(rw, (uint32_t)(r * F) + off, 0, 2);
-            if constexpr (!FUSED)
-                xb[kk] = __builtin_amdgcn_raw_buffer_load_b128(rq, any ? (uint32_t)(ld_slot * F) + off : OOB, 0, 0);
+            wb[kk] = __builtin_amdgcn_raw_buffer_load_b128(rw, (uint32_t)(r * F) + off, 0, 0);
+            if constexpr (!FUSED) xb[kk] = __builtin_amdgcn_raw_buffer_load_b128(rq, any ? row + off : OOB, 0, 0);
         }
-        if (any && ++ld.c == ld.end) {
-            next_item(ld);
-            if (!FUSED && ld.c < ld.end)
-                ld_slot = __shfl(slot_of_rank(ld.m0, ld.m1, ld.first), min(r, min(ld.count - ld.first, 16) - 1));
-        }
+        step(ld);
+        __builtin_amdgcn_sched_barrier(0);
     };
     v4u wb[DP][4], xb[DP][4];
-    Walk at = ld;
-    int n_at = 0, slot = 0;
-    auto enter = [&] {                                   // the compute side's next item
-        n_at = min(at.count - at.first, 16);
-        if (at.c < at.end) slot = __shfl(slot_of_rank(at.m0, at.m1, at.first), min(r, n_at - 1));
-    };
-    enter();
-    ld_slot = slot;
+    if (pieces > 0) {
 #pragma unroll
-    for (int i = 0; i < DP; ++i) load(wb[i], xb[i]);
-    __syncthreads();
+        for (int i = 0; i < DP; ++i) load(wb[i], xb[i]);
+    }
+    for (int i = threadIdx.x; i < p.S * 16; i += 64 * DNW) {
+        const int e = expert_of[i >> 4];
+        factor[0][i] = e < 0 ? 0.0f : p.s1[(int64_t)e * p.K + n0 + (i & 15)];
+    }
     if constexpr (FUSED) quantize_rows<false, LG, DNW>(p.x, [&](int row) { return (int64_t)row * F; }, p.S, F, p.g, smem, stride,
                                                        maxima, scales);
     v4i acc = {};
-    while (at.c < at.end) {
+    while (at.item < items) {
 #pragma unroll
         for (int i = 0; i < DP; ++i) {
-            const bool any = at.c < at.end;
+            const bool any = at.item < items;
+            const int item = any ? at.item : 0, slot = list_slot[item][r], c = at.part * CP + at.c;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
                 if constexpr (FUSED)
-                    xb[i][kk] = *reinterpret_cast<const v4u *>(smem + code_at(slot, stride, any ? at.c : 0, 4 * kk + q));
+                    xb[i][kk] = *reinterpret_cast<const v4u *>(smem + code_at(slot, stride, any ? min(c, SL - 1) : 0, 4 * kk + q));
                 acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, wb[i][kk]), __builtin_bit_cast(v4i, xb[i][kk]),
                                                             acc, 0, 0, 0);
             }
-            load(wb[i], xb[i]);
-            if (any && ++at.c == at.end) {
-                if (r < n_at) {
+            if (any && at.c == CP - 1) {
+                if (r < list_count[item]) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) atomicAdd(&sums[slot][4 * q + v], acc[v]);
                 }
                 acc = v4i{};
-                next_item(at);
-                enter();
             }
+            step(at);
+            load(wb[i], xb[i]);
         }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < p.S / p.top * 16; i += 64 * DNW) {
         const int m = i >> 4, n = i & 15;
+        const int64_t o = (int64_t)m * p.K + n0 + n;
+        const float res = p.residual ? bf16lo_to_f32(p.residual[o]) : 0.0f;
         float v = 0.0f;
         for (int j = 0; j < p.top; ++j) {
-            const int s = m * p.top + j, e = p.experts[s];
-            if ((unsigned)e >= (unsigned)p.E) continue;
-            const float sh = FUSED ? scales[s] : p.qs[s];
-            const float d = __builtin_fmaf((float)sums[s][n], sh * p.s1[(int64_t)e * p.K + n0 + n], 0.0f);
-            v = __builtin_fmaf(p.weights[s], d, v);
+            const int s = m * p.top + j;
+            const float d = __builtin_fmaf((float)sums[s][n], scales[s] * factor[s][n], 0.0f);
+            v = __builtin_fmaf(expert_of[s] < 0 ? 0.0f : share[s], expert_of[s] < 0 ? 0.0f : d, v);
         }
-        const int64_t o = (int64_t)m * p.K + n0 + n;
-        if (p.residual) v += bf16lo_to_f32(p.residual[o]);
-        p.out[o] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
+        p.out[o] = (uint16_t)(pack_bf16x2(v + res, 0.0f) & 0xffffu);
     }
 }
 
