@@ -161,7 +161,7 @@ hipError_t launch_grouped_grad(const GroupedGradArgs &g, hipStream_t stream);
 hipError_t launch_moe_combine(const float *part, const int32_t *row_of, const float *weights, const uint16_t *residual,
                               uint16_t *y, int64_t M, int K, int top, hipStream_t stream);
 
-// The expert layer for at most 128 slots (moe_few.hip), nothing saved: plan_moe_few says whether it takes the call and which of
+// The expert layer for at most 64 slots (moe_few.hip), nothing saved: plan_moe_few says whether it takes the call and which of
 // the two kernels quantizes its rows itself; where one does not, its codes and scales (xq, xs of the tokens; hq, hs of h's
 // slots) are made by launch_rotate_quant before it.
 struct MoeFew {

@@ -1,10 +1,10 @@
-// moe_few.hip -- the gated expert layer for a few tokens (at most 128 slots): two kernels, or up to two more that quantize
+// moe_few.hip -- the gated expert layer for a few tokens (at most 64 slots): two kernels, or up to two more that quantize
 // (gfx950).
 //
 // With few tokens the layer is its experts' weights streamed once, and the launches around that.  Here
 //   moe_few_gate_kernel  h[slot] = bf16(act(g) u):  a workgroup per 16 features and expert
 //   moe_few_down_kernel  y = bf16(sum_j weight d + residual):  a workgroup per 16 output channels, all experts
-// find the experts' slots from the table of experts themselves (two slots per lane, ballots), and rotate and
+// find the experts' slots from the table of experts themselves (a slot per lane, ballots), and rotate and
 // quantize the rows they use themselves, into LDS, where that repeated work is short (FUSED): it runs while the
 // workgroup's first weights arrive.  Otherwise the codes come from launch_rotate_quant.
 // The weights go from memory to the matrix core's operand registers: v_mfma_i32_16x16x64_i8 takes 16 rows (lane % 16) of 64
@@ -20,76 +20,67 @@
 namespace convrot {
 namespace {
 
-constexpr int MAX_SLOTS = 128;
+constexpr int MAX_SLOTS = 64;
 constexpr int KC = 256;                                  // bytes of a row per chunk
 
-// The table of experts, two slots per lane: slot l in a lane's first, slot 64 + l in its second entry (-1: none).
-struct Slots {
-    int e0, e1;
-    uint64_t v0, v1;                                     // slots with an expert
-
-    __device__ __forceinline__ Slots(const int32_t *experts, int S, int E)
-    {
-        const int lane = threadIdx.x & 63;
-        e0 = lane < S ? experts[lane] : -1;
-        e1 = lane + 64 < S ? experts[lane + 64] : -1;
-        if ((unsigned)e0 >= (unsigned)E) e0 = -1;
-        if ((unsigned)e1 >= (unsigned)E) e1 = -1;
-        v0 = __builtin_amdgcn_ballot_w64(e0 >= 0);
-        v1 = __builtin_amdgcn_ballot_w64(e1 >= 0);
-    }
-    __device__ __forceinline__ int expert(int slot) const
-    {
-        const int a = __builtin_amdgcn_readlane(e0, slot & 63), b = __builtin_amdgcn_readlane(e1, slot & 63);
-        return slot < 64 ? a : b;
-    }
-};
-
-// Index of the set bit number i (from 0) of m0, then m1, for i < their count, in lane i; any number in other lanes.
-// Every set bit's lane sends its own number to the lane of its rank (from 64 on: nowhere that is read).
-__device__ __forceinline__ int slot_of_rank(uint64_t m0, uint64_t m1, int first)
+// The expert of slot `lane`, -1 without one (or without a slot).
+__device__ __forceinline__ int expert_of_lane(const int32_t *experts, int S, int E)
 {
     const int lane = threadIdx.x & 63;
-    const int below0 = __builtin_amdgcn_mbcnt_hi((uint32_t)(m0 >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m0, 0));
-    const int below1 = __builtin_amdgcn_mbcnt_hi((uint32_t)(m1 >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m1, 0));
-    const int n0 = __builtin_popcountll(m0);
-    const int r0 = below0 - first, r1 = n0 + below1 - first;
-    const bool in0 = (m0 >> lane & 1) && r0 >= 0 && r0 < 16, in1 = (m1 >> lane & 1) && r1 >= 0 && r1 < 16;
-    const int a = __builtin_amdgcn_ds_permute(4 * (in0 ? r0 : 63), lane);
-    const int b = __builtin_amdgcn_ds_permute(4 * (in1 ? r1 : 63), lane + 64);
-    return lane + first < n0 ? a : b;
+    const int e = lane < S ? experts[lane] : -1;
+    return (unsigned)e < (unsigned)E ? e : -1;
 }
 
-// One unit of rotation, 256 channels jj of a row, in the 8 lanes of a slot (rotate_common.hpp).
-template <bool F32, int LG>
-__device__ __forceinline__ void rotated(const void *x, int64_t row0, int K, int jj, bool ok, float (&v)[4][8])
+__device__ __forceinline__ int bits_below(uint64_t m)
 {
-    const int lane = threadIdx.x & 63, qd = lane & 3, h = lane >> 5;
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
+// The set bit number first + i of m, for i < min(16, their count - first), in lane i; any number in other lanes.  Every set
+// bit's lane sends its own number to the lane of its rank (others to lane 63, where nobody looks).
+__device__ __forceinline__ int slot_of_rank(uint64_t m, int first)
+{
+    const int lane = threadIdx.x & 63, rank = bits_below(m) - first;
+    return __builtin_amdgcn_ds_permute(4 * ((m >> lane & 1) && rank >= 0 && rank < 16 ? rank : 63), lane);
+}
+
+// One unit of rotation, 256 channels jj of a row, in the 8 lanes of a slot (rotate_common.hpp): requested, and rotated.
+template <bool F32>
+struct Unit {
+    v4u raw[4][F32 ? 2 : 1];
+    bool ok;
+
+    __device__ __forceinline__ void fetch(const void *x, int64_t row0, int K, int jj, bool in)
+    {
+        const int lane = threadIdx.x & 63, qd = lane & 3, h = lane >> 5;
+        ok = in;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int k = 256 * jj + 64 * r + 32 * h + 8 * qd;
-        const bool in = ok && k < K;
-        const int64_t at = in ? row0 + k : 0;
-        if constexpr (F32) {
-            const v4f *src = reinterpret_cast<const v4f *>(static_cast<const float *>(x) + at);
-            const v4f a = src[0], b = src[1];
+        for (int r = 0; r < 4; ++r) {
+            const int k = 256 * jj + 64 * r + 32 * h + 8 * qd;
+            const int64_t at = in && k < K ? row0 + k : 0;           // others read something that is there
+            const v4u *src = reinterpret_cast<const v4u *>(static_cast<const uint8_t *>(x) + at * (F32 ? 4 : 2));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[r][e] = in ? a[e] : 0.0f;
-                v[r][e + 4] = in ? b[e] : 0.0f;
-            }
-        } else {
-            v4u d = *reinterpret_cast<const v4u *>(static_cast<const uint16_t *>(x) + at);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t p = in ? d[e] : 0u;
-                v[r][2 * e] = bf16lo_to_f32(p);
-                v[r][2 * e + 1] = bf16hi_to_f32(p);
-            }
+            for (int i = 0; i < (F32 ? 2 : 1); ++i) raw[r][i] = src[i];
         }
     }
-    fwht_slot<LG>(v, qd);
-}
+    template <int LG>
+    __device__ __forceinline__ void rotate(int K, int jj, float (&v)[4][8])
+    {
+        const int lane = threadIdx.x & 63, qd = lane & 3, h = lane >> 5;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const bool in = ok && 256 * jj + 64 * r + 32 * h + 8 * qd < K;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float f;
+                if constexpr (F32) f = __uint_as_float(raw[r][e >> 2][e & 3]);
+                else f = e & 1 ? bf16hi_to_f32(raw[r][0][e >> 1]) : bf16lo_to_f32(raw[r][0][e >> 1]);
+                v[r][e] = in ? f : 0.0f;
+            }
+        }
+        fwht_slot<LG>(v, qd);
+    }
+};
 
 __device__ __forceinline__ float slot_max(const float (&v)[4][8])
 {
@@ -160,34 +151,50 @@ __device__ __forceinline__ void store_codes(float (&v)[4][8], float sc, const Ro
 
 // Rows 0 .. n - 1 (row r from element start(r) of x) to codes and scales in LDS, by a workgroup of NW wavefronts; all of it
 // calls.  maxima: n words, zeroed.  A wavefront rotates 8 units at a time; its first stay in registers until the
-// rows' maxima are known, later ones are rotated again.
-template <bool F32, int LG, int NW, typename Start>
+// rows' maxima are known, later ones are rotated again.  requested(): called once the first units are on their way.
+template <bool F32, int LG, int NW, typename Start, typename Requested>
 __device__ __forceinline__ void quantize_rows(const void *x, Start start, int n, int K, const Rotation &g, uint8_t *codes, int stride,
-                                              uint32_t *maxima, float *scales)
+                                              uint32_t *maxima, float *scales, Requested requested)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, sl = (lane >> 2) & 7;
     const bool lead = (lane & 3) == 0 && lane < 32;
     const int SL = (K + KC - 1) / KC, units = n * SL;
+    Unit<F32> unit;
     float kept[4][8];
-    for (int u0 = 8 * w; u0 < units; u0 += 8 * NW) {
-        const int u = u0 + sl, row = u < units ? u / SL : 0;
-        float v[4][8];
-        rotated<F32, LG>(x, start(row), K, u - row * SL, u < units, v);
+    auto place = [&](int u0, int &row, int &jj) {
+        const int u = u0 + sl;
+        row = u < units ? u / SL : 0;
+        jj = u - row * SL;
+        return u < units;
+    };
+    auto maximum = [&](const float (&v)[4][8], int row, bool in) {
         const float m = slot_max(v);
-        if (lead && u < units) atomicMax(&maxima[row], __float_as_uint(m));
-        if (u0 == 8 * w) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) kept[r][e] = v[r][e];
-        }
+        if (lead && in) atomicMax(&maxima[row], __float_as_uint(m));
+    };
+    int row, jj;
+    const bool first = place(8 * w, row, jj);
+    unit.fetch(x, start(row), K, jj, first);
+    __builtin_amdgcn_sched_barrier(0);
+    requested();
+    __builtin_amdgcn_sched_barrier(0);
+    unit.template rotate<LG>(K, jj, kept);
+    maximum(kept, row, first);
+    for (int u0 = 8 * (w + NW); u0 < units; u0 += 8 * NW) {
+        float v[4][8];
+        const bool in = place(u0, row, jj);
+        unit.fetch(x, start(row), K, jj, in);
+        unit.template rotate<LG>(K, jj, v);
+        maximum(v, row, in);
     }
     __syncthreads();
     for (int u0 = 8 * w; u0 < units; u0 += 8 * NW) {
-        const int u = u0 + sl, row = u < units ? u / SL : 0, jj = u - row * SL;
-        if (u0 != 8 * w) rotated<F32, LG>(x, start(row), K, jj, u < units, kept);
+        const bool in = place(u0, row, jj);
+        if (u0 != 8 * w) {
+            unit.fetch(x, start(row), K, jj, in);
+            unit.template rotate<LG>(K, jj, kept);
+        }
         const float sc = row_scale<LG>(__uint_as_float(maxima[row]), g);
-        if (u < units) {
+        if (in) {
             store_codes<LG>(kept, sc, g, codes, row, stride, jj);
             if (jj == 0 && lead) scales[row] = sc;
         }
@@ -210,108 +217,120 @@ struct FewParams {
 };
 
 // ---------------------------------------------------------------------------------------------
-// h: workgroup (feature tile, slot); the first slot of each expert does the expert's work, the others end.  4 wavefronts take
-// every fourth chunk of K for 16 rows of gate and 16 of up; their sums meet in LDS.
-constexpr int GNW = 4, GP = 3;
+// h: workgroup (x, slot); the first slot of each expert does the expert's work, the others end.  It takes the tiles x,
+// x + gridDim.x, ... of 16 features, so that the rows are quantized once for several; 4 wavefronts take every fourth chunk of K
+// for 16 rows of gate and 16 of up, GP chunks in flight across tiles, and their sums meet in LDS.
+constexpr int GNW = 4, GP = 3, GSUMS = GNW * 2 * 4 * 64;
 
 template <bool FUSED, bool F32, int LG>
 __global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
 {
-    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];       // codes, then the sums
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];       // two tiles' sums, then the codes
     __shared__ uint32_t maxima[16];
     __shared__ float scales[16];
+    int32_t *red = reinterpret_cast<int32_t *>(smem);
+    uint8_t *codes = smem + 2 * GSUMS * 4;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int K = p.K, SL = (K + KC - 1) / KC, stride = KC * SL;
-    const Slots t(p.experts, p.S, p.E);
-    const int s = blockIdx.y, e = t.expert(s);
+    const int mine = expert_of_lane(p.experts, p.S, p.E);
+    const int s = blockIdx.y, e = __builtin_amdgcn_readlane(mine, s);
     if (e < 0) return;
-    const uint64_t m0 = __builtin_amdgcn_ballot_w64(t.e0 == e), m1 = __builtin_amdgcn_ballot_w64(t.e1 == e);
-    if ((m0 ? __builtin_ctzll(m0) : 64 + __builtin_ctzll(m1)) != s) return;
-    const int count = __builtin_popcountll(m0) + __builtin_popcountll(m1);
-    const int f0 = 16 * (int)blockIdx.x;
-    // this thread's output: row r of the pass, feature f0 + 4 q + w
-    const int64_t fs = (int64_t)e * p.F + f0 + 4 * q + w;
-    const float sg = p.s1[fs], su = p.s2[fs];
-    const int64_t w0 = ((int64_t)e * p.F + f0) * K;
-    const __amdgpu_buffer_rsrc_t rg = uniform_rsrc(reinterpret_cast<uint64_t>(p.w1 + w0), 16 * K);
-    const __amdgpu_buffer_rsrc_t ru = uniform_rsrc(reinterpret_cast<uint64_t>(p.w2 + w0), 16 * K);
+    const uint64_t of = __builtin_amdgcn_ballot_w64(mine == e);          // the expert's slots
+    if (__builtin_ctzll(of) != s) return;
+    const int count = __builtin_popcountll(of);
+    const int tiles = (p.F / 16 - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int CW = (SL + GNW - 1) / GNW, L = tiles * CW;                 // chunks per tile of a wavefront, in all
     const __amdgpu_buffer_rsrc_t rq = uniform_rsrc(reinterpret_cast<uint64_t>(p.q), NUM_RECORDS);
-    // chunk c's operands: rows r, bytes 256 c + 64 kk + 16 q (past K: zeros)
-    auto load_weights = [&](v4u (&b)[2][4], int c) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const int k = KC * c + 64 * kk;
-            const uint32_t off = k < K ? (uint32_t)(r * K + k + 16 * q) : OOB;
-            b[0][kk] = __builtin_amdgcn_raw_buffer_load_b128(rg, off, 0, 0);
-            b[1][kk] = __builtin_amdgcn_raw_buffer_load_b128(ru, off, 0, 0);
-        }
-    };
+    auto feature = [&](int tile) { return 16 * ((int)blockIdx.x + tile * (int)gridDim.x); };
     for (int first = 0; first < count; first += p.rmax) {
         const int n = min(count - first, p.rmax);
-        const int slots = slot_of_rank(m0, m1, first);
+        const int slots = slot_of_rank(of, first);
         const int slot = __shfl(slots, min(r, n - 1));   // of this lane's column
-        v4u wb[GP][2][4], xb[GP][4];
-#pragma unroll
-        for (int i = 0; i < GP; ++i) load_weights(wb[i], w + GNW * i);
         const uint32_t xrow = (uint32_t)(slot / p.top) * (uint32_t)K;
-        auto load_rows = [&](v4u (&b)[4], int c) {       // from memory; FUSED reads LDS when the chunk's turn comes
-            if constexpr (!FUSED) {
+        int ld_tile = 0, ld_c = 0;
+        // a chunk's operands: rows r, bytes 256 c + 64 kk + 16 q (past K, and past the last tile: zeros)
+        auto load = [&](v4u (&wb)[2][4], v4u (&xb)[4]) {
+            const bool any = ld_tile < tiles;
+            const int64_t at = ((int64_t)e * p.F + (any ? feature(ld_tile) : 0)) * K;
+            const __amdgpu_buffer_rsrc_t rg = uniform_rsrc(reinterpret_cast<uint64_t>(p.w1 + at), any ? 16 * K : 0);
+            const __amdgpu_buffer_rsrc_t ru = uniform_rsrc(reinterpret_cast<uint64_t>(p.w2 + at), any ? 16 * K : 0);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const int k = KC * c + 64 * kk;
-                    b[kk] = __builtin_amdgcn_raw_buffer_load_b128(rq, k < K ? xrow + (uint32_t)(k + 16 * q) : OOB, 0, 0);
-                }
+            for (int kk = 0; kk < 4; ++kk) {
+                const int k = KC * (w + GNW * ld_c) + 64 * kk;
+                const uint32_t off = k < K ? (uint32_t)(k + 16 * q) : OOB;
+                wb[0][kk] = __builtin_amdgcn_raw_buffer_load_b128(rg, (uint32_t)(r * K) + off, 0, 0);
+                wb[1][kk] = __builtin_amdgcn_raw_buffer_load_b128(ru, (uint32_t)(r * K) + off, 0, 0);
+                if constexpr (!FUSED) xb[kk] = __builtin_amdgcn_raw_buffer_load_b128(rq, any ? xrow + off : OOB, 0, 0);
             }
+            if (++ld_c == CW) {
+                ld_c = 0;
+                ++ld_tile;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        v4u wb[GP][2][4], xb[GP][4];
+        auto begin = [&] {
+#pragma unroll
+            for (int i = 0; i < GP; ++i) load(wb[i], xb[i]);
         };
         float sx = FUSED ? 0.0f : p.qs[slot / p.top];
         if constexpr (FUSED) {
             if (threadIdx.x < 16) maxima[threadIdx.x] = 0u;
             __syncthreads();
-            quantize_rows<F32, LG, GNW>(p.x, [&](int row) { return (int64_t)(__shfl(slots, row) / p.top) * K; }, n, K, p.g, smem,
-                                        stride, maxima, scales);
+            quantize_rows<F32, LG, GNW>(p.x, [&](int row) { return (int64_t)(__shfl(slots, row) / p.top) * K; }, n, K, p.g, codes,
+                                        stride, maxima, scales, begin);
             sx = scales[min(r, n - 1)];
         } else {
-#pragma unroll
-            for (int i = 0; i < GP; ++i) load_rows(xb[i], w + GNW * i);
+            begin();
         }
+        // this thread's output of a tile: row r of the pass, feature 4 q + w
+        float sg = 0.0f, su = 0.0f;
+        int tile = 0, c = 0;
         v4i acc[2] = {};
-        for (int c0 = w; c0 < SL; c0 += GNW * GP) {
+        for (int x0 = 0; x0 < L; x0 += GP) {
 #pragma unroll
             for (int i = 0; i < GP; ++i) {
-                const int c = min(c0 + GNW * i, SL - 1); // past the end: weights are zeros
+                if (c == 0 && tile < tiles) {
+                    const int64_t fs = (int64_t)e * p.F + feature(tile) + 4 * q + w;
+                    sg = p.s1[fs];
+                    su = p.s2[fs];
+                }
+                const int cc = min(w + GNW * c, SL - 1); // past the end: weights are zeros
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     if constexpr (FUSED)
-                        xb[i][kk] = *reinterpret_cast<const v4u *>(smem + code_at(min(r, n - 1), stride, c, 4 * kk + q));
+                        xb[i][kk] = *reinterpret_cast<const v4u *>(codes + code_at(min(r, n - 1), stride, cc, 4 * kk + q));
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
                         acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, wb[i][b][kk]),
                                                                        __builtin_bit_cast(v4i, xb[i][kk]), acc[b], 0, 0, 0);
                 }
-                load_weights(wb[i], c0 + GNW * (i + GP));
-                load_rows(xb[i], c0 + GNW * (i + GP));
-                __builtin_amdgcn_sched_barrier(0);
+                load(wb[i], xb[i]);
+                if (++c < CW || tile >= tiles) continue;
+                // lane: column r, features 4 q + v
+                int32_t *to = red + (tile & 1) * GSUMS;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) to[((w * 2 + b) * 4 + v) * 64 + lane] = acc[b][v];
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // loads stay in flight
+                int32_t ga = 0, ua = 0;
+#pragma unroll
+                for (int j = 0; j < GNW; ++j) {
+                    ga += to[((j * 2 + 0) * 4 + w) * 64 + lane];
+                    ua += to[((j * 2 + 1) * 4 + w) * 64 + lane];
+                }
+                if (r < n) {
+                    const float gv = __builtin_fmaf((float)ga, sx * sg, 0.0f), uv = __builtin_fmaf((float)ua, sx * su, 0.0f);
+                    p.out[(int64_t)slot * p.F + feature(tile) + 4 * q + w] =
+                        (uint16_t)(pack_bf16x2(act_value(gv, p.act) * uv, 0.0f) & 0xffffu);
+                }
+                acc[0] = acc[1] = v4i{};
+                c = 0;
+                ++tile;
             }
-        }
-        // lane: column r, features 4 q + v
-        __syncthreads();                                 // the codes have been read
-        int32_t *red = reinterpret_cast<int32_t *>(smem);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) red[((w * 2 + b) * 4 + v) * 64 + lane] = acc[b][v];
-        __syncthreads();
-        int32_t ga = 0, ua = 0;
-#pragma unroll
-        for (int i = 0; i < GNW; ++i) {
-            ga += red[((i * 2 + 0) * 4 + w) * 64 + lane];
-            ua += red[((i * 2 + 1) * 4 + w) * 64 + lane];
-        }
-        if (r < n) {
-            const float gv = __builtin_fmaf((float)ga, sx * sg, 0.0f), uv = __builtin_fmaf((float)ua, sx * su, 0.0f);
-            p.out[(int64_t)slot * p.F + f0 + 4 * q + w] = (uint16_t)(pack_bf16x2(act_value(gv, p.act) * uv, 0.0f) & 0xffffu);
         }
         __syncthreads();
     }
@@ -319,10 +338,10 @@ __global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
 
 // ---------------------------------------------------------------------------------------------
 // y: workgroup = 16 output channels, all experts.  A list in LDS holds the experts' products, at most 16 slots each; each
-// is cut along F into `parts` of CP chunks, so that 8 wavefronts have about 4 each, and wavefront w takes pieces w, w + 8, ...
+// is cut along F into `parts` of CP chunks, so that 4 wavefronts have about 4 each, and wavefront w takes pieces w, w + 4, ...
 // It adds its int32 sums to the slots' in LDS (exact in any order).  Then a thread per token and channel scales,
 // weighs and adds up its slots in their order; what that needs from memory is requested at the start.
-constexpr int DNW = 8, DP = 4;
+constexpr int DNW = 4, DP = 4;
 
 template <bool FUSED, int LG>
 __global__ void __launch_bounds__(64 * DNW) moe_few_down_kernel(FewParams p)
@@ -334,37 +353,36 @@ __global__ void __launch_bounds__(64 * DNW) moe_few_down_kernel(FewParams p)
     __shared__ float scales[MAX_SLOTS], share[MAX_SLOTS];
     __shared__ int expert_of[MAX_SLOTS];                 // of a slot
     __shared__ int list_expert[MAX_SLOTS], list_count[MAX_SLOTS];
-    __shared__ uint8_t list_slot[MAX_SLOTS][16];
+    __shared__ __attribute__((aligned(16))) uint8_t list_slot[MAX_SLOTS][16];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int F = p.F, SL = (F + KC - 1) / KC, stride = KC * SL;
     const int n0 = 16 * (int)blockIdx.x;
-    const Slots t(p.experts, p.S, p.E);
-    // the list: every wavefront walks the experts in the order of their first slots, wavefront 0 writes
-    int items = 0;
-    for (uint64_t r0 = t.v0, r1 = t.v1; r0 | r1;) {
-        const int e = t.expert(r0 ? __builtin_ctzll(r0) : 64 + __builtin_ctzll(r1));
-        const uint64_t m0 = __builtin_amdgcn_ballot_w64(t.e0 == e), m1 = __builtin_amdgcn_ballot_w64(t.e1 == e);
-        r0 &= ~m0;
-        r1 &= ~m1;
-        const int count = __builtin_popcountll(m0) + __builtin_popcountll(m1);
-        for (int first = 0; first < count; first += 16, ++items) {
-            if (w == 0) {
-                const int n = min(count - first, 16), slot = __shfl(slot_of_rank(m0, m1, first), min(r, n - 1));
-                if (lane < 16) list_slot[items][lane] = (uint8_t)slot;
-                if (lane == 0) {
-                    list_expert[items] = e;
-                    list_count[items] = n;
-                }
-            }
+    const int mine = expert_of_lane(p.experts, p.S, p.E);
+    // The list, a slot per lane: how many earlier slots have its expert (rank), and the first of its 16 of them.
+    int rank = 0, start = lane;
+    for (int i = 0; i < p.S; ++i) {
+        const bool same = __builtin_amdgcn_readlane(mine, i) == mine && i < lane;
+        if (same && rank % 16 == 0) start = i;
+        rank += same;
+    }
+    if (rank % 16 == 0) start = lane;
+    const uint64_t starts = __builtin_amdgcn_ballot_w64(mine >= 0 && start == lane);
+    const int items = __builtin_popcountll(starts);
+    if (w == 0) {
+        const int item = __builtin_popcountll(starts & ((1ull << start) - 1));
+        expert_of[lane] = mine;
+        list_count[lane] = 0;
+        *reinterpret_cast<v4u *>(list_slot[lane]) = v4u{};
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (mine >= 0) {
+            list_expert[item] = mine;
+            list_slot[item][rank % 16] = (uint8_t)lane;
+            atomicAdd(&list_count[item], 1);
         }
     }
-    if (w == 0) {
-        expert_of[lane] = t.e0;
-        expert_of[64 + lane] = t.e1;
-    }
-    for (int i = threadIdx.x; i < p.S * 16; i += 64 * DNW) sums[0][i] = 0;
+    for (int i = threadIdx.x; i < p.S * 16; i += 64 * DNW) (&sums[0][0])[i] = 0;
     if ((int)threadIdx.x < p.S) {
         share[threadIdx.x] = p.weights[threadIdx.x];
         if constexpr (FUSED) maxima[threadIdx.x] = 0u;
@@ -413,16 +431,19 @@ __global__ void __launch_bounds__(64 * DNW) moe_few_down_kernel(FewParams p)
         __builtin_amdgcn_sched_barrier(0);
     };
     v4u wb[DP][4], xb[DP][4];
-    if (pieces > 0) {
+    auto begin = [&] {
+        if (pieces > 0) {
 #pragma unroll
-        for (int i = 0; i < DP; ++i) load(wb[i], xb[i]);
-    }
-    for (int i = threadIdx.x; i < p.S * 16; i += 64 * DNW) {
-        const int e = expert_of[i >> 4];
-        factor[0][i] = e < 0 ? 0.0f : p.s1[(int64_t)e * p.K + n0 + (i & 15)];
-    }
+            for (int i = 0; i < DP; ++i) load(wb[i], xb[i]);
+        }
+        for (int i = threadIdx.x; i < p.S * 16; i += 64 * DNW) {
+            const int e = expert_of[i >> 4];
+            (&factor[0][0])[i] = e < 0 ? 0.0f : p.s1[(int64_t)e * p.K + n0 + (i & 15)];
+        }
+    };
     if constexpr (FUSED) quantize_rows<false, LG, DNW>(p.x, [&](int row) { return (int64_t)row * F; }, p.S, F, p.g, smem, stride,
-                                                       maxima, scales);
+                                                       maxima, scales, begin);
+    else begin();
     v4i acc = {};
     while (at.item < items) {
 #pragma unroll
@@ -470,6 +491,8 @@ Rotation rotation(int log2g)
     g.cg_lo = (float)(1.0 / g.root - (double)g.cg);
     return g;
 }
+
+constexpr int GWG = 512;
 
 template <bool F32, int LG>
 void launch_gate(const FewParams &p, dim3 grid, size_t lds, hipStream_t stream)
@@ -522,9 +545,10 @@ hipError_t launch_moe_few_gate(const MoeFewArgs &a, const MoeFew &plan, hipStrea
     p.rmax = a.M < 16 ? (int)a.M : 16;
     const int log2g = a.log2g;
     p.g = rotation(log2g);
-    const dim3 grid((unsigned)(a.F / 16), (unsigned)p.S);
-    const size_t sums = GNW * 2 * 4 * 64 * 4, codes = plan.fuse_x ? (size_t)p.rmax * ((a.K + KC - 1) / KC) * KC : 0;
-    const size_t lds = codes > sums ? codes : sums;
+    // about GWG workgroups in all, each with as many tiles
+    const int used = p.S < a.E ? p.S : a.E, tiles = a.F / 16, wgs = used < GWG ? (GWG + used - 1) / used : 1;
+    const dim3 grid((unsigned)(tiles < wgs ? tiles : wgs), (unsigned)p.S);
+    const size_t lds = 2 * GSUMS * 4 + (plan.fuse_x ? (size_t)p.rmax * ((a.K + KC - 1) / KC) * KC : 0);
     if (!plan.fuse_x) {
         hipLaunchKernelGGL((moe_few_gate_kernel<false, false, 0>), grid, dim3(64 * GNW), lds, stream, p);
         return hipGetLastError();
