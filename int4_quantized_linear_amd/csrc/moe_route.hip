@@ -10,8 +10,8 @@
 // softmax), so they stay defined where every s is 0 in fp32.  They and their gradients are formed in 64 bits:
 // a handful of values per token, next to differences that cancel.
 //
-// One wavefront per token, PER logits per lane.  A choice is the largest (key, lowest index) over the wavefront, six
-// exchanges; the winner's lane drops it.  Bound by those exchanges: memory would take a quarter of the time.
+// One wavefront per token, PER logits per lane.  A choice is the largest key over the wavefront, by six DPP steps, and the
+// lowest index that has it, by ballots; the winner's lane drops it.
 #include "device_common.hpp"
 #include "launchers.hpp"
 
@@ -36,18 +36,66 @@ __device__ __forceinline__ float load_logit(const void *p, bool f32, int64_t i)
     return f32 ? static_cast<const float *>(p)[i] : bf16lo_to_f32(static_cast<const uint16_t *>(p)[i]);
 }
 
+// v of another lane by DPP control CTRL, `none` where that control has no source.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float none, float v)
+{
+    return __uint_as_float(dpp<CTRL, ROWS>(__float_as_uint(none), __float_as_uint(v)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double none, double v)
+{
+    const uint64_t a = __builtin_bit_cast(uint64_t, none), b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = dpp<CTRL, ROWS>((uint32_t)a, (uint32_t)b), hi = dpp<CTRL, ROWS>((uint32_t)(a >> 32), (uint32_t)(b >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
+__device__ __forceinline__ float last_lane(float v) { return __uint_as_float(last_lane(__float_as_uint(v))); }
+__device__ __forceinline__ double last_lane(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)last_lane((uint32_t)(b >> 32)) << 32 | last_lane((uint32_t)b));
+}
+
+// op over the wavefront, in every lane: within rows of 16 lanes by row_shr 1, 2, 4, 8, then row_bcast 15 and 31.  (Exchanges
+// through LDS take several times as long, and the choice is a chain of them.)
+template <typename T, typename Op>
+__device__ __forceinline__ T wave_all(T v, T none, Op op)
+{
+    v = op(v, dpp<0x111, 0xf>(none, v));
+    v = op(v, dpp<0x112, 0xf>(none, v));
+    v = op(v, dpp<0x114, 0xf>(none, v));
+    v = op(v, dpp<0x118, 0xf>(none, v));
+    v = op(v, dpp<0x142, 0xa>(none, v));
+    v = op(v, dpp<0x143, 0xc>(none, v));
+    return last_lane(v);
+}
 __device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v = __builtin_fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return wave_all(v, -__builtin_inff(), [](float a, float b) { return __builtin_fmaxf(a, b); });
 }
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v)
+__device__ __forceinline__ double wave_max(double v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-    return v;
+    return wave_all(v, -__builtin_inf(), [](double a, double b) { return fmax(a, b); });
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    return wave_all(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v)
+{
+    const uint32_t hi = wave_max((uint32_t)(v >> 32));
+    return (uint64_t)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+}
+__device__ __forceinline__ double wave_sum(double v)
+{
+    return wave_all(v, 0.0, [](double a, double b) { return a + b; });
 }
 
 // Unsigned integers in the order of the floats (-0 as 0; 0 for NaN and -inf, which no choice takes).
@@ -76,9 +124,7 @@ __device__ __forceinline__ double chosen_share(bool sigmoid, bool normalize, dou
         return sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)zmax) / z;
     }
     const double v = sigmoid ? log_sigmoid(l) : l;
-    double most = valid ? v : -__builtin_inf();
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) most = fmax(most, __shfl_xor(most, d));
+    const double most = wave_max(valid ? v : -__builtin_inf());
     const double e = valid ? exp(v - most) : 0.0;
     return e / wave_sum(e);
 }
@@ -128,32 +174,25 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_kernel(RouteParams p)
     int chosen = -1;                                     // lane j: the j-th expert
     float value = 0.0f;                                  // and its logit
     for (int j = 0; j < p.top; ++j) {
-        KEY best = 0u;
-        int at = 0;
+        KEY best = key[0];
 #pragma unroll
-        for (int r = 0; r < PER; ++r)
-            if (key[r] > best) {                         // the lowest index of equal ones
-                best = key[r];
-                at = 64 * r + lane;
-            }
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const KEY other = __shfl_xor(best, d);
-            const int oat = __shfl_xor(at, d);
-            if (other > best || (other == best && oat < at)) {
-                best = other;
-                at = oat;
-            }
-        }
+        for (int r = 1; r < PER; ++r) best = key[r] > best ? key[r] : best;
+        best = wave_max(best);
         if (best == 0u) break;                           // nothing left that may be chosen
+        int at = -1;                                     // the lowest index of equal ones
         float v = 0.0f;
 #pragma unroll
-        for (int r = 0; r < PER; ++r)
-            if (at == 64 * r + lane) {
-                key[r] = 0u;
-                v = l[r];
+        for (int r = PER - 1; r >= 0; --r) {
+            const uint64_t m = __builtin_amdgcn_ballot_w64(key[r] == best);
+            if (m) {
+                const int from = __builtin_ctzll(m);
+                at = 64 * r + from;
+                v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[r]), from));
             }
-        v = __shfl(v, at & 63);
+        }
+#pragma unroll
+        for (int r = 0; r < PER; ++r)
+            if (at == 64 * r + lane) key[r] = 0u;
         if (lane == j) {
             chosen = at;
             value = v;
@@ -232,8 +271,8 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_backward_kernel(RouteGra
     // in slot order, so that an expert chosen twice gets the same sum at every call
     const float df = (float)d;
     for (int j = 0; j < p.top; ++j) {
-        const int at = __shfl(chosen, j);
-        const float add = __shfl(df, j);
+        const int at = __builtin_amdgcn_readlane(chosen, j);
+        const float add = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(df), j));
 #pragma unroll
         for (int r = 0; r < PER; ++r)
             if (at == 64 * r + lane) out[r] += add;
