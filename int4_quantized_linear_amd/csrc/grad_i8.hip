@@ -15,7 +15,7 @@
 //      channels, whole groups), or in grad_join_kernel where tiles are split along n.
 // Grouped: rows sorted by group (expert), each through its own group's weight.  The operand then comes from
 // grad_rows_kernel, a tile holds rows of one group, nothing is split, and the result may also go to
-// fp32 rows that moe_combine_kernel adds up.
+// rows that moe_combine_kernel adds up.
 #include "activation.hpp"
 #include "device_common.hpp"
 #include "grouped_common.hpp"
@@ -50,7 +50,8 @@ struct GradParams {
     // Grouped (M rows in all, w1, w2 [groups, N, K], next's scales [groups, K]; tiles_m, T_dp and S unused):
     const int32_t *offsets;
     const int32_t *slot_of;    // the row of next.pre that a row has, or null: its own
-    float *rows_out;           // non-null: fp32 [M, K] instead of dx
+    uint16_t *part16;          // non-null: 16-bit rows [M, K] (pack_fixed16) instead of dx
+    float *part_scale;         // and their scales [M, K / 64]
     int groups;
 };
 
@@ -74,9 +75,10 @@ __device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float
         *reinterpret_cast<v4u *>(dst) = d;
     };
     int64_t o = (int64_t)m * p.K + c;
-    if (GROUPED && p.rows_out) {
-        *reinterpret_cast<v4f *>(p.rows_out + o) = v4f{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<v4f *>(p.rows_out + o + 4) = v4f{v[4], v[5], v[6], v[7]};
+    if (GROUPED && p.part16) {
+        float scale;                                     // (8 lanes take 64 channels of a row)
+        *reinterpret_cast<v4u *>(p.part16 + o) = pack_fixed16(v, scale);
+        if (c % 64 == 0) p.part_scale[o / 64] = scale;
         return;
     }
     if (!p.next.a) {
@@ -1163,7 +1165,8 @@ hipError_t launch_grouped_grad(const GroupedGradArgs &g, hipStream_t stream)
     p.w2 = g.wq2 ? g.wq2 : g.wq1;
     p.add = g.add;
     p.dx = g.dx;
-    p.rows_out = g.rows_out;
+    p.part16 = g.part;
+    p.part_scale = g.part_scale;
     p.lda = grouped_grad_lda(g.N) * (g.wq2 ? 2 : 1);
     p.M = (int)g.rows;
     p.N = (int)g.N;

@@ -28,12 +28,14 @@ struct OrderParams {
     int S, E, top;
 };
 
-template <int NT>
+// HELD > 0: at most 4 HELD slots per thread, requested at once and kept in registers between the two passes
+// (24576 slots of 64 experts: 14 us read twice, @@ so).
+template <int NT, int HELD>
 __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
 {
     __shared__ int2 part[NT / 64];
     const int t = (int)threadIdx.x, lane = t & 63, e = (int)blockIdx.x;
-    const int chunk = (((p.S + NT - 1) / NT) + 3) & ~3;
+    const int chunk = HELD ? 4 * HELD : (((p.S + NT - 1) / NT) + 3) & ~3;
     const int s0 = min(t * (int64_t)chunk, (int64_t)p.S), s1 = min(s0 + chunk, p.S);
     const bool none = e == p.E;
     // mine: of this expert (or of none); less: with a smaller one
@@ -41,7 +43,24 @@ __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
     auto less = [&](int x) { return (unsigned)x < (unsigned)e; };
     int n_mine = 0, n_less = 0;
     typedef v4i v4i_any __attribute__((aligned(4)));
+    v4i held[HELD ? HELD : 1];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const int s = s0 + 4 * i;
+        if (s + 4 <= s1) held[i] = *reinterpret_cast<const v4i_any *>(p.experts + s);
+        else
+#pragma unroll
+            for (int k = 0; k < 4; ++k) held[i][k] = s + k < s1 ? p.experts[s + k] : 0;
+    }
     auto each = [&](auto f) {
+        if constexpr (HELD > 0) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (s0 + 4 * i + k < s1) f(s0 + 4 * i + k, held[i][k]);
+            return;
+        }
         int s = s0;
         for (; s + 4 <= s1; s += 4) {
             const v4i x = *reinterpret_cast<const v4i_any *>(p.experts + s);
@@ -102,7 +121,8 @@ struct GroupedParams {
     const int8_t *wq, *wq2;    // [groups, N, K]
     const float *sw, *sw2;     // [groups, N]
     uint16_t *y;               // Plain: bf16 [rows, N]; Gated: bf16(act(g) u) [rows, N]
-    float *part;               // Part: fp32 [rows, N]
+    uint16_t *part;            // Part: 16-bit rows [rows, N]
+    float *part_scale;         // and their scales [rows, N / 64]
     uint16_t *pre;             // Gated: bf16 [2, pre_rows, N] or null
     uint16_t *d;               // Part: bf16 [slots, N] or null
     int64_t pre_rows;
@@ -303,9 +323,9 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
                 z8(ch, c1, z);
                 if constexpr (E == Epi::Bf16) store8<VEC>(p.y + row * p.N + n, n, p.N, z);
                 if constexpr (E == Epi::Part) {
-                    float *dst = p.part + row * p.N + n;
-                    *reinterpret_cast<v4f *>(dst) = v4f{z[0], z[1], z[2], z[3]};
-                    *reinterpret_cast<v4f *>(dst + 4) = v4f{z[4], z[5], z[6], z[7]};
+                    float scale;
+                    *reinterpret_cast<v4u *>(p.part + row * p.N + n) = pack_fixed16(z, scale);
+                    if (lcol == 0) p.part_scale[row * (p.N / 64) + n / 64] = scale;
                     if (p.d) store8<VEC>(p.d + to * p.N + n, n, p.N, z);
                 }
                 if constexpr (E == Epi::Gated) {
@@ -331,7 +351,8 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
 // A thread takes 8 channels of one token; all slots' parts are requested before the first is added, in slot
 // order.  Slots without an expert add nothing.
 struct CombineParams {
-    const float *part;         // [rows, K]
+    const uint16_t *part;      // 16-bit rows [rows, K]
+    const float *scale;        // [rows, K / 64]
     const int32_t *row_of;     // [M, top]
     const float *weights;      // [M, top], or null: 1
     const uint16_t *residual;  // bf16 [M, K] or null
@@ -353,29 +374,25 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(CombineParams p)
     float v[8] = {};
 #pragma unroll 1
     for (int j = 0; j < p.top; j += AHEAD) {
-        v4f a[AHEAD], b[AHEAD];
+        v4u a[AHEAD];
         float w[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            a[i] = b[i] = v4f{};
+            a[i] = v4u{};
             w[i] = 0.0f;
             if (j + i < p.top) {
-                const int row = p.row_of[m * p.top + j + i];
+                const int64_t row = p.row_of[m * p.top + j + i];
                 if (row >= 0) {
-                    const float *src = p.part + (int64_t)row * p.K + c;
-                    a[i] = *reinterpret_cast<const v4f *>(src);
-                    b[i] = *reinterpret_cast<const v4f *>(src + 4);
-                    w[i] = p.weights ? p.weights[m * p.top + j + i] : 1.0f;
+                    a[i] = *reinterpret_cast<const v4u *>(p.part + row * p.K + c);
+                    w[i] = p.scale[row * (p.K / 64) + c / 64];
+                    if (p.weights) w[i] *= p.weights[m * p.top + j + i];
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = __builtin_fmaf(w[i], a[i][e], v[e]);
-                v[e + 4] = __builtin_fmaf(w[i], b[i][e], v[e + 4]);
-            }
+            for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(w[i], fixed16(a[i][e >> 1], e & 1), v[e]);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += e & 1 ? bf16hi_to_f32(res[e >> 1]) : bf16lo_to_f32(res[e >> 1]);
@@ -449,8 +466,11 @@ hipError_t launch_moe_order(const int32_t *experts, int64_t S, int E, int top, c
     p.S = (int)S;
     p.E = E;
     p.top = top;
-    if (S <= 2048) hipLaunchKernelGGL(moe_order_kernel<256>, dim3(E + 1), dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL(moe_order_kernel<1024>, dim3(E + 1), dim3(1024), 0, stream, p);
+    const dim3 grid(E + 1);
+    if (S <= 1024) hipLaunchKernelGGL((moe_order_kernel<256, 1>), grid, dim3(256), 0, stream, p);
+    else if (S <= 8192) hipLaunchKernelGGL((moe_order_kernel<1024, 2>), grid, dim3(1024), 0, stream, p);
+    else if (S <= 32768) hipLaunchKernelGGL((moe_order_kernel<1024, 8>), grid, dim3(1024), 0, stream, p);
+    else hipLaunchKernelGGL((moe_order_kernel<1024, 0>), grid, dim3(1024), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -471,6 +491,7 @@ hipError_t launch_grouped_i8(const GroupedArgs &g, Epi epi, hipStream_t stream)
     p.sw2 = g.sw2;
     p.y = g.y;
     p.part = g.part;
+    p.part_scale = g.part_scale;
     p.pre = g.pre;
     p.d = g.d;
     p.pre_rows = g.rows;
@@ -492,18 +513,19 @@ hipError_t launch_grouped_i8(const GroupedArgs &g, Epi epi, hipStream_t stream)
         launch_rows<Epi::Gated, true>(p, bm, stream);
         break;
     default:
-        if (!vec) return hipErrorInvalidValue;
+        if (g.N % 64) return hipErrorInvalidValue;
         launch_rows<Epi::Part, true>(p, bm, stream);
     }
     return hipGetLastError();
 }
 
-hipError_t launch_moe_combine(const float *part, const int32_t *row_of, const float *weights, const uint16_t *residual,
-                              uint16_t *y, int64_t M, int K, int top, hipStream_t stream)
+hipError_t launch_moe_combine(const uint16_t *part, const float *part_scale, const int32_t *row_of, const float *weights,
+                              const uint16_t *residual, uint16_t *y, int64_t M, int K, int top, hipStream_t stream)
 {
     if (M <= 0) return hipSuccess;
     CombineParams p;
     p.part = part;
+    p.scale = part_scale;
     p.row_of = row_of;
     p.weights = weights;
     p.residual = residual;

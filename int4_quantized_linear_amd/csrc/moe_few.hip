@@ -212,6 +212,7 @@ struct FewParams {
     const float *s1, *s2;
     const uint16_t *residual;  // bf16 [tokens, K] or null
     uint16_t *out;             // h [S, F]; y [tokens, K]
+    uint16_t *saved;           // pre [2, S, F]; d [S, K]; or null
     Rotation g;
     int S, E, top, K, F, act, rmax;
 };
@@ -324,8 +325,13 @@ __global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
                 }
                 if (r < n) {
                     const float gv = __builtin_fmaf((float)ga, sx * sg, 0.0f), uv = __builtin_fmaf((float)ua, sx * su, 0.0f);
-                    p.out[(int64_t)slot * p.F + feature(tile) + 4 * q + w] =
-                        (uint16_t)(pack_bf16x2(act_value(gv, p.act) * uv, 0.0f) & 0xffffu);
+                    const int64_t o = (int64_t)slot * p.F + feature(tile) + 4 * q + w;
+                    p.out[o] = (uint16_t)(pack_bf16x2(act_value(gv, p.act) * uv, 0.0f) & 0xffffu);
+                    if (p.saved) {
+                        const uint32_t gu = pack_bf16x2(gv, uv);
+                        p.saved[o] = (uint16_t)(gu & 0xffffu);
+                        p.saved[o + (int64_t)p.S * p.F] = (uint16_t)(gu >> 16);
+                    }
                 }
                 acc[0] = acc[1] = v4i{};
                 c = 0;
@@ -477,7 +483,9 @@ __global__ void __launch_bounds__(64 * DNW) moe_few_down_kernel(FewParams p)
         for (int j = 0; j < p.top; ++j) {
             const int s = m * p.top + j;
             const float d = __builtin_fmaf((float)sums[s][n], scales[s] * factor[s][n], 0.0f);
-            v = __builtin_fmaf(expert_of[s] < 0 ? 0.0f : share[s], expert_of[s] < 0 ? 0.0f : d, v);
+            if (expert_of[s] < 0) continue;
+            v = __builtin_fmaf(share[s], d, v);
+            if (p.saved) p.saved[(int64_t)s * p.K + n0 + n] = (uint16_t)(pack_bf16x2(d, 0.0f) & 0xffffu);
         }
         p.out[o] = (uint16_t)(pack_bf16x2(v + res, 0.0f) & 0xffffu);
     }
@@ -536,6 +544,7 @@ hipError_t launch_moe_few_gate(const MoeFewArgs &a, const MoeFew &plan, hipStrea
     p.s1 = a.gate_scale;
     p.s2 = a.up_scale;
     p.out = a.h;
+    p.saved = a.pre;
     p.S = (int)a.M * a.top;
     p.E = a.E;
     p.top = a.top;
@@ -573,6 +582,7 @@ hipError_t launch_moe_few_down(const MoeFewArgs &a, const MoeFew &plan, hipStrea
     p.s1 = a.down_scale;
     p.residual = a.residual;
     p.out = a.y;
+    p.saved = a.d;
     p.S = (int)a.M * a.top;
     p.E = a.E;
     p.top = a.top;

@@ -2,7 +2,8 @@
 (the products are exact integer sums with the same epilogue), the weighted sum against 64 bits, gradients against their
 formulas in 64 bits and against differences, and the whole chain as a training step runs it.
 
-Bounds.  y: each d is within 3 u |acc sx sw| of its 64-bit value (linear_z), the sum of top terms and the residual in fp32
+Bounds.  y: each d is within 3 u |acc sx sw| of its 64-bit value (linear_z); on its way to the sum it may be held in 16 bits with a
+scale of max / 32767 per 64 channels, off by half a step, 2^-16 of that maximum; the sum of top terms and the residual in fp32
 adds (top + 2) u of the sum of their magnitudes, then one bf16 rounding.
 Grouped gradients: the operand bf16(dy sw) is reproduced exactly, so dx is off by fp32 sums alone: (N + 16) u of the sum of
 absolute terms, then the bf16 rounding.
@@ -207,7 +208,8 @@ def test_moe_ffn_gated(cr, M, top, E, F, K, gh, g, kind):
             wn = _np(w)[:, :, None]
             ref = (d64 * wn).sum(1) + _np(res)
             size = (np.abs(d64) * wn).sum(1) + np.abs(_np(res))
-            bound = (dd * wn).sum(1) + (top + 2) * R.U * size
+            held = np.repeat(np.abs(d64).reshape(M, top, K // 64, 64).max(3), 64, 2) * (2.0 ** -16 * (1 + 8 * R.U))
+            bound = ((dd + held) * wn).sum(1) + (top + 2) * R.U * size
             R.check(_np(y), ref, R.rounded(ref, bound), "y")
             assert torch.equal(cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, residual=res, **call), y), "not saving"
             place = res.clone()
@@ -226,8 +228,8 @@ FEW = [(1, 8, 64), (2, 8, 16), (3, 4, 4), (2, 32, 40), (8, 8, 64), (16, 4, 24), 
 @pytest.mark.parametrize("kind", ["mixed", "twice", "one", "dropped", "none"])
 @pytest.mark.parametrize("M,top,E", FEW)
 def test_moe_ffn_gated_few_slots(cr, M, top, E, kind):
-    """At most 64 slots take kernels of their own; nothing saved, they give the other path's bits.  The rotation groups
-    go through all sizes, the widths through whole and part 256-channel pieces and more pieces than wavefronts."""
+    """At most 64 slots take kernels of their own, here against the dense linears.  The rotation groups go through all sizes,
+    the widths through whole and part 256-channel pieces and more pieces than wavefronts."""
     experts, w = _experts(M, top, E, M + top, kind)
     for i, (F, K, gh, g) in enumerate([(64, 64, 1, 2), (128, 320, 4, 8), (192, 1088, 16, 32), (320, 2688, 64, 128), (2304, 512, 256, 256)]):
         if E > 100 and i != M % 5:
@@ -239,9 +241,19 @@ def test_moe_ffn_gated_few_slots(cr, M, top, E, kind):
             x[M // 2] *= 1e-37 if dtype is torch.float32 else 1.0
             x[M // 3] = 0
             call = dict(act=R.ACTS[i % 5], group=g, group_h=gh)
+            ok, wn = (experts >= 0) & (experts < E), _np(w)[:, :, None]
+            want_pre, want_d, d64, dd = _expert_by_expert(cr, x, experts, gate, up, down, call["act"], g, gh)
+            held = np.repeat(np.abs(d64).reshape(M, top, K // 64, 64).max(3), 64, 2) * (2.0 ** -16 * (1 + 8 * R.U))
+            if M * top <= 64:
+                held = 0.0                                       # nothing between the product and the sum
             for r in (res, None):
-                want = cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, residual=r, save=True, **call)[0]
-                assert torch.equal(cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, residual=r, **call), want)
+                y, pre, d = cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, residual=r, save=True, **call)
+                assert torch.equal(pre[:, ok], want_pre[:, ok]) and torch.equal(d[ok], want_d[ok])
+                add = 0.0 if r is None else _np(r)
+                ref = (d64 * wn).sum(1) + add
+                bound = ((dd + held) * wn).sum(1) + (top + 2) * R.U * ((np.abs(d64) * wn).sum(1) + np.abs(add))
+                R.check(_np(y), ref, R.rounded(ref, bound), "y")
+                assert torch.equal(cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, residual=r, **call), y), "not saving"
         place = x.bfloat16()                                     # y in the place of x
         want = cr.moe_ffn_gated(place, experts, w, *gate, *up, *down, residual=res, save=True, **call)[0]
         assert cr.moe_ffn_gated(place, experts, w, *gate, *up, *down, residual=res, out=place, **call) is place
