@@ -55,13 +55,65 @@ struct GradParams {
     int groups;
 };
 
+// What the gated product's gradient reads of a row for 8 channels, and of the group's scales.
+struct NextRow {
+    v4u g, u;
+
+    __device__ __forceinline__ void fetch(const GradParams &p, int64_t row, int c)
+    {
+        const int64_t o = row * p.K + c;
+        g = *reinterpret_cast<const v4u *>(p.next.pre + o);
+        u = *reinterpret_cast<const v4u *>(p.next.pre + (int64_t)p.M * p.K + o);
+    }
+};
+struct NextScales {
+    v4f gate[2], up[2];
+
+    __device__ __forceinline__ void fetch(const GradParams &p, int group, int c)
+    {
+        const int64_t o = (int64_t)group * p.K + c;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                gate[h][e] = p.next.sw_gate[o + 4 * h + e];
+                up[h][e] = p.next.sw_up[o + 4 * h + e];
+            }
+    }
+};
+
+// 8 neighbouring channels of dh, to both operands of the next contraction.
+__device__ __forceinline__ void next8(const GradParams &p, int m, int c, const float (&v)[8], const NextRow &r,
+                                      const NextScales &s)
+{
+    float g[8], u[8], slope[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        g[e] = e & 1 ? bf16hi_to_f32(r.g[e >> 1]) : bf16lo_to_f32(r.g[e >> 1]);
+        u[e] = e & 1 ? bf16hi_to_f32(r.u[e >> 1]) : bf16lo_to_f32(r.u[e >> 1]);
+    }
+    act_values_slopes(g, slope, p.next.act);
+    v4u a, b;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const uint32_t d = pack_bf16x2(v[e], v[e + 1]);
+        const float d0 = bf16lo_to_f32(d), d1 = bf16hi_to_f32(d);
+        const int h = e >> 2, i = e & 3;
+        a[e >> 1] = pack_bf16x2(d0 * u[e] * slope[e] * s.gate[h][i], d1 * u[e + 1] * slope[e + 1] * s.gate[h][i + 1]);
+        b[e >> 1] = pack_bf16x2(d0 * g[e] * s.up[h][i], d1 * g[e + 1] * s.up[h][i + 1]);
+    }
+    uint16_t *to = p.next.a + (int64_t)m * 2 * p.K + c;
+    *reinterpret_cast<v4u *>(to) = a;
+    *reinterpret_cast<v4u *>(to + p.K) = b;
+}
+
 // 8 rotated channels c .. of token m to where the launch puts them:
 //   dx = bf16(v + add), or, for the hidden gradient of a gated block, dh = bf16(v) and on to
 //   both operands of the next contraction, bf16(dh u act'(g) sw_gate) and bf16(dh act(g) sw_up), which
 //   saves writing dh and reading it back in a pass of its own.
 // (16 bytes each; K % 64 == 0, so all 8 exist.)
 template <bool GROUPED>
-__device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float (&v)[8], int group = 0)
+__device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float (&v)[8])
 {
     auto load = [](const uint16_t *src, float (&to)[8]) {
         const v4u d = *reinterpret_cast<const v4u *>(src);
@@ -74,7 +126,7 @@ __device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float
         for (int e = 0; e < 4; ++e) d[e] = pack_bf16x2(from[2 * e], from[2 * e + 1]);
         *reinterpret_cast<v4u *>(dst) = d;
     };
-    int64_t o = (int64_t)m * p.K + c;
+    const int64_t o = (int64_t)m * p.K + c;
     if (GROUPED && p.part16) {
         float scale;                                     // (8 lanes take 64 channels of a row)
         *reinterpret_cast<v4u *>(p.part16 + o) = pack_fixed16(v, scale);
@@ -89,25 +141,13 @@ __device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float
         store(p.dx + o, v);
         return;
     }
-    if (GROUPED && p.slot_of) o = (int64_t)p.slot_of[m] * p.K + c;
-    const float *sw_gate = p.next.sw_gate + (GROUPED ? (int64_t)group * p.K : 0);
-    const float *sw_up = p.next.sw_up + (GROUPED ? (int64_t)group * p.K : 0);
-    float g[8], u[8], slope[8];
-    load(p.next.pre + o, g);
-    load(p.next.pre + (int64_t)p.M * p.K + o, u);
-    act_values_slopes(g, slope, p.next.act);
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        const uint32_t d = pack_bf16x2(v[e], v[e + 1]);
-        const float d0 = bf16lo_to_f32(d), d1 = bf16hi_to_f32(d);
-        u[e] = d0 * u[e] * slope[e] * sw_gate[c + e];
-        u[e + 1] = d1 * u[e + 1] * slope[e + 1] * sw_gate[c + e + 1];
-        g[e] = d0 * g[e] * sw_up[c + e];
-        g[e + 1] = d1 * g[e + 1] * sw_up[c + e + 1];
+    if constexpr (!GROUPED) {                            // (sorted rows' pre is requested ahead, by their kernels)
+        NextRow row;
+        NextScales scales;
+        row.fetch(p, m, c);
+        scales.fetch(p, 0, c);
+        next8(p, m, c, v, row, scales);
     }
-    uint16_t *a = p.next.a + (int64_t)m * 2 * p.K + c;       // K % 64 == 0: no padding between the two
-    store(a, u);
-    store(a + p.K, g);
 }
 
 // One step of the rotation.  Sums are normalised before the first: |a + b| or |a - b| is at least the larger of |a| and
@@ -236,6 +276,60 @@ __device__ __forceinline__ v8bf16 codes_to_bf16(v2i raw)
     return __builtin_bit_cast(v8bf16, d);
 }
 
+// 64 rows whose rotation over 64 channels is done, in LDS as rows of 1 KiB with 16-byte chunk c at c ^ row % 16: its last
+// two steps and the result, by 32 threads per row, 8 channels each.  For a gradient that goes on to a gated product, the
+// first 4 rows' values of pre and the scales are requested before the rotation and each next row's 4 rows ahead (every row's
+// own where it is needed: 121 us for an expert layer's 8192 slots, N x K = 2048 x 1408, 108 so).
+template <bool GROUPED>
+__device__ __forceinline__ void finish_rows(const GradParams &p, const uint8_t *smem, int m0, int end, int c0, int group,
+                                            const int *slots, NextRow (&ahead)[4], const NextScales &scales)
+{
+    const int lg = p.lg, cc = (int)threadIdx.x & 31, c = c0 + 8 * cc, first = (int)threadIdx.x >> 5;
+    auto rotated8 = [&](int row, float (&v)[8]) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            auto chunk = [&](int i) -> v4f {
+                return *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * (((2 * cc + q) ^ i) ^ (row & 15)));
+            };
+            v4f x = chunk(0);
+            if (lg > 6) x = cc & 8 ? chunk(16) - x : x + chunk(16);
+            if (lg > 7) {
+                const v4f y = cc & 8 ? chunk(48) - chunk(32) : chunk(32) + chunk(48);
+                x = cc & 16 ? y - x : x + y;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
+        }
+    };
+    if constexpr (GROUPED) {
+        if (p.next.a) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (m0 + 32 * half >= end) return;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 8 * (4 * half + i) + first, m = m0 + row;
+                    if (m < end && c < p.K) {
+                        float v[8];
+                        rotated8(row, v);
+                        next8(p, m, c, v, ahead[i], scales);
+                    }
+                    if (half == 0) ahead[i].fetch(p, slots[4 + i], c < p.K ? c : 0);
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll 1
+    for (int it = 0; it < 8; ++it) {
+        const int row = 8 * it + first, m = m0 + row;
+        if (m >= end || c >= p.K) continue;
+        float v[8];
+        rotated8(row, v);
+        finish8<GROUPED>(p, m, c, v);
+    }
+}
+
 // 64 tokens x 256 channels, for batches whose 256-token tiles would not fill the GPU or would mostly compute
 // padding: 256 threads, 72 KiB of LDS, two workgroups per CU; each of the 4 wavefronts takes 64 channels of all
 // 64 tokens.  The codes go to LDS as they are, both operands without passing registers, in three stages
@@ -290,6 +384,16 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
         c0 = tc * BC;
     }
 
+    int slots[8];                                        // Grouped: the rows of pre that this thread finishes
+    if constexpr (GROUPED) {
+        if (p.next.a) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int m = min(m0 + 8 * i + ((int)threadIdx.x >> 5), end - 1);
+                slots[i] = p.slot_of ? p.slot_of[m] : m;
+            }
+        }
+    }
     // tokens: instruction i of wave w fills rows 8 (4 i + w) .. + 7 (lane -> row + lane / 8, position lane % 8);
     // codes: rows 4 (4 i + w) .. + 3 (lane -> row + lane / 16, position lane % 16)
     uint32_t offx[XL], offw[WL];
@@ -382,6 +486,16 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
     // every load into LDS has landed and every wave is done reading before the epilogue reuses it
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
+    NextRow ahead[4];
+    NextScales scales;
+    if constexpr (GROUPED) {
+        if (p.next.a) {
+            const int cn = c0 + 8 * ((int)threadIdx.x & 31), cl = cn < K ? cn : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ahead[i].fetch(p, slots[i], cl);
+            scales.fetch(p, group, cl);
+        }
+    }
 
     // lane: token lane % 16 of block b, channels 16 (4 w + a) + 4 fq + v
     if (!GROUPED && slot >= 0) {
@@ -424,28 +538,7 @@ __global__ void __launch_bounds__(256, 2) grad_tile_kernel(GradParams p)
         for (int a = 0; a < 4; ++a)
             *reinterpret_cast<v4f *>(smem + (16 * b + frow) * 1024 + 16 * ((4 * (4 * w + a) + fq) ^ frow)) = acc[a][b];
     __syncthreads();
-    const int cc = (int)threadIdx.x & 31, c = c0 + 8 * cc;
-#pragma unroll 1
-    for (int it = 0; it < 8; ++it) {
-        const int row = 8 * it + ((int)threadIdx.x >> 5), m = m0 + row;
-        if (m >= end || c >= K) continue;
-        float v[8];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            auto chunk = [&](int flip) {
-                return *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * (((2 * cc + q) ^ flip) ^ (row & 15)));
-            };
-            v4f x = chunk(0);
-            if (lg > 6) x = cc & 8 ? chunk(16) - x : x + chunk(16);
-            if (lg > 7) {
-                const v4f y = cc & 8 ? chunk(48) - chunk(32) : chunk(32) + chunk(48);
-                x = cc & 16 ? y - x : x + y;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
-        }
-        finish8<GROUPED>(p, m, c, v, group);
-    }
+    finish_rows<GROUPED>(p, smem, m0, end, c0, group, slots, ahead, scales);
 }
 
 // The same for 256 tokens x 256 channels, when there are enough of them: 512 threads, one workgroup per CU, 144 KiB of
@@ -674,19 +767,50 @@ __global__ void __launch_bounds__(512, 1) grad_gemm_kernel(GradParams p)
             }
             __syncthreads();
         }
-        const int cc = (int)threadIdx.x & 31, c = c0 + 8 * cc;
-#pragma unroll 1
-        for (int it = 0; it < 8; ++it) {
-            const int row = 16 * it + ((int)threadIdx.x >> 5), m = m0 + 128 * pass + row;
-            if (m >= end || c >= K) continue;
-            float v[8];
+        const int cc = (int)threadIdx.x & 31, c = c0 + 8 * cc, first = (int)threadIdx.x >> 5;
+        auto rotated8 = [&](int row, float (&v)[8]) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const v4f x = *reinterpret_cast<const v4f *>(smem + row * 1024 + 16 * ((2 * cc + q) ^ (row & 15)));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
             }
-            finish8<GROUPED>(p, m, c, v, group);
+        };
+        if constexpr (GROUPED) {
+            if (p.next.a) {
+                // pre of the next row on its way
+                const int cl = c < K ? c : 0;
+                auto slot_at = [&](int it) {
+                    const int m = min(m0 + 128 * pass + 16 * it + first, end - 1);
+                    return p.slot_of ? p.slot_of[m] : m;
+                };
+                NextScales scales;
+                NextRow ahead;
+                scales.fetch(p, group, cl);
+                ahead.fetch(p, slot_at(0), cl);
+                int then = slot_at(1);
+#pragma unroll 1
+                for (int it = 0; it < 8; ++it) {
+                    const int row = 16 * it + first, m = m0 + 128 * pass + row;
+                    if (m - first >= end) break;
+                    const NextRow now = ahead;
+                    ahead.fetch(p, then, cl);
+                    then = slot_at(it + 2);
+                    if (m >= end || c >= K) continue;
+                    float v[8];
+                    rotated8(row, v);
+                    next8(p, m, c, v, now, scales);
+                }
+                continue;
+            }
+        }
+#pragma unroll 1
+        for (int it = 0; it < 8; ++it) {
+            const int row = 16 * it + first, m = m0 + 128 * pass + row;
+            if (m >= end || c >= K) continue;
+            float v[8];
+            rotated8(row, v);
+            finish8<GROUPED>(p, m, c, v);
         }
     }
 }
@@ -1114,9 +1238,9 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
 // Rows per tile, 64 or 256, by a model with measured constants (us): a CU takes `step` per contraction step and `end` per
 // unit; a group's last tile is half empty, and so is the last round unless the tiles are surely no more than the CUs.
 // Measured, whole calls, 64 / 256 rows:
-//   linear_grouped_backward, rows, groups, N x K:  1000, 4, 2048 x 2688: 37 / 66;   3000, 12, 2048 x 2048: 52 / 66
-//     2000, 8, 2688 x 5376: 90 / 82;   4097, 8, 5376 x 2688: 167 / 151;   8000, 8, 2688 x 2688: 161 / 160
-//   expert layer, tokens, top of E, K x F:  2048, 4 of 32, 2048 x 1408: 288 / 359;   4096, 2 of 16, 2688 x 2688: 537 / 515
+//   linear_grouped_backward, rows, groups, N x K:  1000, 4, 2048 x 2688: 36 / 66;   3000, 12, 2048 x 2048: 52 / 67
+//     2000, 8, 2688 x 5376: 92 / 83;   4097, 8, 5376 x 2688: 169 / 153;   8000, 8, 2688 x 2688: 163 / 162
+//   expert layer, tokens, top of E, K x F:  2048, 4 of 32, 2048 x 1408: 276 / 354;   4096, 2 of 16, 2688 x 2688: 505 / 513
 int grouped_rows_per_tile(int64_t rows, int groups, int tiles_c, int nt)
 {
     const double used = (double)(groups < rows ? groups : rows);
