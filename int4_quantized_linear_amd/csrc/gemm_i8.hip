@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                     float v[8];
                     z8(ch, cl, v);
                     if constexpr (E == Epi::Part) {
-                        // (in fp32 the expert layer of 4096 tokens takes @@ us, @@ so; stored straight from the
+                        // (in fp32 the expert layer of 4096 tokens takes 436 us, 416 so; stored straight from the
                         // accumulators, 64 bytes of a row at a time, 443 against 435 then)
                         float scale;
                         const v4u d16 = pack_fixed16(v, scale);

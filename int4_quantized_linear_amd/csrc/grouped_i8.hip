@@ -28,8 +28,9 @@ struct OrderParams {
     int S, E, top;
 };
 
-// HELD > 0: at most 4 HELD slots per thread, requested at once and kept in registers between the two passes
-// (24576 slots of 64 experts: 14 us read twice, @@ so).
+// HELD > 0: at most 4 HELD <= 32 slots per thread, requested at once and kept between the two passes as a bit each, so that
+// the second takes as many steps as the fullest lane has rows.  Rows' tokens and scales are filled in by whole waves at the
+// end (24576 slots of 64 experts: 19 us with a division and a load in the second pass's branch over every slot, 11 us so).
 template <int NT, int HELD>
 __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
 {
@@ -41,26 +42,8 @@ __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
     // mine: of this expert (or of none); less: with a smaller one
     auto mine = [&](int x) { return none ? (unsigned)x >= (unsigned)p.E : x == e; };
     auto less = [&](int x) { return (unsigned)x < (unsigned)e; };
-    int n_mine = 0, n_less = 0;
     typedef v4i v4i_any __attribute__((aligned(4)));
-    v4i held[HELD ? HELD : 1];
-#pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-        const int s = s0 + 4 * i;
-        if (s + 4 <= s1) held[i] = *reinterpret_cast<const v4i_any *>(p.experts + s);
-        else
-#pragma unroll
-            for (int k = 0; k < 4; ++k) held[i][k] = s + k < s1 ? p.experts[s + k] : 0;
-    }
-    auto each = [&](auto f) {
-        if constexpr (HELD > 0) {
-#pragma unroll
-            for (int i = 0; i < HELD; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (s0 + 4 * i + k < s1) f(s0 + 4 * i + k, held[i][k]);
-            return;
-        }
+    auto each = [&](auto f) {                            // HELD == 0: from memory
         int s = s0;
         for (; s + 4 <= s1; s += 4) {
             const v4i x = *reinterpret_cast<const v4i_any *>(p.experts + s);
@@ -69,10 +52,35 @@ __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
         }
         for (; s < s1; ++s) f(s, p.experts[s]);
     };
-    each([&](int, int x) {
-        n_mine += mine(x);
-        n_less += less(x);
-    });
+    int n_mine = 0, n_less = 0;
+    uint32_t mask = 0;
+    if constexpr (HELD > 0) {
+        v4i held[HELD];
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int s = s0 + 4 * i;
+            if (s + 4 <= s1) held[i] = *reinterpret_cast<const v4i_any *>(p.experts + s);
+            else
+#pragma unroll
+                for (int k = 0; k < 4; ++k) held[i][k] = s + k < s1 ? p.experts[s + k] : 0;
+        }
+        const int n = s1 - s0;
+        const uint32_t real = n >= 32 ? ~0u : (1u << n) - 1u;
+        uint32_t below = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * HELD; ++i) {
+            mask |= (uint32_t)mine(held[i / 4][i % 4]) << i;
+            below |= (uint32_t)less(held[i / 4][i % 4]) << i;
+        }
+        mask &= real;
+        n_mine = __popc(mask);
+        n_less = __popc(below & real);
+    } else {
+        each([&](int, int x) {
+            n_mine += mine(x);
+            n_less += less(x);
+        });
+    }
     int before = n_mine, all = n_less;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -83,24 +91,34 @@ __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
     for (int d = 1; d < 64; d *= 2) all += __shfl_xor(all, d);
     if (lane == 63) part[t >> 6] = int2{before, all};
     __syncthreads();
-    int row = before - n_mine, first = 0;
+    int row = before - n_mine, first = 0, rows = 0;
 #pragma unroll
     for (int i = 0; i < NT / 64; ++i) {
         if (i < (t >> 6)) row += part[i].x;
+        rows += part[i].x;
         first += part[i].y;
     }
     if (t == 0) p.offsets[e] = first;
     row += first;
-    if (n_mine == 0) return;
-    each([&](int s, int x) {
-        if (!mine(x)) return;
+    auto put = [&](int s) {
         p.row_of[s] = none ? -1 : row;
-        if (none) return;
-        p.slot_of[row] = s;
-        p.token_of[row] = s / p.top;
-        if (p.sx) p.sx_of[row] = p.sx[s / p.top];
+        if (!none) p.slot_of[row] = s;
         ++row;
-    });
+    };
+    if constexpr (HELD > 0) {
+        for (; mask; mask &= mask - 1) put(s0 + __ffs(mask) - 1);
+    } else {
+        each([&](int s, int x) {
+            if (mine(x)) put(s);
+        });
+    }
+    if (none) return;
+    __syncthreads();
+    for (int r = first + t; r < first + rows; r += NT) {
+        const int token = p.slot_of[r] / p.top;
+        p.token_of[r] = token;
+        if (p.sx) p.sx_of[r] = p.sx[token];
+    }
 }
 
 // ---------------------------------------------------------------------------------------------
