@@ -10,8 +10,11 @@
 // softmax), so they stay defined where every s is 0 in fp32.  They and their gradients are formed in 64 bits:
 // a handful of values per token, next to differences that cancel.
 //
-// One wavefront per token, PER logits per lane.  A choice is the largest key over the wavefront, by six DPP steps, and the
-// lowest index that has it, by ballots; the winner's lane drops it.
+// One wavefront per token, PER logits per lane.  A choice is the largest of the lanes' largest keys' 32 high bits, by six DPP
+// steps and a ballot; only where several lanes have it the low bits and the index decide.  The winner's lane drops it.
+// One token's choice, 8 of 64: 3 us, latency.  8192 tokens, 8 of 256, with a bias: 14 us, bound by instructions, about 1000
+// per token of which the 256 keys take 400 and a choice 45 (both halves of the key reduced and the logits carried: 15.5);
+// their logits are 8 MB, 2 us.  Its gradient, 6 of 128 in bf16: 7 us.
 #include "device_common.hpp"
 #include "launchers.hpp"
 
@@ -34,6 +37,26 @@ struct RouteParams {
 __device__ __forceinline__ float load_logit(const void *p, bool f32, int64_t i)
 {
     return f32 ? static_cast<const float *>(p)[i] : bf16lo_to_f32(static_cast<const uint16_t *>(p)[i]);
+}
+
+// Logits 64 r + lane of token m, -inf past the last: every load at once, without a branch between them.
+template <int PER>
+__device__ __forceinline__ void load_row(const void *logits, bool f32, int64_t m, int E, int lane, float (&l)[PER])
+{
+    if (f32) {
+        const float *src = static_cast<const float *>(logits) + m * E;
+#pragma unroll
+        for (int r = 0; r < PER; ++r) l[r] = src[min(64 * r + lane, E - 1)];
+    } else {
+        const uint16_t *src = static_cast<const uint16_t *>(logits) + m * E;
+        uint32_t raw[PER];
+#pragma unroll
+        for (int r = 0; r < PER; ++r) raw[r] = src[min(64 * r + lane, E - 1)];
+#pragma unroll
+        for (int r = 0; r < PER; ++r) l[r] = bf16lo_to_f32(raw[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < PER; ++r) l[r] = 64 * r + lane < E ? l[r] : -__builtin_inff();
 }
 
 // v of another lane by DPP control CTRL, `none` where that control has no source.
@@ -88,11 +111,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
     return wave_all(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
-__device__ __forceinline__ uint64_t wave_max(uint64_t v)
-{
-    const uint32_t hi = wave_max((uint32_t)(v >> 32));
-    return (uint64_t)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-}
 __device__ __forceinline__ double wave_sum(double v)
 {
     return wave_all(v, 0.0, [](double a, double b) { return a + b; });
@@ -136,13 +154,16 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_kernel(RouteParams p)
     const int lane = threadIdx.x & 63;
     const int64_t m = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
     if (m >= p.M) return;
-    float l[PER];
+    float l[PER], bias[BIAS ? PER : 1];
+    if constexpr (BIAS) {
+#pragma unroll
+        for (int r = 0; r < PER; ++r) bias[r] = p.bias[min(64 * r + lane, p.E - 1)];
+    }
+    load_row(p.logits, p.f32, m, p.E, lane, l);
     bool bad = false;
     float most = -__builtin_inff();
 #pragma unroll
     for (int r = 0; r < PER; ++r) {
-        const int i = 64 * r + lane;
-        l[r] = i < p.E ? load_logit(p.logits, p.f32, m * p.E + i) : -__builtin_inff();
         bad |= l[r] != l[r];
         most = __builtin_fmaxf(most, l[r]);
     }
@@ -160,44 +181,42 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_kernel(RouteParams p)
 #pragma unroll
     for (int r = 0; r < PER; ++r) {
         if constexpr (BIAS) {
-            const int i = 64 * r + lane;
-            key[r] = 0u;
-            if (i < p.E && l[r] > -__builtin_inff()) {
-                const double x = (double)l[r];
-                const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)most) / z;
-                key[r] = ordered(s + (double)p.bias[i]);
-            }
+            const double x = (double)l[r];
+            const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)most) / z;
+            key[r] = l[r] > -__builtin_inff() ? ordered(s + (double)bias[r]) : 0u;
         } else {
             key[r] = ordered(l[r]);
         }
     }
     int chosen = -1;                                     // lane j: the j-th expert
-    float value = 0.0f;                                  // and its logit
     for (int j = 0; j < p.top; ++j) {
-        KEY best = key[0];
+        KEY best = key[0];                               // the lane's own, the lowest index of equal ones
+        int at = lane;
 #pragma unroll
-        for (int r = 1; r < PER; ++r) best = key[r] > best ? key[r] : best;
-        best = wave_max(best);
-        if (best == 0u) break;                           // nothing left that may be chosen
-        int at = -1;                                     // the lowest index of equal ones
-        float v = 0.0f;
-#pragma unroll
-        for (int r = PER - 1; r >= 0; --r) {
-            const uint64_t m = __builtin_amdgcn_ballot_w64(key[r] == best);
-            if (m) {
-                const int from = __builtin_ctzll(m);
-                at = 64 * r + from;
-                v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[r]), from));
+        for (int r = 1; r < PER; ++r) {
+            const bool more = key[r] > best;
+            best = more ? key[r] : best;
+            at = more ? 64 * r + lane : at;
+        }
+        const uint32_t high = (uint32_t)(best >> (BIAS ? 32 : 0)), most_high = wave_max(high);
+        if (most_high == 0u) break;                      // nothing left that may be chosen
+        uint64_t lanes = __builtin_amdgcn_ballot_w64(high == most_high);
+        if (lanes & (lanes - 1)) {                       // several: by the low half, then by index
+            bool first = high == most_high;
+            if constexpr (BIAS) {
+                const uint32_t low = first ? (uint32_t)best : 0u, most_low = wave_max(low);
+                first = first && low == most_low;
             }
+            at = (int)~wave_max(first ? ~(uint32_t)at : 0u);
+        } else {
+            at = __builtin_amdgcn_readlane(at, __builtin_ctzll(lanes));
         }
 #pragma unroll
         for (int r = 0; r < PER; ++r)
             if (at == 64 * r + lane) key[r] = 0u;
-        if (lane == j) {
-            chosen = at;
-            value = v;
-        }
+        if (lane == j) chosen = at;
     }
+    const float value = chosen >= 0 ? load_logit(p.logits, p.f32, m * p.E + chosen) : 0.0f;
     const double share = chosen_share(p.sigmoid, p.normalize, (double)value, chosen >= 0, most, z);
     if (lane < p.top) {
         p.experts[m * p.top + lane] = chosen;
@@ -228,6 +247,8 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_backward_kernel(RouteGra
     const int lane = threadIdx.x & 63;
     const int64_t m = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
     if (m >= p.M) return;
+    float s[PER] = {};
+    if (all) load_row(p.logits, p.f32, m, p.E, lane, s);
     int chosen = -1;
     double g = 0.0, l = 0.0;
     if (lane < p.top) {
@@ -239,15 +260,11 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_backward_kernel(RouteGra
             if (l == -__builtin_inf()) chosen = -1;      // masked: its weight is a constant 0
         }
     }
-    float s[PER] = {}, most = -__builtin_inff();
+    float most = -__builtin_inff();
     double z = 1.0;
     if (all) {
 #pragma unroll
-        for (int r = 0; r < PER; ++r) {
-            const int i = 64 * r + lane;
-            s[r] = i < p.E ? load_logit(p.logits, p.f32, m * p.E + i) : -__builtin_inff();
-            most = __builtin_fmaxf(most, s[r]);
-        }
+        for (int r = 0; r < PER; ++r) most = __builtin_fmaxf(most, s[r]);
         most = wave_max(most);
         double sum = 0.0;
 #pragma unroll
