@@ -439,7 +439,7 @@ def test_large_rows(cr):
         bound = (N + 16) * R.U * R.rotate_abs(np.abs(a) @ np.abs(q), 64)
         R.check(_np(dx[lo:hi]), ref, R.rounded(ref, bound), "dx")
     del y, dx
-    M, top, F, K = 80_000, 8, 64, 4096                            # 2.6e9 elements of d and of the fp32 parts
+    M, top, F, K = 80_000, 8, 64, 4096                            # 2.6e9 elements of d and of its 16-bit copies
     gate, up, down = _layer(cr, 8, F, K, 64, 256)
     experts = torch.arange(8, dtype=torch.int32, device=DEV).repeat(M, 1)
     w = torch.rand(M, top, device=DEV)
