@@ -273,9 +273,11 @@ def test_bad_values_stay_in_their_tokens(cr, M, top, value):
     others = torch.arange(M, device=DEV) != bad
     x, r, call = _randn(M, K, seed=1), _randn(M, K, seed=2), dict(group=64, group_h=64)
     y, pre, d = cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, residual=r, save=True, **call)
-    for which in ("weight", "residual", "d"):
-        w2, r2, p = w.clone(), r.clone(), [gate, up, down]
-        if which == "weight":
+    for which in ("x", "weight", "residual", "d"):
+        x2, w2, r2, p = x.clone(), w.clone(), r.clone(), [gate, up, down]
+        if which == "x":                                         # (what the quantizer makes of it is the linears' matter)
+            x2[bad, 3] = value
+        elif which == "weight":
             w2[bad, 1] = value
         elif which == "residual":
             r2[bad, 7] = value
@@ -283,10 +285,10 @@ def test_bad_values_stay_in_their_tokens(cr, M, top, value):
             s = down[1].clone()
             s[2, 5] = value
             p[2] = (down[0], s)
-        got = cr.moe_ffn_gated(x, experts, w2, *p[0], *p[1], *p[2], residual=r2, **call)
+        got = cr.moe_ffn_gated(x2, experts, w2, *p[0], *p[1], *p[2], residual=r2, **call)
         hit = ~others if which != "d" else (experts == 2).any(1)
         assert torch.equal(got[~hit], y[~hit]), which
-        assert not got[hit].isfinite().all(1).any(), which
+        assert which == "x" or not got[hit].isfinite().all(1).any(), which
     dy, add = _randn(M, K, seed=3), _randn(M, K, seed=4)
     dx, dw = cr.moe_ffn_gated_backward(dy, pre, d, experts, w, *gate, *up, *down, dx_add=add, **call)
     for which in ("dy", "pre", "d", "weight"):
