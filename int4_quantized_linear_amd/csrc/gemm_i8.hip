@@ -434,7 +434,162 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                 }
                 fence();
             }
-        } else if constexpr (E == Epi::Act || E == Epi::Gated || E == Epi::Part) {
+        } else if constexpr (GROUPED && E != Epi::Bf16) {
+            // Outputs are formed where the accumulators are, and only their 16 bits pass through the wave's own 8 KiB of LDS
+            // (that of the bf16 branch below).
+            const float *ls = reinterpret_cast<const float *>(smem + SCALE_OFF + (j & (NSCALE - 1)) * SCALE_BYTES);
+            uint8_t *reg = smem + (g & (NST - 1)) * STAGE + w * 1024;
+            const int mw = m0 + wm * 64;
+            const bool rows = mw < Mi;                   // (else the stores below are all dropped, but made)
+            auto value4 = [&](int bi, int bj, const v4f &s4, float sxm, float *v) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)acc[bi][bj][i], sxm * s4[i], 0.0f);
+            };
+            auto bf16x4 = [](const float *v) { return v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; };
+            if constexpr (E == Epi::Gated) {
+                // 64 rows of 64 features: row r of the wave's is the part r % 8 of piece r / 8, its 8 chunks at chunk ^ swz(r);
+                // what: h, or for the backward pass g or u alone
+                auto pass = [&](auto what) {
+                    constexpr int W = decltype(what)::value;     // 0: h, 1: g, 2: u
+#pragma unroll
+                    for (int bj = 0; bj < 4; ++bj) {
+                        if (!rows) break;
+                        int row = erow, quad = efq;
+                        asm volatile("" : "+v"(row), "+v"(quad));
+                        const float sxm = ls[2 * BN + wm * 64 + 16 * bj + row];
+                        uint8_t *to = reg + OPB * (bj >> 1) + 8192 * (2 * (bj & 1) + (row >> 3)) + (row & 7) * 128 + 8 * (quad & 1);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float gv[8], uv[8];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float *s = ls + wn * 64 + 16 * (2 * q + i) + 4 * quad;
+                                if (W != 2) value4(4 * q + 2 * i, bj, *reinterpret_cast<const v4f *>(s), sxm, gv + 4 * i);
+                                if (W != 1) value4(4 * q + 2 * i + 1, bj, *reinterpret_cast<const v4f *>(s + NF), sxm, uv + 4 * i);
+                            }
+                            if constexpr (W == 0) {
+                                act_values(gv, p.f.act);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) gv[e] *= uv[e];
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                *reinterpret_cast<v2u *>(to + 16 * ((2 * (2 * q + i) + (quad >> 1)) ^ swz(row))) =
+                                    bf16x4((W == 2 ? uv : gv) + 4 * i);
+                            fence();
+                        }
+                    }
+                    int r8 = lane >> 3, chunk = lane & 7;
+                    asm volatile("" : "+v"(r8), "+v"(chunk));
+                    const int n = n0 + wn * 64 + 8 * chunk;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        v4u out[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            out[q] = *reinterpret_cast<const v4u *>(reg + OPB * half + 8192 * q + r8 * 128 +
+                                                                    16 * (chunk ^ swz(8 * (q & 1) + r8)));
+                        if constexpr (W == 0) {
+                            if (half == 1) issue_after_epilogue_reads(g);
+                            const __amdgpu_buffer_rsrc_t ry = __builtin_amdgcn_make_buffer_rsrc(
+                                static_cast<uint16_t *>(p.y) + (int64_t)(mw + 32 * half) * p.N, (short)0, NUM_RECORDS, 0x00020000);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int r = 8 * q + r8;
+                                const uint32_t off = mw + 32 * half + r < Mi && n < Ni ? (uint32_t)(r * Ni + n) * 2u : OOB;
+                                __builtin_amdgcn_raw_buffer_store_b128(out[q], ry, off, 0, 0);
+                            }
+                        } else {
+                            uint16_t *pre = p.f.pre + (W == 2 ? (int64_t)p.M * p.N : 0);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int r = mw + 32 * half + 8 * q + r8;
+                                if (r < Mi && n < Ni) *reinterpret_cast<v4u *>(pre + (int64_t)p.slot_of[r] * p.N + n) = out[q];
+                            }
+                        }
+                        fence();
+                    }
+                };
+                if (p.f.pre) {
+                    pass(std::integral_constant<int, 1>{});
+                    pass(std::integral_constant<int, 2>{});
+                }
+                pass(std::integral_constant<int, 0>{});
+            } else {
+                // the bf16 branch's blocks of 32 rows, of the 16-bit rows, or of d's
+                auto pass = [&](auto what) {
+                    constexpr bool D = decltype(what)::value;
+#pragma unroll
+                    for (int bp = 0; bp < 2; ++bp) {
+                        int row = erow, quad = efq;
+                        asm volatile("" : "+v"(row), "+v"(quad));
+                        uint8_t *to = reg + 8192 * ((row >> 2) & 3) + (row & 3) * 256 + 8 * (quad & 1);
+#pragma unroll
+                        for (int b2 = 0; b2 < 2; ++b2) {
+                            if (!rows) break;
+                            const int bj = 2 * bp + b2;
+                            const float sxm = ls[2 * BN + wm * 64 + 16 * bj + row];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float v[16];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    value4(4 * h + i, bj, *reinterpret_cast<const v4f *>(ls + wn * 128 + 16 * (4 * h + i) + 4 * quad), sxm,
+                                           v + 4 * i);
+                                v2u d[4];
+                                if constexpr (D) {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) d[i] = bf16x4(v + 4 * i);
+                                } else {
+                                    // 64 channels of a row, 16 in each of 4 lanes, 16 apart
+                                    float scale;
+                                    pack_fixed16_quads(v, d, scale);
+                                    const int n = n0 + wn * 128 + 64 * h;
+                                    if (quad == h && mw + 16 * bj + row < Mi && n < Ni)
+                                        p.part_scale[(int64_t)(mw + 16 * bj + row) * (p.N / 64) + n / 64] = scale;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    *reinterpret_cast<v2u *>(to + b2 * OPB + 16 * ((2 * (4 * h + i) + (quad >> 1)) ^ row)) = d[i];
+                                fence();
+                            }
+                        }
+                        int rrow = lane >> 4, chunk = lane & 15;
+                        asm volatile("" : "+v"(rrow), "+v"(chunk));
+                        const int n = n0 + wn * 128 + 8 * chunk;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int mr = mw + 32 * bp + 16 * half;
+                            v4u out[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                out[q] = *reinterpret_cast<const v4u *>(reg + half * OPB + 8192 * q + rrow * 256 +
+                                                                        16 * ((chunk ^ rrow) ^ (4 * q)));
+                            if constexpr (D) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int r = mr + 4 * q + rrow;
+                                    if (r < Mi && n < Ni) *reinterpret_cast<v4u *>(p.d + (int64_t)p.slot_of[r] * p.N + n) = out[q];
+                                }
+                            } else {
+                                if (bp == 1 && half == 1) issue_after_epilogue_reads(g);
+                                const __amdgpu_buffer_rsrc_t ry = __builtin_amdgcn_make_buffer_rsrc(
+                                    static_cast<uint16_t *>(p.y) + (int64_t)mr * p.N, (short)0, NUM_RECORDS, 0x00020000);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int r = 4 * q + rrow;
+                                    const uint32_t off = mr + r < Mi && n < Ni ? (uint32_t)(r * Ni + n) * 2u : OOB;
+                                    __builtin_amdgcn_raw_buffer_store_b128(out[q], ry, off, 0, 0);
+                                }
+                            }
+                            fence();
+                        }
+                    }
+                };
+                if (p.d) pass(std::true_type{});
+                pass(std::false_type{});
+            }
+        } else if constexpr (E == Epi::Act || E == Epi::Gated) {
             // Two phases per 16-token block, so that the activation's code exists once and not per
             // accumulator register.  (Applied where the accumulators are, fully unrolled, it spilled
             // 64 (Gated) and 145 (Act) registers.)  First the block's int32 sums go to the wave's own 8 KiB
@@ -462,15 +617,8 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
             };
             const __amdgpu_buffer_rsrc_t ry = rows_of(static_cast<uint16_t *>(p.y));
             const __amdgpu_buffer_rsrc_t rres = rows_of(E == Epi::Act ? p.f.residual : nullptr);
-            const __amdgpu_buffer_rsrc_t rpre = rows_of(GROUPED ? nullptr : p.f.pre);
-            const __amdgpu_buffer_rsrc_t rpre2 =
-                rows_of(E == Epi::Gated && !GROUPED && p.f.pre ? p.f.pre + (int64_t)Mi * p.N : nullptr);
-            // Grouped: pre and d go to the row's slot
-            auto store_slot = [&](const float (&v)[8], uint16_t *to, int r) {
-                if (mw + r < Mi && n < Ni)
-                    *reinterpret_cast<v4u *>(to + (int64_t)p.slot_of[mw + r] * p.N + n) = v4u{
-                        pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-            };
+            const __amdgpu_buffer_rsrc_t rpre = rows_of(p.f.pre);
+            const __amdgpu_buffer_rsrc_t rpre2 = rows_of(E == Epi::Gated && p.f.pre ? p.f.pre + (int64_t)Mi * p.N : nullptr);
             const int act = p.f.act;
             auto offset = [&](int r) {                                 // r: row in the wave's 64
                 return (r < 64 && mw + r < Mi && n < Ni) ? (uint32_t)(r * Ni + n) * 2u : OOB;
@@ -531,23 +679,11 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                     const uint32_t off = offset(r);
                     float v[8];
                     z8(ch, cl, v);
-                    if constexpr (E == Epi::Part) {
-                        // (in fp32 the expert layer of 4096 tokens takes 436 us, 416 so; stored straight from the
-                        // accumulators, 64 bytes of a row at a time, 443 against 435 then)
-                        float scale;
-                        const v4u d16 = pack_fixed16(v, scale);
-                        __builtin_amdgcn_raw_buffer_store_b128(d16, ry, off, 0, 0);
-                        if (lcol % 8 == 0 && off != OOB) p.part_scale[(int64_t)(mw + r) * (p.N / 64) + n / 64] = scale;
-                        if (p.d) store_slot(v, p.d, r);
-                        continue;
-                    }
-                    if (!GROUPED && p.f.pre) store8(v, rpre, off);
-                    if (GROUPED && E == Epi::Gated && p.f.pre) store_slot(v, p.f.pre, r);
+                    if (p.f.pre) store8(v, rpre, off);
                     if constexpr (E == Epi::Gated) {
                         float u[8];
                         z8(ch + 4, cl + NF, u);
-                        if (!GROUPED && p.f.pre) store8(u, rpre2, off);
-                        if (GROUPED && p.f.pre) store_slot(u, p.f.pre + (int64_t)p.M * p.N, r);
+                        if (p.f.pre) store8(u, rpre2, off);
                         act_values(v, act);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[i] *= u[i];
@@ -662,8 +798,8 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
     // Stores each wavefront issues after the loads of the next job's second K-tile, in an
     // epilogue (vmcnt counts them too; the int32 and split-unit epilogues issue all 32 of theirs
     // after those loads; the bf16 one 8 of its 16).
-    // The Act and Gated epilogues issue theirs before those loads.
-    constexpr int EPI_STORES = E == Epi::Int32 ? 32 : E == Epi::Bf16 ? 8 : 0;
+    // The Act and Gated epilogues issue theirs before those loads, Grouped's but the last 4.
+    constexpr int EPI_STORES = E == Epi::Int32 ? 32 : E == Epi::Bf16 ? 8 : GROUPED ? 4 : 0;
     // Instruction interleaving inside one sub-step's scheduling region (sched_group_barrier masks:
     // 0x008 MFMA, 0x100 LDS read, 0x020 global read): the matrix pipe keeps its queue while the
     // fragment reads and the global loads go out between its instructions.
@@ -771,6 +907,10 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
             fence();
         }
         epilogue(job(j), j, g - 1);
+        if constexpr (GROUPED) {                         // (again: not to be held across the epilogue, which needs the registers)
+            read_a(g, 0, 0);
+            read_b(g, 0);
+        }
     }
     // the stream's last (out-of-range) loads write zeros into LDS: let them land before the
     // workgroup's LDS is released
