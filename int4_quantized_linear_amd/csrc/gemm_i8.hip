@@ -123,7 +123,9 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
     int last = 0;
     if constexpr (GROUPED) {
         p.tiles_m = group_tiles<NTHREADS>(p.offsets, p.groups, p.M, BM, gl.table, reinterpret_cast<int *>(smem), last);
-        p.T_dp = p.tiles_m * p.tiles_n;
+        const int T = p.tiles_m * p.tiles_n, r = T % (int)gridDim.x;
+        p.S = 2 * r <= (int)gridDim.x ? 2 : 1;
+        p.T_dp = p.S == 2 ? T - r : T;
     }
     const int T = p.tiles_m * p.tiles_n;
     const int U = p.T_dp + (T - p.T_dp) * p.S;
@@ -141,7 +143,9 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
         J.kb = 0;
         J.ke = KT;
         J.slot = -1;
-        if (u >= p.T_dp) {
+        if (GROUPED && u >= p.T_dp) {
+            q = p.T_dp + ((u - p.T_dp) >> 1);
+        } else if (u >= p.T_dp) {
             // slice-major: the units an XCD runs at once are neighbouring tiles at the same K-slice,
             // so they share operand rows in its L2 like whole tiles do
             const int r = T - p.T_dp, v = u - p.T_dp, sl = v / r;
@@ -151,7 +155,14 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
             J.slot = v;
         }
         tile_coords(q, p.tiles_m, p.tiles_n, J.tm, J.tn);
-        if constexpr (GROUPED) J.g = group_of_tile(gl.table, BM, last, J.tm);
+        if constexpr (GROUPED) {
+            J.g = group_of_tile(gl.table, BM, last, J.tm);
+            if (u >= p.T_dp) {                           // its lower or upper 128 rows
+                const int end = J.g.end;
+                J.g.first = min(J.g.first + 128 * ((u - p.T_dp) & 1), end);
+                J.g.end = min(J.g.first + 128, end);
+            }
+        }
         return J;
     };
     // Per-lane load geometry (independent of the tile): instruction i (0..3) of wave w fills
