@@ -103,7 +103,14 @@ constexpr int tile_features() { return E == Epi::Gated ? BN / 2 : BN; }
 // Grouped: the same walk over the tiles of rows sorted by group (grouped_common.hpp), each with its group's weight.  Only
 // where a tile's rows begin and end, its weight and, where rows are taken from elsewhere, the addresses of its rows
 // differ.  Those rows' numbers are requested one tile ahead, each wavefront its own 32, into its part of LDS: waiting
-// for them at the tile's start would drain the K-tiles in flight.
+// for them at the tile's start would drain the K-tiles in flight.  Where the last round would be at most half full, its tiles
+// run as two of 128 rows (8192 rows, 16 groups, 5376 x 5376: 322 -> 310 us).
+// 24576 rows of 64 groups: gate and up of 2048 x 1408 211 us, 1340 TOP/s, its down 124 us, 1140 TOP/s; 8192 rows of 16 groups,
+// 5376 x 5376: 291 us, 1630 TOP/s, where one group's 8192 take 212.  The difference is the groups' part tiles (a seventh to a
+// quarter of all), the last round and, with short K, the epilogue, which nothing overlaps.
+// (Tiles of 128 x 256 with two workgroups per CU, one's epilogue under the other's products: 97 KiB of operands requested for
+// 64 KiB here, in K-tiles of 64 bytes since three of 128 do not fit, so every line twice: 360 us against 322.  All whole tiles
+// before all part tiles: 348 against 320, a weight tile's readers are then further apart.)
 struct GroupedLds {
     GroupTable table;
     int source[8][64];
@@ -447,7 +454,8 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
             }
         } else if constexpr (GROUPED && E != Epi::Bf16) {
             // Outputs are formed where the accumulators are, and only their 16 bits pass through the wave's own 8 KiB of LDS
-            // (that of the bf16 branch below).
+            // (that of the bf16 branch below).  Expert layer of 4096 tokens, top 6 of 64, 2048 x 1408: 394 us; with the sums
+            // through LDS, as Act and Gated below, 410.  Part in fp32 instead of 16 bits: 20 us more.
             const float *ls = reinterpret_cast<const float *>(smem + SCALE_OFF + (j & (NSCALE - 1)) * SCALE_BYTES);
             uint8_t *reg = smem + (g & (NST - 1)) * STAGE + w * 1024;
             const int mw = m0 + wm * 64;

@@ -433,9 +433,10 @@ void launch_tiles(const GroupedParams &p, hipStream_t stream)
 // unit of several, a lone workgroup `lone` per K-tile; a group's last tile is half empty; the weights stream at 4.9 TB/s.
 // Measured, whole calls, 64 / 128 / 256 rows:
 //   linear_grouped, rows, groups, K x N:  2500, 6, 2688 x 1001: 38 / 42 / 67;   2000, 8, 2048 x 2048: 39 / 29 / 36
-//     4000, 8, 2688 x 5376: 149 / 107 / 95;   8192, 16, 5376 x 5376: 595 / 389 / 325
-//   expert layer, tokens, top of E, K x F:  12, 6 of 64, 2048 x 1408: 101 / 107 / 134;  1000, 4 of 32, the same: 160 / 149 / 154
-//     4096, 6 of 64, the same: 623 / 494 / 438
+//     4000, 8, 2688 x 5376: 148 / 107 / 94;   8192, 16, 5376 x 5376: 591 / 388 / 310
+//   expert layer, tokens, top of E, K x F:  12, 6 of 64, 2048 x 1408: 101 / 107 / 134;  600, 2 of 8, 2688 x 2688: 110 / 122 / 115
+//     1000, 4 of 32, 2048 x 1408: 156 / 145 / 138;   1500, 2 of 8, 5120 x 1280: 192 / 200 / 162;   4096, 6 of 64, 2048 x 1408:
+//     592 / 464 / 382
 int rows_per_tile(int64_t rows, int groups, int64_t N, int K, Epi epi)
 {
     const double cols = (double)N * (epi == Epi::Gated ? 2.0 : 1.0), used = (double)(groups < rows ? groups : rows);
@@ -446,11 +447,12 @@ int rows_per_tile(int64_t rows, int groups, int64_t N, int K, Epi epi)
     for (int bm = 64; bm <= 256; bm *= 2) {
         const double width = bm == 256 ? 256.0 : 128.0;
         const double step = bm == 64 ? 0.55 : bm == 128 ? 0.72 : 1.72, lone = bm == 64 ? 0.85 : bm == 128 ? 1.1 : 1.72;
-        const double end = bm == 64 ? 1.5 : bm == 128 ? 2.5 : epi == Epi::Bf16 ? 5.0 : 10.0;
+        const double end = bm == 64 ? 1.5 : bm == 128 ? 2.5 : epi == Epi::Bf16 ? 5.0 : 7.0;
         const double tiles = (double)rows / bm + 0.5 * used;
         const double units = (tiles > used ? tiles : used) * __builtin_ceil(cols / width);
-        // rounds: the last one is half full on average, unless the tiles are surely no more than the CUs
-        const double rounds = units < 220.0 ? 1.0 : units / 256.0 + 0.5;
+        // rounds: the last one is half full on average (in 256 rows, then it takes less), unless the tiles are surely no more
+        // than the CUs
+        const double rounds = units < 220.0 ? 1.0 : units / 256.0 + (bm == 256 ? 0.33 : 0.5);
         const double many = rounds * (KT * step + end), one = KT * lone + end;
         double t = many > one ? many : one;
         if (t < stream) t = stream + end;

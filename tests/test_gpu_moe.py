@@ -57,7 +57,13 @@ GROUPED = [([1], 1, 64, 64), ([0, 0, 3, 0], 7, 320, 64), ([1] * 40, 264, 512, 25
            ([1, 0] * 512, 40, 64, 2), ([300] * 9, 200, 2688, 128)]
 
 
-@pytest.mark.parametrize("counts,N,K,g", GROUPED)
+# sizes that take tiles of 128 rows, and of 256 with a last round that is more and less than half full, whole and odd N, one
+# K-tile and many, whole and half
+LARGE_GROUPED = [([700, 1, 900, 130], 1408, 1088, 64), ([1041, 0, 257, 700, 5, 1500], 2688, 1088, 64), ([3000, 100, 5900], 2001, 64, 64),
+                 ([1041, 0, 257, 700, 5, 1500], 2001, 1344, 64), ([3000, 100, 5900], 2688, 128, 128), ([513, 512, 511, 1], 5376, 192, 64)]
+
+
+@pytest.mark.parametrize("counts,N,K,g", GROUPED + LARGE_GROUPED)
 def test_linear_grouped(cr, counts, N, K, g):
     P.say("linear_grouped %d groups N=%d K=%d" % (len(counts), N, K))
     wq, ws = _weights(cr, len(counts), N, K, g, N + K)
@@ -165,6 +171,11 @@ LAYERS = [(1, 1, 1, 64, 64, 64, 64, "mixed"), (1, 8, 64, 256, 512, 256, 256, "mi
           (700, 1, 3, 256, 320, 256, 64, "mixed"), (333, 6, 12, 384, 256, 128, 256, "one"), (1200, 2, 4, 128, 192, 128, 64, "dropped")]
 
 
+# the same for layers: tiles of 128 and 256 rows in the first, the second or both products
+LARGE_LAYERS = [(901, 3, 3, 1088, 1344, 64, 64, "mixed"), (2100, 2, 4, 1344, 4096, 64, 256, "dropped"), (4000, 2, 3, 1344, 64, 64, 64, "twice"),
+                (1500, 3, 5, 2112, 1024, 64, 256, "mixed"), (2100, 2, 4, 1344, 2688, 64, 128, "one")]
+
+
 def _layer(cr, E, F, K, gh, g, seed=1):
     return _weights(cr, E, F, K, g, seed), _weights(cr, E, F, K, g, seed + 1), _weights(cr, E, K, F, gh, seed + 2)
 
@@ -189,7 +200,7 @@ def _expert_by_expert(cr, x, experts, gate, up, down, act, g, gh):
     return pre, d, d64, bound
 
 
-@pytest.mark.parametrize("M,top,E,F,K,gh,g,kind", LAYERS)
+@pytest.mark.parametrize("M,top,E,F,K,gh,g,kind", LAYERS + LARGE_LAYERS)
 def test_moe_ffn_gated(cr, M, top, E, F, K, gh, g, kind):
     P.say("moe_ffn_gated M=%d top=%d E=%d F=%d K=%d %s" % (M, top, E, F, K, kind))
     gate, up, down = _layer(cr, E, F, K, gh, g)
