@@ -117,7 +117,7 @@ def test_linear_grouped_offsets_are_held_to_the_rows(cr):
 
 
 @pytest.mark.parametrize("counts,N,K,g", GROUPED + [([257, 0, 700, 256], 72, 1280, 256), ([1024, 511], 321, 512, 32),
-                                                    ([300, 1], 264, 192, 1)])
+                                                    ([300, 1], 264, 192, 1), ([3000, 100, 5900], 65, 1344, 64), ([4097], 1001, 2688, 128)])
 def test_linear_grouped_backward(cr, counts, N, K, g):
     P.say("linear_grouped_backward %d groups N=%d K=%d" % (len(counts), N, K))
     wq, ws = _weights(cr, len(counts), N, K, g, N + K)
@@ -307,7 +307,9 @@ def test_moe_ffn_gated_extremes(cr):
         assert np.linalg.norm(_np(y[m]) - ref[m]) <= R.BF16 * np.linalg.norm(ref[m]), m
 
 
-BACKWARD = [c for c in LAYERS if c[0] != 16] + [(900, 2, 3, 512, 256, 256, 256, "mixed"), (1100, 1, 4, 320, 448, 64, 64, "one")]
+# (the last two: tiles of 256 rows for both contractions, and for the first alone)
+BACKWARD = [c for c in LAYERS if c[0] != 16] + [(900, 2, 3, 512, 256, 256, 256, "mixed"), (1100, 1, 4, 320, 448, 64, 64, "one"),
+                                                (4000, 2, 3, 1344, 1344, 64, 64, "dropped"), (9000, 1, 2, 1344, 128, 64, 128, "mixed")]
 
 
 @pytest.mark.parametrize("M,top,E,F,K,gh,g,kind", BACKWARD)
