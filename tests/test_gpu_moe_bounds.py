@@ -261,6 +261,24 @@ def test_smallest_alignment(cr):
                            cr.linear_grouped_backward(dh, *gate, offsets, group=64))
 
 
+@pytest.mark.parametrize("M", [5, 90, 700])
+def test_rows_without_an_expert_are_not_read(cr, M):
+    """pre and d of slots without an expert may hold anything, NaN included."""
+    E, top, F, K = 3, 2, 192, 320
+    gate, up, down = _stacked(cr, E, F, K, 64, 1), _stacked(cr, E, F, K, 64, 2), _stacked(cr, E, K, F, 64, 3)
+    experts, w = _routing(M, top, E, 2)
+    experts[0, 1], experts[M // 2] = -1, E
+    none = (experts < 0) | (experts >= E)
+    pre, d, dy = _randn(2, M, top, F, seed=1), _randn(M, top, K, seed=2), _randn(M, K, seed=3)
+    want = cr.moe_ffn_gated_backward(dy, pre, d, experts, w, *gate, *up, *down, group=64, group_h=64)
+    pre[:, none], d[none], w[none] = float("nan"), float("inf"), float("nan")
+    got = cr.moe_ffn_gated_backward(dy, pre, d, experts, w, *gate, *up, *down, group=64, group_h=64)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (got[1][none] == 0).all()
+    x = _randn(M, K, seed=4)
+    y = cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, group=64, group_h=64)
+    assert torch.equal(y, cr.moe_ffn_gated(x, experts, torch.where(none, 0.5, w), *gate, *up, *down, group=64, group_h=64))
+
+
 @pytest.mark.parametrize("M,top", [(5, 2), (90, 2), (700, 2)])
 @pytest.mark.parametrize("value", [float("inf"), float("nan")])
 def test_bad_values_stay_in_their_tokens(cr, M, top, value):
