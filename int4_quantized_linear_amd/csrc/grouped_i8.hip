@@ -28,60 +28,56 @@ struct OrderParams {
     int S, E, top;
 };
 
-// HELD > 0: at most 4 HELD <= 32 slots per thread, requested at once and kept between the two passes as a bit each, so that
-// the second takes as many steps as the fullest lane has rows.  Rows' tokens and scales are filled in by whole waves at the
-// end (24576 slots of 64 experts: 19 us with a division and a load in the second pass's branch over every slot, 11 us so).
+typedef v4i v4i_any __attribute__((aligned(4)));
+
+// Whether a slot with expert x is workgroup e's own (e == E: of none), and whether it has a smaller expert.
+__device__ __forceinline__ bool order_mine(const OrderParams &p, int e, int x)
+{
+    return e == p.E ? (unsigned)x >= (unsigned)p.E : x == e;
+}
+__device__ __forceinline__ bool order_less(int e, int x) { return (unsigned)x < (unsigned)e; }
+
+// Tokens and scales of the rows that the workgroup has put in their places.
+template <int NT>
+__device__ __forceinline__ void order_end(const OrderParams &p, int first, int rows)
+{
+    __syncthreads();
+    for (int r = first + (int)threadIdx.x; r < first + rows; r += NT) {
+        const int token = p.slot_of[r] / p.top;
+        p.token_of[r] = token;
+        if (p.sx) p.sx_of[r] = p.sx[token];
+    }
+}
+
+// Up to 4 HELD <= 32 slots per thread, requested at once and kept between the two passes as a bit each, so that the
+// second takes as many steps as the fullest lane has rows (24576 slots of 64 experts: 19 us with a division and a load in
+// the second pass's branch over every slot, 10 so).
 template <int NT, int HELD>
 __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
 {
     __shared__ int2 part[NT / 64];
     const int t = (int)threadIdx.x, lane = t & 63, e = (int)blockIdx.x;
-    const int chunk = HELD ? 4 * HELD : (((p.S + NT - 1) / NT) + 3) & ~3;
-    const int s0 = min(t * (int64_t)chunk, (int64_t)p.S), s1 = min(s0 + chunk, p.S);
-    const bool none = e == p.E;
-    // mine: of this expert (or of none); less: with a smaller one
-    auto mine = [&](int x) { return none ? (unsigned)x >= (unsigned)p.E : x == e; };
-    auto less = [&](int x) { return (unsigned)x < (unsigned)e; };
-    typedef v4i v4i_any __attribute__((aligned(4)));
-    auto each = [&](auto f) {                            // HELD == 0: from memory
-        int s = s0;
-        for (; s + 4 <= s1; s += 4) {
-            const v4i x = *reinterpret_cast<const v4i_any *>(p.experts + s);
+    const int s0 = min(t * 4 * HELD, p.S), s1 = min(s0 + 4 * HELD, p.S);
+    v4i held[HELD];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f(s + i, x[i]);
-        }
-        for (; s < s1; ++s) f(s, p.experts[s]);
-    };
-    int n_mine = 0, n_less = 0;
-    uint32_t mask = 0;
-    if constexpr (HELD > 0) {
-        v4i held[HELD];
+    for (int i = 0; i < HELD; ++i) {
+        const int s = s0 + 4 * i;
+        if (s + 4 <= s1) held[i] = *reinterpret_cast<const v4i_any *>(p.experts + s);
+        else
 #pragma unroll
-        for (int i = 0; i < HELD; ++i) {
-            const int s = s0 + 4 * i;
-            if (s + 4 <= s1) held[i] = *reinterpret_cast<const v4i_any *>(p.experts + s);
-            else
-#pragma unroll
-                for (int k = 0; k < 4; ++k) held[i][k] = s + k < s1 ? p.experts[s + k] : 0;
-        }
-        const int n = s1 - s0;
-        const uint32_t real = n >= 32 ? ~0u : (1u << n) - 1u;
-        uint32_t below = 0;
-#pragma unroll
-        for (int i = 0; i < 4 * HELD; ++i) {
-            mask |= (uint32_t)mine(held[i / 4][i % 4]) << i;
-            below |= (uint32_t)less(held[i / 4][i % 4]) << i;
-        }
-        mask &= real;
-        n_mine = __popc(mask);
-        n_less = __popc(below & real);
-    } else {
-        each([&](int, int x) {
-            n_mine += mine(x);
-            n_less += less(x);
-        });
+            for (int k = 0; k < 4; ++k) held[i][k] = s + k < s1 ? p.experts[s + k] : 0;
     }
-    int before = n_mine, all = n_less;
+    const int n = s1 - s0;
+    const uint32_t real = n >= 32 ? ~0u : (1u << n) - 1u;
+    uint32_t mask = 0, below = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * HELD; ++i) {
+        mask |= (uint32_t)order_mine(p, e, held[i / 4][i % 4]) << i;
+        below |= (uint32_t)order_less(e, held[i / 4][i % 4]) << i;
+    }
+    mask &= real;
+    const int n_mine = __popc(mask);
+    int before = n_mine, all = __popc(below & real);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
         const int o = __shfl_up(before, d);
@@ -100,25 +96,94 @@ __global__ void __launch_bounds__(NT) moe_order_kernel(OrderParams p)
     }
     if (t == 0) p.offsets[e] = first;
     row += first;
-    auto put = [&](int s) {
-        p.row_of[s] = none ? -1 : row;
-        if (!none) p.slot_of[row] = s;
-        ++row;
+    for (; mask; mask &= mask - 1, ++row) {
+        const int s = s0 + __ffs(mask) - 1;
+        p.row_of[s] = e == p.E ? -1 : row;
+        if (e < p.E) p.slot_of[row] = s;
+    }
+    if (e < p.E) order_end<NT>(p, first, rows);
+}
+
+// Any number of slots: each wavefront takes a run of them, 256 at a time (lane l: 4 l .. 4 l + 3), reads it twice and
+// ranks its own by ballots.  131072 slots of 256 experts: 42 us, each workgroup's two reads of all slots (with the threads' own
+// runs, as above but read twice, 91: a lane's lines are then its own and leave the cache between its reads).
+__global__ void __launch_bounds__(1024) moe_order_long_kernel(OrderParams p)
+{
+    constexpr int NT = 1024, NW = NT / 64, AHEAD = 4;    // blocks requested at once
+    __shared__ int2 part[NW];
+    const int t = (int)threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), e = (int)blockIdx.x;
+    const int run = (((p.S + NW - 1) / NW) + 255) & ~255;
+    const int s0 = (int)min((int64_t)w * run, (int64_t)p.S), s1 = min(s0 + run, p.S);
+    auto load = [&](int b) {                             // (no branch among lanes: one would wait for each load)
+        v4i x = {};
+        const int s = b + 4 * lane;
+        if (b + 256 <= s1) {
+            x = *reinterpret_cast<const v4i_any *>(p.experts + s);
+        } else if (b < s1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = p.experts[min(s + k, p.S - 1)];
+        }
+        return x;
     };
-    if constexpr (HELD > 0) {
-        for (; mask; mask &= mask - 1) put(s0 + __ffs(mask) - 1);
-    } else {
-        each([&](int s, int x) {
-            if (mine(x)) put(s);
-        });
+    auto each = [&](auto f) {
+        for (int b = s0; b < s1; b += 256 * AHEAD) {
+            v4i x[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) x[i] = load(b + 256 * i);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (b + 256 * i < s1) f(b + 256 * i + 4 * lane, x[i]);
+        }
+    };
+    int n_mine = 0, n_less = 0;
+    each([&](int s, const v4i &x) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            n_mine += s + k < s1 && order_mine(p, e, x[k]);
+            n_less += s + k < s1 && order_less(e, x[k]);
+        }
+    });
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        n_mine += __shfl_xor(n_mine, d);
+        n_less += __shfl_xor(n_less, d);
     }
-    if (none) return;
+    if (lane == 0) part[w] = int2{n_mine, n_less};
     __syncthreads();
-    for (int r = first + t; r < first + rows; r += NT) {
-        const int token = p.slot_of[r] / p.top;
-        p.token_of[r] = token;
-        if (p.sx) p.sx_of[r] = p.sx[token];
+    int row = 0, first = 0, rows = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        if (i < w) row += part[i].x;
+        rows += part[i].x;
+        first += part[i].y;
     }
+    if (t == 0) p.offsets[e] = first;
+    row += first;
+    if (__builtin_amdgcn_readfirstlane(n_mine) > 0)
+        each([&](int s, const v4i &x) {
+            bool m[4];
+            uint64_t lanes[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                m[k] = s + k < s1 && order_mine(p, e, x[k]);
+                lanes[k] = __builtin_amdgcn_ballot_w64(m[k]);
+            }
+            if ((lanes[0] | lanes[1] | lanes[2] | lanes[3]) == 0) return;
+            int at = row;                                // the lane's first
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                at += __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes[k] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes[k], 0u));
+                row += __builtin_popcountll(lanes[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (m[k]) {
+                    p.row_of[s + k] = e == p.E ? -1 : at;
+                    if (e < p.E) p.slot_of[at] = s + k;
+                    ++at;
+                }
+        });
+    if (e < p.E) order_end<NT>(p, first, rows);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -490,7 +555,7 @@ hipError_t launch_moe_order(const int32_t *experts, int64_t S, int E, int top, c
     if (S <= 1024) hipLaunchKernelGGL((moe_order_kernel<256, 1>), grid, dim3(256), 0, stream, p);
     else if (S <= 8192) hipLaunchKernelGGL((moe_order_kernel<1024, 2>), grid, dim3(1024), 0, stream, p);
     else if (S <= 32768) hipLaunchKernelGGL((moe_order_kernel<1024, 8>), grid, dim3(1024), 0, stream, p);
-    else hipLaunchKernelGGL((moe_order_kernel<1024, 0>), grid, dim3(1024), 0, stream, p);
+    else hipLaunchKernelGGL(moe_order_long_kernel, grid, dim3(1024), 0, stream, p);
     return hipGetLastError();
 }
 

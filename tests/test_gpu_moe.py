@@ -436,6 +436,25 @@ def test_router_layer_and_gradients_together(cr):
     assert far(y, out) <= 0.03 and far(x.grad, a.grad) <= 0.03 and far(wr.grad, r.grad) <= 0.03
 
 
+@pytest.mark.parametrize("M,top,E,kind", [(11003, 3, 37, "dropped"), (32769, 1, 1024, "mixed"), (16500, 4, 5, "twice"), (40001, 1, 2, "none")])
+def test_many_slots_as_in_parts(cr, M, top, E, kind):
+    """Slots beyond what one pass of the sort keeps: the same bits as the tokens taken a third at a time."""
+    F, K = 64, 128
+    gate, up, down = _layer(cr, E, F, K, 64, 128)
+    experts, w = _experts(M, top, E, M, kind)
+    x, dy, call = _randn(M, K, seed=1), _randn(M, K, seed=2), dict(group=128, group_h=64)
+    y, pre, d = cr.moe_ffn_gated(x, experts, w, *gate, *up, *down, save=True, **call)
+    dx, dw = cr.moe_ffn_gated_backward(dy, pre, d, experts, w, *gate, *up, *down, **call)
+    ok = (experts >= 0) & (experts < E)
+    for at in (slice(0, M // 3), slice(M // 3, 2 * M // 3), slice(2 * M // 3, M)):
+        own = lambda t: t[at].clone()
+        wy, wp, wd = cr.moe_ffn_gated(own(x), own(experts), own(w), *gate, *up, *down, save=True, **call)
+        o = ok[at]
+        assert torch.equal(y[at], wy) and torch.equal(pre[:, at][:, o], wp[:, o]) and torch.equal(d[at][o], wd[o])
+        wx, ww = cr.moe_ffn_gated_backward(own(dy), pre[:, at].clone(), own(d), own(experts), own(w), *gate, *up, *down, **call)
+        assert torch.equal(dx[at], wx) and torch.equal(dw[at], ww)
+
+
 def test_large_rows(cr):
     """Row offsets past 32 bits: 2^31 elements of y, of dy's operand and of the saved arrays."""
     E, N, K, rows = 2, 4096, 64, 600_000                           # 2.46e9 outputs
