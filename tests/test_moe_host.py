@@ -141,7 +141,8 @@ def test_workspace_queries(lib):
     for bad in ((-1, 2, 4, 64, 64), (1, 0, 4, 64, 64), (1, 5, 4, 64, 64), (1, 33, 64, 64, 64), (1, 1, 1025, 64, 64), (1, 1, 4, 65, 64),
                 (1, 1, 4, 64, 0), (1 << 20, 1, 4, 64, 2048)):
         assert cr.workspace_bytes_moe_ffn(*bad) == 0 and cr.workspace_bytes_moe_ffn_backward(*bad) == 0
-    assert cr.workspace_bytes_moe_ffn(9, 2, 4, 64, 128) > 9 * 128 + 18 * 64 * 3 + 18 * 128 * 4
+    # codes of x, h and its codes, and d in 16 bits with a scale per 64 channels
+    assert cr.workspace_bytes_moe_ffn(9, 2, 4, 64, 128) > 9 * 128 + 18 * 64 * 3 + 18 * 128 * 2 + 18 * 2 * 4
 
 
 def test_binding_checks():
