@@ -990,7 +990,8 @@ __global__ void __launch_bounds__(256) grad_bias_kernel(const float *sums, int c
 // mixture-of-experts layer, the gradient of their weights, dweight = sum_n dy[source, n] d[slot, n] in fp32.
 // A workgroup takes one row.  MoE (experts non-null): workgroup = slot, its group the slot's expert, its source the
 // slot's token, its row where the sort put it; slots without an expert get dweight 0 and no row.  Otherwise the
-// workgroup's row itself, and the group whose offsets hold it.  Columns from N to lda are zeros.  Bound by memory.
+// workgroup's row itself, and the group whose offsets hold it.  Columns from N to lda are zeros.  Bound by memory: 8192
+// slots of 2048 tokens, 2048 channels, with dweights 24 us; 4097 rows of 5376 20 us, 4.4 TB/s.
 struct RowsParams {
     const uint16_t *dy;        // [., N]
     const float *sw;           // [groups, N]

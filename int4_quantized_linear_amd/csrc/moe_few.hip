@@ -220,7 +220,8 @@ struct FewParams {
 // ---------------------------------------------------------------------------------------------
 // h: workgroup (x, slot); the first slot of each expert does the expert's work, the others end.  It takes the tiles x,
 // x + gridDim.x, ... of 16 features, so that the rows are quantized once for several; 4 wavefronts take every fourth chunk of K
-// for 16 rows of gate and 16 of up, GP chunks in flight across tiles, and their sums meet in LDS.
+// for 16 rows of gate and 16 of up, GP chunks in flight across tiles, and their sums meet in LDS.  One token, 8 of 64 experts,
+// 2048 -> 2 x 1024: 12 us, of which the 34 MB of weights would take 7 and a launch, the row's rotation and the end the rest.
 constexpr int GNW = 4, GP = 3, GSUMS = GNW * 2 * 4 * 64;
 
 template <bool FUSED, bool F32, int LG>
@@ -346,7 +347,8 @@ __global__ void __launch_bounds__(64 * GNW) moe_few_gate_kernel(FewParams p)
 // y: workgroup = 16 output channels, all experts.  A list in LDS holds the experts' products, at most 16 slots each; each
 // is cut along F into `parts` of CP chunks, so that 4 wavefronts have about 4 each, and wavefront w takes pieces w, w + 4, ...
 // It adds its int32 sums to the slots' in LDS (exact in any order).  Then a thread per token and channel scales,
-// weighs and adds up its slots in their order; what that needs from memory is requested at the start.
+// weighs and adds up its slots in their order; what that needs from memory is requested at the start.  The same token, 1024
+// -> 2048: 11 us, 17 MB: the list, the rotation of 8 rows, one pass of loads and the sums, one after another.
 constexpr int DNW = 4, DP = 4;
 
 template <bool FUSED, int LG>
@@ -526,9 +528,14 @@ void launch_gate(const FewParams &p, dim3 grid, size_t lds, hipStream_t stream)
 bool plan_moe_few(int64_t M, int top, int K, int F, MoeFew &plan)
 {
     if (M * top > MAX_SLOTS) return false;
-    const int rows = M < 16 ? (int)M : 16, slk = (K + KC - 1) / KC, slf = (F + KC - 1) / KC;
-    plan.fuse_x = (int)M * slk <= 64 && rows * slk * KC <= 64 * 1024;
-    plan.fuse_h = (int)M * top * slf <= 64;
+    // How many 256-channel units a workgroup may rotate.  x: the rows of one expert, at most 16 at a time (so the codes take at
+    // most 32 KiB), under its weights' loads; layer calls, us, apart / fused: 12 tokens, 2 of 8, 2048 -> 512, 96 units 26.5 / 24.1;
+    // 4, 2 of 8, 5120 -> 5120, 80 units 113 / 105; 20, 3 of 16, 2048 -> 512, 160 units 34.6 / 31.5; 32, 2 of 8, 2048, 256
+    // units 38.6 / 38.6.  h: all slots, in every workgroup; 8 of 64, 2048 -> 1024, 1 token, 32 units 26.5 / 22.1; 2, 64 units
+    // 33.2 / 32.7; 3, 96 units 41.0 / 42.2; 4, 128 units 52.1 / 54.7.
+    const int slk = (K + KC - 1) / KC, slf = (F + KC - 1) / KC;
+    plan.fuse_x = M * slk <= 256 && (M < 16 ? M : 16) * slk <= 128;
+    plan.fuse_h = M * top * slf <= 64;
     return true;
 }
 
