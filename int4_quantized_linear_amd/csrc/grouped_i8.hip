@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(1024) moe_order_long_kernel(OrderParams p)
 // units, so a unit's epilogue (in the stage of its last K-tile) runs while the next one's first K-tiles arrive; what a
 // unit's start needs from memory, its source rows, scales and slots, is requested one unit ahead, into registers.
 // Few rows per group: bound by the weights' stream; 12 tokens, 8 of 128 experts, 5120 -> 2 x 1280: 166 us, 4.5 TB/s.  301 tokens,
-// 3 of 16, 2688 -> 2 x 1344: 39 us, 3 TB/s: 350 tiles of 21 K-tiles, which wait for their loads.
+// 3 of 16, 2688 -> 2 x 1344: 39 us, 3 TB/s: a K-tile of all 350 tiles takes 1.4 us, 3.9 TB/s, a tile's start and end 8 us.
 constexpr int BN = 128, BK = 128;
 constexpr int NTHREADS = 256;
 
