@@ -284,8 +284,9 @@ enum { CONVROT_SCORE_SOFTMAX = 0, CONVROT_SCORE_SIGMOID = 1 };
  *   experts = the top largest keys, in falling order, ties to the lowest index; keys are compared exactly (in 64 bits with a
  *   bias).  weights[j] = scale * s[experts[j]], or with normalize != 0  scale * s[experts[j]] / (their sum over j).
  * A logit of -inf (or a bias of -inf) masks its expert.  Where fewer than top are left, the rest of the row is expert -1 with
- * weight 0.  A NaN among a row's logits makes the row's weights NaN, as does +inf under a softmax; its experts stay
- * distinct and in range.
+ * weight 0.  A NaN among a row's logits makes all of the row's weights NaN, and a NaN in the bias those of every row; an expert
+ * with one is never chosen.  +inf under a softmax makes the row's weights NaN too, and its experts are then those of the largest
+ * logits that no bias masks.  Experts stay distinct and in range, whatever the logits and the bias hold.
  * Pointers need only their elements' alignment here and in the backward call.  M == 0 is a no-op.
  */
 int convrot_moe_route(const void *logits, int dtype, int64_t M, int64_t E, int top, int score, int normalize,

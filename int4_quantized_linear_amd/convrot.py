@@ -441,8 +441,9 @@ def moe_route(logits: torch.Tensor, top: int, bias: torch.Tensor | None = None, 
     """Router of a mixture of experts: logits [M, E] fp32 or bf16 -> (experts int32 [M, top], weights fp32
     [M, top]).  The experts are the top scores' (s = softmax or sigmoid of the logits; with bias fp32 [E] those of s +
     bias), in falling order, ties to the lowest index; the weights scale * s, divided by the chosen ones' sum with
-    normalize.  A logit of -inf masks its expert; slots that find none get expert -1 and weight 0.  The weights have no
-    autograd history: moe_route_backward."""
+    normalize.  A logit of -inf masks its expert; slots that find none get expert -1 and weight 0.  A NaN logit, or +inf
+    under a softmax, makes its row's weights NaN, a NaN in the bias every row's.  The weights have no autograd history:
+    moe_route_backward."""
     _no_history("moe_route", logits)
     code = _score_code(score)
     M, E = logits.shape

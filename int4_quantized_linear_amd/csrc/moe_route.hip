@@ -160,14 +160,18 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_kernel(RouteParams p)
         for (int r = 0; r < PER; ++r) bias[r] = p.bias[min(64 * r + lane, p.E - 1)];
     }
     load_row(p.logits, p.f32, m, p.E, lane, l);
-    bool bad = false;
+    bool bad = false, infinite = false;
     float most = -__builtin_inff();
 #pragma unroll
     for (int r = 0; r < PER; ++r) {
         bad |= l[r] != l[r];
+        if constexpr (BIAS) bad |= bias[r] != bias[r];
+        infinite |= l[r] == __builtin_inff();
         most = __builtin_fmaxf(most, l[r]);
     }
-    bad = __builtin_amdgcn_ballot_w64(bad) != 0;
+    // a softmax has no shares next to an infinite logit: the row's weights are NaN, and the logits order its experts
+    infinite = !p.sigmoid && __builtin_amdgcn_ballot_w64(infinite) != 0;
+    bad = infinite || __builtin_amdgcn_ballot_w64(bad) != 0;
     double z = 1.0;
     if (!p.sigmoid && (BIAS || !p.normalize)) {
         most = wave_max(most);
@@ -183,7 +187,8 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_kernel(RouteParams p)
         if constexpr (BIAS) {
             const double x = (double)l[r];
             const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)most) / z;
-            key[r] = l[r] > -__builtin_inff() ? ordered(s + (double)bias[r]) : 0u;
+            const double v = infinite && bias[r] > -__builtin_inff() ? x : s + (double)bias[r];
+            key[r] = l[r] > -__builtin_inff() ? ordered(v) : 0u;
         } else {
             key[r] = ordered(l[r]);
         }
