@@ -80,11 +80,14 @@ __device__ __forceinline__ double dpp(double none, double v)
 
 __device__ __forceinline__ uint32_t last_lane(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
 __device__ __forceinline__ float last_lane(float v) { return __uint_as_float(last_lane(__float_as_uint(v))); }
-__device__ __forceinline__ double last_lane(double v)
+__device__ __forceinline__ double from_lane(double v, int lane)
 {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    return __builtin_bit_cast(double, (uint64_t)last_lane((uint32_t)(b >> 32)) << 32 | last_lane((uint32_t)b));
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+__device__ __forceinline__ double last_lane(double v) { return from_lane(v, 63); }
 
 // op over the wavefront, in every lane: within rows of 16 lanes by row_shr 1, 2, 4, 8, then row_bcast 15 and 31.  (Exchanges
 // through LDS take several times as long, and the choice is a chain of them.)
@@ -134,15 +137,19 @@ __device__ __forceinline__ uint64_t ordered(double v)
 __device__ __forceinline__ double log_sigmoid(double l) { return l < 0.0 ? l - log1p(exp(l)) : -log1p(exp(-l)); }
 
 // The weights' common part for lane j < n, which holds the chosen logit l (other lanes: nothing): with normalize the
-// softmax of log s, else s itself.  zmax, z: the row's largest logit and sum of exponentials (softmax scores).
-__device__ __forceinline__ double chosen_share(bool sigmoid, bool normalize, double l, bool valid, float zmax, double z)
+// softmax of log s, else s itself.  zmax, z: the row's largest logit and sum of exponentials (softmax scores).  With normalize,
+// lead: a lane with the largest share.
+__device__ __forceinline__ double chosen_share(bool sigmoid, bool normalize, double l, bool valid, float zmax, double z, int &lead)
 {
+    lead = 0;
     if (!normalize) {
         if (!valid) return 0.0;
         return sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)zmax) / z;
     }
     const double v = sigmoid ? log_sigmoid(l) : l;
     const double most = wave_max(valid ? v : -__builtin_inf());
+    const uint64_t first = __builtin_amdgcn_ballot_w64(valid && v == most);
+    if (first) lead = __builtin_ctzll(first);
     const double e = valid ? exp(v - most) : 0.0;
     return e / wave_sum(e);
 }
@@ -222,7 +229,8 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_kernel(RouteParams p)
         if (lane == j) chosen = at;
     }
     const float value = chosen >= 0 ? load_logit(p.logits, p.f32, m * p.E + chosen) : 0.0f;
-    const double share = chosen_share(p.sigmoid, p.normalize, (double)value, chosen >= 0, most, z);
+    int lead;
+    const double share = chosen_share(p.sigmoid, p.normalize, (double)value, chosen >= 0, most, z, lead);
     if (lane < p.top) {
         p.experts[m * p.top + lane] = chosen;
         p.weights[m * p.top + lane] = bad ? __builtin_nanf("") : chosen < 0 ? 0.0f : (float)(share * (double)p.scale);
@@ -240,11 +248,14 @@ struct RouteGradParams {
     bool f32, sigmoid, normalize;
 };
 
-// With q the shares above and g = scale dweights:
-//   softmax:  dl_i = s_i ((sum of g over the slots that chose i) - sum_j g_j s_j)
-//   softmax normalised: dl_t = q_t (g_t - sum_j g_j q_j);   sigmoid: dl_t = s_t (1 - s_t) g_t, normalised
-//   q_t (1 - s_t) (g_t - sum_j g_j q_j);   the logits that no slot chose get 0.
-// An expert chosen twice gets the sum.
+// With q the shares above, g = scale dweights and G_i the sum of g over the slots that chose i (0 without one):
+//   softmax:  dl_i = s_i (G_i - sum_k s_k G_k)
+//   softmax normalised: dl_t = q_t (g_t - sum_j q_j g_j);   sigmoid: dl_t = s_t (1 - s_t) g_t, normalised
+//   q_t (1 - s_t) (g_t - sum_j q_j g_j);   the logits that no slot chose get 0, and one chosen twice the sum.
+// Where one share is nearly 1 the two terms of its difference agree in all but their last digits, 18 logits ahead of the rest in
+// all that fp32 has, 37 ahead in all of 64 bits.  Both are therefore taken relative to the leading logit's own G (or g), which leaves
+// every difference as it is: the leader's term of the sum is then 0 and the others are small by themselves.  All of it in 64
+// bits, rounded once.
 template <int PER>
 __global__ void __launch_bounds__(64 * WAVES) moe_route_backward_kernel(RouteGradParams p)
 {
@@ -252,8 +263,8 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_backward_kernel(RouteGra
     const int lane = threadIdx.x & 63;
     const int64_t m = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
     if (m >= p.M) return;
-    float s[PER] = {};
-    if (all) load_row(p.logits, p.f32, m, p.E, lane, s);
+    float row[PER] = {};
+    if (all) load_row(p.logits, p.f32, m, p.E, lane, row);
     int chosen = -1;
     double g = 0.0, l = 0.0;
     if (lane < p.top) {
@@ -265,46 +276,64 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_backward_kernel(RouteGra
             if (l == -__builtin_inf()) chosen = -1;      // masked: its weight is a constant 0
         }
     }
-    float most = -__builtin_inff();
-    double z = 1.0;
-    if (all) {
-#pragma unroll
-        for (int r = 0; r < PER; ++r) most = __builtin_fmaxf(most, s[r]);
-        most = wave_max(most);
-        double sum = 0.0;
-#pragma unroll
-        for (int r = 0; r < PER; ++r) {
-            s[r] = s[r] == -__builtin_inff() ? 0.0f : expf(s[r] - most);   // a NaN stays one
-            sum += (double)s[r];
-        }
-        z = wave_sum(sum);
-    }
     const bool valid = chosen >= 0;
-    const double share = chosen_share(p.sigmoid, p.normalize, l, valid, most, z);
-    const double inner = wave_sum(valid ? share * g : 0.0);
-    double d = share * (p.normalize ? g - inner : g);
-    if (p.sigmoid) d *= 1.0 / (1.0 + exp(l));            // 1 - s
-    if (!valid) d = 0.0;
-    // every logit's part: 0 where a row is masked whole (z == 0), NaN in a row with one
-    const float rest = !all || z == 0.0 ? 0.0f : (float)(-inner / z);
-    float out[PER];
-#pragma unroll
-    for (int r = 0; r < PER; ++r) out[r] = s[r] * rest;
+    double d = valid ? g : 0.0;                          // what the slot adds to its logit's entry: G's part, or the gradient
+    if (!all) {
+        int lead;
+        const double share = chosen_share(p.sigmoid, p.normalize, l, valid, 0.0f, 1.0, lead);
+        if (p.normalize) {
+            d = g - from_lane(g, lead);
+            d -= wave_sum(valid ? share * d : 0.0);
+        }
+        d *= share;
+        if (p.sigmoid) d *= 1.0 / (1.0 + exp(l));        // 1 - s
+        if (!valid) d = 0.0;
+    }
+    double v[PER] = {};
     // in slot order, so that an expert chosen twice gets the same sum at every call
-    const float df = (float)d;
     for (int j = 0; j < p.top; ++j) {
         const int at = __builtin_amdgcn_readlane(chosen, j);
-        const float add = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(df), j));
+        const double add = from_lane(d, j);
 #pragma unroll
         for (int r = 0; r < PER; ++r)
-            if (at == 64 * r + lane) out[r] += add;
+            if (at == 64 * r + lane) v[r] += add;
+    }
+    if (all) {
+        float most = -__builtin_inff();
+#pragma unroll
+        for (int r = 0; r < PER; ++r) most = __builtin_fmaxf(most, row[r]);
+        most = wave_max(most);
+        double e[PER], sum = 0.0, lead = 0.0;
+        bool leads = false;
+#pragma unroll
+        for (int r = 0; r < PER; ++r) {
+            e[r] = row[r] == -__builtin_inff() ? 0.0 : exp((double)row[r] - (double)most);   // a NaN stays one
+            sum += e[r];
+            const bool first = row[r] == most && !leads;
+            lead = first ? v[r] : lead;
+            leads |= first;
+        }
+        const double z = wave_sum(sum);
+        const uint64_t lanes = __builtin_amdgcn_ballot_w64(leads);
+        lead = from_lane(lead, lanes ? __builtin_ctzll(lanes) : 0);
+        sum = 0.0;
+#pragma unroll
+        for (int r = 0; r < PER; ++r) {
+            v[r] -= lead;
+            sum += e[r] * v[r];
+        }
+        // (z == 0: a row masked whole; with a NaN in the row it is one)
+        const double inv = z == 0.0 ? 0.0 : 1.0 / z, mean = wave_sum(sum) * inv;
+#pragma unroll
+        for (int r = 0; r < PER; ++r) v[r] = e[r] * inv * (v[r] - mean);
     }
 #pragma unroll
     for (int r = 0; r < PER; ++r) {
         const int i = 64 * r + lane;
         if (i >= p.E) continue;
-        if (p.f32) static_cast<float *>(p.dlogits)[m * p.E + i] = out[r];
-        else static_cast<uint16_t *>(p.dlogits)[m * p.E + i] = (uint16_t)(pack_bf16x2(out[r], 0.0f) & 0xffffu);
+        const float out = (float)v[r];
+        if (p.f32) static_cast<float *>(p.dlogits)[m * p.E + i] = out;
+        else static_cast<uint16_t *>(p.dlogits)[m * p.E + i] = (uint16_t)(pack_bf16x2(out, 0.0f) & 0xffffu);
     }
 }
 
