@@ -340,8 +340,6 @@ size_t convrot_workspace_bytes_grouped_backward(int64_t rows, int64_t groups, in
  *   g, u = the gate and up linears of x[m] with expert e's weights;  h = bf16( act(g) * u )
  *   d[m, j] = linear(h) with expert e's down weight (h rotated in groups of group_h and quantized per slot)
  *   y[m] = bf16( sum_j weights[m, j] * d[m, j] + residual[m] )    in fp32, j in order
- *   (with more than 64 slots, each d goes to the sum in 16 bits with a scale per 64 channels: within 2^-16 of the largest of
- *   the 64)
  * A slot without an expert (one outside [0, E): dropped, or another GPU's) adds nothing; a token with none gets its
  * residual.  The same expert may stand in several slots of a token.
  *   x bf16/fp32 [M, K], M K < 2^31; experts int32 [M, top]; weights fp32 [M, top];
@@ -368,7 +366,6 @@ size_t convrot_workspace_bytes_moe_ffn(int64_t M, int top, int64_t E, int64_t F,
  *   dweights[m, j] = sum_k dy[m,k] * d[m,j,k]   (fp32; 0 for a slot without an expert)
  *   dh = bf16( (bf16(weights[m, j] dy[m] * down_scale) . wq_down) R_h ),  dg = dh * u * act'(g),  du = dh * act(g)
  *   dx[m] = bf16( sum_j (bf16(dg * gate_scale) . wq_gate + bf16(du * up_scale) . wq_up) R + dx_add[m] )
- *   (each slot's part goes to the sum in 16 bits, as d does forward)
  * with the sums in fp32 and in a fixed order (the same call gives the same bits).
  *   dy bf16 [M, K]; pre, d as the forward call saved them (d may be NULL where dweights is); experts, weights
  *   and the expert weights as there; dx bf16 [M, K]; dx_add bf16 [M, K] or NULL, may be dx itself (where the forward's residual

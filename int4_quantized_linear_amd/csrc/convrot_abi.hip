@@ -965,13 +965,12 @@ int check_workspace(const char *who, const void *workspace, size_t bytes, size_t
 }
 
 // The expert layer's workspace: the sort's arrays, then, forward, the codes and scales of x, each row's scale, h, its codes and
-// scales, and d; backward, the two contractions' operands, and dx's parts in the place of the first.  (d and the parts
-// in 16 bits with a scale per 64 values.)
+// scales, and d; backward, the two contractions' operands, and dx's parts over the first.  (d and the parts in fp32.)
 struct MoeLayout {
     size_t offsets = 0, slot_of = 0, token_of = 0, row_of = 0;
     size_t xq = 0, xs = 0, rs = 0, h = 0, hq = 0, hs = 0;
     size_t a = 0, a2 = 0;
-    size_t part = 0, scale = 0, total = 0;
+    size_t part = 0, total = 0;
 };
 
 MoeLayout moe_layout(int64_t M, int top, int64_t E, int64_t F, int64_t K, bool backward)
@@ -990,7 +989,7 @@ MoeLayout moe_layout(int64_t M, int top, int64_t E, int64_t F, int64_t K, bool b
     L.row_of = take(S * 4);
     if (backward) {
         L.a2 = take(S * (size_t)F * 4);
-        L.a = L.part = take(S * (size_t)K * 2);
+        L.a = L.part = take(S * (size_t)K * 4);
     } else {
         L.xq = take((size_t)M * (size_t)K);
         L.xs = take((size_t)M * 4);
@@ -998,9 +997,8 @@ MoeLayout moe_layout(int64_t M, int top, int64_t E, int64_t F, int64_t K, bool b
         L.h = take(S * (size_t)F * 2);
         L.hq = take(S * (size_t)F);
         L.hs = take(S * 4);
-        L.part = take(S * (size_t)K * 2);
+        L.part = take(S * (size_t)K * 4);
     }
-    L.scale = take(S * (size_t)(K / 64) * 4);
     L.total = off;
     return L;
 }
@@ -1225,8 +1223,7 @@ int convrot_moe_ffn_gated(const void *x, int x_dtype, const int32_t *experts, co
     int8_t *xq = reinterpret_cast<int8_t *>(ws + L.xq), *hq = reinterpret_cast<int8_t *>(ws + L.hq);
     float *xs = reinterpret_cast<float *>(ws + L.xs), *hs = reinterpret_cast<float *>(ws + L.hs);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h);
-    uint16_t *part = reinterpret_cast<uint16_t *>(ws + L.part);
-    float *part_scale = reinterpret_cast<float *>(ws + L.scale);
+    float *part = reinterpret_cast<float *>(ws + L.part);
     convrot::MoeFew few;
     if (convrot::plan_moe_few(M, top, (int)K, (int)F, few)) {
         convrot::MoeFewArgs a;
@@ -1303,14 +1300,13 @@ int convrot_moe_ffn_gated(const void *x, int x_dtype, const int32_t *experts, co
     w.wq = wq_down;
     w.sw = down_scale;
     w.part = part;
-    w.part_scale = part_scale;
     w.d = static_cast<uint16_t *>(d);
     w.rows = (int64_t)S;
     w.N = K;
     w.groups = (int)E;
     w.K = (int)F;
     if ((rc = hip_status(convrot::launch_grouped_i8(w, convrot::Epi::Part, stream), "grouped_i8"))) return rc;
-    return hip_status(convrot::launch_moe_combine(part, part_scale, o.row_of, weights, static_cast<const uint16_t *>(residual),
+    return hip_status(convrot::launch_moe_combine(part, o.row_of, weights, static_cast<const uint16_t *>(residual),
                                                   static_cast<uint16_t *>(y), M, (int)K, top, stream),
                       "moe_combine");
 }
@@ -1351,8 +1347,7 @@ int convrot_moe_ffn_gated_backward(const void *dy, const void *pre, const void *
     if ((rc = check_device())) return rc;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const convrot::MoeOrder o = moe_order(ws, L);
-    uint16_t *part = reinterpret_cast<uint16_t *>(ws + L.part);
-    float *part_scale = reinterpret_cast<float *>(ws + L.scale);
+    float *part = reinterpret_cast<float *>(ws + L.part);
     if ((rc = hip_status(convrot::launch_moe_order(experts, (int64_t)S, (int)E, top, o, stream), "moe_order"))) return rc;
     convrot::GroupedRowsArgs r;
     r.dy = static_cast<const uint16_t *>(dy);
@@ -1390,14 +1385,13 @@ int convrot_moe_ffn_gated_backward(const void *dy, const void *pre, const void *
     up.wq1 = wq_gate;
     up.wq2 = wq_up;
     up.part = part;
-    up.part_scale = part_scale;
     up.rows = (int64_t)S;
     up.N = F;
     up.groups = (int)E;
     up.K = (int)K;
     up.log2g = log2i(group);
     if ((rc = hip_status(convrot::launch_grouped_grad(up, stream), "grouped_grad"))) return rc;
-    return hip_status(convrot::launch_moe_combine(part, part_scale, o.row_of, nullptr, static_cast<const uint16_t *>(dx_add),
+    return hip_status(convrot::launch_moe_combine(part, o.row_of, nullptr, static_cast<const uint16_t *>(dx_add),
                                                   static_cast<uint16_t *>(dx), M, (int)K, top, stream),
                       "moe_combine");
 }

@@ -112,65 +112,6 @@ __device__ __forceinline__ uint32_t pack4_i8(uint32_t t0, uint32_t t1, uint32_t 
     return __builtin_amdgcn_perm(p23, p01, 0x05040100u);
 }
 
-// Rows between two kernels in 16 bits: each 64 consecutive values are integers of one scale, max|v| / 32767, off by at most
-// 2^-16 of that maximum (bf16 would be off by 2^-8 of each value).  A NaN or an infinity makes the scale one.
-__device__ __forceinline__ void fixed16_scale(uint32_t most_bits, float &scale, float &inv)
-{
-    const float most = __uint_as_float(most_bits);
-    const float held = most < 0x1p-100f ? 0x1p-100f : most;       // 32767 / held stays finite
-    scale = held * (1.0f / 32767.0f);
-    inv = 32767.0f / held;
-}
-
-// Of 64 values in 8 neighbouring lanes, 8 each; all call, and scale is the same in the 8.
-__device__ __forceinline__ v4u pack_fixed16(const float (&v)[8], float &scale)
-{
-    uint32_t m = 0u;                                     // as integers: a NaN is the largest
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t a = __float_as_uint(v[e]) & 0x7fffffffu;
-        m = a > m ? a : m;
-    }
-    auto larger = [&](uint32_t o) { m = o > m ? o : m; };
-    larger((uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));    // lane ^ 1
-    larger((uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));    // lane ^ 2
-    larger((uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));   // 7 - lane of each 8
-    float inv;
-    fixed16_scale(m, scale, inv);
-    uint32_t t[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = rne_bits(v[e], inv);
-    v4u d;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) d[e] = __builtin_amdgcn_perm(t[2 * e + 1], t[2 * e], 0x05040100u);
-    return d;
-}
-// The same where lanes l, l + 16, l + 32 and l + 48 hold the 64 values, 16 each.
-__device__ __forceinline__ void pack_fixed16_quads(const float (&v)[16], v2u (&d)[4], float &scale)
-{
-    uint32_t m = 0u;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const uint32_t a = __float_as_uint(v[e]) & 0x7fffffffu;
-        m = a > m ? a : m;
-    }
-    const auto r16 = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-    m = r16[0] > r16[1] ? r16[0] : r16[1];
-    const auto r32 = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-    m = r32[0] > r32[1] ? r32[0] : r32[1];
-    float inv;
-    fixed16_scale(m, scale, inv);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            d[e][h] = __builtin_amdgcn_perm(rne_bits(v[4 * e + 2 * h + 1], inv), rne_bits(v[4 * e + 2 * h], inv), 0x05040100u);
-}
-__device__ __forceinline__ float fixed16(uint32_t pair, int high)
-{
-    return (float)(high ? (int)pair >> 16 : (int)(pair << 16) >> 16);
-}
-
 // Low nibbles of eight rne_bits() results -> one dword (nibble i = t[i]).
 __device__ __forceinline__ uint32_t pack8_i4(const uint32_t *t)
 {

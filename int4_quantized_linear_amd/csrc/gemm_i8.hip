@@ -85,8 +85,7 @@ struct GemmParams {
     const int32_t *offsets;
     const int32_t *source;     // the row of xq that a row takes, or null: its own
     const int32_t *slot_of;    // the row of f.pre, or of d, that a row goes to
-    uint16_t *d;               // Part: bf16 [M, N] or null
-    float *part_scale;         // Part: [M, N / 64]; y is its 16-bit rows
+    uint16_t *d;               // Part: bf16 [M, N] or null (y: fp32 [M, N])
     int groups;
 };
 
@@ -105,7 +104,7 @@ constexpr int tile_features() { return E == Epi::Gated ? BN / 2 : BN; }
 // differ.  Those rows' numbers are requested one tile ahead, each wavefront its own 32, into its part of LDS: waiting
 // for them at the tile's start would drain the K-tiles in flight.  Where the last round would be at most half full, its tiles
 // run as two of 128 rows (8192 rows, 16 groups, 5376 x 5376: 322 -> 310 us).
-// 24576 rows of 64 groups: gate and up of 2048 x 1408 211 us, 1340 TOP/s, its down 124 us, 1140 TOP/s; 8192 rows of 16 groups,
+// 24576 rows of 64 groups: gate and up of 2048 x 1408 211 us, 1340 TOP/s, its down to fp32 129 us, 1100 TOP/s; 8192 rows of 16 groups,
 // 5376 x 5376: 291 us, 1630 TOP/s, where one group's 8192 take 212.  The difference is the groups' part tiles (a seventh to a
 // quarter of all), the last round and, with short K, the epilogue, which nothing overlaps.
 // (Tiles of 128 x 256 with two workgroups per CU, one's epilogue under the other's products: 97 KiB of operands requested for
@@ -453,9 +452,9 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                 fence();
             }
         } else if constexpr (GROUPED && E != Epi::Bf16) {
-            // Outputs are formed where the accumulators are, and only their 16 bits pass through the wave's own 8 KiB of LDS
-            // (that of the bf16 branch below).  Expert layer of 4096 tokens, top 6 of 64, 2048 x 1408: 394 us; with the sums
-            // through LDS, as Act and Gated below, 410.  Part in fp32 instead of 16 bits: 20 us more.
+            // Outputs are formed where the accumulators are, and only they pass through the wave's own 8 KiB of LDS (that of the
+            // bf16 branch below).  Gate and up of 24576 rows of 64 groups, 2048 x 1408: 216 us; with the sums through LDS, as Act
+            // and Gated below, 226.
             const float *ls = reinterpret_cast<const float *>(smem + SCALE_OFF + (j & (NSCALE - 1)) * SCALE_BYTES);
             uint8_t *reg = smem + (g & (NST - 1)) * STAGE + w * 1024;
             const int mw = m0 + wm * 64;
@@ -535,9 +534,7 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                 }
                 pass(std::integral_constant<int, 0>{});
             } else {
-                // the bf16 branch's blocks of 32 rows, of the 16-bit rows, or of d's
-                auto pass = [&](auto what) {
-                    constexpr bool D = decltype(what)::value;
+                if (p.d) {                               // the bf16 branch's blocks of 32 rows
 #pragma unroll
                     for (int bp = 0; bp < 2; ++bp) {
                         int row = erow, quad = efq;
@@ -549,64 +546,72 @@ __global__ void __launch_bounds__(NTHREADS, WG_PER_CU) gemm_i8_kernel(GemmParams
                             const int bj = 2 * bp + b2;
                             const float sxm = ls[2 * BN + wm * 64 + 16 * bj + row];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float v[16];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    value4(4 * h + i, bj, *reinterpret_cast<const v4f *>(ls + wn * 128 + 16 * (4 * h + i) + 4 * quad), sxm,
-                                           v + 4 * i);
-                                v2u d[4];
-                                if constexpr (D) {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) d[i] = bf16x4(v + 4 * i);
-                                } else {
-                                    // 64 channels of a row, 16 in each of 4 lanes, 16 apart
-                                    float scale;
-                                    pack_fixed16_quads(v, d, scale);
-                                    const int n = n0 + wn * 128 + 64 * h;
-                                    if (quad == h && mw + 16 * bj + row < Mi && n < Ni)
-                                        p.part_scale[(int64_t)(mw + 16 * bj + row) * (p.N / 64) + n / 64] = scale;
-                                }
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    *reinterpret_cast<v2u *>(to + b2 * OPB + 16 * ((2 * (4 * h + i) + (quad >> 1)) ^ row)) = d[i];
-                                fence();
+                            for (int bi = 0; bi < 8; ++bi) {
+                                float v[4];
+                                value4(bi, bj, *reinterpret_cast<const v4f *>(ls + wn * 128 + 16 * bi + 4 * quad), sxm, v);
+                                *reinterpret_cast<v2u *>(to + b2 * OPB + 16 * ((2 * bi + (quad >> 1)) ^ row)) = bf16x4(v);
                             }
+                            fence();
                         }
                         int rrow = lane >> 4, chunk = lane & 15;
                         asm volatile("" : "+v"(rrow), "+v"(chunk));
                         const int n = n0 + wn * 128 + 8 * chunk;
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            const int mr = mw + 32 * bp + 16 * half;
                             v4u out[4];
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 out[q] = *reinterpret_cast<const v4u *>(reg + half * OPB + 8192 * q + rrow * 256 +
                                                                         16 * ((chunk ^ rrow) ^ (4 * q)));
-                            if constexpr (D) {
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int r = mr + 4 * q + rrow;
-                                    if (r < Mi && n < Ni) *reinterpret_cast<v4u *>(p.d + (int64_t)p.slot_of[r] * p.N + n) = out[q];
-                                }
-                            } else {
-                                if (bp == 1 && half == 1) issue_after_epilogue_reads(g);
-                                const __amdgpu_buffer_rsrc_t ry = __builtin_amdgcn_make_buffer_rsrc(
-                                    static_cast<uint16_t *>(p.y) + (int64_t)mr * p.N, (short)0, NUM_RECORDS, 0x00020000);
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int r = 4 * q + rrow;
-                                    const uint32_t off = mr + r < Mi && n < Ni ? (uint32_t)(r * Ni + n) * 2u : OOB;
-                                    __builtin_amdgcn_raw_buffer_store_b128(out[q], ry, off, 0, 0);
-                                }
+                            for (int q = 0; q < 4; ++q) {
+                                const int r = mw + 32 * bp + 16 * half + 4 * q + rrow;
+                                if (r < Mi && n < Ni) *reinterpret_cast<v4u *>(p.d + (int64_t)p.slot_of[r] * p.N + n) = out[q];
                             }
                             fence();
                         }
                     }
-                };
-                if (p.d) pass(std::true_type{});
-                pass(std::false_type{});
+                }
+                // fp32, 16 rows of 128 columns at a time: row r is the part r % 2 of piece r / 2 (four of 1 KiB, 8 KiB apart, and
+                // four OPB on), its 32 chunks of 16 bytes at chunk ^ r, so that a write's rows and a read's chunks fall on
+                // distinct banks
+#pragma unroll
+                for (int bj = 0; bj < 4; ++bj) {
+                    if (rows) {
+                        int row = erow, quad = efq;
+                        asm volatile("" : "+v"(row), "+v"(quad));
+                        const float sxm = ls[2 * BN + wm * 64 + 16 * bj + row];
+                        uint8_t *to = reg + OPB * (row >> 3) + 8192 * ((row >> 1) & 3) + 512 * (row & 1);
+#pragma unroll
+                        for (int bi = 0; bi < 8; ++bi) {
+                            float v[4];
+                            value4(bi, bj, *reinterpret_cast<const v4f *>(ls + wn * 128 + 16 * bi + 4 * quad), sxm, v);
+                            *reinterpret_cast<v4f *>(to + 16 * ((4 * bi + quad) ^ row)) = v4f{v[0], v[1], v[2], v[3]};
+                        }
+                        fence();
+                    }
+                    int odd = lane >> 5, chunk = lane & 31;
+                    asm volatile("" : "+v"(odd), "+v"(chunk));
+                    const int n = n0 + wn * 128 + 4 * chunk, mr = mw + 16 * bj;
+                    const __amdgpu_buffer_rsrc_t ry = __builtin_amdgcn_make_buffer_rsrc(
+                        static_cast<float *>(p.y) + (int64_t)mr * p.N, (short)0, NUM_RECORDS, 0x00020000);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        v4u out[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            out[q] = *reinterpret_cast<const v4u *>(reg + OPB * half + 8192 * q + 512 * odd +
+                                                                    16 * (chunk ^ (8 * half + 2 * q + odd)));
+                        if (bj == 3 && half == 1) issue_after_epilogue_reads(g);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = 8 * half + 2 * q + odd;
+                            const uint32_t off = mr + r < Mi && n < Ni ? (uint32_t)(r * Ni + n) * 4u : OOB;
+                            __builtin_amdgcn_raw_buffer_store_b128(out[q], ry, off, 0, 0);
+                        }
+                        fence();
+                    }
+                }
             }
         } else if constexpr (E == Epi::Act || E == Epi::Gated) {
             // Two phases per 16-token block, so that the activation's code exists once and not per
@@ -1222,8 +1227,7 @@ hipError_t launch_grouped_gemm_i8(const GroupedArgs &g, Epi epi, hipStream_t str
     p.wq = g.wq;
     p.sx = g.sx;
     p.sw = g.sw;
-    p.y = epi == Epi::Part ? g.part : g.y;
-    p.part_scale = g.part_scale;
+    p.y = epi == Epi::Part ? static_cast<void *>(g.part) : g.y;
     p.M = (int)g.rows;
     p.N = (int)g.N;
     p.K = g.K;

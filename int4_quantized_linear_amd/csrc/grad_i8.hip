@@ -50,8 +50,7 @@ struct GradParams {
     // Grouped (M rows in all, w1, w2 [groups, N, K], next's scales [groups, K]; tiles_m, T_dp and S unused):
     const int32_t *offsets;
     const int32_t *slot_of;    // the row of next.pre that a row has, or null: its own
-    uint16_t *part16;          // non-null: 16-bit rows [M, K] (pack_fixed16) instead of dx
-    float *part_scale;         // and their scales [M, K / 64]
+    float *rows;               // non-null: fp32 rows [M, K] instead of dx
     int groups;
 };
 
@@ -127,10 +126,10 @@ __device__ __forceinline__ void finish8(const GradParams &p, int m, int c, float
         *reinterpret_cast<v4u *>(dst) = d;
     };
     const int64_t o = (int64_t)m * p.K + c;
-    if (GROUPED && p.part16) {
-        float scale;                                     // (8 lanes take 64 channels of a row)
-        *reinterpret_cast<v4u *>(p.part16 + o) = pack_fixed16(v, scale);
-        if (c % 64 == 0) p.part_scale[o / 64] = scale;
+    if (GROUPED && p.rows) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<v4f *>(p.rows + o + 4 * h) = v4f{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
         return;
     }
     if (!p.next.a) {
@@ -1290,8 +1289,7 @@ hipError_t launch_grouped_grad(const GroupedGradArgs &g, hipStream_t stream)
     p.w2 = g.wq2 ? g.wq2 : g.wq1;
     p.add = g.add;
     p.dx = g.dx;
-    p.part16 = g.part;
-    p.part_scale = g.part_scale;
+    p.rows = g.part;
     p.lda = grouped_grad_lda(g.N) * (g.wq2 ? 2 : 1);
     p.M = (int)g.rows;
     p.N = (int)g.N;

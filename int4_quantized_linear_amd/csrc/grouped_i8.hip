@@ -206,8 +206,7 @@ struct GroupedParams {
     const int8_t *wq, *wq2;    // [groups, N, K]
     const float *sw, *sw2;     // [groups, N]
     uint16_t *y;               // Plain: bf16 [rows, N]; Gated: bf16(act(g) u) [rows, N]
-    uint16_t *part;            // Part: 16-bit rows [rows, N]
-    float *part_scale;         // and their scales [rows, N / 64]
+    float *part;               // Part: fp32 [rows, N]
     uint16_t *pre;             // Gated: bf16 [2, pre_rows, N] or null
     uint16_t *d;               // Part: bf16 [slots, N] or null
     int64_t pre_rows;
@@ -408,9 +407,9 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
                 z8(ch, c1, z);
                 if constexpr (E == Epi::Bf16) store8<VEC>(p.y + row * p.N + n, n, p.N, z);
                 if constexpr (E == Epi::Part) {
-                    float scale;
-                    *reinterpret_cast<v4u *>(p.part + row * p.N + n) = pack_fixed16(z, scale);
-                    if (lcol == 0) p.part_scale[row * (p.N / 64) + n / 64] = scale;
+                    float *dst = p.part + row * p.N + n;
+                    *reinterpret_cast<v4f *>(dst) = v4f{z[0], z[1], z[2], z[3]};
+                    *reinterpret_cast<v4f *>(dst + 4) = v4f{z[4], z[5], z[6], z[7]};
                     if (p.d) store8<VEC>(p.d + to * p.N + n, n, p.N, z);
                 }
                 if constexpr (E == Epi::Gated) {
@@ -433,16 +432,17 @@ __global__ void __launch_bounds__(NTHREADS, 2) grouped_tile_kernel(GroupedParams
 }
 
 // ---------------------------------------------------------------------------------------------
-// A thread takes 8 channels of one token; all slots' parts are requested before the first is added, in slot
-// order.  Slots without an expert add nothing.  Bound by memory: 4096 tokens of 6 slots, 2048 channels: 30 us, 4.4 TB/s.
+// A thread takes 4 channels of one token; all slots' parts are requested before the first is added, in slot
+// order.  Slots without an expert add nothing.  Bound by memory: 4096 tokens of 6 slots, 2048 channels: 40 us, 5.8
+// TB/s.  (The parts as 16-bit integers with a scale per 64 channels are half the bytes, 30 us and 5% of that layer, but a channel
+// 1000 times smaller than the largest of the 64 then keeps fewer bits than bf16 has.)
 struct CombineParams {
-    const uint16_t *part;      // 16-bit rows [rows, K]
-    const float *scale;        // [rows, K / 64]
+    const float *part;         // [rows, K]
     const int32_t *row_of;     // [M, top]
     const float *weights;      // [M, top], or null: 1
     const uint16_t *residual;  // bf16 [M, K] or null
     uint16_t *y;
-    int64_t units;             // M K / 8
+    int64_t units;             // M K / 4
     int K, top;
 };
 
@@ -451,38 +451,36 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(CombineParams p)
     constexpr int AHEAD = 8;
     const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (u >= p.units) return;
-    const int per = p.K / 8;
+    const int per = p.K / 4;
     const int64_t m = u / per;
-    const int c = 8 * (int)(u - m * per);
-    v4u res = {};
-    if (p.residual) res = *reinterpret_cast<const v4u *>(p.residual + m * p.K + c);
-    float v[8] = {};
+    const int c = 4 * (int)(u - m * per);
+    v2u res = {};
+    if (p.residual) res = *reinterpret_cast<const v2u *>(p.residual + m * p.K + c);
+    float v[4] = {};
 #pragma unroll 1
     for (int j = 0; j < p.top; j += AHEAD) {
-        v4u a[AHEAD];
+        v4f a[AHEAD];
         float w[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            a[i] = v4u{};
+            a[i] = v4f{};
             w[i] = 0.0f;
             if (j + i < p.top) {
                 const int64_t row = p.row_of[m * p.top + j + i];
                 if (row >= 0) {
-                    a[i] = *reinterpret_cast<const v4u *>(p.part + row * p.K + c);
-                    w[i] = p.scale[row * (p.K / 64) + c / 64];
-                    if (p.weights) w[i] *= p.weights[m * p.top + j + i];
+                    a[i] = *reinterpret_cast<const v4f *>(p.part + row * p.K + c);
+                    w[i] = p.weights ? p.weights[m * p.top + j + i] : 1.0f;
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(w[i], fixed16(a[i][e >> 1], e & 1), v[e]);
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(w[i], a[i][e], v[e]);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += e & 1 ? bf16hi_to_f32(res[e >> 1]) : bf16lo_to_f32(res[e >> 1]);
-    *reinterpret_cast<v4u *>(p.y + m * p.K + c) =
-        v4u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    for (int e = 0; e < 4; ++e) v[e] += e & 1 ? bf16hi_to_f32(res[e >> 1]) : bf16lo_to_f32(res[e >> 1]);
+    *reinterpret_cast<v2u *>(p.y + m * p.K + c) = v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
 constexpr int GRID = 512;                                // two workgroups per CU
@@ -578,7 +576,6 @@ hipError_t launch_grouped_i8(const GroupedArgs &g, Epi epi, hipStream_t stream)
     p.sw2 = g.sw2;
     p.y = g.y;
     p.part = g.part;
-    p.part_scale = g.part_scale;
     p.pre = g.pre;
     p.d = g.d;
     p.pre_rows = g.rows;
@@ -600,24 +597,23 @@ hipError_t launch_grouped_i8(const GroupedArgs &g, Epi epi, hipStream_t stream)
         launch_rows<Epi::Gated, true>(p, bm, stream);
         break;
     default:
-        if (g.N % 64) return hipErrorInvalidValue;
+        if (!vec) return hipErrorInvalidValue;
         launch_rows<Epi::Part, true>(p, bm, stream);
     }
     return hipGetLastError();
 }
 
-hipError_t launch_moe_combine(const uint16_t *part, const float *part_scale, const int32_t *row_of, const float *weights,
-                              const uint16_t *residual, uint16_t *y, int64_t M, int K, int top, hipStream_t stream)
+hipError_t launch_moe_combine(const float *part, const int32_t *row_of, const float *weights, const uint16_t *residual,
+                              uint16_t *y, int64_t M, int K, int top, hipStream_t stream)
 {
     if (M <= 0) return hipSuccess;
     CombineParams p;
     p.part = part;
-    p.scale = part_scale;
     p.row_of = row_of;
     p.weights = weights;
     p.residual = residual;
     p.y = y;
-    p.units = M * (K / 8);
+    p.units = M * (K / 4);
     p.K = K;
     p.top = top;
     const int64_t blocks = (p.units + 255) / 256;

@@ -19,7 +19,7 @@ hipError_t launch_rotate_quant_fp6(const void *x, bool x_f32, int64_t rows, int 
 // Epilogue selector of the integer GEMM / GEMV kernels.
 //   Act:   z = acc * sx[m] * sw[n] + bias[n];  y = bf16(act(z) + residual);  pre = bf16(z)
 //   Gated: two weights share the tokens: g, u as z;  y = bf16(act(g) * u);  pre = bf16([g; u])
-//   Part:  z in 16 bits with a scale per 64 columns (pack_fixed16), d = bf16(z)  (rows sorted by group only)
+//   Part:  z in fp32, d = bf16(z)  (rows sorted by group only)
 enum class Epi { Bf16 = 0, Int32 = 1, Act = 2, Gated = 3, Part = 4 };
 
 // What the Act and Gated epilogues take besides the plain one's arguments (activation.hpp holds
@@ -106,8 +106,8 @@ struct MoeOrder {
 hipError_t launch_moe_order(const int32_t *experts, int64_t S, int E, int top, const MoeOrder &o, hipStream_t stream);
 
 // Products of rows sorted by group with their group's weight, z = acc sx sw:
-//   Bf16: y = bf16(z);   Gated: y = bf16(act(g) u), pre = bf16([g; u]);   Part: part = z in 16 bits, d = bf16(z)
-// Rows of no group are neither read nor written.  Gated: N % 8 == 0; Part: N % 64 == 0.
+//   Bf16: y = bf16(z);   Gated: y = bf16(act(g) u), pre = bf16([g; u]);   Part: part = z in fp32, d = bf16(z)
+// Rows of no group are neither read nor written.  Gated and Part: N % 8 == 0.
 struct GroupedArgs {
     const int8_t *xq = nullptr;           // [rows, K], or with `source` any rows, of fewer than 2^31 bytes in all
     const float *sx = nullptr;            // [rows]
@@ -117,8 +117,7 @@ struct GroupedArgs {
     const int8_t *wq = nullptr, *wq2 = nullptr;   // [groups, N, K]
     const float *sw = nullptr, *sw2 = nullptr;    // [groups, N]
     uint16_t *y = nullptr, *pre = nullptr, *d = nullptr;   // pre [2, rows, N] (or null), d [rows, N] (or null)
-    uint16_t *part = nullptr;             // [rows, N], and its scales [rows, N / 64]
-    float *part_scale = nullptr;
+    float *part = nullptr;                // [rows, N]
     int64_t rows = 0, N = 0;
     int groups = 0, K = 0, act = 0;
 };
@@ -130,8 +129,8 @@ hipError_t launch_grouped_gemm_i8(const GroupedArgs &g, Epi epi, hipStream_t str
 // per weight):
 //   rows:  a[row] = bf16(share dy[source] sw[group]);  with `experts` (one workgroup per slot) share, source and row are the
 //          slot's weight, token and place in the sort, and dweights[slot] = sum dy[token] d[slot] (0 without an expert)
-//   grad:  v = (a . wq[group]) R;  to dx = bf16(v + add), to part = v in 16 bits (with its scales), or on to next.a (GradNext,
-//          its pre [2, rows, K] read at row slot_of[row], its scales [groups, K])
+//   grad:  v = (a . wq[group]) R;  to dx = bf16(v + add), to part = v in fp32, or on to next.a (GradNext, its pre [2, rows, K]
+//          read at row slot_of[row], its scales [groups, K])
 int64_t grouped_grad_lda(int64_t N);
 struct GroupedRowsArgs {
     const uint16_t *dy = nullptr;
@@ -151,17 +150,16 @@ struct GroupedGradArgs {
     const int8_t *wq1 = nullptr, *wq2 = nullptr;
     const uint16_t *add = nullptr;
     uint16_t *dx = nullptr;
-    uint16_t *part = nullptr;
-    float *part_scale = nullptr;
+    float *part = nullptr;                // fp32 [rows, K]
     GradNext next;
     int64_t rows = 0, N = 0;
     int groups = 0, K = 0, log2g = 0;
 };
 hipError_t launch_grouped_grad(const GroupedGradArgs &g, hipStream_t stream);
 
-// y[m] = bf16(sum_j weights[m, j] part[row_of[m, j]] + residual[m])  (weights null: 1; K % 64 == 0).
-hipError_t launch_moe_combine(const uint16_t *part, const float *part_scale, const int32_t *row_of, const float *weights,
-                              const uint16_t *residual, uint16_t *y, int64_t M, int K, int top, hipStream_t stream);
+// y[m] = bf16(sum_j weights[m, j] part[row_of[m, j]] + residual[m])  (weights null: 1; K % 4 == 0).
+hipError_t launch_moe_combine(const float *part, const int32_t *row_of, const float *weights, const uint16_t *residual,
+                              uint16_t *y, int64_t M, int K, int top, hipStream_t stream);
 
 // The expert layer for at most 64 slots (moe_few.hip): plan_moe_few says whether it takes the call and which of
 // the two kernels quantizes its rows itself; where one does not, its codes and scales (xq, xs of the tokens; hq, hs of h's
