@@ -268,8 +268,9 @@ size_t convrot_workspace_bytes_ffn_backward(int64_t M, int64_t F, int64_t K);
  * gated blocks and adds up the results.  Weights of E experts are stacked: int8 [E, N, K] and fp32 [E, N], as
  * convrot_prepare_weight(bits = 8) gives them for the [E N, K] rows.
  * E (and the groups of convrot_linear_grouped) is 1 .. CONVROT_MAX_GROUPS, top 1 .. min(E, CONVROT_MOE_MAX_TOP), and M top (the
- * rows of the grouped calls) below CONVROT_GROUPED_MAX_ROWS; else CONVROT_ERR_SHAPE.  The calls need nothing from the
- * host that depends on the routing, so they can be captured into a graph and replayed on other routings.
+ * rows of the grouped calls) below CONVROT_GROUPED_MAX_ROWS, in the grouped gradients also (rows / 64 + groups) of 256 output
+ * channels each below 2^24; else CONVROT_ERR_SHAPE.  The calls need nothing from the host that depends on the routing, so they
+ * can be captured into a graph and replayed on other routings.
  */
 #define CONVROT_MAX_GROUPS 1024
 #define CONVROT_MOE_MAX_TOP 32

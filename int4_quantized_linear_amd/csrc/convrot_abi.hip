@@ -927,13 +927,14 @@ convrot::RouteArgs route_args(const void *logits, int dtype, const float *bias, 
     return a;
 }
 
-// Rows sorted by group: the rules of check_shape, the limits of the group table, and units (of 64 rows and, forward, 64
-// features) that int can count.
+// Rows sorted by group: the rules of check_shape, the limits of the group table, units (of 64 rows and, forward, 64
+// features) that int can count, and, backward, tiles (of at least 64 rows x 256 channels, 256 threads) that one launch can hold.
 bool grouped_shape_ok(int64_t rows, int64_t groups, int64_t N, int64_t K, bool backward)
 {
     if (rows < 0 || rows >= CONVROT_GROUPED_MAX_ROWS || groups < 1 || groups > CONVROT_MAX_GROUPS || N < 1 ||
         N >= (backward ? CONVROT_BACKWARD_MAX_N : CONVROT_GEMM_MAX_N) || K < 64 || K > CONVROT_MAX_K || K % 64)
         return false;
+    if (backward && (rows / 64 + groups) * ((K + 255) / 256) > ((int64_t)1 << 24) - 8) return false;
     return (rows / 64 + groups) * (((backward ? K : N) + 63) / 64) < ((int64_t)1 << 30);
 }
 
@@ -943,8 +944,9 @@ int check_grouped(const char *who, int64_t rows, int64_t groups, int64_t N, int6
     if (rc) return rc;
     if (!grouped_shape_ok(rows, groups, N, K, backward))
         return fail(CONVROT_ERR_SHAPE, "%s: rows=%lld groups=%lld N=%lld: rows must be in [0, %d), groups in [1, %d], N in "
-                    "[1, %d), and the tiles fewer than 2^30", who, (long long)rows, (long long)groups, (long long)N,
-                    CONVROT_GROUPED_MAX_ROWS, CONVROT_MAX_GROUPS, backward ? CONVROT_BACKWARD_MAX_N : CONVROT_GEMM_MAX_N);
+                    "[1, %d), and the tiles fewer than 2^30 (backward, of 64 rows by 256 channels, than 2^24)", who,
+                    (long long)rows, (long long)groups, (long long)N, CONVROT_GROUPED_MAX_ROWS, CONVROT_MAX_GROUPS,
+                    backward ? CONVROT_BACKWARD_MAX_N : CONVROT_GEMM_MAX_N);
     return CONVROT_OK;
 }
 

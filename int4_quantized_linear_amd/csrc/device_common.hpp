@@ -112,6 +112,15 @@ __device__ __forceinline__ uint32_t pack4_i8(uint32_t t0, uint32_t t1, uint32_t 
     return __builtin_amdgcn_perm(p23, p01, 0x05040100u);
 }
 
+// Grid of a kernel that takes a number of workgroups, of at most 512 threads, without end: a dimension of a launch has to hold
+// fewer than 2^32 work-items.  grid_workgroup: which one this is (past the last: none, they return).
+inline dim3 workgroup_grid(int64_t n)
+{
+    constexpr int64_t MOST = (int64_t)1 << 22;
+    return n <= MOST ? dim3((unsigned)n) : dim3((unsigned)MOST, (unsigned)((n + MOST - 1) / MOST));
+}
+__device__ __forceinline__ int grid_workgroup() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
+
 // Low nibbles of eight rne_bits() results -> one dword (nibble i = t[i]).
 __device__ __forceinline__ uint32_t pack8_i4(const uint32_t *t)
 {

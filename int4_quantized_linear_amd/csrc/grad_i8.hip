@@ -1009,7 +1009,8 @@ __global__ void __launch_bounds__(256) grad_rows_kernel(RowsParams p)
     __shared__ float red[4];
     typedef v4u unaligned __attribute__((aligned(2)));
     typedef v4f v4f_any __attribute__((aligned(4)));
-    const int s = (int)blockIdx.x, t = (int)threadIdx.x;
+    const int s = grid_workgroup(), t = (int)threadIdx.x;
+    if (s >= p.rows) return;
     int64_t row = s, source = s;
     int group = -1;
     float share = 1.0f;
@@ -1276,7 +1277,7 @@ hipError_t launch_grouped_rows(const GroupedRowsArgs &g, hipStream_t stream)
     p.groups = g.groups;
     p.N = (int)g.N;
     p.top = g.top;
-    hipLaunchKernelGGL(grad_rows_kernel, dim3((unsigned)g.rows), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL(grad_rows_kernel, workgroup_grid(g.rows), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 

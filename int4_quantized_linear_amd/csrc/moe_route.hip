@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_kernel(RouteParams p)
 {
     constexpr bool BIAS = sizeof(KEY) == 8;
     const int lane = threadIdx.x & 63;
-    const int64_t m = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
+    const int64_t m = (int64_t)grid_workgroup() * WAVES + (threadIdx.x >> 6);
     if (m >= p.M) return;
     float l[PER], bias[BIAS ? PER : 1];
     if constexpr (BIAS) {
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(64 * WAVES) moe_route_backward_kernel(RouteGra
 {
     const bool all = !p.sigmoid && !p.normalize;         // every logit has a gradient
     const int lane = threadIdx.x & 63;
-    const int64_t m = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
+    const int64_t m = (int64_t)grid_workgroup() * WAVES + (threadIdx.x >> 6);
     if (m >= p.M) return;
     float row[PER] = {};
     if (all) load_row(p.logits, p.f32, m, p.E, lane, row);
@@ -358,7 +358,7 @@ hipError_t launch_moe_route(const RouteArgs &a, int32_t *experts, float *weights
 {
     if (a.M <= 0) return hipSuccess;
     const RouteParams p = {a.logits, a.bias, experts, weights, a.M, a.E, a.top, a.scale, a.f32, a.score != 0, a.normalize};
-    const dim3 grid((unsigned)((a.M + WAVES - 1) / WAVES));
+    const dim3 grid = workgroup_grid((a.M + WAVES - 1) / WAVES);
     if (a.bias) route_per<uint64_t>(p, grid, stream);
     else route_per<uint32_t>(p, grid, stream);
     return hipGetLastError();
@@ -369,7 +369,7 @@ hipError_t launch_moe_route_backward(const RouteArgs &a, const float *dweights, 
 {
     if (a.M <= 0) return hipSuccess;
     const RouteGradParams p = {a.logits, experts, dweights, dlogits, a.M, a.E, a.top, a.scale, a.f32, a.score != 0, a.normalize};
-    const dim3 grid((unsigned)((a.M + WAVES - 1) / WAVES));
+    const dim3 grid = workgroup_grid((a.M + WAVES - 1) / WAVES);
     const dim3 block(64 * WAVES);
     switch (per_lane(a.E)) {
     case 1: hipLaunchKernelGGL(moe_route_backward_kernel<1>, grid, block, 0, stream, p); break;
