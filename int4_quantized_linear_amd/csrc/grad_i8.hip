@@ -1241,7 +1241,8 @@ hipError_t launch_grad_i8(const GradArgs &g, bool gated, hipStream_t stream)
 // Measured, whole calls, 64 / 256 rows:
 //   linear_grouped_backward, rows, groups, N x K:  1000, 4, 2048 x 2688: 36 / 66;   3000, 12, 2048 x 2048: 52 / 67
 //     2000, 8, 2688 x 5376: 92 / 83;   4097, 8, 5376 x 2688: 169 / 153;   8000, 8, 2688 x 2688: 163 / 162
-//   expert layer, tokens, top of E, K x F:  2048, 4 of 32, 2048 x 1408: 276 / 354;   4096, 2 of 16, 2688 x 2688: 505 / 513
+//   expert layer, tokens, top of E, K x F:  2048, 4 of 32, 2048 x 1408: 282 / 343;   4096, 2 of 16, 2688 x 2688: 526 / 505 (the
+//     model takes 64 there)
 int grouped_rows_per_tile(int64_t rows, int groups, int tiles_c, int nt)
 {
     const double used = (double)(groups < rows ? groups : rows);

@@ -499,9 +499,9 @@ void launch_tiles(const GroupedParams &p, hipStream_t stream)
 // Measured, whole calls, 64 / 128 / 256 rows:
 //   linear_grouped, rows, groups, K x N:  2500, 6, 2688 x 1001: 38 / 42 / 67;   2000, 8, 2048 x 2048: 39 / 29 / 36
 //     4000, 8, 2688 x 5376: 148 / 107 / 94;   8192, 16, 5376 x 5376: 591 / 388 / 310
-//   expert layer, tokens, top of E, K x F:  12, 6 of 64, 2048 x 1408: 101 / 107 / 134;  600, 2 of 8, 2688 x 2688: 110 / 122 / 115
-//     1000, 4 of 32, 2048 x 1408: 156 / 145 / 138;   1500, 2 of 8, 5120 x 1280: 192 / 200 / 162;   4096, 6 of 64, 2048 x 1408:
-//     592 / 464 / 382
+//   expert layer, tokens, top of E, K x F:  12, 6 of 64, 2048 x 1408: 100 / 107 / 123;  600, 2 of 8, 2688 x 2688: 111 / 122 / 115
+//     (107 with a height for each product);   1000, 4 of 32, 2048 x 1408: 159 / 147 / 140;   1500, 2 of 8, 5120 x 1280:
+//     196 / 203 / 165;   4096, 6 of 64, 2048 x 1408: 617 / 488 / 406
 int rows_per_tile(int64_t rows, int groups, int64_t N, int K, Epi epi)
 {
     const double cols = (double)N * (epi == Epi::Gated ? 2.0 : 1.0), used = (double)(groups < rows ? groups : rows);

@@ -14,7 +14,7 @@
 // steps and a ballot; only where several lanes have it the low bits and the index decide.  The winner's lane drops it.
 // One token's choice, 8 of 64: 3 us, latency.  8192 tokens, 8 of 256, with a bias: 14 us, bound by instructions, about 1000
 // per token of which the 256 keys take 400 and a choice 45 (both halves of the key reduced and the logits carried: 15.5);
-// their logits are 8 MB, 2 us.  Its gradient, 6 of 128 in bf16: 7 us.
+// their logits are 8 MB, 2 us.  Its gradient, 6 of 128 in bf16: 7.7 us.
 #include "device_common.hpp"
 #include "launchers.hpp"
 
